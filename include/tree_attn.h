@@ -340,6 +340,163 @@ int tree_attn_decode_noalloc(const ta_shape *shape, const void *q, const void *k
                              const void *v_cache, const int32_t *seqlens, float *out, float *lse,
                              int num_splits, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Around the decode step: head vectors of a list of tokens.
+ *
+ * A model's projection yields queries, keys and values as one vector of
+ * head_dim channels per token and head.  The three calls below norm and
+ * rotate them, store them in the caches that the decode calls read, and read
+ * a cache back.  Their vectors are BF16 or FP32 (ta_shape.q_dtype), and all
+ * arithmetic on them is FP32 with one rounding at the end.
+ * ------------------------------------------------------------------------ */
+
+/* Vectors of a token list: element (token t, head h, channel i) is at
+ * data + t*stride_t + h*stride_h + i (elements).  data is 16-byte aligned and
+ * both strides times the element size are multiples of 16 bytes (views of one
+ * packed projection output are fine). */
+typedef struct {
+    void *data;         /* device */
+    int64_t stride_t;
+    int64_t stride_h;
+} ta_heads;
+
+/* The tokens themselves. */
+typedef struct {
+    int32_t num_tokens;        /* T >= 0; a call with T = 0 enqueues nothing */
+    int32_t reserved;          /* must be 0 */
+    const int32_t *positions;  /* device int32 [T]: the token's position in its sequence; a negative
+                                  one marks a padding token, whose outputs are left as they were */
+    const int32_t *rows;       /* device int32 [T]: the token's batch row (cache calls only; negative:
+                                  a padding token), or NULL: token t belongs to row t (T <= batch) */
+} ta_tokens;
+
+/* Per-head RMS norm and position rotation of queries and keys, in one pass:
+ *  norm       y = x * w / sqrt(mean(x^2) + eps)   over the head's channels
+ *  rotation   pair i < rot_dim/2 of y is turned by the angle position * inv_freq[i]:
+ *             (a, b) -> (a cos - b sin, b cos + a sin); the pair is the channels
+ *             (i, i + rot_dim/2), or (2i, 2i+1) with `interleaved`.  Channels from
+ *             rot_dim on are not turned.  The angle is reduced modulo a full turn in
+ *             64-bit fixed point, so far positions lose nothing. */
+typedef struct {
+    const float *inv_freq;   /* device float [rot_dim/2]; NULL only when rot_dim is 0 */
+    const void *q_weight;    /* device [head_dim] of weight_dtype, or NULL: ones (norm only) */
+    const void *k_weight;    /* likewise for keys */
+    int32_t weight_dtype;    /* TA_BF16 or TA_F32 */
+    int32_t rot_dim;         /* a multiple of 16 in [0, head_dim]; 0: no rotation */
+    int32_t interleaved;     /* 0 or 1 */
+    int32_t norm;            /* 0 or 1 */
+    float eps;               /* >= 0 */
+    int32_t reserved;        /* must be 0 */
+} ta_rope;
+
+/* Norm and rotate the queries and keys of a token list.  Of `shape` only
+ * num_q_heads, num_kv_heads, head_dim and q_dtype (the vectors' type) are used;
+ * tokens->rows is ignored.  q and q_out (or k and k_out) may both be NULL: only
+ * the other is done.  An output may be its input (same data and strides), and
+ * must not overlap it otherwise. */
+int tree_attn_norm_rope(const ta_shape *shape, const ta_tokens *tokens, const ta_rope *rope,
+                        const ta_heads *q, const ta_heads *q_out, const ta_heads *k,
+                        const ta_heads *k_out, void *stream);
+
+/* Store the keys and values of a token list in a cache, dense (`paged` NULL)
+ * or paged, with the layouts of tree_attn_decode and tree_attn_decode_paged.
+ * `shape` describes the cache (head_dim 64 or 128, any cache type) and the
+ * vectors' type (q_dtype).
+ *  rope NULL    keys are stored as they are
+ *  rope given   keys are normed and rotated first, in the same pass; with q and
+ *               q_out (both or neither) the tokens' queries are too
+ *  TA_E4M3      a channel x of KV head g is stored as the E4M3 rounding (nearest
+ *               even, finite values saturate at 448) of the FP32 quotient
+ *               x / k_scale[g] (v_scale for values): device float [num_kv_heads],
+ *               positive; both NULL for other caches
+ * Positions not in the list keep what they hold.  A (row, position) should be in the
+ * list once: of several vectors for one place, which is stored is not defined.
+ * A row outside [0, batch), a position outside [0, max_seqlen) or a block-table
+ * entry outside the pool stores nothing for that token and sets the device
+ * error word (TA_ERR_DEVICE_DATA). */
+int tree_attn_cache_write(const ta_shape *shape, const ta_paged_kv *paged, const ta_tokens *tokens,
+                          const ta_rope *rope, const ta_heads *q, const ta_heads *q_out,
+                          const ta_heads *k, const ta_heads *v, void *k_cache, void *v_cache,
+                          const float *k_scale, const float *v_scale, void *stream);
+
+/* Read the keys and values of a token list back: k_out, v_out of type q_dtype,
+ * [T][num_kv_heads][head_dim] by their strides.  E4M3 codes are multiplied by
+ * their head's scale (FP32) before the rounding.  Bad rows, positions or pages
+ * give NaN vectors and set the device error word, as above. */
+int tree_attn_cache_read(const ta_shape *shape, const ta_paged_kv *paged, const ta_tokens *tokens,
+                         const void *k_cache, const void *v_cache, const ta_heads *k_out,
+                         const ta_heads *v_out, const float *k_scale, const float *v_scale,
+                         void *stream);
+
+/* ------------------------------------------------------------------------
+ * Attention to selected pages of a paged cache.
+ *
+ * A decode step over a long cache can leave out the pages whose keys cannot
+ * matter to its queries.  tree_attn_page_bounds keeps, per page and KV head,
+ * the smallest and largest value of every key channel; tree_attn_select_pages
+ * ranks a row's pages by an upper bound of its query group's logits and lists
+ * the best; tree_attn_decode_selected attends to the listed pages only.  With
+ * every page listed the result is tree_attn_decode_paged's.
+ * ------------------------------------------------------------------------ */
+
+/* Update the bounds of the pages that hold a row's last `new_tokens` tokens
+ * [seqlens[b] - new_tokens, seqlens[b]) (<= 0: all of the row's pages), each over
+ * all of the page's valid tokens.
+ *  k_pages   device pool, as for tree_attn_decode_paged
+ *  seqlens   device int32 [batch]
+ *  bounds    device [num_pages][num_kv_heads][2][head_dim], minima then maxima, in
+ *            physical page order: FP32 for FP32 caches, else BF16 (exact: the codes of
+ *            an E4M3 cache without its scale); 16-byte aligned.  A NaN key makes the
+ *            channel's bounds NaN.  Other pages' bounds are left as they were.
+ * Rows may share pages that are full; a partly filled page belongs to one row.
+ * A length outside [0, max_seqlen] or a page outside the pool is skipped and
+ * sets the device error word.  num_q_heads and q_dtype of `shape` are not used
+ * beyond its validation. */
+int tree_attn_page_bounds(const ta_shape *shape, const ta_paged_kv *paged, const void *k_pages,
+                          const int32_t *seqlens, int new_tokens, void *bounds, void *stream);
+
+/* Bytes of device workspace for tree_attn_select_pages (0 for invalid input). */
+size_t tree_attn_select_workspace_bytes(const ta_shape *shape, const ta_paged_kv *paged);
+
+/* List up to `num_select` pages for every (row, KV head).  Of a row's
+ * n = ceil(seqlens[b] / page_size) pages all are listed when n <= num_select; else
+ * the first `first_pages`, the last `last_pages` and, of the rest, those of the
+ * highest score
+ *      score(page) = sum over the group's query heads h and channels i of
+ *                    max(q[h][i] * lo[i], q[h][i] * hi[i])
+ * (the sum over the heads of an upper bound of the page's logits).  Scores are
+ * compared at about twice FP32 precision, equal ones by the lower page; a
+ * page whose bounds or score are not finite ranks first.
+ *  q         device [batch][num_q_heads][head_dim], dense, q_dtype
+ *  bounds    as written by tree_attn_page_bounds
+ *  selected  device int32 [batch][num_kv_heads][num_select]: logical pages in
+ *            ascending order, -1 behind them
+ *  num_select in [1, 65536], first_pages + last_pages <= num_select
+ *  workspace device, >= tree_attn_select_workspace_bytes, 16-byte aligned; contents
+ *            on entry are ignored; calls sharing one must be ordered on the GPU
+ * A bad length lists nothing (-1) and sets the device error word; a page outside the
+ * pool ranks first (decoding it then reports it). */
+int tree_attn_select_pages(const ta_shape *shape, const ta_paged_kv *paged, const void *q,
+                           const void *bounds, const int32_t *seqlens, int num_select,
+                           int first_pages, int last_pages, int32_t *selected, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/* One decode step over the listed pages: tree_attn_decode_paged with row b, KV
+ * head g attending only to the tokens below seqlens[b] of the pages
+ * selected[b][g][0 .. num_select) (logical pages, any order).  Negative entries
+ * and pages past the row's end hold no token; a page listed twice counts
+ * twice; a query that sees no token gives out = 0, lse = -inf.  An entry not
+ * below max_pages_per_seq, a valid page whose block-table entry is outside the
+ * pool, or a bad length makes the affected (row, KV head) NaN and sets the device error
+ * word.  Types: BF16 q with a BF16 cache, BF16 q with an E4M3 cache (head_dim
+ * 128; k_scale, v_scale as in ta_options), FP32 q with an FP32 cache.  Results
+ * are bitwise reproducible; nothing is allocated and no workspace is needed.
+ *  num_select in [1, 65536] */
+int tree_attn_decode_selected(const ta_shape *shape, const ta_paged_kv *paged, const void *q,
+                              const void *k_pages, const void *v_pages, const int32_t *seqlens,
+                              const int32_t *selected, int num_select, float *out, float *lse,
+                              const float *k_scale, const float *v_scale, void *stream);
+
 /* Synchronise `stream`, then read and clear the current device's error word.
  * Returns TA_OK, TA_ERR_DEVICE_DATA, TA_ERR_DEVICE_TIMEOUT or (bounds-checking
  * build) TA_ERR_DEVICE_BOUNDS, or TA_ERR_CUDA when the synchronisation itself

@@ -38,7 +38,9 @@ _EXPORTS = ["tree_attn_status_string", "tree_attn_version", "tree_attn_check_sha
             "tree_attn_workspace_bytes", "tree_attn_pick_splits", "tree_attn_decode",
             "tree_attn_decode_ex", "tree_attn_combine", "tree_attn_get_device_error",
             "tree_attn_decode_noalloc", "tree_attn_launch_count", "tree_attn_decode_paged",
-            "tree_attn_decode_multi", "tree_attn_pick_splits_paged"]
+            "tree_attn_decode_multi", "tree_attn_pick_splits_paged", "tree_attn_norm_rope",
+            "tree_attn_cache_write", "tree_attn_cache_read", "tree_attn_page_bounds",
+            "tree_attn_select_workspace_bytes", "tree_attn_select_pages", "tree_attn_decode_selected"]
 
 
 class TaShape(ctypes.Structure):
@@ -60,6 +62,21 @@ class TaPagedKV(ctypes.Structure):
     _fields_ = [("block_table", ctypes.c_void_p), ("max_pages_per_seq", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class TaHeads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_t", ctypes.c_int64), ("stride_h", ctypes.c_int64)]
+
+
+class TaTokens(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("positions", ctypes.c_void_p), ("rows", ctypes.c_void_p)]
+
+
+class TaRope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("weight_dtype", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("norm", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
 class TreeAttnError(RuntimeError):
@@ -113,6 +130,17 @@ def load(path: str = LIB_PATH):
         lib.tree_attn_launch_count.argtypes = [SP, I32, ctypes.POINTER(TaOptions)]
         lib.tree_attn_launch_count.restype = I32
         lib.tree_attn_get_device_error.argtypes = [P]
+        GP, TP, RP, HP = (ctypes.POINTER(s) for s in (TaPagedKV, TaTokens, TaRope, TaHeads))
+        lib.tree_attn_norm_rope.argtypes = [SP, TP, RP, HP, HP, HP, HP, P]
+        lib.tree_attn_cache_write.argtypes = [SP, GP, TP, RP, HP, HP, HP, HP, P, P, P, P, P]
+        lib.tree_attn_cache_read.argtypes = [SP, GP, TP, P, P, HP, HP, P, P, P]
+        lib.tree_attn_page_bounds.argtypes = [SP, GP, P, P, I32, P, P]
+        lib.tree_attn_select_workspace_bytes.argtypes = [SP, GP]
+        lib.tree_attn_select_workspace_bytes.restype = SZ
+        lib.tree_attn_select_pages.argtypes = [SP, GP, P, P, P, I32, I32, I32, P, P, SZ, P]
+        lib.tree_attn_decode_selected.argtypes = [SP, GP, P, P, P, P, P, I32, P, P, P, P, P]
+        for name in ("norm_rope", "cache_write", "cache_read", "page_bounds", "select_pages", "decode_selected"):
+            getattr(lib, "tree_attn_" + name).restype = I32
         lib.tree_attn_get_device_error.restype = I32
         _lib = lib
         return lib

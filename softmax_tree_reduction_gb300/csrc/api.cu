@@ -16,6 +16,7 @@
 #include <vector>
 
 #include "../../include/tree_attn.h"
+#include "host.h"
 #include "kernels.h"
 
 namespace {
@@ -722,6 +723,36 @@ int decode_impl(const ta_shape* shape, const ta_paged_kv* paged, int nq, int cau
 }
 
 }  // namespace
+
+namespace ta {
+
+int device_info(DeviceInfo* out) {
+    DeviceState* ds = nullptr;
+    const int rc = device_state(&ds);
+    if (rc != TA_OK) return rc;
+    out->device = ds->device;
+    out->num_sms = ds->num_sms;
+    out->err = ds->err;
+    return TA_OK;
+}
+
+int cache_layout(const ta_shape* shape, const ta_paged_kv* paged, CacheLayout* out) {
+    if (!shape) return TA_ERR_NULL;
+    int rc = paged ? check_paged(shape, paged) : TA_OK;
+    if (rc != TA_OK) return rc;
+    Strides st;
+    rc = check_shape(shape, &st, paged ? paged->page_size : 0);
+    if (rc != TA_OK) return rc;
+    out->stride_b = st.b;
+    out->stride_h = st.h;
+    out->stride_t = st.t;
+    out->elem_bytes = elem_bytes(shape->kv_dtype);
+    out->page_shift = 0;
+    while (paged && (1 << out->page_shift) < paged->page_size) ++out->page_shift;
+    return TA_OK;
+}
+
+}  // namespace ta
 
 extern "C" {
 

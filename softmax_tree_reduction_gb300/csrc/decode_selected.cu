@@ -1,0 +1,804 @@
+// Decode attention over listed pages of a paged cache.
+//
+// For (row b, KV head g) the tokens are those of the pages selected[b][g][..]
+// below the row's length; the state (m, l, o) over them and its merges are
+// those of the split-KV kernels.  A list is short against the cache (a few
+// thousand tokens), so the call is bound by HBM bandwidth only when many
+// lists run at once, and otherwise by the chain of one block: length and list
+// -> block table -> keys and values -> merge.
+//
+// The unit of work is a slab of 16 tokens of one page (pages hold a multiple
+// of 16).  The thread blocks of one list form a cluster (up to 16 blocks) and
+// slab u goes to warp u mod (warps of the cluster), so neighbouring warps read
+// neighbouring tokens.  Every warp copies its slabs itself, row by row with
+// 16-byte cp.async, into a ring of its own (stages x (16 keys + 16 values)): no
+// barrier between warps until the end, any layout and page order at the same
+// cost, and rows past the length are zero-filled instead of read.  Page
+// numbers are looked up for 32 of a warp's slabs at a time, one per lane, a
+// window ahead.  The products are the warp-level ones of the split-KV kernels
+// (memory-bound: at 4 heads per KV head the tensor pipe has an order of
+// magnitude to spare), and the blocks' states merge through distributed shared
+// memory, so a step is one launch with no workspace and no counters.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <mutex>
+
+#include "common.cuh"
+#include "host.h"
+#include "kernels.h"
+#include "warp_mma.cuh"
+
+namespace ta {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kSelThreads = 32 * kWarps;
+constexpr int kMaxCluster = 16;
+constexpr int kSlab = 16;           // tokens
+constexpr float kPScale = 16384.f;  // 2^14: P's FP16 hi + lo parts keep small weights (E4M3 caches)
+
+struct SelParams {
+    const void* q;             // [B][Hq][d]
+    const void* k;
+    const void* v;
+    const int32_t* seqlens;
+    const int32_t* selected;   // [B][Hkv][num_select]
+    const int32_t* block_table;
+    const float* k_scale;
+    const float* v_scale;
+    float* out;
+    float* lse;
+    int* err;
+    int64_t sb, sh, st;        // elements
+    int Hq, Hkv, G, S, num_select, ngroups;  // ngroups: column groups per KV head
+    int max_pages, page_shift, num_pages;
+    int C;                     // blocks per cluster
+    float scale_log2;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t pair16) {
+    uint32_t r;
+    const uint16_t x = static_cast<uint16_t>(pair16);
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t d;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+    return d;
+}
+
+// One list's slabs as seen by one warp: lane i of a window holds the place of
+// the warp's slab 32 w + i (element offset into the pools, valid tokens).
+struct SlabWindow {
+    int64_t off;
+    int nv;
+};
+
+struct SlabList {
+    const SelParams& p;
+    const int32_t* sel;
+    const int32_t* table;
+    int N, g, gw, W, U;  // length, KV head, this warp, warps, slabs of the list
+    int lane;
+    int bad;
+
+    __device__ __forceinline__ SlabList(const SelParams& p_, int b, int g_, int N_, int gw_, int W_)
+        : p(p_), g(g_), N(N_), gw(gw_), W(W_), bad(0) {
+        lane = threadIdx.x & 31;
+        sel = p.selected + (static_cast<int64_t>(b) * p.Hkv + g) * p.num_select;
+        table = p.block_table + static_cast<int64_t>(b) * p.max_pages;
+        U = N > 0 ? p.num_select << (p.page_shift - 4) : 0;  // at most 2^16 * 2^6
+    }
+    __device__ __forceinline__ int count() const { return U > gw ? (U - gw + W - 1) / W : 0; }
+    // list entry of this lane's slab in the window starting at the warp's slab i0 (-1: none)
+    __device__ __forceinline__ int entry(int i0) const {
+        const int64_t u = gw + static_cast<int64_t>(i0 + lane) * W;
+        return u < U ? __ldg(sel + (u >> (p.page_shift - 4))) : -1;
+    }
+    // its place, once the entry has arrived
+    __device__ __forceinline__ SlabWindow place(int i0, int e) {
+        SlabWindow w;
+        w.off = 0;
+        w.nv = 0;
+        if (e >= p.max_pages) {
+            bad = 1;
+            return w;
+        }
+        const int64_t u = gw + static_cast<int64_t>(i0 + lane) * W;
+        const int sub = static_cast<int>(u & ((1 << (p.page_shift - 4)) - 1));
+        const int64_t t0 = (static_cast<int64_t>(e) << p.page_shift) + sub * kSlab;
+        if (e < 0 || t0 >= N) return w;
+        const int page = __ldg(table + e);
+        if (page < 0 || page >= p.num_pages) {
+            bad = 1;
+            return w;
+        }
+        w.nv = static_cast<int>(min(static_cast<int64_t>(kSlab), N - t0));
+        w.off = page * p.sb + g * p.sh + static_cast<int64_t>(sub) * kSlab * p.st;
+        return w;
+    }
+};
+
+// The warps' states, [warp][column][D + 4] numerators and [warp][column]
+// maxima (log2 units) and denominators in shared memory, become the outputs of
+// the list's columns [0, ncol): merged over the block's warps, then over the
+// cluster's blocks.  kFp8: numerators of channel c sit at (c % 16) * 8 + c / 16
+// and still lack V's scale.
+template <int D, bool kFp8>
+__device__ void finish_list(const SelParams& p, int b, int hq0, int ncol, int kCols, float vscale, const float* mg_o,
+                            const float* mg_m, const float* mg_l, float* cs_o, float* cs_m, float* cs_l, bool poison) {
+    constexpr int MS = D + 4;
+    const int tid = threadIdx.x;
+    const float nan = __int_as_float(0x7fc00000);
+    const size_t row0 = static_cast<size_t>(b) * p.Hq + hq0;
+    for (int idx = tid; idx < ncol * D; idx += kSelThreads) {
+        const int h = idx / D, dd = idx - h * D;
+        const int pos = kFp8 ? (dd % 16) * 8 + dd / 16 : dd;
+        float mw[kWarps], M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            mw[w] = mg_m[w * kCols + h];
+            M = fmaxf(M, mw[w]);
+        }
+        const float Ms = (M == -INFINITY) ? 0.f : M;
+        float ow[kWarps], lw[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float wt = ex2(mw[w] - Ms);
+            ow[w] = wt * mg_o[(w * kCols + h) * MS + pos];
+            lw[w] = wt * mg_l[w * kCols + h];
+        }
+        float o = tree_sum<kWarps>(ow);
+        const float l = tree_sum<kWarps>(lw);
+        if (kFp8) o *= vscale;
+        if (p.C > 1) {
+            cs_o[idx] = poison ? nan : o;
+            if (dd == 0) {
+                cs_m[h] = poison ? nan : M;
+                cs_l[h] = poison ? nan : l;
+            }
+        } else {
+            p.out[(row0 + h) * D + dd] = poison ? nan : (l == 0.f ? 0.f : o / l);
+            if (dd == 0 && p.lse) p.lse[row0 + h] = poison ? nan : (l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2);
+        }
+    }
+    if (p.C == 1) return;
+    cluster_sync_all();
+    const int rank = static_cast<int>(cluster_rank());
+    const int items = ncol * D, per = (items + p.C - 1) / p.C;
+    const int i1 = min(items, (rank + 1) * per);
+    for (int idx = rank * per + tid; idx < i1; idx += kSelThreads) {
+        const int h = idx / D, dd = idx - h * D;
+        float mq[kMaxCluster], lq[kMaxCluster], oq[kMaxCluster], M = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+            const bool on = c < p.C;
+            mq[c] = on ? ld_dsmem(dsmem_addr(cs_m + h, c)) : -INFINITY;
+            lq[c] = on ? ld_dsmem(dsmem_addr(cs_l + h, c)) : 0.f;
+            oq[c] = on ? ld_dsmem(dsmem_addr(cs_o + idx, c)) : 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) M = fmaxf(M, mq[c]);
+        const float Ms = (M == -INFINITY) ? 0.f : M;
+        float L = 0.f, O = 0.f;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+            const float w = (mq[c] == -INFINITY) ? 0.f : ex2(mq[c] - Ms);
+            L = fmaf(w, lq[c], L);
+            O = fmaf(w, oq[c], O);
+        }
+        p.out[(row0 + h) * D + dd] = (L == 0.f) ? 0.f : O / L;  // NaN of a poisoned block propagates
+        if (dd == 0 && p.lse) p.lse[row0 + h] = (L == 0.f) ? -INFINITY : (M + log2f(L)) * kLn2;
+    }
+    cluster_sync_all();  // no block's state goes away while a peer reads it
+}
+
+// ------------------------------------------------------------ tensor cores
+template <int D, bool kFp8>
+struct SelCfg {
+    static constexpr int kRowBytes = kFp8 ? D : 2 * D;
+    static constexpr int kChunks = kRowBytes / 16;            // 16-byte chunks per row
+    static constexpr int kSlabBytes = kSlab * kRowBytes;
+    static constexpr int kStageBytes = 2 * kSlabBytes;        // keys, values
+    static constexpr int kStages = 24576 / kStageBytes;       // 24 KB a warp
+    static constexpr int kCols = 16;
+    static constexpr int kRing = kWarps * kStages * kStageBytes;
+    static constexpr int kMeta = kWarps * kStages * 4 + 16;
+    static constexpr int kSmem = kRing + kMeta;
+    // merge buffers reuse the ring
+    static_assert((kWarps * kCols * (D + 4 + 2) + kCols * (D + 2)) * 4 <= kRing, "merge buffers");
+    static_assert(kStages >= 3 && kSmem <= 227 * 1024, "ring");
+};
+
+template <int D, int NT, bool kFp8>
+__global__ void __launch_bounds__(kSelThreads, 1) decode_selected_kernel(const SelParams p) {
+    using Cf = SelCfg<D, kFp8>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    int* nvs_all = reinterpret_cast<int*>(smem + Cf::kRing);
+    int* bad_flag = nvs_all + kWarps * Cf::kStages;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int gid = lane >> 2, tig = lane & 3, r8 = lane & 7;
+    const int g = blockIdx.y / p.ngroups, cg = blockIdx.y - g * p.ngroups, b = blockIdx.z;
+    const int ncol = min(16, p.G - 16 * cg);
+    const int hq0 = g * p.G + 16 * cg;
+    if (threadIdx.x == 0) *bad_flag = 0;
+    __syncthreads();
+    wait_primary();
+    allow_dependents();
+
+    int N = p.seqlens[b];
+    const bool bad_len = N < 0 || N > p.S;
+    if (bad_len) N = 0;
+    SlabList list(p, b, g, N, blockIdx.x * kWarps + warp, p.C * kWarps);
+    const int n_it = list.count();
+    int e_next = list.entry(0);
+
+    // q fragments (B operand of S^T = K Q^T): column n of n-tile t is query head
+    // hq0 + 8 t + n.  BF16 caches: as it is.  E4M3: FP16, times the power of two
+    // that brings the largest |q| of the group into [2^14, 2^15), in the channel
+    // order of the key bytes (k-step kk of lane tig: channels 32 tig + 4 kk ..).
+    uint32_t qb[NT][D / 16][2];
+    float sl2 = p.scale_log2, vscale = 1.f;
+    {
+        const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(p.q) + (static_cast<size_t>(b) * p.Hq + hq0) * D;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int c = nt * 8 + gid;
+            const bool on = c < ncol;
+            const __nv_bfloat16* qh = q0 + (on ? c : 0) * D;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t* w = reinterpret_cast<const uint32_t*>(qh + (kFp8 ? 32 * tig + 4 * kk : 16 * kk + 2 * tig));
+                qb[nt][kk][0] = on ? w[0] : 0u;
+                qb[nt][kk][1] = on ? w[kFp8 ? 1 : 4] : 0u;
+            }
+        }
+        if constexpr (kFp8) {
+            auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
+            auto hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
+            float amax = 0.f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        amax = fmaxf(amax, fmaxf(fabsf(lo(qb[nt][kk][i])), fabsf(hi(qb[nt][kk][i]))));
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+            int qexp = 0;
+            if (amax > 0.f && amax < INFINITY) {
+                int e;
+                frexpf(amax, &e);
+                qexp = max(-100, min(100, 15 - e));
+            }
+            const float qs = ldexpf(1.f, qexp);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        qb[nt][kk][i] = half2_bits(__floats2half2_rn(lo(qb[nt][kk][i]) * qs, hi(qb[nt][kk][i]) * qs));
+            sl2 *= __ldg(p.k_scale + g) / qs;
+            vscale = __ldg(p.v_scale + g) / kPScale;
+        }
+    }
+
+    float m[NT][2], l[NT][2], oacc[NT][D / 16][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt)
+            oacc[nt][mt][0] = oacc[nt][mt][1] = oacc[nt][mt][2] = oacc[nt][mt][3] = 0.f;
+    }
+
+    const uint32_t ring = smem_u32(smem) + warp * Cf::kStages * Cf::kStageBytes;
+    volatile int* nvs = nvs_all + warp * Cf::kStages;
+    SlabWindow win = list.place(0, e_next), win_next = win;
+    const uint8_t* kbytes = static_cast<const uint8_t*>(p.k);
+    const uint8_t* vbytes = static_cast<const uint8_t*>(p.v);
+    const int es = kFp8 ? 1 : 2;
+
+    // Start the copies of the warp's slab i into stage i % kStages (one group).
+    auto issue = [&](int i) {
+        if (i < n_it) {
+            const int j = i & 31;
+            if (j == 0 && i > 0) win = win_next;
+            if (j == 0) e_next = list.entry(i + 32);
+            if (j == 16) win_next = list.place(i - 16 + 32, e_next);
+            const int nv = __shfl_sync(0xffffffffu, win.nv, j);
+            const int64_t off = __shfl_sync(0xffffffffu, win.off, j) * es;
+            const int s = i % Cf::kStages;
+            if (lane == 0) nvs[s] = nv;
+            if (nv > 0) {
+                const uint32_t dst = ring + s * Cf::kStageBytes;
+#pragma unroll
+                for (int x = 0; x < kSlab * Cf::kChunks / 32; ++x) {
+                    const int idx = x * 32 + lane, r = idx / Cf::kChunks, c = idx % Cf::kChunks;
+                    const int bytes = r < nv ? 16 : 0;
+                    const int64_t o = off + (r < nv ? r : 0) * p.st * es + c * 16;
+                    const uint32_t d = dst + r * Cf::kRowBytes + ((c ^ (r & 7)) << 4);
+                    cp_async16(d, kbytes + o, bytes);
+                    cp_async16(d + Cf::kSlabBytes, vbytes + o, bytes);
+                }
+            }
+        }
+        cp_async_commit();
+    };
+
+    // fragment addresses within a slab; chunk c of row r sits at chunk c ^ (r & 7)
+    const uint32_t k_lane = (r8 + 8 * ((lane >> 3) & 1)) * Cf::kRowBytes;
+    const int k_chi = lane >> 4;
+    const uint32_t v_lane = (r8 + 8 * (lane >> 4)) * Cf::kRowBytes;
+    const int v_chi = (lane >> 3) & 1;
+
+#pragma unroll
+    for (int i = 0; i < Cf::kStages - 1; ++i) issue(i);
+    for (int it = 0; it < n_it; ++it) {
+        cp_async_wait<Cf::kStages - 2>();
+        __syncwarp();  // the slab is in shared memory for every lane; every lane is done with the one before
+        issue(it + Cf::kStages - 1);
+        const int s = it % Cf::kStages;
+        const int nv = nvs[s];
+        if (nv <= 0) continue;
+        const uint32_t kbase = ring + s * Cf::kStageBytes, vbase = kbase + Cf::kSlabBytes;
+
+        // S^T[16 tokens x columns] = K Q^T, two accumulators per n-tile
+        float sacc[2][NT][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sacc[u][nt][e] = 0.f;
+        if constexpr (kFp8) {
+            const uint32_t ra = kbase + gid * 128, rb = ra + 8 * 128;
+            const int c0 = ((2 * tig) ^ gid) << 4, c1 = ((2 * tig + 1) ^ gid) << 4;
+            const uint4 ka0 = lds128(ra + c0), ka1 = lds128(ra + c1), kb0 = lds128(rb + c0), kb1 = lds128(rb + c1);
+            const uint32_t wa[8] = {ka0.x, ka0.y, ka0.z, ka0.w, ka1.x, ka1.y, ka1.z, ka1.w};
+            const uint32_t wb[8] = {kb0.x, kb0.y, kb0.z, kb0.w, kb1.x, kb1.y, kb1.z, kb1.w};
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t a[4] = {e4m3x2_to_f16x2(wa[kk] & 0xffffu), e4m3x2_to_f16x2(wb[kk] & 0xffffu),
+                                       e4m3x2_to_f16x2(wa[kk] >> 16), e4m3x2_to_f16x2(wb[kk] >> 16)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_f16(sacc[kk & 1][nt], a, qb[nt][kk][0], qb[nt][kk][1]);
+            }
+        } else {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                uint32_t a[4];
+                ldsm_x4(a, kbase + k_lane + (((2 * kk + k_chi) ^ r8) << 4));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_bf16(sacc[kk & 1][nt], a, qb[nt][kk][0], qb[nt][kk][1]);
+            }
+        }
+        // online softmax per column; P^T as B fragments in two parts
+        uint32_t bh[NT][2], bl[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float s0 = (sacc[0][nt][0] + sacc[1][nt][0]) * sl2, s1 = (sacc[0][nt][1] + sacc[1][nt][1]) * sl2;
+            float s2 = (sacc[0][nt][2] + sacc[1][nt][2]) * sl2, s3 = (sacc[0][nt][3] + sacc[1][nt][3]) * sl2;
+            if (nv < kSlab) {
+                if (gid >= nv) s0 = s1 = -INFINITY;
+                if (gid + 8 >= nv) s2 = s3 = -INFINITY;
+            }
+            float bm0 = fmaxf(s0, s2), bm1 = fmaxf(s1, s3);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) {
+                bm0 = fmaxf(bm0, __shfl_xor_sync(0xffffffffu, bm0, off));
+                bm1 = fmaxf(bm1, __shfl_xor_sync(0xffffffffu, bm1, off));
+            }
+            const float mn0 = fmaxf(m[nt][0], bm0), mn1 = fmaxf(m[nt][1], bm1);
+            const float ms0 = (mn0 == -INFINITY) ? 0.f : mn0, ms1 = (mn1 == -INFINITY) ? 0.f : mn1;
+            const float al0 = ex2(m[nt][0] - ms0), al1 = ex2(m[nt][1] - ms1);
+            const float p0 = ex2(s0 - ms0), p1 = ex2(s1 - ms1), p2 = ex2(s2 - ms0), p3 = ex2(s3 - ms1);
+            l[nt][0] = l[nt][0] * al0 + (p0 + p2);
+            l[nt][1] = l[nt][1] * al1 + (p1 + p3);
+            m[nt][0] = mn0;
+            m[nt][1] = mn1;
+            if (__any_sync(0xffffffffu, (al0 != 1.f) || (al1 != 1.f))) {
+#pragma unroll
+                for (int mt = 0; mt < D / 16; ++mt) {
+                    oacc[nt][mt][0] *= al0;
+                    oacc[nt][mt][1] *= al1;
+                    oacc[nt][mt][2] *= al0;
+                    oacc[nt][mt][3] *= al1;
+                }
+            }
+            if constexpr (kFp8) {
+                const float q0 = p0 * kPScale, q1 = p1 * kPScale, q2 = p2 * kPScale, q3 = p3 * kPScale;
+                const __half2 h01 = __floats2half2_rn(q0, q1), h23 = __floats2half2_rn(q2, q3);
+                const float2 f01 = __half22float2(h01), f23 = __half22float2(h23);
+                bh[nt][0] = movtrans(half2_bits(h01));
+                bh[nt][1] = movtrans(half2_bits(h23));
+                bl[nt][0] = movtrans(half2_bits(__floats2half2_rn(q0 - f01.x, q1 - f01.y)));
+                bl[nt][1] = movtrans(half2_bits(__floats2half2_rn(q2 - f23.x, q3 - f23.y)));
+            } else {
+                const __nv_bfloat162 h01 = __floats2bfloat162_rn(p0, p1), h23 = __floats2bfloat162_rn(p2, p3);
+                const float2 f01 = __bfloat1622float2(h01), f23 = __bfloat1622float2(h23);
+                bh[nt][0] = movtrans(bf16x2_bits(h01));
+                bh[nt][1] = movtrans(bf16x2_bits(h23));
+                bl[nt][0] = movtrans(bf16x2_bits(__floats2bfloat162_rn(p0 - f01.x, p1 - f01.y)));
+                bl[nt][1] = movtrans(bf16x2_bits(__floats2bfloat162_rn(p2 - f23.x, p3 - f23.y)));
+            }
+        }
+        // O^T += V^T P^T (rows past the length were zero-filled)
+        if constexpr (kFp8) {
+            const int t0 = 2 * tig;  // rows t0, t0 + 1, t0 + 8, t0 + 9; channels 16 gid ..
+            const uint32_t c0 = (gid ^ t0) << 4, c1 = (gid ^ (t0 + 1)) << 4;
+            const uint4 va = lds128(vbase + t0 * 128 + c0), vb = lds128(vbase + (t0 + 1) * 128 + c1);
+            const uint4 vc = lds128(vbase + (t0 + 8) * 128 + c0), vd = lds128(vbase + (t0 + 9) * 128 + c1);
+            const uint32_t xa[4] = {va.x, va.y, va.z, va.w}, xb[4] = {vb.x, vb.y, vb.z, vb.w};
+            const uint32_t xc[4] = {vc.x, vc.y, vc.z, vc.w}, xd[4] = {vd.x, vd.y, vd.z, vd.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t sel = half ? 0x7362u : 0x5140u;  // byte pairs of two token rows
+                    const uint32_t pa = prmt(xa[w], xb[w], sel), pc = prmt(xc[w], xd[w], sel);
+                    const uint32_t a[4] = {e4m3x2_to_f16x2(pa & 0xffffu), e4m3x2_to_f16x2(pa >> 16),
+                                           e4m3x2_to_f16x2(pc & 0xffffu), e4m3x2_to_f16x2(pc >> 16)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f16(oacc[nt][2 * w + half], a, bh[nt][0], bh[nt][1]);
+                        mma_f16(oacc[nt][2 * w + half], a, bl[nt][0], bl[nt][1]);
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt) {
+                uint32_t a[4];
+                ldsm_x4_t(a, vbase + v_lane + (((2 * mt + v_chi) ^ r8) << 4));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma_bf16(oacc[nt][mt], a, bh[nt][0], bh[nt][1]);
+                    mma_bf16(oacc[nt][mt], a, bl[nt][0], bl[nt][1]);
+                }
+            }
+        }
+    }
+    cp_async_wait<0>();
+    if (list.bad) *bad_flag = 1;
+    if (list.bad || (bad_len && threadIdx.x == 0)) atomicOr(p.err, kErrBadSeqlen);
+
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+            l[nt][0] += __shfl_xor_sync(0xffffffffu, l[nt][0], off);
+            l[nt][1] += __shfl_xor_sync(0xffffffffu, l[nt][1], off);
+        }
+    __syncthreads();  // every warp is done with its ring
+    constexpr int kCols = 8 * NT, MS = D + 4;
+    float* mg_o = reinterpret_cast<float*>(smem);
+    float* mg_m = mg_o + kWarps * kCols * MS;
+    float* mg_l = mg_m + kWarps * kCols;
+    float* cs_o = mg_l + kWarps * kCols;
+    float* cs_m = cs_o + kCols * D;
+    float* cs_l = cs_m + kCols;
+    float* mo = mg_o + warp * kCols * MS;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int c0 = nt * 8 + 2 * tig;
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt) {
+            mo[c0 * MS + 16 * mt + gid] = oacc[nt][mt][0];
+            mo[(c0 + 1) * MS + 16 * mt + gid] = oacc[nt][mt][1];
+            mo[c0 * MS + 16 * mt + gid + 8] = oacc[nt][mt][2];
+            mo[(c0 + 1) * MS + 16 * mt + gid + 8] = oacc[nt][mt][3];
+        }
+        if (gid == 0) {
+            mg_m[warp * kCols + c0] = m[nt][0];
+            mg_m[warp * kCols + c0 + 1] = m[nt][1];
+            mg_l[warp * kCols + c0] = l[nt][0];
+            mg_l[warp * kCols + c0 + 1] = l[nt][1];
+        }
+    }
+    __syncthreads();
+    finish_list<D, kFp8>(p, b, hq0, ncol, kCols, vscale, mg_o, mg_m, mg_l, cs_o, cs_m, cs_l, bad_len || *bad_flag);
+}
+
+// -------------------------------------------------------------- FP32 caches
+// CUDA cores (BF16 operands would lose the FP32 tolerance).  Eight lanes hold
+// a token's channels, four tokens a warp step, straight from global memory;
+// each eight-lane group keeps a running state for GC query heads.
+template <int D, int GC>
+__global__ void __launch_bounds__(kSelThreads) decode_selected_f32_kernel(const SelParams p) {
+    constexpr int J = D / 32;  // float4 per lane: channels 4 (l8 + 8 j) ..
+    constexpr int MS = D + 4;
+    __shared__ __align__(16) float qs[GC][D];
+    __shared__ __align__(16) float mg_o[kWarps * GC * MS];
+    __shared__ float mg_m[kWarps * GC], mg_l[kWarps * GC];
+    __shared__ float cs_o[GC * D], cs_m[GC], cs_l[GC];
+    __shared__ int bad_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l8 = lane & 7, tok = lane >> 3;
+    const int g = blockIdx.y / p.ngroups, cg = blockIdx.y - g * p.ngroups, b = blockIdx.z;
+    const int ncol = min(GC, p.G - GC * cg);
+    const int hq0 = g * p.G + GC * cg;
+    wait_primary();
+    allow_dependents();
+    if (threadIdx.x == 0) bad_flag = 0;
+    for (int i = threadIdx.x; i < GC * D; i += kSelThreads)
+        qs[i / D][i % D] = i / D < ncol
+                               ? static_cast<const float*>(p.q)[(static_cast<size_t>(b) * p.Hq + hq0) * D + i] * p.scale_log2
+                               : 0.f;
+    __syncthreads();
+    int N = p.seqlens[b];
+    const bool bad_len = N < 0 || N > p.S;
+    if (bad_len) N = 0;
+    SlabList list(p, b, g, N, blockIdx.x * kWarps + warp, p.C * kWarps);
+    const int n_it = list.count();
+    float m[GC], l[GC];
+    float4 o[GC][J];
+#pragma unroll
+    for (int h = 0; h < GC; ++h) {
+        m[h] = -INFINITY;
+        l[h] = 0.f;
+#pragma unroll
+        for (int j = 0; j < J; ++j) o[h][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const float* kp = static_cast<const float*>(p.k);
+    const float* vp = static_cast<const float*>(p.v);
+    SlabWindow win;
+    win.off = 0;
+    win.nv = 0;
+    for (int it = 0; it < n_it; ++it) {
+        if ((it & 31) == 0) win = list.place(it, list.entry(it));
+        const int nv = __shfl_sync(0xffffffffu, win.nv, it & 31);
+        const int64_t off = __shfl_sync(0xffffffffu, win.off, it & 31);
+#pragma unroll 1
+        for (int t = 0; t < nv; t += 4) {
+            const int r = t + tok;
+            const bool on = r < nv;
+            const int64_t at = off + (on ? r : 0) * p.st + 4 * l8;
+            float4 k4[J], v4[J];
+#pragma unroll
+            for (int j = 0; j < J; ++j) k4[j] = __ldg(reinterpret_cast<const float4*>(kp + at + 32 * j));
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                v4[j] = on ? __ldg(reinterpret_cast<const float4*>(vp + at + 32 * j)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int h = 0; h < GC; ++h) {
+                float s = 0.f;
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const float4 q4 = *reinterpret_cast<const float4*>(&qs[h][4 * l8 + 32 * j]);
+                    s = fmaf(q4.x, k4[j].x, s);
+                    s = fmaf(q4.y, k4[j].y, s);
+                    s = fmaf(q4.z, k4[j].z, s);
+                    s = fmaf(q4.w, k4[j].w, s);
+                }
+#pragma unroll
+                for (int x = 4; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+                if (!on) s = -INFINITY;
+                const float mn = fmaxf(m[h], s), ms = (mn == -INFINITY) ? 0.f : mn;
+                const float al = ex2(m[h] - ms), w = ex2(s - ms);
+                m[h] = mn;
+                l[h] = fmaf(l[h], al, w);
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    o[h][j].x = fmaf(o[h][j].x, al, w * v4[j].x);
+                    o[h][j].y = fmaf(o[h][j].y, al, w * v4[j].y);
+                    o[h][j].z = fmaf(o[h][j].z, al, w * v4[j].z);
+                    o[h][j].w = fmaf(o[h][j].w, al, w * v4[j].w);
+                }
+            }
+        }
+    }
+    if (list.bad) bad_flag = 1;
+    if (list.bad || (bad_len && threadIdx.x == 0)) atomicOr(p.err, kErrBadSeqlen);
+    // the warp's four token groups, then its state into shared memory
+#pragma unroll
+    for (int h = 0; h < GC; ++h) {
+#pragma unroll
+        for (int x = 8; x < 32; x <<= 1) {
+            const float mo = __shfl_xor_sync(0xffffffffu, m[h], x);
+            const float mn = fmaxf(m[h], mo), ms = (mn == -INFINITY) ? 0.f : mn;
+            const float a = ex2(m[h] - ms), c = ex2(mo - ms);
+            l[h] = l[h] * a + __shfl_xor_sync(0xffffffffu, l[h], x) * c;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                o[h][j].x = o[h][j].x * a + __shfl_xor_sync(0xffffffffu, o[h][j].x, x) * c;
+                o[h][j].y = o[h][j].y * a + __shfl_xor_sync(0xffffffffu, o[h][j].y, x) * c;
+                o[h][j].z = o[h][j].z * a + __shfl_xor_sync(0xffffffffu, o[h][j].z, x) * c;
+                o[h][j].w = o[h][j].w * a + __shfl_xor_sync(0xffffffffu, o[h][j].w, x) * c;
+            }
+            m[h] = mn;
+        }
+        if (tok == 0) {
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                *reinterpret_cast<float4*>(&mg_o[(warp * GC + h) * MS + 4 * l8 + 32 * j]) = o[h][j];
+            if (l8 == 0) {
+                mg_m[warp * GC + h] = m[h];
+                mg_l[warp * GC + h] = l[h];
+            }
+        }
+    }
+    __syncthreads();
+    finish_list<D, false>(p, b, hq0, ncol, GC, 1.f, mg_o, mg_m, mg_l, cs_o, cs_m, cs_l, bad_len || bad_flag);
+}
+
+// ---------------------------------------------------------------- host side
+constexpr int kMaxDevices = 64;
+
+// One kernel instance's device-side limits, set up once per device: dynamic
+// shared memory, clusters of more than 8 blocks, and how many clusters of
+// each size fit on the device at once.
+struct Instance {
+    std::mutex mu;
+    bool ready[kMaxDevices] = {};
+    int clusters[kMaxDevices][5];  // of 1, 2, 4, 8, 16 blocks
+};
+
+template <typename Kernel>
+int prepare_instance(Kernel kernel, int smem, int device, Instance* inst, int* fit) {
+    std::lock_guard<std::mutex> lock(inst->mu);
+    if (!inst->ready[device]) {
+        if (smem > 0 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return TA_ERR_CUDA;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+            return TA_ERR_CUDA;
+        for (int i = 0; i < 5; ++i) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(1 << i, 1, 1);
+            cfg.blockDim = dim3(kSelThreads, 1, 1);
+            cfg.dynamicSmemBytes = smem;
+            cudaLaunchAttribute a = {};
+            a.id = cudaLaunchAttributeClusterDimension;
+            a.val.clusterDim.x = 1 << i;
+            a.val.clusterDim.y = a.val.clusterDim.z = 1;
+            cfg.attrs = &a;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+                (void)cudaGetLastError();  // size not available here
+                n = 0;
+            }
+            inst->clusters[device][i] = n;
+        }
+        inst->ready[device] = true;
+    }
+    std::copy(inst->clusters[device], inst->clusters[device] + 5, fit);
+    return TA_OK;
+}
+
+// Blocks per list: the largest power of two that gives every warp at least one
+// slab and keeps all lists resident at once; one block when there are more
+// lists than that.
+int pick_cluster(int64_t lists, int64_t slabs, const int* fit) {
+    int c = 1;
+    for (int i = 1; i < 5; ++i) {
+        const int n = 1 << i;
+        if (slabs < static_cast<int64_t>(n) * kWarps || lists > fit[i]) break;
+        c = n;
+    }
+    return c;
+}
+
+template <typename Kernel>
+int launch_selected(Kernel kernel, int smem, Instance* inst, int device, SelParams p, int batch, cudaStream_t stream) {
+    int fit[5];
+    const int rc = prepare_instance(kernel, smem, device, inst, fit);
+    if (rc != TA_OK) return rc;
+    const int64_t lists = static_cast<int64_t>(batch) * p.Hkv * p.ngroups;
+    p.C = pick_cluster(lists, static_cast<int64_t>(p.num_select) << (p.page_shift - 4), fit);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.C, p.Hkv * p.ngroups, batch);
+    cfg.blockDim = dim3(kSelThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0] = programmatic_launch();
+    attr[1] = {};
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.C);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.C > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? TA_OK : TA_ERR_CUDA;
+}
+
+template <int D, int NT, bool kFp8>
+int launch_mma(int device, const SelParams& p, int batch, cudaStream_t s) {
+    static Instance inst;
+    return launch_selected(decode_selected_kernel<D, NT, kFp8>, SelCfg<D, kFp8>::kSmem, &inst, device, p, batch, s);
+}
+
+template <int D, int GC>
+int launch_f32(int device, const SelParams& p, int batch, cudaStream_t s) {
+    static Instance inst;
+    return launch_selected(decode_selected_f32_kernel<D, GC>, 0, &inst, device, p, batch, s);
+}
+
+}  // namespace
+}  // namespace ta
+
+extern "C" int tree_attn_decode_selected(const ta_shape* shape, const ta_paged_kv* paged, const void* q,
+                                         const void* k_pages, const void* v_pages, const int32_t* seqlens,
+                                         const int32_t* selected, int num_select, float* out, float* lse,
+                                         const float* k_scale, const float* v_scale, void* stream) {
+    using namespace ta;
+    if (!shape || !paged) return TA_ERR_NULL;
+    CacheLayout lay;
+    int rc = cache_layout(shape, paged, &lay);
+    if (rc != TA_OK) return rc;
+    if (!q || !k_pages || !v_pages || !seqlens || !selected || !out) return TA_ERR_NULL;
+    if (!aligned_to(q, 16) || !aligned_to(k_pages, 16) || !aligned_to(v_pages, 16) || !aligned_to(out, 16) ||
+        !aligned_to(seqlens, 4) || !aligned_to(selected, 4) || !aligned_to(lse, 4))
+        return TA_ERR_ALIGN;
+    if (num_select < 1 || num_select > 65536) return TA_ERR_SHAPE;
+    const bool fp8 = shape->kv_dtype == TA_E4M3, f32 = shape->kv_dtype == TA_F32;
+    if (shape->q_dtype != (f32 ? TA_F32 : TA_BF16) || (fp8 && shape->head_dim != 128)) return TA_ERR_DTYPE;
+    if (fp8) {
+        if (!k_scale || !v_scale) return TA_ERR_NULL;
+        if (!aligned_to(k_scale, 4) || !aligned_to(v_scale, 4)) return TA_ERR_ALIGN;
+    } else if (k_scale || v_scale) {
+        return TA_ERR_DTYPE;
+    }
+    const int G = shape->num_q_heads / shape->num_kv_heads;
+    const int cols = f32 ? (G >= 3 ? 4 : G) : 16;  // columns a block serves
+    SelParams p;
+    std::memset(&p, 0, sizeof p);
+    p.ngroups = (G + cols - 1) / cols;
+    if (shape->batch > 65535 || static_cast<int64_t>(shape->num_kv_heads) * p.ngroups > 65535) return TA_ERR_SHAPE;
+    DeviceInfo dev;
+    if ((rc = device_info(&dev)) != TA_OK) return rc;
+    p.q = q;
+    p.k = k_pages;
+    p.v = v_pages;
+    p.seqlens = seqlens;
+    p.selected = selected;
+    p.block_table = paged->block_table;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.out = out;
+    p.lse = lse;
+    p.err = dev.err;
+    p.sb = lay.stride_b;
+    p.sh = lay.stride_h;
+    p.st = lay.stride_t;
+    p.Hq = shape->num_q_heads;
+    p.Hkv = shape->num_kv_heads;
+    p.G = G;
+    p.S = shape->max_seqlen;
+    p.num_select = num_select;
+    p.max_pages = paged->max_pages_per_seq;
+    p.page_shift = lay.page_shift;
+    p.num_pages = paged->num_pages;
+    const float scale = shape->scale > 0.f ? shape->scale : 1.0f / std::sqrt(static_cast<float>(shape->head_dim));
+    p.scale_log2 = scale * kLog2e;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int B = shape->batch, d = dev.device;
+    const bool two = G > 8, d128 = shape->head_dim == 128;
+    if (fp8) return two ? launch_mma<128, 2, true>(d, p, B, s) : launch_mma<128, 1, true>(d, p, B, s);
+    if (!f32) {
+        if (d128) return two ? launch_mma<128, 2, false>(d, p, B, s) : launch_mma<128, 1, false>(d, p, B, s);
+        return two ? launch_mma<64, 2, false>(d, p, B, s) : launch_mma<64, 1, false>(d, p, B, s);
+    }
+    switch (cols) {
+        case 1: return d128 ? launch_f32<128, 1>(d, p, B, s) : launch_f32<64, 1>(d, p, B, s);
+        case 2: return d128 ? launch_f32<128, 2>(d, p, B, s) : launch_f32<64, 2>(d, p, B, s);
+        default: return d128 ? launch_f32<128, 4>(d, p, B, s) : launch_f32<64, 4>(d, p, B, s);
+    }
+}

@@ -1,0 +1,600 @@
+// Head vectors of a token list: per-head RMS norm and position rotation of
+// queries and keys, storing keys and values in a cache (rounded to its type),
+// and reading a cache back.
+//
+// A vector is the head_dim channels of one (token, head).  A group of
+// head_dim/8 lanes holds one vector, 8 consecutive channels a lane (one
+// 16-byte access of BF16), and walks the heads of its token, four vectors in
+// flight, so that the token's cosines and sines are computed once per group
+// and stay in registers.  With few tokens a token's heads are spread over
+// several groups instead (heads_per_group): then the call is bound by the
+// latency of one load, the angles and one store, and recomputing the angles
+// costs nothing.
+//
+// Rotation angles.  The angle p * f of position p is needed modulo 2 pi.  The
+// frequency is turned into a 64-bit binary fraction of a full turn per
+// position, u = f / (2 pi) * 2^64, by an integer product with 2^64 / (2 pi);
+// u * p in 64-bit wrap-around arithmetic is then the angle modulo one turn,
+// with an error of at most about p * 2^-63 turns whatever the position, and its
+// top bits go to sincospi.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "common.cuh"
+#include "host.h"
+
+namespace ta {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kFlight = 4;  // vectors a group keeps in flight
+
+struct Vectors {
+    void* data;
+    int64_t st, sh;  // elements between tokens, heads
+};
+
+struct TokenParams {
+    Vectors q, qo, k, ko, v, vo;  // unused ones have data == nullptr
+    void* kc;
+    void* vc;
+    int64_t cb, ch, ct;           // cache strides (row or page, head, token)
+    const int32_t* positions;
+    const int32_t* rows;
+    const int32_t* block_table;
+    const float* inv_freq;
+    const void* qw;
+    const void* kw;
+    const float* ks;
+    const float* vs;
+    int* err;
+    int T, Hq, Hkv, B, S;
+    int max_pages, page_shift, num_pages;
+    int chunks, hpg;              // groups per token, heads per group
+    int rot, interleaved, norm, w_bf16;
+    float eps;
+};
+
+// 8 channels of a vector in memory, and as FP32.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+    uint4 x;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { x = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void unpack(float (&f)[8]) const {
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+template <>
+struct Eight<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = reinterpret_cast<const float4*>(p)[0];
+        b = reinterpret_cast<const float4*>(p)[1];
+    }
+    __device__ __forceinline__ void unpack(float (&f)[8]) const {
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+};
+template <>
+struct Eight<__nv_fp8_e4m3> {
+    uint2 x;
+    __device__ __forceinline__ void load(const __nv_fp8_e4m3* p) { x = *reinterpret_cast<const uint2*>(p); }
+    __device__ __forceinline__ void unpack(float (&f)[8]) const {
+        const uint32_t w[2] = {x.x, x.y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                static_cast<__nv_fp8x2_storage_t>(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+            const float2 v = __half22float2(__half2(h));
+            f[2 * i] = v.x;
+            f[2 * i + 1] = v.y;
+        }
+    }
+};
+
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+// Nearest even; finite values saturate at +-448, NaN stays NaN.
+__device__ __forceinline__ void store8(__nv_fp8_e4m3* p, const float (&f)[8]) {
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i >> 1] |= static_cast<uint32_t>(
+                         __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i], f[2 * i + 1]), __NV_SATFINITE, __NV_E4M3))
+                     << (16 * (i & 1));
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+
+// cos and sin of pos * f.  f / (2 pi) in units of 2^-64 turns: f = m * 2^e with a
+// 24-bit integer m, so m * (2^64 / (2 pi)) is an 88-bit integer to be shifted by e.
+__device__ __forceinline__ void turn(int pos, float f, float* c, float* s) {
+    constexpr unsigned long long kPerRadian = 0x28be60db9391054aull;  // 2^64 / (2 pi)
+    const uint32_t bits = __float_as_uint(f);
+    const int ef = (bits >> 23) & 0xff;
+    const unsigned long long m = (bits & 0x7fffffu) | (ef ? 0x800000u : 0u);
+    const int sh = 150 - (ef ? ef : 1);  // f = m * 2^-sh
+    const unsigned long long lo = m * kPerRadian, hi = __umul64hi(m, kPerRadian);
+    unsigned long long u;
+    if (sh >= 128)
+        u = 0;
+    else if (sh >= 64)
+        u = hi >> (sh - 64);
+    else if (sh > 0)
+        u = (lo >> sh) | (hi << (64 - sh));
+    else
+        u = sh > -64 ? lo << -sh : 0;
+    if (bits >> 31) u = 0 - u;
+    const long long a = static_cast<long long>(u * static_cast<unsigned long long>(static_cast<long long>(pos)));
+    float half_turns = static_cast<float>(a) * 1.0842021724855044e-19f;  // 2^-63
+    if (ef == 0xff) half_turns = __int_as_float(0x7fc00000);
+    sincospif(half_turns, s, c);
+}
+
+// What a lane holds of its token's rotation: for each of its channels the
+// cosine and the signed sine that its partner channel is multiplied with.
+struct Rotation {
+    float c[8], s[8];
+    int src;      // lane holding the partner channels (halves); the lane itself if interleaved
+    bool on;      // the lane's channels are rotated
+};
+
+template <int L>
+__device__ __forceinline__ Rotation make_rotation(const TokenParams& p, int pos, int l, int lane) {
+    Rotation r;
+    const int half = p.rot >> 1;
+    r.on = 8 * l < p.rot;
+    r.src = lane;
+    if (!r.on) return r;
+    if (p.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float c, s;
+            turn(pos, __ldg(p.inv_freq + 4 * l + i), &c, &s);
+            r.c[2 * i] = r.c[2 * i + 1] = c;
+            r.s[2 * i] = -s;
+            r.s[2 * i + 1] = s;
+        }
+        return r;
+    }
+    const bool second = 8 * l >= half;
+    const int j0 = 8 * l - (second ? half : 0);
+    r.src = second ? lane - half / 8 : lane + half / 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float s;
+        turn(pos, __ldg(p.inv_freq + j0 + i), &r.c[i], &s);
+        r.s[i] = second ? s : -s;
+    }
+    return r;
+}
+
+__device__ __forceinline__ void load_weight(const void* w, int bf16, int ch, float (&f)[8]) {
+    if (w == nullptr) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = 1.f;
+    } else if (bf16) {
+        Eight<__nv_bfloat16> e;
+        e.load(static_cast<const __nv_bfloat16*>(w) + ch);
+        e.unpack(f);
+    } else {
+        Eight<float> e;
+        e.load(static_cast<const float*>(w) + ch);
+        e.unpack(f);
+    }
+}
+
+template <int L>
+__device__ __forceinline__ void norm_rotate(const TokenParams& p, const Rotation& r, const float (&w)[8],
+                                            float (&f)[8], unsigned mask) {
+    if (p.norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
+#pragma unroll
+        for (int off = L / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(mask, ss, off);
+        const float inv = rsqrtf(ss * (1.f / (8 * L)) + p.eps);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = f[i] * inv * w[i];
+    }
+    if (p.rot) {
+        float o[8];
+        if (p.interleaved) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = f[i ^ 1];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(mask, f[i], r.src);
+        }
+        if (r.on) {  // channels past rot_dim keep their value (also an infinite one)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = f[i] * r.c[i] + o[i] * r.s[i];
+        }
+    }
+}
+
+// Heads [h0, h1) of a token: load, transform, store, kFlight vectors at a time.
+template <typename TIn, typename Fn>
+__device__ __forceinline__ void walk_heads(const TIn* src, int64_t sh, int h0, int h1, Fn&& fn) {
+    for (int h = h0; h < h1; h += kFlight) {
+        Eight<TIn> e[kFlight];
+#pragma unroll
+        for (int j = 0; j < kFlight; ++j)
+            if (h + j < h1) e[j].load(src + (h + j) * sh);
+#pragma unroll
+        for (int j = 0; j < kFlight; ++j) {
+            if (h + j < h1) {
+                float f[8];
+                e[j].unpack(f);
+                fn(h + j, f);
+            }
+        }
+    }
+}
+
+// Start of the token's place in the cache (elements), or -1 (bad data: the
+// error word is set).
+__device__ __forceinline__ int64_t cache_place(const TokenParams& p, int t, int row, int pos) {
+    if (row < p.B && pos < p.S) {
+        if (!p.block_table) return row * p.cb + pos * p.ct;
+        const int page = __ldg(p.block_table + static_cast<int64_t>(row) * p.max_pages + (pos >> p.page_shift));
+        if (page >= 0 && page < p.num_pages) return page * p.cb + (pos & ((1 << p.page_shift) - 1)) * p.ct;
+    }
+    atomicOr(p.err, kErrBadSeqlen);
+    return -1;
+}
+
+// Which of a token's vectors a group takes.  False: nothing to do.
+template <int L>
+__device__ __forceinline__ bool group_work(const TokenParams& p, int heads, int* t, int* h0, int* h1) {
+    const int64_t g = static_cast<int64_t>(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
+    *t = static_cast<int>(g / p.chunks);
+    if (*t >= p.T) return false;
+    *h0 = static_cast<int>(g - static_cast<int64_t>(*t) * p.chunks) * p.hpg;
+    *h1 = min(heads, *h0 + p.hpg);
+    return true;
+}
+
+// Heads of a token: [0, Hq) queries, [Hq, Hq + Hkv) keys, then (with a cache)
+// the values.  TC void: keys go to ko and there are no values.
+template <int D, typename T, typename TC>
+__global__ void __launch_bounds__(kThreads) token_write_kernel(const TokenParams p) {
+    constexpr int L = D / 8;
+    constexpr bool kCache = !std::is_void<TC>::value;
+    wait_primary();
+    allow_dependents();
+    int t, h0, h1;
+    if (!group_work<L>(p, p.Hq + p.Hkv + (kCache ? p.Hkv : 0), &t, &h0, &h1)) return;
+    const int pos = p.positions[t];
+    const int row = !kCache || !p.rows ? t : p.rows[t];
+    if (pos < 0 || row < 0) return;  // a padding token
+    const int lane = threadIdx.x & 31, l = lane % L;
+    const unsigned mask = (L == 32 ? 0xffffffffu : ((1u << L) - 1u)) << (lane & ~(L - 1));
+    const int ch = 8 * l;
+
+    const int kend = p.Hq + p.Hkv;
+    Rotation r;
+    if (p.rot && h0 < kend) r = make_rotation<L>(p, pos, l, lane);
+    if (h0 < p.Hq) {
+        float w[8];
+        if (p.norm) load_weight(p.qw, p.w_bf16, ch, w);
+        const T* src = static_cast<const T*>(p.q.data) + t * p.q.st + ch;
+        T* dst = static_cast<T*>(p.qo.data) + t * p.qo.st + ch;
+        walk_heads(src, p.q.sh, h0, min(h1, p.Hq), [&](int h, float (&f)[8]) {
+            norm_rotate<L>(p, r, w, f, mask);
+            store8(dst + h * p.qo.sh, f);
+        });
+    }
+    if (h1 <= p.Hq) return;
+    int64_t place = 0;
+    if constexpr (kCache) {
+        place = cache_place(p, t, row, pos);
+        if (place < 0) return;
+    }
+    if (h0 < kend) {
+        float w[8];
+        if (p.norm) load_weight(p.kw, p.w_bf16, ch, w);
+        const T* src = static_cast<const T*>(p.k.data) + t * p.k.st + ch;
+        walk_heads(src, p.k.sh, max(h0 - p.Hq, 0), min(h1 - p.Hq, p.Hkv), [&](int h, float (&f)[8]) {
+            norm_rotate<L>(p, r, w, f, mask);
+            if constexpr (!kCache) {
+                store8(static_cast<T*>(p.ko.data) + t * p.ko.st + h * p.ko.sh + ch, f);
+            } else {
+                if constexpr (std::is_same<TC, __nv_fp8_e4m3>::value) {
+                    const float sc = __ldg(p.ks + h);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] = f[i] / sc;
+                }
+                store8(static_cast<TC*>(p.kc) + place + h * p.ch + ch, f);
+            }
+        });
+    }
+    if constexpr (kCache) {
+        if (h1 <= kend) return;
+        const T* src = static_cast<const T*>(p.v.data) + t * p.v.st + ch;
+        walk_heads(src, p.v.sh, max(h0 - kend, 0), h1 - kend, [&](int h, float (&f)[8]) {
+            if constexpr (std::is_same<TC, __nv_fp8_e4m3>::value) {
+                const float sc = __ldg(p.vs + h);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = f[i] / sc;
+            }
+            store8(static_cast<TC*>(p.vc) + place + h * p.ch + ch, f);
+        });
+    }
+}
+
+// Heads of a token: [0, Hkv) keys, then values.
+template <int D, typename T, typename TC>
+__global__ void __launch_bounds__(kThreads) token_read_kernel(const TokenParams p) {
+    constexpr int L = D / 8;
+    wait_primary();
+    allow_dependents();
+    int t, h0, h1;
+    if (!group_work<L>(p, 2 * p.Hkv, &t, &h0, &h1)) return;
+    const int pos = p.positions[t];
+    const int row = p.rows ? p.rows[t] : t;
+    if (pos < 0 || row < 0) return;  // a padding token
+    const int ch = 8 * ((threadIdx.x & 31) % L);
+    const int64_t place = cache_place(p, t, row, pos);
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+        const int a = max(h0 - kv * p.Hkv, 0), b = min(h1 - kv * p.Hkv, p.Hkv);
+        if (a >= b) continue;
+        const Vectors& out = kv ? p.vo : p.ko;
+        const float* scale = kv ? p.vs : p.ks;
+        T* dst = static_cast<T*>(out.data) + t * out.st + ch;
+        if (place < 0) {
+            const float nan = __int_as_float(0x7fc00000);
+            const float f[8] = {nan, nan, nan, nan, nan, nan, nan, nan};
+            for (int h = a; h < b; ++h) store8(dst + h * out.sh, f);
+            continue;
+        }
+        const TC* src = static_cast<const TC*>(kv ? p.vc : p.kc) + place + ch;
+        walk_heads(src, p.ch, a, b, [&](int h, float (&f)[8]) {
+            if constexpr (std::is_same<TC, __nv_fp8_e4m3>::value) {
+                const float sc = __ldg(scale + h);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] *= sc;
+            }
+            store8(dst + h * out.sh, f);
+        });
+    }
+}
+
+// ---------------------------------------------------------------- host side
+// Heads per group: all of a token's vectors while the tokens alone fill the
+// device, fewer for short lists.
+void plan_groups(TokenParams* p, int heads, int num_sms) {
+    const int64_t want = static_cast<int64_t>(num_sms) * 64;  // groups in flight on a full device
+    int64_t hpg = (static_cast<int64_t>(p->T) * heads + want - 1) / want;
+    hpg = std::max<int64_t>(1, std::min<int64_t>(hpg, heads));
+    if (hpg > 1) hpg = std::min<int64_t>(heads, (hpg + kFlight - 1) / kFlight * kFlight);
+    p->hpg = static_cast<int>(hpg);
+    p->chunks = (heads + p->hpg - 1) / p->hpg;
+}
+
+template <typename Kernel>
+cudaError_t launch(Kernel kernel, const TokenParams& p, int d, cudaStream_t stream) {
+    const int64_t per_block = kThreads / (d / 8);
+    const int64_t blocks = (static_cast<int64_t>(p.T) * p.chunks + per_block - 1) / per_block;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = programmatic_launch();
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int D, typename T>
+cudaError_t launch_write(int cache, const TokenParams& p, cudaStream_t s) {
+    switch (cache) {
+        case TA_F32: return launch(token_write_kernel<D, T, float>, p, D, s);
+        case TA_BF16: return launch(token_write_kernel<D, T, __nv_bfloat16>, p, D, s);
+        case TA_E4M3: return launch(token_write_kernel<D, T, __nv_fp8_e4m3>, p, D, s);
+        default: return launch(token_write_kernel<D, T, void>, p, D, s);
+    }
+}
+
+template <int D, typename T>
+cudaError_t launch_read(int cache, const TokenParams& p, cudaStream_t s) {
+    switch (cache) {
+        case TA_F32: return launch(token_read_kernel<D, T, float>, p, D, s);
+        case TA_BF16: return launch(token_read_kernel<D, T, __nv_bfloat16>, p, D, s);
+        default: return launch(token_read_kernel<D, T, __nv_fp8_e4m3>, p, D, s);
+    }
+}
+
+// (an empty list's vectors need no memory)
+int check_heads(const ta_heads* h, int dtype, const ta_tokens* tokens, Vectors* out) {
+    if (!h || (!h->data && tokens->num_tokens > 0)) return TA_ERR_NULL;
+    const int64_t es = dtype == TA_BF16 ? 2 : 4;
+    const int64_t lim = int64_t(1) << 40;
+    if (!aligned_to(h->data, 16) || (h->stride_t * es) % 16 != 0 || (h->stride_h * es) % 16 != 0) return TA_ERR_ALIGN;
+    if (h->stride_t < 0 || h->stride_h < 0 || h->stride_t >= lim || h->stride_h >= lim) return TA_ERR_SHAPE;
+    out->data = h->data;
+    out->st = h->stride_t;
+    out->sh = h->stride_h;
+    return TA_OK;
+}
+
+int check_tokens(const ta_tokens* t) {
+    if (!t) return TA_ERR_NULL;
+    if (t->num_tokens < 0 || t->reserved != 0) return TA_ERR_SHAPE;
+    if (t->num_tokens > 0 && !t->positions) return TA_ERR_NULL;
+    if (!aligned_to(t->positions, 4) || !aligned_to(t->rows, 4)) return TA_ERR_ALIGN;
+    return TA_OK;
+}
+
+int check_rope(const ta_rope* r, int head_dim, TokenParams* p) {
+    if (!r) return TA_ERR_NULL;
+    if (r->rot_dim < 0 || r->rot_dim > head_dim || r->rot_dim % 16 != 0 || r->reserved != 0) return TA_ERR_SHAPE;
+    if ((r->interleaved | 1) != 1 || (r->norm | 1) != 1) return TA_ERR_SHAPE;
+    if (!(r->eps >= 0.f) || std::isinf(r->eps)) return TA_ERR_SHAPE;
+    if (r->rot_dim > 0 && !r->inv_freq) return TA_ERR_NULL;
+    if (!r->norm && (r->q_weight || r->k_weight)) return TA_ERR_SHAPE;
+    if ((r->q_weight || r->k_weight) && r->weight_dtype != TA_BF16 && r->weight_dtype != TA_F32) return TA_ERR_DTYPE;
+    if (!aligned_to(r->inv_freq, 4) || !aligned_to(r->q_weight, 16) || !aligned_to(r->k_weight, 16)) return TA_ERR_ALIGN;
+    p->inv_freq = r->inv_freq;
+    p->qw = r->q_weight;
+    p->kw = r->k_weight;
+    p->w_bf16 = r->weight_dtype == TA_BF16;
+    p->rot = r->rot_dim;
+    p->interleaved = r->interleaved;
+    p->norm = r->norm;
+    p->eps = r->eps;
+    return TA_OK;
+}
+
+int check_scales(const ta_shape* s, const float* ks, const float* vs) {
+    if (s->kv_dtype != TA_E4M3) return (ks || vs) ? TA_ERR_DTYPE : TA_OK;
+    if (!ks || !vs) return TA_ERR_NULL;
+    return aligned_to(ks, 4) && aligned_to(vs, 4) ? TA_OK : TA_ERR_ALIGN;
+}
+
+// The parts that writing and reading a cache share.
+int check_cache_call(const ta_shape* shape, const ta_paged_kv* paged, const ta_tokens* tokens, const void* kc,
+                     const void* vc, const float* ks, const float* vs, TokenParams* p) {
+    CacheLayout lay;
+    int rc = cache_layout(shape, paged, &lay);
+    if (rc != TA_OK) return rc;
+    if ((rc = check_tokens(tokens)) != TA_OK) return rc;
+    if (!kc || !vc) return TA_ERR_NULL;
+    if (!aligned_to(kc, 16) || !aligned_to(vc, 16)) return TA_ERR_ALIGN;
+    if ((rc = check_scales(shape, ks, vs)) != TA_OK) return rc;
+    if (!tokens->rows && tokens->num_tokens > shape->batch) return TA_ERR_SHAPE;
+    p->kc = const_cast<void*>(kc);
+    p->vc = const_cast<void*>(vc);
+    p->cb = lay.stride_b;
+    p->ch = lay.stride_h;
+    p->ct = lay.stride_t;
+    p->positions = tokens->positions;
+    p->rows = tokens->rows;
+    p->ks = ks;
+    p->vs = vs;
+    p->T = tokens->num_tokens;
+    p->Hkv = shape->num_kv_heads;
+    p->B = shape->batch;
+    p->S = shape->max_seqlen;
+    if (paged) {
+        p->block_table = paged->block_table;
+        p->max_pages = paged->max_pages_per_seq;
+        p->page_shift = lay.page_shift;
+        p->num_pages = paged->num_pages;
+    }
+    return TA_OK;
+}
+
+// Enqueue a checked call.  `cache`: the cache's type, -1 without a cache.
+int enqueue(const ta_shape* shape, TokenParams* p, int heads, int cache, bool read, void* stream) {
+    if (p->T == 0 || heads == 0) return TA_OK;
+    DeviceInfo dev;
+    const int rc = device_info(&dev);
+    if (rc != TA_OK) return rc;
+    p->err = dev.err;
+    plan_groups(p, heads, dev.num_sms);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool d128 = shape->head_dim == 128, bf16 = shape->q_dtype == TA_BF16;
+    cudaError_t e;
+    if (read)
+        e = d128 ? (bf16 ? launch_read<128, __nv_bfloat16>(cache, *p, s) : launch_read<128, float>(cache, *p, s))
+                 : (bf16 ? launch_read<64, __nv_bfloat16>(cache, *p, s) : launch_read<64, float>(cache, *p, s));
+    else
+        e = d128 ? (bf16 ? launch_write<128, __nv_bfloat16>(cache, *p, s) : launch_write<128, float>(cache, *p, s))
+                 : (bf16 ? launch_write<64, __nv_bfloat16>(cache, *p, s) : launch_write<64, float>(cache, *p, s));
+    return e == cudaSuccess ? TA_OK : TA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace ta
+
+extern "C" int tree_attn_norm_rope(const ta_shape* shape, const ta_tokens* tokens, const ta_rope* rope,
+                                   const ta_heads* q, const ta_heads* q_out, const ta_heads* k,
+                                   const ta_heads* k_out, void* stream) {
+    using namespace ta;
+    if (!shape) return TA_ERR_NULL;
+    if (shape->head_dim != 64 && shape->head_dim != 128) return TA_ERR_SHAPE;
+    if (shape->q_dtype != TA_BF16 && shape->q_dtype != TA_F32) return TA_ERR_DTYPE;
+    TokenParams p;
+    std::memset(&p, 0, sizeof p);
+    int rc = check_tokens(tokens);
+    if (rc != TA_OK) return rc;
+    if ((rc = check_rope(rope, shape->head_dim, &p)) != TA_OK) return rc;
+    if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr) || (!q && !k)) return TA_ERR_NULL;
+    if (q) {
+        if (shape->num_q_heads < 1 || shape->num_q_heads > 65536) return TA_ERR_SHAPE;
+        if ((rc = check_heads(q, shape->q_dtype, tokens, &p.q)) != TA_OK) return rc;
+        if ((rc = check_heads(q_out, shape->q_dtype, tokens, &p.qo)) != TA_OK) return rc;
+        p.Hq = shape->num_q_heads;
+    }
+    if (k) {
+        if (shape->num_kv_heads < 1 || shape->num_kv_heads > 65536) return TA_ERR_SHAPE;
+        if ((rc = check_heads(k, shape->q_dtype, tokens, &p.k)) != TA_OK) return rc;
+        if ((rc = check_heads(k_out, shape->q_dtype, tokens, &p.ko)) != TA_OK) return rc;
+        p.Hkv = shape->num_kv_heads;
+    }
+    p.T = tokens->num_tokens;
+    p.positions = tokens->positions;
+    return enqueue(shape, &p, p.Hq + p.Hkv, -1, false, stream);
+}
+
+extern "C" int tree_attn_cache_write(const ta_shape* shape, const ta_paged_kv* paged, const ta_tokens* tokens,
+                                     const ta_rope* rope, const ta_heads* q, const ta_heads* q_out,
+                                     const ta_heads* k, const ta_heads* v, void* k_cache, void* v_cache,
+                                     const float* k_scale, const float* v_scale, void* stream) {
+    using namespace ta;
+    TokenParams p;
+    std::memset(&p, 0, sizeof p);
+    int rc = check_cache_call(shape, paged, tokens, k_cache, v_cache, k_scale, v_scale, &p);
+    if (rc != TA_OK) return rc;
+    if ((q == nullptr) != (q_out == nullptr)) return TA_ERR_NULL;
+    if (q && !rope) return TA_ERR_SHAPE;  // without a norm or rotation there is nothing to do for queries
+    if (rope && (rc = check_rope(rope, shape->head_dim, &p)) != TA_OK) return rc;
+    if ((rc = check_heads(k, shape->q_dtype, tokens, &p.k)) != TA_OK) return rc;
+    if ((rc = check_heads(v, shape->q_dtype, tokens, &p.v)) != TA_OK) return rc;
+    if (q) {
+        if ((rc = check_heads(q, shape->q_dtype, tokens, &p.q)) != TA_OK) return rc;
+        if ((rc = check_heads(q_out, shape->q_dtype, tokens, &p.qo)) != TA_OK) return rc;
+        p.Hq = shape->num_q_heads;
+    }
+    return enqueue(shape, &p, p.Hq + 2 * p.Hkv, shape->kv_dtype, false, stream);
+}
+
+extern "C" int tree_attn_cache_read(const ta_shape* shape, const ta_paged_kv* paged, const ta_tokens* tokens,
+                                    const void* k_cache, const void* v_cache, const ta_heads* k_out,
+                                    const ta_heads* v_out, const float* k_scale, const float* v_scale,
+                                    void* stream) {
+    using namespace ta;
+    TokenParams p;
+    std::memset(&p, 0, sizeof p);
+    int rc = check_cache_call(shape, paged, tokens, k_cache, v_cache, k_scale, v_scale, &p);
+    if (rc != TA_OK) return rc;
+    if ((rc = check_heads(k_out, shape->q_dtype, tokens, &p.ko)) != TA_OK) return rc;
+    if ((rc = check_heads(v_out, shape->q_dtype, tokens, &p.vo)) != TA_OK) return rc;
+    return enqueue(shape, &p, 2 * p.Hkv, shape->kv_dtype, true, stream);
+}
