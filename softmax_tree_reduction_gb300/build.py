@@ -11,6 +11,10 @@ their buffers, skip an access that falls outside and report it through the
 device error word (TA_ERR_DEVICE_BOUNDS).  Point the binding at it with the
 TREE_ATTN_LIBRARY environment variable.
 
+The argument marshalling of the calls around the decode step
+(csrc/serving_calls.cpp) is compiled with g++ against torch's headers into
+``softmax_tree_reduction_gb300/_serving_calls.so``.
+
     python -m softmax_tree_reduction_gb300.build [--verbose-ptxas] [--force] [--debug]
 """
 from __future__ import annotations
@@ -19,11 +23,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtreeattn.so")
+CALLS_SOURCE = os.path.join(CSRC, "serving_calls.cpp")
+CALLS = os.path.join(HERE, "_serving_calls.so")
 LIB_DEBUG = os.path.join(HERE, "libtreeattn_debug.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
@@ -41,6 +48,18 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def _calls_command(out: str) -> list:
+    """The compiler call that makes the marshalling module."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            "-I" + os.path.join(root, "include"), "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"), CALLS_SOURCE, "-o", out, "-L" + lib,
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ldl", "-Wl,-rpath," + lib]
+
+
 def _deps_mtime() -> float:
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     files.append(os.path.join(INCLUDE, "tree_attn.h"))
@@ -49,7 +68,7 @@ def _deps_mtime() -> float:
 
 
 def up_to_date(lib: str = LIB) -> bool:
-    return os.path.exists(lib) and os.path.getmtime(lib) >= _deps_mtime()
+    return all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (lib, CALLS))
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True, debug: bool = False) -> str:
@@ -70,6 +89,9 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True, 
         cmd = [cc, *ARCH, *FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
         procs.append((src, cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
                                                  text=True)))
+    cmd = _calls_command(CALLS + ".tmp")
+    procs.append((os.path.basename(CALLS_SOURCE), cmd,
+                  subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
     failed = []
     for src, cmd, pr in procs:
         out, _ = pr.communicate()
@@ -80,6 +102,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True, 
     if failed:
         msg = "\n".join(f"--- {s}\n{o}" for s, o in failed)
         raise RuntimeError(f"nvcc failed:\n{msg}")
+    os.replace(CALLS + ".tmp", CALLS)
     tmp = lib + ".tmp"
     subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lrt",
                     "-lpthread"], check=True)

@@ -140,17 +140,15 @@ def test_binding_refuses_host_tensors_and_bad_layouts(ta):
                  lambda: ta.tree_attn_decode_selected(q, pool, pool, bt, sl, torch.zeros(1, 2, 4, dtype=torch.int32))):
         with pytest.raises(ValueError, match="CUDA device"):
             call()
-    from softmax_tree_reduction_gb300 import _serving as s
-    assert s._vec_strides(torch.zeros(5, 6, 64)[:, 2:4], "k") == (384, 64)
-    assert s._vec_strides(torch.zeros(1, 1, 64), "k", True) == (0, 0)
-    with pytest.raises(ValueError):
-        s._vec_strides(torch.zeros(5, 64, 6).transpose(1, 2), "k")
-    with pytest.raises(ValueError, match="share memory"):
-        s._vec_strides(torch.zeros(1, 6, 64).expand(5, 6, 64), "k_out", True)
-    with pytest.raises(ValueError, match="norm=True"):
-        s._rope_struct(64, 0, None, torch.ones(64), None, False, 1e-6, False)
-    with pytest.raises(ValueError):
-        s._rope_struct(64, 0, None, torch.ones(64), torch.ones(64, dtype=torch.bfloat16), True, 1e-6, False)
+    for call in (lambda: ta.tree_attn_norm_rope(None, None, pos), lambda: ta.tree_attn_norm_rope(k, k, pos, norm=False),
+                 lambda: ta.tree_attn_cache_write(k, k, kc, kc, pos, q=k), lambda: ta.tree_attn_cache_write(k, k, kc, kc, pos, k_weight=k[0, 0])):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        ta.tree_attn_norm_rope([1.0], None, pos, q_out=k)
+    from softmax_tree_reduction_gb300 import _serving_calls as c
+    with pytest.raises(TypeError, match="number of arguments"):
+        c.norm_rope(k)
 
 
 def test_reference_by_hand():
