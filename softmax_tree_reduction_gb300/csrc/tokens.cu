@@ -3,13 +3,20 @@
 // and reading a cache back.
 //
 // A vector is the head_dim channels of one (token, head).  A group of
-// head_dim/8 lanes holds one vector, 8 consecutive channels a lane (one
-// 16-byte access of BF16), and walks the heads of its token, four vectors in
-// flight, so that the token's cosines and sines are computed once per group
-// and stay in registers.  With few tokens a token's heads are spread over
-// several groups instead (heads_per_group): then the call is bound by the
-// latency of one load, the angles and one store, and recomputing the angles
-// costs nothing.
+// head_dim/8 lanes holds one vector, 8 channels a lane as two runs of four, and
+// walks the heads of its token, several vectors in flight, so that the token's
+// cosines and sines are computed once per group and stay in registers.  The
+// runs are placed so that every rotated pair lies in one lane: channels
+// [4 l, 4 l + 4) with their partners half the rotated range further on, or eight
+// neighbours where pairs are adjacent or nothing is rotated.  (First version: 16-byte
+// accesses and eight shuffles a vector to bring partners together; the runs need half
+// the cosines and registers too: 152 -> 131 us for 32768 tokens of 32 + 16 BF16
+// heads, 806 MB, 119 us at the copy rate.)  Blocks of 128 threads: with 256 the last
+// ones of a long list leave SMs idle (145 us).
+//
+// With few tokens a token's heads are spread over several groups instead
+// (heads_per_group): then the call is bound by the latency of one load, the
+// angles and one store, and recomputing the angles costs nothing.
 //
 // Rotation angles.  The angle p * f of position p is needed modulo 2 pi.  The
 // frequency is turned into a 64-bit binary fraction of a full turn per
@@ -24,6 +31,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "common.cuh"
 #include "host.h"
@@ -31,7 +39,7 @@
 namespace ta {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kFlight = 4;  // vectors a group keeps in flight
 
 struct Vectors {
@@ -60,44 +68,36 @@ struct TokenParams {
     float eps;
 };
 
-// 8 channels of a vector in memory, and as FP32.
+// Four channels of a vector in memory, and as FP32.
 template <typename T>
-struct Eight;
+struct Four;
 template <>
-struct Eight<__nv_bfloat16> {
-    uint4 x;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { x = *reinterpret_cast<const uint4*>(p); }
-    __device__ __forceinline__ void unpack(float (&f)[8]) const {
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    }
-};
-template <>
-struct Eight<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float* p) {
-        a = reinterpret_cast<const float4*>(p)[0];
-        b = reinterpret_cast<const float4*>(p)[1];
-    }
-    __device__ __forceinline__ void unpack(float (&f)[8]) const {
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-    }
-};
-template <>
-struct Eight<__nv_fp8_e4m3> {
+struct Four<__nv_bfloat16> {
     uint2 x;
-    __device__ __forceinline__ void load(const __nv_fp8_e4m3* p) { x = *reinterpret_cast<const uint2*>(p); }
-    __device__ __forceinline__ void unpack(float (&f)[8]) const {
-        const uint32_t w[2] = {x.x, x.y};
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { x = *reinterpret_cast<const uint2*>(p); }
+    __device__ __forceinline__ void unpack(float* f) const {
+        f[0] = __uint_as_float(x.x << 16);
+        f[1] = __uint_as_float(x.x & 0xffff0000u);
+        f[2] = __uint_as_float(x.y << 16);
+        f[3] = __uint_as_float(x.y & 0xffff0000u);
+    }
+};
+template <>
+struct Four<float> {
+    float4 x;
+    __device__ __forceinline__ void load(const float* p) { x = *reinterpret_cast<const float4*>(p); }
+    __device__ __forceinline__ void unpack(float* f) const {
+        f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+    }
+};
+template <>
+struct Four<__nv_fp8_e4m3> {
+    uint32_t x;
+    __device__ __forceinline__ void load(const __nv_fp8_e4m3* p) { x = *reinterpret_cast<const uint32_t*>(p); }
+    __device__ __forceinline__ void unpack(float* f) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-                static_cast<__nv_fp8x2_storage_t>(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+        for (int i = 0; i < 2; ++i) {
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(x >> (16 * i)), __NV_E4M3);
             const float2 v = __half22float2(__half2(h));
             f[2 * i] = v.x;
             f[2 * i + 1] = v.y;
@@ -105,28 +105,58 @@ struct Eight<__nv_fp8_e4m3> {
     }
 };
 
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+// Eight neighbouring channels: one 16-byte access of BF16 (values and vectors read
+// back, which need no pairs; halving the accesses is worth 63 against 75 us on
+// 65536 tokens of 8 + 8 heads read from an E4M3 cache).
+template <typename T>
+struct Eight {
+    Four<T> x, y;
+    __device__ __forceinline__ void load(const T* p) {
+        x.load(p);
+        y.load(p + 4);
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    __device__ __forceinline__ void unpack(float (&f)[8]) const {
+        x.unpack(f);
+        y.unpack(f + 4);
+    }
+};
+template <>
+__device__ __forceinline__ void Eight<__nv_bfloat16>::load(const __nv_bfloat16* p) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    x.x = make_uint2(v.x, v.y);
+    y.x = make_uint2(v.z, v.w);
 }
-__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+template <>
+__device__ __forceinline__ void Eight<__nv_fp8_e4m3>::load(const __nv_fp8_e4m3* p) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    x.x = v.x;
+    y.x = v.y;
+}
+__device__ __forceinline__ uint2 pack4(const float* f) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 // Nearest even; finite values saturate at +-448, NaN stays NaN.
+__device__ __forceinline__ uint32_t codes4(const float* f) {
+    const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3);
+    return a | (b << 16);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* f) { *reinterpret_cast<uint2*>(p) = pack4(f); }
+__device__ __forceinline__ void store4(float* p, const float* f) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+}
+__device__ __forceinline__ void store4(__nv_fp8_e4m3* p, const float* f) { *reinterpret_cast<uint32_t*>(p) = codes4(f); }
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
+    const uint2 a = pack4(f), b = pack4(f + 4);
+    *reinterpret_cast<uint4*>(p) = make_uint4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
+    store4(p, f);
+    store4(p + 4, f + 4);
+}
 __device__ __forceinline__ void store8(__nv_fp8_e4m3* p, const float (&f)[8]) {
-    uint32_t w[2] = {0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i >> 1] |= static_cast<uint32_t>(
-                         __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i], f[2 * i + 1]), __NV_SATFINITE, __NV_E4M3))
-                     << (16 * (i & 1));
-    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(p) = make_uint2(codes4(f), codes4(f + 4));
 }
 
 // cos and sin of pos * f.  f / (2 pi) in units of 2^-64 turns: f = m * 2^e with a
@@ -154,62 +184,46 @@ __device__ __forceinline__ void turn(int pos, float f, float* c, float* s) {
     sincospif(half_turns, s, c);
 }
 
-// What a lane holds of its token's rotation: for each of its channels the
-// cosine and the signed sine that its partner channel is multiplied with.
-struct Rotation {
-    float c[8], s[8];
-    int src;      // lane holding the partner channels (halves); the lane itself if interleaved
-    bool on;      // the lane's channels are rotated
+// The lane's channels: runs [a, a + 4) and [b, b + 4), and whether they are rotated.
+struct Lane {
+    int a, b;
+    bool on;
 };
 
-template <int L>
-__device__ __forceinline__ Rotation make_rotation(const TokenParams& p, int pos, int l, int lane) {
-    Rotation r;
-    const int half = p.rot >> 1;
-    r.on = 8 * l < p.rot;
-    r.src = lane;
-    if (!r.on) return r;
-    if (p.interleaved) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float c, s;
-            turn(pos, __ldg(p.inv_freq + 4 * l + i), &c, &s);
-            r.c[2 * i] = r.c[2 * i + 1] = c;
-            r.s[2 * i] = -s;
-            r.s[2 * i + 1] = s;
-        }
-        return r;
-    }
-    const bool second = 8 * l >= half;
-    const int j0 = 8 * l - (second ? half : 0);
-    r.src = second ? lane - half / 8 : lane + half / 8;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float s;
-        turn(pos, __ldg(p.inv_freq + j0 + i), &r.c[i], &s);
-        r.s[i] = second ? s : -s;
-    }
-    return r;
+__device__ __forceinline__ Lane make_lane(const TokenParams& p, int l) {
+    const int pairs = p.rot >> 3;  // lanes that hold rotated channels
+    Lane c;
+    c.on = l < pairs;
+    const bool split = c.on && !p.interleaved;
+    c.a = split ? 4 * l : 8 * l;
+    c.b = split ? 4 * l + (p.rot >> 1) : 8 * l + 4;
+    return c;
 }
 
-__device__ __forceinline__ void load_weight(const void* w, int bf16, int ch, float (&f)[8]) {
+__device__ __forceinline__ void load_weight(const void* w, int bf16, const Lane& c, float (&f)[8]) {
     if (w == nullptr) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = 1.f;
     } else if (bf16) {
-        Eight<__nv_bfloat16> e;
-        e.load(static_cast<const __nv_bfloat16*>(w) + ch);
-        e.unpack(f);
+        Four<__nv_bfloat16> x, y;
+        x.load(static_cast<const __nv_bfloat16*>(w) + c.a);
+        y.load(static_cast<const __nv_bfloat16*>(w) + c.b);
+        x.unpack(f);
+        y.unpack(f + 4);
     } else {
-        Eight<float> e;
-        e.load(static_cast<const float*>(w) + ch);
-        e.unpack(f);
+        Four<float> x, y;
+        x.load(static_cast<const float*>(w) + c.a);
+        y.load(static_cast<const float*>(w) + c.b);
+        x.unpack(f);
+        y.unpack(f + 4);
     }
 }
 
+// cs, sn: the lane's four pairs; pair i is channels (i, i + 4) of f, or (2 i, 2 i + 1)
+// with adjacent pairs.
 template <int L>
-__device__ __forceinline__ void norm_rotate(const TokenParams& p, const Rotation& r, const float (&w)[8],
-                                            float (&f)[8], unsigned mask) {
+__device__ __forceinline__ void norm_rotate(const TokenParams& p, const Lane& c, const float (&cs)[4], const float (&sn)[4],
+                                            const float (&w)[8], float (&f)[8], unsigned mask) {
     if (p.norm) {
         float ss = 0.f;
 #pragma unroll
@@ -220,38 +234,88 @@ __device__ __forceinline__ void norm_rotate(const TokenParams& p, const Rotation
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = f[i] * inv * w[i];
     }
-    if (p.rot) {
-        float o[8];
+    if (c.on) {  // channels past rot_dim keep their value (also an infinite one)
         if (p.interleaved) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = f[i ^ 1];
+            for (int i = 0; i < 4; ++i) {
+                const float x = f[2 * i], y = f[2 * i + 1];
+                f[2 * i] = x * cs[i] - y * sn[i];
+                f[2 * i + 1] = y * cs[i] + x * sn[i];
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(mask, f[i], r.src);
-        }
-        if (r.on) {  // channels past rot_dim keep their value (also an infinite one)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = f[i] * r.c[i] + o[i] * r.s[i];
+            for (int i = 0; i < 4; ++i) {
+                const float x = f[i], y = f[i + 4];
+                f[i] = x * cs[i] - y * sn[i];
+                f[i + 4] = y * cs[i] + x * sn[i];
+            }
         }
     }
 }
 
 // Heads [h0, h1) of a token: load, transform, store, kFlight vectors at a time.
-template <typename TIn, typename Fn>
-__device__ __forceinline__ void walk_heads(const TIn* src, int64_t sh, int h0, int h1, Fn&& fn) {
+// `load(x, h)` fills a held vector, `use(x, h)` finishes it.
+template <typename Held, typename Load, typename Use>
+__device__ __forceinline__ void walk_heads(int h0, int h1, Load&& load, Use&& use) {
     for (int h = h0; h < h1; h += kFlight) {
-        Eight<TIn> e[kFlight];
+        Held x[kFlight];
 #pragma unroll
         for (int j = 0; j < kFlight; ++j)
-            if (h + j < h1) e[j].load(src + (h + j) * sh);
+            if (h + j < h1) load(x[j], h + j);
 #pragma unroll
-        for (int j = 0; j < kFlight; ++j) {
-            if (h + j < h1) {
-                float f[8];
-                e[j].unpack(f);
-                fn(h + j, f);
-            }
-        }
+        for (int j = 0; j < kFlight; ++j)
+            if (h + j < h1) use(x[j], h + j);
+    }
+}
+
+// A lane's two runs of a vector.
+template <typename T>
+struct Runs {
+    Four<T> x, y;
+};
+
+template <typename T, typename Use>
+__device__ __forceinline__ void walk_runs(const T* src, int64_t sh, const Lane& c, int h0, int h1, Use&& use) {
+    const T* sa = src + c.a;
+    const T* sb = src + c.b;
+    walk_heads<Runs<T>>(
+        h0, h1,
+        [&](Runs<T>& r, int h) {
+            r.x.load(sa + h * sh);
+            r.y.load(sb + h * sh);
+        },
+        [&](const Runs<T>& r, int h) {
+            float f[8];
+            r.x.unpack(f);
+            r.y.unpack(f + 4);
+            use(h, f);
+        });
+}
+
+// Whole vectors, the lane's eight channels from `src` on.
+template <typename T, typename Use>
+__device__ __forceinline__ void walk_whole(const T* src, int64_t sh, int h0, int h1, Use&& use) {
+    walk_heads<Eight<T>>(
+        h0, h1, [&](Eight<T>& e, int h) { e.load(src + h * sh); },
+        [&](const Eight<T>& e, int h) {
+            float f[8];
+            e.unpack(f);
+            use(h, f);
+        });
+}
+
+template <typename T>
+__device__ __forceinline__ void store_runs(T* dst, const Lane& c, const float (&f)[8]) {
+    store4(dst + c.a, f);
+    store4(dst + c.b, f + 4);
+}
+
+template <typename TC>
+__device__ __forceinline__ void to_codes(const float* scale, int h, float (&f)[8]) {
+    if constexpr (std::is_same<TC, __nv_fp8_e4m3>::value) {
+        const float sc = __ldg(scale + h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = f[i] / sc;
     }
 }
 
@@ -291,21 +355,22 @@ __global__ void __launch_bounds__(kThreads) token_write_kernel(const TokenParams
     const int pos = p.positions[t];
     const int row = !kCache || !p.rows ? t : p.rows[t];
     if (pos < 0 || row < 0) return;  // a padding token
-    const int lane = threadIdx.x & 31, l = lane % L;
-    const unsigned mask = (L == 32 ? 0xffffffffu : ((1u << L) - 1u)) << (lane & ~(L - 1));
-    const int ch = 8 * l;
-
+    const int lane = threadIdx.x & 31;
+    const unsigned mask = ((1u << L) - 1u) << (lane & ~(L - 1));
+    const Lane c = make_lane(p, lane % L);
     const int kend = p.Hq + p.Hkv;
-    Rotation r;
-    if (p.rot && h0 < kend) r = make_rotation<L>(p, pos, l, lane);
+    float cs[4], sn[4];
+    if (c.on && h0 < kend) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) turn(pos, __ldg(p.inv_freq + 4 * (lane % L) + i), &cs[i], &sn[i]);
+    }
     if (h0 < p.Hq) {
         float w[8];
-        if (p.norm) load_weight(p.qw, p.w_bf16, ch, w);
-        const T* src = static_cast<const T*>(p.q.data) + t * p.q.st + ch;
-        T* dst = static_cast<T*>(p.qo.data) + t * p.qo.st + ch;
-        walk_heads(src, p.q.sh, h0, min(h1, p.Hq), [&](int h, float (&f)[8]) {
-            norm_rotate<L>(p, r, w, f, mask);
-            store8(dst + h * p.qo.sh, f);
+        if (p.norm) load_weight(p.qw, p.w_bf16, c, w);
+        T* dst = static_cast<T*>(p.qo.data) + t * p.qo.st;
+        walk_runs(static_cast<const T*>(p.q.data) + t * p.q.st, p.q.sh, c, h0, min(h1, p.Hq), [&](int h, float (&f)[8]) {
+            norm_rotate<L>(p, c, cs, sn, w, f, mask);
+            store_runs(dst + h * p.qo.sh, c, f);
         });
     }
     if (h1 <= p.Hq) return;
@@ -316,33 +381,26 @@ __global__ void __launch_bounds__(kThreads) token_write_kernel(const TokenParams
     }
     if (h0 < kend) {
         float w[8];
-        if (p.norm) load_weight(p.kw, p.w_bf16, ch, w);
-        const T* src = static_cast<const T*>(p.k.data) + t * p.k.st + ch;
-        walk_heads(src, p.k.sh, max(h0 - p.Hq, 0), min(h1 - p.Hq, p.Hkv), [&](int h, float (&f)[8]) {
-            norm_rotate<L>(p, r, w, f, mask);
-            if constexpr (!kCache) {
-                store8(static_cast<T*>(p.ko.data) + t * p.ko.st + h * p.ko.sh + ch, f);
-            } else {
-                if constexpr (std::is_same<TC, __nv_fp8_e4m3>::value) {
-                    const float sc = __ldg(p.ks + h);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] = f[i] / sc;
-                }
-                store8(static_cast<TC*>(p.kc) + place + h * p.ch + ch, f);
-            }
-        });
+        if (p.norm) load_weight(p.kw, p.w_bf16, c, w);
+        walk_runs(static_cast<const T*>(p.k.data) + t * p.k.st, p.k.sh, c, max(h0 - p.Hq, 0), min(h1 - p.Hq, p.Hkv),
+                  [&](int h, float (&f)[8]) {
+                      norm_rotate<L>(p, c, cs, sn, w, f, mask);
+                      if constexpr (!kCache) {
+                          store_runs(static_cast<T*>(p.ko.data) + t * p.ko.st + h * p.ko.sh, c, f);
+                      } else {
+                          to_codes<TC>(p.ks, h, f);
+                          store_runs(static_cast<TC*>(p.kc) + place + h * p.ch, c, f);
+                      }
+                  });
     }
     if constexpr (kCache) {
         if (h1 <= kend) return;
-        const T* src = static_cast<const T*>(p.v.data) + t * p.v.st + ch;
-        walk_heads(src, p.v.sh, max(h0 - kend, 0), h1 - kend, [&](int h, float (&f)[8]) {
-            if constexpr (std::is_same<TC, __nv_fp8_e4m3>::value) {
-                const float sc = __ldg(p.vs + h);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = f[i] / sc;
-            }
-            store8(static_cast<TC*>(p.vc) + place + h * p.ch + ch, f);
-        });
+        const int ch = 8 * (lane % L);
+        walk_whole(static_cast<const T*>(p.v.data) + t * p.v.st + ch, p.v.sh, max(h0 - kend, 0), h1 - kend,
+                   [&](int h, float (&f)[8]) {
+                       to_codes<TC>(p.vs, h, f);
+                       store8(static_cast<TC*>(p.vc) + place + h * p.ch + ch, f);
+                   });
     }
 }
 
@@ -372,8 +430,7 @@ __global__ void __launch_bounds__(kThreads) token_read_kernel(const TokenParams 
             for (int h = a; h < b; ++h) store8(dst + h * out.sh, f);
             continue;
         }
-        const TC* src = static_cast<const TC*>(kv ? p.vc : p.kc) + place + ch;
-        walk_heads(src, p.ch, a, b, [&](int h, float (&f)[8]) {
+        walk_whole(static_cast<const TC*>(kv ? p.vc : p.kc) + place + ch, p.ch, a, b, [&](int h, float (&f)[8]) {
             if constexpr (std::is_same<TC, __nv_fp8_e4m3>::value) {
                 const float sc = __ldg(scale + h);
 #pragma unroll
@@ -386,13 +443,15 @@ __global__ void __launch_bounds__(kThreads) token_read_kernel(const TokenParams 
 
 // ---------------------------------------------------------------- host side
 // Heads per group: all of a token's vectors while the tokens alone fill the
-// device, fewer for short lists.
-void plan_groups(TokenParams* p, int heads, int num_sms) {
-    const int64_t want = static_cast<int64_t>(num_sms) * 64;  // groups in flight on a full device
+// device (1024 threads an SM), else the token's heads in even shares, each of a
+// few kFlight vectors, down to one vector a group.
+void plan_groups(TokenParams* p, int heads, int lanes, int num_sms) {
+    const int64_t want = static_cast<int64_t>(num_sms) * 1024 / lanes;
     int64_t hpg = (static_cast<int64_t>(p->T) * heads + want - 1) / want;
     hpg = std::max<int64_t>(1, std::min<int64_t>(hpg, heads));
     if (hpg > 1) hpg = std::min<int64_t>(heads, (hpg + kFlight - 1) / kFlight * kFlight);
-    p->hpg = static_cast<int>(hpg);
+    p->chunks = static_cast<int>((heads + hpg - 1) / hpg);
+    p->hpg = (heads + p->chunks - 1) / p->chunks;
     p->chunks = (heads + p->hpg - 1) / p->hpg;
 }
 
@@ -517,7 +576,7 @@ int enqueue(const ta_shape* shape, TokenParams* p, int heads, int cache, bool re
     const int rc = device_info(&dev);
     if (rc != TA_OK) return rc;
     p->err = dev.err;
-    plan_groups(p, heads, dev.num_sms);
+    plan_groups(p, heads, shape->head_dim / 8, dev.num_sms);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool d128 = shape->head_dim == 128, bf16 = shape->q_dtype == TA_BF16;
     cudaError_t e;
