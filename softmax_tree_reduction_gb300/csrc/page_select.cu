@@ -12,19 +12,28 @@
 // product of 2 d terms per page with A[i] = sum_h max(q_h[i], 0) and
 // B[i] = sum_h min(q_h[i], 0).
 //
-// Precision.  The list must not depend on the order of summation, so scores
-// are carried as the unevaluated sum of two FP32 numbers: A and B are summed
-// with exact two-term additions (Knuth's two-sum), each coefficient is split
-// into a part of 16 significant bits, whose product with a BF16 bound is exact
-// in FP32, and a rest, whose product is added to the low part.  About 2^-40
-// relative to the largest partial sum remains, against gaps of 2^-10 or so
-// between neighbouring scores.  FP32 bounds use an FMA for the product's error.
+// Precision.  The list must not depend on the order of summation, yet FP32
+// scores of a few hundred terms differ from the real ones by more than some
+// neighbouring pages do.  So the score kernel sums in FP32 and also returns
+// mag = sum_i |A[i] hi[i]| + |B[i] lo[i]|: coefficients are rounded once, a lane
+// chains at most 8 products and 5 levels join the lanes, so a score is off by
+// less than 16 u mag (u = 2^-24), taken as eps = 20 u max(mag).  With t the
+// FP32 score of the last page to be taken, pages above t + 2 eps are in and those
+// below t - 2 eps are out whatever the rounding; usually nothing but that page
+// lies between.  Otherwise the pages between are scored again as unevaluated sums
+// of two FP32 numbers (Knuth's two-sum; each coefficient is split into 16
+// significant bits, whose product with a BF16 bound is exact, and a rest), which
+// leaves about 2^-40 mag, and the places left go to the best of those.
 //
-// Selection.  One block per (row, KV head): the score of the last page to be
-// taken is found by four passes of an 8-bit radix select over the high parts
-// (order-preserving integers), then, only if several pages share that value,
-// over their low parts; ties that remain go to the lowest pages.  Counting is in
-// shared memory with integer atomics, whose order cannot change the counts.
+// Selection.  One block per (row, KV head): scores are kept in shared memory as
+// order-preserving integers, whose common leading bits are skipped, and the
+// last page's is found digit by digit (8 bits a pass, counted with integer
+// atomics in shared memory: their order cannot change the counts).  Ties go to
+// the lowest pages.
+//
+// Measured (GB300, cold L2): the two-FP32-number sum for every page cost 135
+// instructions a page and bound the score kernel by issue (28 us for 131072
+// page scores of 512 bytes, 10 us of HBM time).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -34,6 +43,7 @@
 
 #include "common.cuh"
 #include "host.h"
+#include "kernels.h"
 
 namespace ta {
 namespace {
@@ -242,9 +252,13 @@ struct SelectParams {
     const int32_t* seqlens;
     const int32_t* block_table;
     int32_t* selected;
-    float2* scores;             // [B][Hkv][pages]
+    float* scores;              // [B][Hkv][stride]: FP32 scores
+    float* mags;                // [B][Hkv][stride / 8]: largest sum of term magnitudes of 8 pages
+    float2* exact;              // [B][Hkv][pages]: the pages FP32 cannot rank, as two FP32 numbers
+    float2* coef;               // [B][Hkv][2 d]: the coefficients, as two FP32 numbers
     int* err;
     int B, Hq, Hkv, G, S, pages;  // pages: most pages a row can have
+    int stride;                 // pages rounded up to 32
     int num_select, first, last;
     int max_pages, page_shift, num_pages;
     int per_block;              // pages a block scores
@@ -269,13 +283,58 @@ __device__ __forceinline__ float q_value(const void* q, size_t i) {
         return __bfloat162float(static_cast<const __nv_bfloat16*>(q)[i]);
 }
 
+// Coefficient i of (row b, KV head g) as the sum of two FP32 numbers: i < D for
+// the minima, then for the maxima.
+template <int D, typename TQ>
+__device__ __forceinline__ float2 coefficient(const SelectParams& p, int b, int g, int i) {
+    const bool up = i >= D;
+    const size_t at = (static_cast<size_t>(b) * p.Hq + g * p.G) * D + (up ? i - D : i);
+    float s = 0.f, e = 0.f;
+#pragma unroll 4
+    for (int h = 0; h < p.G; ++h) {
+        const float x = q_value<TQ>(p.q, at + static_cast<size_t>(h) * D);
+        float err;
+        // (a NaN must stay one: fmaxf and fminf would drop it)
+        two_sum(s, (up ? x > 0.f : x < 0.f) || x != x ? x : 0.f, &s, &err);
+        e = __fadd_rn(e, err);
+    }
+    return make_float2(s, e);
+}
+
+// A lane's share of one page's bounds.
+template <int D, typename TB>
+struct PageBounds {
+    static constexpr bool kF32 = std::is_same<TB, float>::value;
+    static constexpr int E = 2 * D / 32;                              // elements per lane: 4 or 8
+    static constexpr int W = E * static_cast<int>(sizeof(TB)) / 4;  // words per lane: 2, 4 or 8
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const TB* src) {
+        if constexpr (W == 2) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+            w[0] = v.x; w[1] = v.y;
+        } else {
+#pragma unroll
+            for (int x = 0; x < W / 4; ++x) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + x);
+                w[4 * x] = v.x; w[4 * x + 1] = v.y; w[4 * x + 2] = v.z; w[4 * x + 3] = v.w;
+            }
+        }
+    }
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (kF32)
+            return __uint_as_float(w[i]);
+        else
+            return __uint_as_float((i & 1) ? (w[i >> 1] & 0xffff0000u) : (w[i >> 1] << 16));
+    }
+};
+
 // Pages [blockIdx.x * per_block, ..) of (KV head blockIdx.y, row blockIdx.z).  A warp
 // takes 8 pages at a time; a lane holds the coefficients of its channels.
 template <int D, typename TQ, typename TB>
-__global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const SelectParams p) {
-    constexpr bool kF32 = std::is_same<TB, float>::value;
-    constexpr int E = 2 * D / 32;                     // bound elements per lane: 4 or 8
-    __shared__ float2 coef[2 * D];                    // for the minima, then the maxima
+__global__ void __launch_bounds__(kScoreThreads, std::is_same<TB, float>::value ? 2 : 4) page_score_kernel(const SelectParams p) {
+    using PB = PageBounds<D, TB>;
+    constexpr int E = PB::E;
+    __shared__ float coef[2 * D];
     wait_primary();
     allow_dependents();
     const int g = blockIdx.y, b = blockIdx.z;
@@ -284,74 +343,44 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const SelectP
     const int n = static_cast<int>((static_cast<int64_t>(N) + (1 << p.page_shift) - 1) >> p.page_shift);
     const int p0 = blockIdx.x * p.per_block, p1 = min(n, p0 + p.per_block);
     if (n <= p.num_select || p0 >= n) return;         // every page is taken, or no page here
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.max_pages;
+    float* scores = p.scores + (static_cast<int64_t>(b) * p.Hkv + g) * p.stride;
+    float* mags = p.mags + (static_cast<int64_t>(b) * p.Hkv + g) * (p.stride / 8);
+    const TB* bounds = static_cast<const TB*>(p.bounds) + static_cast<int64_t>(g) * 2 * D + lane * E;
+    auto lookup = [&](int q0) { return (lane < 8 && q0 + lane < p1) ? __ldg(table + q0 + lane) : -1; };
+    // the first pages' numbers are on their way while the coefficients are summed
+    int q0 = p0 + warp * 8;
+    int phys = lookup(q0);
     for (int i = threadIdx.x; i < 2 * D; i += kScoreThreads) {
-        const bool up = i >= D;
-        float s = 0.f, e = 0.f;
-        for (int h = 0; h < p.G; ++h) {
-            const float x = q_value<TQ>(p.q, (static_cast<size_t>(b) * p.Hq + g * p.G + h) * D + (up ? i - D : i));
-            float err;
-            // (a NaN must stay one: fmaxf and fminf would drop it)
-            two_sum(s, (up ? x > 0.f : x < 0.f) || x != x ? x : 0.f, &s, &err);
-            e = __fadd_rn(e, err);
-        }
-        if constexpr (kF32) {
-            coef[i] = make_float2(s, e);
-        } else {
-            const float top = __uint_as_float(__float_as_uint(s) & 0xffffff00u);
-            coef[i] = make_float2(top, __fadd_rn(__fsub_rn(s, top), e));
-        }
+        const float2 c = coefficient<D, TQ>(p, b, g, i);
+        coef[i] = __fadd_rn(c.x, c.y);
+        if (blockIdx.x == 0) p.coef[(static_cast<int64_t>(b) * p.Hkv + g) * 2 * D + i] = c;
     }
     __syncthreads();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float ca[E], cb[E];
+    float c[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const float2 c = coef[lane * E + i];
-        ca[i] = c.x;
-        cb[i] = c.y;
-    }
-    const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.max_pages;
-    float2* scores = p.scores + (static_cast<int64_t>(b) * p.Hkv + g) * p.pages;
-    const TB* bounds = static_cast<const TB*>(p.bounds) + static_cast<int64_t>(g) * 2 * D + lane * E;
-    for (int q0 = p0 + warp * 8; q0 < p1; q0 += kScoreWarps * 8) {
-        int phys = -1;
-        if (lane < 8 && q0 + lane < p1) phys = __ldg(table + q0 + lane);
-        float s[8], e[8];
-        constexpr int W = E * static_cast<int>(sizeof(TB)) / 4;  // words per lane: 2, 4 or 8
-        uint32_t w[8][W];
-        bool ok[8];
+    for (int i = 0; i < E; ++i) c[i] = coef[lane * E + i];
+    while (q0 < p1) {
+        const unsigned ok = __ballot_sync(0xffffffffu, phys >= 0 && phys < p.num_pages);
+        PB x[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int ph = __shfl_sync(0xffffffffu, phys, j);
-            ok[j] = ph >= 0 && ph < p.num_pages;
-            const TB* src = bounds + (ok[j] ? static_cast<int64_t>(ph) * p.Hkv * 2 * D : 0);
-            if constexpr (W == 2) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
-                w[j][0] = v.x; w[j][1] = v.y;
-            } else {
-#pragma unroll
-                for (int x = 0; x < W / 4; ++x) {
-                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + x);
-                    w[j][4 * x] = v.x; w[j][4 * x + 1] = v.y; w[j][4 * x + 2] = v.z; w[j][4 * x + 3] = v.w;
-                }
-            }
+            x[j].load(bounds + (((ok >> j) & 1u) ? static_cast<int64_t>(ph) * p.Hkv * 2 * D : 0));
         }
+        const int next = q0 + kScoreWarps * 8;
+        phys = lookup(next);
+        float s[8], m[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             s[j] = 0.f;
-            e[j] = 0.f;
+            m[j] = 0.f;
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                float x;
-                if constexpr (kF32)
-                    x = __uint_as_float(w[j][i]);
-                else
-                    x = __uint_as_float((i & 1) ? (w[j][i >> 1] & 0xffff0000u) : (w[j][i >> 1] << 16));
-                const float pr = __fmul_rn(ca[i], x);
-                if constexpr (kF32) e[j] = __fadd_rn(e[j], __fmaf_rn(ca[i], x, -pr));
-                float err;
-                two_sum(s[j], pr, &s[j], &err);
-                e[j] = __fadd_rn(__fmaf_rn(cb[i], x, e[j]), err);
+                const float v = x[j][i];
+                s[j] = fmaf(c[i], v, s[j]);
+                m[j] = fmaf(fabsf(c[i]), fabsf(v), m[j]);
             }
         }
         // 8 pages over 32 lanes: halve the pages held three times, then the lanes
@@ -361,125 +390,128 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const SelectP
             const bool up = (lane & off) != 0;
 #pragma unroll
             for (int j = 0; j < half; ++j) {
-                const float ss = up ? s[j] : s[j + half], se = up ? e[j] : e[j + half];
-                const float ks = up ? s[j + half] : s[j], ke = up ? e[j + half] : e[j];
-                const float rs = __shfl_xor_sync(0xffffffffu, ss, off), re = __shfl_xor_sync(0xffffffffu, se, off);
-                float err;
-                two_sum(ks, rs, &s[j], &err);
-                e[j] = __fadd_rn(__fadd_rn(ke, re), err);
+                const float ss = up ? s[j] : s[j + half], sm = up ? m[j] : m[j + half];
+                const float ks = up ? s[j + half] : s[j], km = up ? m[j + half] : m[j];
+                s[j] = ks + __shfl_xor_sync(0xffffffffu, ss, off);
+                m[j] = km + __shfl_xor_sync(0xffffffffu, sm, off);
             }
         }
 #pragma unroll
         for (int off = 2; off > 0; off >>= 1) {
-            const float rs = __shfl_xor_sync(0xffffffffu, s[0], off), re = __shfl_xor_sync(0xffffffffu, e[0], off);
-            float err;
-            two_sum(s[0], rs, &s[0], &err);
-            e[0] = __fadd_rn(__fadd_rn(e[0], re), err);
+            s[0] += __shfl_xor_sync(0xffffffffu, s[0], off);
+            m[0] += __shfl_xor_sync(0xffffffffu, m[0], off);
         }
         const int mine = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
-        const unsigned okmask = (ok[0] ? 1u : 0u) | (ok[1] ? 2u : 0u) | (ok[2] ? 4u : 0u) | (ok[3] ? 8u : 0u) |
-                                (ok[4] ? 16u : 0u) | (ok[5] ? 32u : 0u) | (ok[6] ? 64u : 0u) | (ok[7] ? 128u : 0u);
-        if ((lane & 3) == 0 && q0 + mine < p1) {
-            // normalised, so that comparing (high, low) compares the sums; + 0 makes -0 one zero
-            float h = __fadd_rn(s[0], e[0]);
-            float l = __fadd_rn(__fadd_rn(__fsub_rn(s[0], h), e[0]), 0.f);
-            h = __fadd_rn(h, 0.f);
-            if (!((okmask >> mine) & 1u) || !(fabsf(h) < INFINITY)) {
-                h = INFINITY;
-                l = 0.f;
-            }
-            scores[q0 + mine] = make_float2(h, l);
-        }
+        const bool mine_in = q0 + mine < p1;
+        const bool fin = ((ok >> mine) & 1u) && fabsf(s[0]) < INFINITY;
+        if ((lane & 3) == 0 && mine_in) scores[q0 + mine] = fin ? s[0] + 0.f : INFINITY;  // + 0: one zero
+        // (magnitudes are not negative, so their bits are ordered; NaN last)
+        const uint32_t big = __reduce_max_sync(0xffffffffu, mine_in && fin ? __float_as_uint(m[0]) : 0u);
+        if (lane == 0) mags[q0 >> 3] = __uint_as_float(big);
+        q0 = next;
     }
 }
 
 // ---------------------------------------------------------------- selection
 constexpr int kPickThreads = 512;
 constexpr int kPickWarps = kPickThreads / 32;
+constexpr int kPickKeep = 24576;  // scores kept in shared memory; longer rows read them again
 
-// Order-preserving integer of a float (no NaN).
+// Order-preserving integer of a float (no NaN), and back.
 __device__ __forceinline__ uint32_t ordered(float x) {
     const uint32_t u = __float_as_uint(x);
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
-
-// Exclusive prefix sum of one value per thread; *total is the block's sum.
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, off);
-        if (lane >= off) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) warp_sums[warp] = x;
-    __syncthreads();
-    int before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kPickWarps; ++w) {
-        const int c = warp_sums[w];
-        before += w < warp ? c : 0;
-        all += c;
-    }
-    *total = all;
-    return before + x - v;
+__device__ __forceinline__ float unordered(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
 
-// The `need`-th largest (need >= 1) of the keys key(i), i in [0, n), that
-// takes(i); *above: how many of them are larger.
-template <typename Key, typename Takes>
-__device__ uint32_t radix_pick(int n, int need, int* hist, int* found, Key&& key, Takes&& takes, int* above) {
-    uint32_t prefix = 0;
+// Sums over the block's warps of two warp-uniform values, and of those of the
+// warps before this one.
+__device__ __forceinline__ void warp_sums(int a, int b, int2* buf, int2* before, int2* all) {
+    const int warp = threadIdx.x >> 5;
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) buf[warp] = make_int2(a, b);
+    __syncthreads();
+    *before = *all = make_int2(0, 0);
+#pragma unroll
+    for (int w = 0; w < kPickWarps; ++w) {
+        const int2 c = buf[w];
+        if (w < warp) {
+            before->x += c.x;
+            before->y += c.y;
+        }
+        all->x += c.x;
+        all->y += c.y;
+    }
+}
+
+// The `need`-th largest (need >= 1) of the keys that are not 0 (0: no key), n4 groups
+// of four that key4(i) gives, where all keys agree with `first` above their `bits`
+// low bits; *above: how many are larger.
+template <typename Key4>
+__device__ uint32_t radix_pick(int n4, int need, uint32_t first, int bits, int* hist, int* found, Key4&& key4, int* above) {
+    uint32_t prefix = bits < 32 ? first >> bits : 0;
     int left = need;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = threadIdx.x; i < 256; i += kPickThreads) hist[i] = 0;
+    while (bits > 0) {
+        const int width = min(8, bits), shift = bits - width;
+        const uint32_t mask = (1u << width) - 1;
+        if (threadIdx.x < 256) hist[threadIdx.x] = 0;
         __syncthreads();
-        for (int i = threadIdx.x; i < n; i += kPickThreads) {
-            const uint32_t k = key(i);
-            if (takes(i) && (shift == 24 || (k >> (shift + 8)) == prefix)) atomicAdd(&hist[(k >> shift) & 255u], 1);
+#pragma unroll 2
+        for (int i = threadIdx.x; i < n4; i += kPickThreads) {
+            const uint4 q = key4(i);
+            const uint32_t k[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (k[j] != 0 && (bits == 32 || (k[j] >> bits) == prefix)) atomicAdd(&hist[(k[j] >> shift) & mask], 1);
         }
         __syncthreads();
         if (threadIdx.x < 32) {  // the largest digit with at least `left` keys at or above it
             const int lane = threadIdx.x;
-            int c[8], sum = 0;
+            const int4 u = reinterpret_cast<const int4*>(hist)[63 - 2 * lane], v = reinterpret_cast<const int4*>(hist)[62 - 2 * lane];
+            const int c[8] = {u.w, u.z, u.y, u.x, v.w, v.z, v.y, v.x};  // digits 255 - 8 lane downwards
+            int sum[8];
+            sum[0] = c[0];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                c[j] = hist[255 - (lane * 8 + j)];
-                sum += c[j];
-            }
-            int x = sum;
+            for (int j = 1; j < 8; ++j) sum[j] = sum[j - 1] + c[j];
+            int x = sum[7];
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, x, off);
                 if (lane >= off) x += y;
             }
-            int before = x - sum;
-            if (before < left && left <= x) {
+            const int before = x - sum[7];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (before < left && left <= before + c[j]) {
-                        found[0] = 255 - (lane * 8 + j);
-                        found[1] = left - before;
-                        break;
-                    }
-                    before += c[j];
+            for (int j = 0; j < 8; ++j) {
+                const int b0 = before + sum[j] - c[j];
+                if (b0 < left && left <= b0 + c[j]) {
+                    found[0] = 255 - (lane * 8 + j);
+                    found[1] = left - b0;
                 }
             }
         }
         __syncthreads();
-        prefix = (prefix << 8) | static_cast<uint32_t>(found[0]);
+        prefix = (prefix << width) | static_cast<uint32_t>(found[0]);
         left = found[1];
+        bits = shift;
     }
     *above = need - left;
     return prefix;
 }
 
-__global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectParams p) {
-    __shared__ int hist[256], found[2], sums[kPickWarps];
+template <int D, typename TQ, typename TB>
+__global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const SelectParams p) {
+    using PB = PageBounds<D, TB>;
+    extern __shared__ __align__(16) uint32_t keys_kept[];
+    __shared__ __align__(16) int hist[256];
+    __shared__ int found[2];
+    __shared__ int2 sums[kPickWarps];
+    __shared__ uint4 range_w[kPickWarps];
     wait_primary();
     allow_dependents();
     const int g = blockIdx.x, b = blockIdx.y;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t* sel = p.selected + (static_cast<int64_t>(b) * p.Hkv + g) * p.num_select;
     const int N = p.seqlens[b];
     const bool bad = N < 0 || N > p.S;
@@ -489,45 +521,229 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectPar
         for (int i = threadIdx.x; i < p.num_select; i += kPickThreads) sel[i] = i < n ? i : -1;
         return;
     }
-    const float2* sc = p.scores + (static_cast<int64_t>(b) * p.Hkv + g) * p.pages;
+    const int64_t row = static_cast<int64_t>(b) * p.Hkv + g;
+    const float* sc = p.scores + row * p.stride;
+    float2* exact = p.exact + row * p.pages;
     const int lo = p.first, hi = n - p.last;             // the pages that compete
     const int need = p.num_select - p.first - p.last;    // places for them; fewer than hi - lo
-    uint32_t T = 0xffffffffu, T2 = 0xffffffffu;
+    const int n4 = (n + 3) / 4;
+    // Pages above `top` are taken, pages below `low` are not; those between are
+    // taken where (T, T2) says so.
+    uint32_t top = 0xffffffffu, low = 0xffffffffu, T = 0, T2 = 0;
     int ties = 0;                                        // pages at (T, T2) to take, lowest first
+    // four pages' keys (0: the page does not compete)
+    auto scored4 = [&](int i) {
+        const float4 s = __ldcg(reinterpret_cast<const float4*>(sc) + i);
+        const int q = 4 * i;
+        uint4 k;
+        k.x = q >= lo && q < hi ? ordered(s.x) : 0u;
+        k.y = q + 1 >= lo && q + 1 < hi ? ordered(s.y) : 0u;
+        k.z = q + 2 >= lo && q + 2 < hi ? ordered(s.z) : 0u;
+        k.w = q + 3 >= lo && q + 3 < hi ? ordered(s.w) : 0u;
+        return k;
+    };
+    const bool kept = n <= kPickKeep;
+    auto key4 = [&](int i) { return kept ? reinterpret_cast<const uint4*>(keys_kept)[i] : scored4(i); };
+    auto key = [&](int i) { return kept ? keys_kept[i] : (i >= lo && i < hi ? ordered(__ldcg(sc + i)) : 0u); };
     if (need > 0) {
-        int above = 0, above2 = 0;
-        auto high = [&](int i) { return ordered(sc[lo + i].x); };
-        auto low = [&](int i) { return ordered(sc[lo + i].y); };
-        T = radix_pick(hi - lo, need, hist, found, high, [](int) { return true; }, &above);
-        T2 = radix_pick(hi - lo, need - above, hist, found, low, [&](int i) { return high(i) == T; }, &above2);
-        ties = need - above - above2;
+        uint32_t kmin = 0xffffffffu, kmax = 0, mag = 0;
+#pragma unroll 2
+        for (int i = threadIdx.x; i < n4; i += kPickThreads) {
+            const uint4 k = scored4(i);
+            if (kept) reinterpret_cast<uint4*>(keys_kept)[i] = k;
+            // (k - 1: no key becomes the largest)
+            kmin = min(min(min(kmin, k.x - 1), k.y - 1), min(k.z - 1, k.w - 1));
+            kmax = max(max(max(kmax, k.x), k.y), max(k.z, k.w));
+        }
+        for (int i = threadIdx.x; i < (n + 7) / 8; i += kPickThreads)
+            mag = max(mag, __float_as_uint(__ldcg(p.mags + row * (p.stride / 8) + i)));
+        kmin = __reduce_min_sync(0xffffffffu, kmin) + 1;
+        kmax = __reduce_max_sync(0xffffffffu, kmax);
+        mag = __reduce_max_sync(0xffffffffu, mag);
+        if (lane == 0) range_w[warp] = make_uint4(kmin - 1, kmax, mag, 0u);
+        __syncthreads();
+        kmin = 0xffffffffu;
+#pragma unroll
+        for (int w = 0; w < kPickWarps; ++w) {
+            const uint4 r = range_w[w];
+            kmin = min(kmin, r.x);
+            kmax = max(kmax, r.y);
+            mag = max(mag, r.z);
+        }
+        kmin += 1;
+        int above;
+        const uint32_t last = radix_pick(n4, need, kmax, 32 - __clz(kmin ^ kmax), hist, found, key4, &above);
+        // 2 eps, and the range around the last page that FP32 cannot tell apart
+        const float t = unordered(last), e2 = fmaf(__uint_as_float(mag), 40.f * 5.9604645e-8f, 1e-42f);
+        const float tu = t + e2, tl = t - e2;
+        top = tu == tu ? ordered(tu) : 0xffffffffu;
+        low = tl == tl ? ordered(tl) : 1u;
+        int over = 0, between = 0;
+#pragma unroll 2
+        for (int i = threadIdx.x; i < n4; i += kPickThreads) {
+            const uint4 k = key4(i);
+            over += (k.x > top) + (k.y > top) + (k.z > top) + (k.w > top);
+            between += (k.x >= low) + (k.y >= low) + (k.z >= low) + (k.w >= low);
+        }
+        int2 before, all;
+        warp_sums(__reduce_add_sync(0xffffffffu, over), __reduce_add_sync(0xffffffffu, between), sums, &before, &all);
+        const int n_over = all.x, n_between = all.y - all.x;
+        if (need - n_over < n_between) {
+            // Score the pages between again, a warp a page.
+            float2 c[PB::E];
+#pragma unroll
+            for (int j = 0; j < PB::E; ++j) {
+                c[j] = p.coef[row * 2 * D + lane * PB::E + j];
+                if constexpr (!PB::kF32) {
+                    const float cut = __uint_as_float(__float_as_uint(c[j].x) & 0xffffff00u);
+                    c[j] = make_float2(cut, __fadd_rn(__fsub_rn(c[j].x, cut), c[j].y));
+                }
+            }
+            const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.max_pages;
+            const TB* bounds = static_cast<const TB*>(p.bounds) + static_cast<int64_t>(g) * 2 * D + lane * PB::E;
+            auto again = [&](int i) -> float2 {
+                const int phys = __ldg(table + i);
+                float s = 0.f, e = 0.f;
+                if (phys >= 0 && phys < p.num_pages) {
+                    PB x;
+                    x.load(bounds + static_cast<int64_t>(phys) * p.Hkv * 2 * D);
+#pragma unroll
+                    for (int j = 0; j < PB::E; ++j) {
+                        const float pr = __fmul_rn(c[j].x, x[j]);
+                        if constexpr (PB::kF32) e = __fadd_rn(e, __fmaf_rn(c[j].x, x[j], -pr));
+                        float err;
+                        two_sum(s, pr, &s, &err);
+                        e = __fadd_rn(__fmaf_rn(c[j].y, x[j], e), err);
+                    }
+                } else {
+                    s = INFINITY;
+                }
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) {
+                    const float rs = __shfl_xor_sync(0xffffffffu, s, off), re = __shfl_xor_sync(0xffffffffu, e, off);
+                    float err;
+                    two_sum(s, rs, &s, &err);
+                    e = __fadd_rn(__fadd_rn(e, re), err);
+                }
+                // normalised, so that comparing (high, low) compares the sums; + 0 makes -0 one zero
+                const float h = __fadd_rn(s, e);
+                if (!(fabsf(h) < INFINITY)) return make_float2(INFINITY, 0.f);
+                return make_float2(__fadd_rn(h, 0.f), __fadd_rn(__fadd_rn(__fsub_rn(s, h), e), 0.f));
+            };
+            const int places = need - n_over;
+            if (kept && n_between <= 32) {
+                // the usual few: listed, scored a warp each and ranked by one warp; a taken page's
+                // key becomes the largest, another's 0
+                __shared__ int few[32], few_n;
+                __shared__ float2 few_s[32];
+                if (threadIdx.x == 0) few_n = 0;
+                __syncthreads();
+                for (int i = threadIdx.x; i < n; i += kPickThreads) {
+                    const uint32_t k = keys_kept[i];
+                    if (k <= top && k >= low) few[atomicAdd(&few_n, 1)] = i;
+                }
+                __syncthreads();
+                for (int j = warp; j < n_between; j += kPickWarps) {
+                    const float2 s = again(few[j]);
+                    if (lane == 0) few_s[j] = s;
+                }
+                __syncthreads();
+                if (warp == 0 && lane < n_between) {
+                    const int i = few[lane];
+                    const uint32_t h = ordered(few_s[lane].x), l = ordered(few_s[lane].y);
+                    int better = 0;
+                    for (int j = 0; j < n_between; ++j) {
+                        const uint32_t h2 = ordered(few_s[j].x), l2 = ordered(few_s[j].y);
+                        better += h2 > h || (h2 == h && (l2 > l || (l2 == l && few[j] < i)));
+                    }
+                    keys_kept[i] = better < places ? 0xffffffffu : 0u;  // above `top`, below `low`
+                }
+                __syncthreads();
+                low = max(low, 1u);
+            } else {
+                for (int i0 = warp * 32; i0 < n; i0 += kPickThreads) {
+                    const uint32_t k = i0 + lane < n ? key(i0 + lane) : 0u;
+                    unsigned todo = __ballot_sync(0xffffffffu, k != 0 && k <= top && k >= low);
+                    while (todo) {
+                        const int i = i0 + __ffs(todo) - 1;
+                        todo &= todo - 1;
+                        const float2 s = again(i);
+                        if (lane == 0) exact[i] = s;
+                    }
+                }
+                __syncthreads();  // (the block's own writes to global memory are visible to it)
+                auto four = [&](int i, auto&& part) {
+                    const uint4 k = key4(i);
+                    uint4 r;
+                    r.x = k.x != 0 && k.x <= top && k.x >= low ? part(4 * i) : 0u;
+                    r.y = k.y != 0 && k.y <= top && k.y >= low ? part(4 * i + 1) : 0u;
+                    r.z = k.z != 0 && k.z <= top && k.z >= low ? part(4 * i + 2) : 0u;
+                    r.w = k.w != 0 && k.w <= top && k.w >= low ? part(4 * i + 3) : 0u;
+                    return r;
+                };
+                int above1, above2;
+                T = radix_pick(n4, places, 0u, 32, hist, found,
+                               [&](int i) { return four(i, [&](int j) { return ordered(exact[j].x); }); }, &above1);
+                T2 = radix_pick(n4, places - above1, 0u, 32, hist, found,
+                                [&](int i) {
+                                    return four(i, [&](int j) { return ordered(exact[j].x) == T ? ordered(exact[j].y) : 0u; });
+                                },
+                                &above2);
+                ties = places - above1 - above2;
+            }
+        }
     }
-    // every thread takes a run of consecutive pages: count, scan, write in order
-    const int per = (n + kPickThreads - 1) / kPickThreads;
-    const int i0 = min(n, static_cast<int>(threadIdx.x) * per), i1 = min(n, i0 + per);
-    int taken = 0, equal = 0;
+    // every warp takes a run of consecutive pages, 32 at a time: count, sum, write in order
+    __syncthreads();
+    const int per = (n + kPickThreads - 1) / kPickThreads * 32;
+    const int i0 = min(n, warp * per), i1 = min(n, i0 + per);
+    const unsigned lower = (1u << lane) - 1u;
+    int2 before, all;
+    if (T == 0 && T2 == 0) {  // one threshold tells them all apart
+        auto takes = [&](int i) {
+            return i < n && (i < lo || i >= hi || (need > 0 && key(i) >= low));
+        };
+        int taken = 0;
+#pragma unroll 4
+        for (int i = i0; i < i1; i += 32) taken += __popc(__ballot_sync(0xffffffffu, takes(i + lane)));
+        warp_sums(taken, 0, sums, &before, &all);
+        int at = before.x;
+#pragma unroll 4
+        for (int i = i0; i < i1; i += 32) {
+            const bool take = takes(i + lane);
+            const unsigned t = __ballot_sync(0xffffffffu, take);
+            if (take) sel[at + __popc(t & lower)] = i + lane;
+            at += __popc(t);
+        }
+        return;
+    }
     auto kind = [&](int i) -> int {  // 2: taken, 1: a tie, 0: not taken
-        if (i < lo || i >= hi) return 2;
-        if (need == 0) return 0;
-        const float2 s = sc[i];
+        if (i < lo || i >= hi) return i < n ? 2 : 0;
+        const uint32_t k = key(i);
+        if (k > top) return 2;
+        if (k < low) return 0;
+        const float2 s = exact[i];
         const uint32_t h = ordered(s.x);
         if (h != T) return h > T ? 2 : 0;
         const uint32_t l = ordered(s.y);
         return l > T2 ? 2 : (l == T2 ? 1 : 0);
     };
-    for (int i = i0; i < i1; ++i) {
-        const int k = kind(i);
-        taken += k == 2;
-        equal += k == 1;
+    int taken = 0, equal = 0;
+    for (int i = i0; i < i1; i += 32) {
+        const int k = kind(i + lane);
+        taken += __popc(__ballot_sync(0xffffffffu, k == 2));
+        equal += __popc(__ballot_sync(0xffffffffu, k == 1));
     }
-    int total;
-    const int eq0 = block_scan(equal, sums, &total);
-    const int eq_take = max(0, min(equal, ties - eq0));
-    int at = block_scan(taken + eq_take, sums, &total);
-    int eq = 0;
-    for (int i = i0; i < i1; ++i) {
-        const int k = kind(i);
-        if (k == 2 || (k == 1 && eq++ < eq_take)) sel[at++] = i;
+    warp_sums(taken, equal, sums, &before, &all);
+    int eq = before.y, at = before.x + min(before.y, ties);  // ties and places before this warp
+    for (int i = i0; i < i1; i += 32) {
+        const int k = kind(i + lane);
+        const unsigned eqs = __ballot_sync(0xffffffffu, k == 1);
+        const bool take = k == 2 || (k == 1 && eq + __popc(eqs & lower) < ties);
+        const unsigned t = __ballot_sync(0xffffffffu, take);
+        if (take) sel[at + __popc(t & lower)] = i + lane;
+        at += __popc(t);
+        eq += __popc(eqs);
     }
 }
 
@@ -536,20 +752,44 @@ int pages_of(const ta_shape* s, int page_shift) {
     return static_cast<int>((static_cast<int64_t>(s->max_seqlen) + (int64_t(1) << page_shift) - 1) >> page_shift);
 }
 
+// Workspace: scores [rows][stride], magnitudes [rows][stride / 8], exact sums
+// [rows][pages] and coefficients [rows][2 d], rows = B * Hkv.
+int score_stride(int pages) { return (pages + 31) / 32 * 32; }
+
 size_t select_bytes(const ta_shape* s, int page_shift) {
-    return static_cast<size_t>(s->batch) * s->num_kv_heads * pages_of(s, page_shift) * sizeof(float2);
+    const size_t rows = static_cast<size_t>(s->batch) * s->num_kv_heads, pages = pages_of(s, page_shift);
+    const size_t stride = (pages + 31) / 32 * 32;
+    return rows * (stride * sizeof(float) + stride / 8 * sizeof(float) + (pages + 2 * s->head_dim) * sizeof(float2));
 }
 
 template <typename Kernel, typename Params>
-cudaError_t launch(Kernel kernel, dim3 grid, int threads, const Params& p, cudaStream_t s) {
+cudaError_t launch(Kernel kernel, dim3 grid, int threads, int smem, const Params& p, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr = programmatic_launch();
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int D, typename TQ, typename TB>
+int launch_select(SelectParams p, const DeviceInfo& dev, cudaStream_t s) {
+    static std::atomic<unsigned long long> configured{0};
+    if (set_smem_once(page_pick_kernel<D, TQ, TB>, kPickKeep * 4, configured) != cudaSuccess) return TA_ERR_CUDA;
+    if (p.pages > p.num_select) {  // else every page is listed
+        // a block's 8 warps take 8 pages each at a time; one wave of four blocks an SM
+        const int64_t all = static_cast<int64_t>(p.B) * p.Hkv * p.pages, wave = 4 * static_cast<int64_t>(dev.num_sms);
+        const int step = kScoreWarps * 8;
+        const int per = static_cast<int>(std::max<int64_t>(1, (all + wave * step - 1) / (wave * step))) * step;
+        p.per_block = per;
+        const dim3 grid((p.pages + per - 1) / per, p.Hkv, p.B);
+        if (launch(page_score_kernel<D, TQ, TB>, grid, kScoreThreads, 0, p, s) != cudaSuccess) return TA_ERR_CUDA;
+    }
+    const int smem = p.pages > p.num_select ? std::min(p.stride, kPickKeep) * 4 : 0;
+    return launch(page_pick_kernel<D, TQ, TB>, dim3(p.Hkv, p.B, 1), kPickThreads, smem, p, s) == cudaSuccess ? TA_OK : TA_ERR_CUDA;
 }
 
 }  // namespace
@@ -596,14 +836,14 @@ extern "C" int tree_attn_page_bounds(const ta_shape* shape, const ta_paged_kv* p
     const bool d128 = shape->head_dim == 128;
     cudaError_t e;
     if (shape->kv_dtype == TA_BF16)
-        e = d128 ? launch(page_bounds_kernel<128, __nv_bfloat16>, grid, kBoundsThreads, p, s)
-                 : launch(page_bounds_kernel<64, __nv_bfloat16>, grid, kBoundsThreads, p, s);
+        e = d128 ? launch(page_bounds_kernel<128, __nv_bfloat16>, grid, kBoundsThreads, 0, p, s)
+                 : launch(page_bounds_kernel<64, __nv_bfloat16>, grid, kBoundsThreads, 0, p, s);
     else if (shape->kv_dtype == TA_E4M3)
-        e = d128 ? launch(page_bounds_kernel<128, E4m3>, grid, kBoundsThreads, p, s)
-                 : launch(page_bounds_kernel<64, E4m3>, grid, kBoundsThreads, p, s);
+        e = d128 ? launch(page_bounds_kernel<128, E4m3>, grid, kBoundsThreads, 0, p, s)
+                 : launch(page_bounds_kernel<64, E4m3>, grid, kBoundsThreads, 0, p, s);
     else
-        e = d128 ? launch(page_bounds_kernel<128, float>, grid, kBoundsThreads, p, s)
-                 : launch(page_bounds_kernel<64, float>, grid, kBoundsThreads, p, s);
+        e = d128 ? launch(page_bounds_kernel<128, float>, grid, kBoundsThreads, 0, p, s)
+                 : launch(page_bounds_kernel<64, float>, grid, kBoundsThreads, 0, p, s);
     return e == cudaSuccess ? TA_OK : TA_ERR_CUDA;
 }
 
@@ -643,7 +883,6 @@ extern "C" int tree_attn_select_pages(const ta_shape* shape, const ta_paged_kv* 
     p.seqlens = seqlens;
     p.block_table = paged->block_table;
     p.selected = selected;
-    p.scores = static_cast<float2*>(workspace);
     p.err = dev.err;
     p.B = shape->batch;
     p.Hq = shape->num_q_heads;
@@ -651,39 +890,26 @@ extern "C" int tree_attn_select_pages(const ta_shape* shape, const ta_paged_kv* 
     p.G = p.Hq / p.Hkv;
     p.S = shape->max_seqlen;
     p.pages = pages_of(shape, lay.page_shift);
+    p.stride = score_stride(p.pages);
+    const size_t rows = static_cast<size_t>(p.B) * p.Hkv;
+    p.scores = static_cast<float*>(workspace);
+    p.mags = p.scores + rows * p.stride;
+    p.exact = reinterpret_cast<float2*>(p.mags + rows * (p.stride / 8));
+    p.coef = p.exact + rows * p.pages;
     p.num_select = num_select;
     p.first = first_pages;
     p.last = last_pages;
     p.max_pages = paged->max_pages_per_seq;
     p.page_shift = lay.page_shift;
     p.num_pages = paged->num_pages;
+    const bool d128 = shape->head_dim == 128, qb = shape->q_dtype == TA_BF16;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaSuccess;
-    if (p.pages > num_select) {  // else every page is listed
-        // blocks of 8 warps x 8 pages, more pages a block once that fills the device
-        const int64_t rows = static_cast<int64_t>(p.B) * p.Hkv;
-        int per = kScoreWarps * 8;
-        while (per < 1024 && rows * ((p.pages + 2 * per - 1) / (2 * per)) >= 4 * static_cast<int64_t>(dev.num_sms)) per *= 2;
-        p.per_block = per;
-        const dim3 grid((p.pages + per - 1) / per, p.Hkv, p.B);
-        const bool d128 = shape->head_dim == 128, qb = shape->q_dtype == TA_BF16;
-        if (f32) {
-            if (qb)
-                e = d128 ? launch(page_score_kernel<128, __nv_bfloat16, float>, grid, kScoreThreads, p, s)
-                         : launch(page_score_kernel<64, __nv_bfloat16, float>, grid, kScoreThreads, p, s);
-            else
-                e = d128 ? launch(page_score_kernel<128, float, float>, grid, kScoreThreads, p, s)
-                         : launch(page_score_kernel<64, float, float>, grid, kScoreThreads, p, s);
-        } else {
-            if (qb)
-                e = d128 ? launch(page_score_kernel<128, __nv_bfloat16, __nv_bfloat16>, grid, kScoreThreads, p, s)
-                         : launch(page_score_kernel<64, __nv_bfloat16, __nv_bfloat16>, grid, kScoreThreads, p, s);
-            else
-                e = d128 ? launch(page_score_kernel<128, float, __nv_bfloat16>, grid, kScoreThreads, p, s)
-                         : launch(page_score_kernel<64, float, __nv_bfloat16>, grid, kScoreThreads, p, s);
-        }
-        if (e != cudaSuccess) return TA_ERR_CUDA;
+    if (f32) {
+        if (qb) return d128 ? launch_select<128, __nv_bfloat16, float>(p, dev, s) : launch_select<64, __nv_bfloat16, float>(p, dev, s);
+        return d128 ? launch_select<128, float, float>(p, dev, s) : launch_select<64, float, float>(p, dev, s);
     }
-    e = launch(page_pick_kernel, dim3(p.Hkv, p.B, 1), kPickThreads, p, s);
-    return e == cudaSuccess ? TA_OK : TA_ERR_CUDA;
+    if (qb)
+        return d128 ? launch_select<128, __nv_bfloat16, __nv_bfloat16>(p, dev, s)
+                    : launch_select<64, __nv_bfloat16, __nv_bfloat16>(p, dev, s);
+    return d128 ? launch_select<128, float, __nv_bfloat16>(p, dev, s) : launch_select<64, float, __nv_bfloat16>(p, dev, s);
 }
