@@ -101,7 +101,7 @@ struct SlabList {
         lane = threadIdx.x & 31;
         sel = p.selected + (static_cast<int64_t>(b) * p.Hkv + g) * p.num_select;
         table = p.block_table + static_cast<int64_t>(b) * p.max_pages;
-        U = N > 0 ? p.num_select << (p.page_shift - 4) : 0;  // at most 2^16 * 2^6
+        U = p.num_select << (p.page_shift - 4);  // at most 2^16 * 2^6
     }
     __device__ __forceinline__ int count() const { return U > gw ? (U - gw + W - 1) / W : 0; }
     // list entry of this lane's slab in the window starting at the warp's slab i0 (-1: none)
@@ -133,19 +133,40 @@ struct SlabList {
     }
 };
 
+// Mailbox of a block: what the cluster's blocks have sent it of their merged
+// states.  Not part of the rings: a block may still be streaming when another
+// sends.
+template <int D, int kCols>
+struct Mailbox {
+    float o[kCols * D + kMaxCluster];     // [sender][share], share = ceil(columns * D / blocks)
+    float2 ml[kMaxCluster][kCols];        // [sender]: maximum (log2 units), denominator
+};
+
+__device__ __forceinline__ void st_dsmem(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 // The warps' states, [warp][column][D + 4] numerators and [warp][column]
 // maxima (log2 units) and denominators in shared memory, become the outputs of
 // the list's columns [0, ncol): merged over the block's warps, then over the
-// cluster's blocks.  kFp8: numerators of channel c sit at (c % 16) * 8 + c / 16
-// and still lack V's scale.
-template <int D, bool kFp8>
-__device__ void finish_list(const SelParams& p, int b, int hq0, int ncol, int kCols, float vscale, const float* mg_o,
-                            const float* mg_m, const float* mg_l, float* cs_o, float* cs_m, float* cs_l, bool poison) {
+// cluster's blocks.  Every block merges a share of the outputs; the others
+// send it theirs (stores into its mailbox), so one barrier suffices and nobody
+// reads a peer's memory.  The caller has arrived once at the cluster's barrier
+// when it started.  kFp8: numerators of channel c sit at (c % 16) * 8 + c / 16 and
+// still lack V's scale.
+template <int D, int kCols, bool kFp8>
+__device__ void finish_list(const SelParams& p, int b, int hq0, int ncol, float vscale, const float* mg_o,
+                            const float* mg_m, const float* mg_l, Mailbox<D, kCols>* box, bool poison) {
     constexpr int MS = D + 4;
     const int tid = threadIdx.x;
     const float nan = __int_as_float(0x7fc00000);
     const size_t row0 = static_cast<size_t>(b) * p.Hq + hq0;
-    for (int idx = tid; idx < ncol * D; idx += kSelThreads) {
+    const int C = p.C, items = ncol * D, share = (items + C - 1) / C;
+    const int rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
+    if (C > 1) cluster_wait();  // every block of the cluster has started
+    for (int idx = tid; idx < items; idx += kSelThreads) {
         const int h = idx / D, dd = idx - h * D;
         const int pos = kFp8 ? (dd % 16) * 8 + dd / 16 : dd;
         float mw[kWarps], M = -INFINITY;
@@ -163,48 +184,41 @@ __device__ void finish_list(const SelParams& p, int b, int hq0, int ncol, int kC
             lw[w] = wt * mg_l[w * kCols + h];
         }
         float o = tree_sum<kWarps>(ow);
-        const float l = tree_sum<kWarps>(lw);
+        float l = tree_sum<kWarps>(lw);
         if (kFp8) o *= vscale;
-        if (p.C > 1) {
-            cs_o[idx] = poison ? nan : o;
-            if (dd == 0) {
-                cs_m[h] = poison ? nan : M;
-                cs_l[h] = poison ? nan : l;
+        if (poison) o = l = M = nan;
+        if (C > 1) {
+            const int to = idx / share;
+            st_dsmem(dsmem_addr(&box->o[rank * share + idx - to * share], to), o);
+            if (dd < C) {  // the column's maximum and denominator, to block dd
+                const uint32_t at = dsmem_addr(&box->ml[rank][h], dd);
+                st_dsmem(at, M);
+                st_dsmem(at + 4, l);
             }
         } else {
-            p.out[(row0 + h) * D + dd] = poison ? nan : (l == 0.f ? 0.f : o / l);
-            if (dd == 0 && p.lse) p.lse[row0 + h] = poison ? nan : (l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2);
+            p.out[(row0 + h) * D + dd] = l == 0.f ? 0.f : o / l;
+            if (dd == 0 && p.lse) p.lse[row0 + h] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
         }
     }
-    if (p.C == 1) return;
-    cluster_sync_all();
-    const int rank = static_cast<int>(cluster_rank());
-    const int items = ncol * D, per = (items + p.C - 1) / p.C;
-    const int i1 = min(items, (rank + 1) * per);
-    for (int idx = rank * per + tid; idx < i1; idx += kSelThreads) {
-        const int h = idx / D, dd = idx - h * D;
-        float mq[kMaxCluster], lq[kMaxCluster], oq[kMaxCluster], M = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c) {
-            const bool on = c < p.C;
-            mq[c] = on ? ld_dsmem(dsmem_addr(cs_m + h, c)) : -INFINITY;
-            lq[c] = on ? ld_dsmem(dsmem_addr(cs_l + h, c)) : 0.f;
-            oq[c] = on ? ld_dsmem(dsmem_addr(cs_o + idx, c)) : 0.f;
-        }
-#pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c) M = fmaxf(M, mq[c]);
+    if (C == 1) return;
+    cluster_arrive();
+    cluster_wait();
+    const int n = min(share, items - rank * share);
+    for (int i = tid; i < n; i += kSelThreads) {
+        const int idx = rank * share + i, h = idx / D, dd = idx - h * D;
+        float M = -INFINITY;
+        for (int c = 0; c < C; ++c) M = fmaxf(M, box->ml[c][h].x);
         const float Ms = (M == -INFINITY) ? 0.f : M;
         float L = 0.f, O = 0.f;
-#pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c) {
-            const float w = (mq[c] == -INFINITY) ? 0.f : ex2(mq[c] - Ms);
-            L = fmaf(w, lq[c], L);
-            O = fmaf(w, oq[c], O);
+        for (int c = 0; c < C; ++c) {
+            const float2 ml = box->ml[c][h];
+            const float w = (ml.x == -INFINITY) ? 0.f : ex2(ml.x - Ms);
+            L = fmaf(w, ml.y, L);
+            O = fmaf(w, box->o[c * share + i], O);
         }
         p.out[(row0 + h) * D + dd] = (L == 0.f) ? 0.f : O / L;  // NaN of a poisoned block propagates
         if (dd == 0 && p.lse) p.lse[row0 + h] = (L == 0.f) ? -INFINITY : (M + log2f(L)) * kLn2;
     }
-    cluster_sync_all();  // no block's state goes away while a peer reads it
 }
 
 // ------------------------------------------------------------ tensor cores
@@ -213,23 +227,31 @@ struct SelCfg {
     static constexpr int kRowBytes = kFp8 ? D : 2 * D;
     static constexpr int kChunks = kRowBytes / 16;            // 16-byte chunks per row
     static constexpr int kSlabBytes = kSlab * kRowBytes;
-    static constexpr int kStageBytes = 2 * kSlabBytes;        // keys, values
-    static constexpr int kStages = 24576 / kStageBytes;       // 24 KB a warp
+    // Slabs a warp takes together.  E4M3 slabs are half the bytes for the same chain of
+    // products, maxima and exponentials, so two share one: one at a time ran at half
+    // the BF16 kernel's bandwidth where warps are few (8 lists of 131072 tokens: 82 us
+    // for half the bytes of BF16's 83 us).
+    static constexpr int kSub = kFp8 ? 2 : 1;
+    static constexpr int kPairBytes = 2 * kSlabBytes;         // keys, values
+    static constexpr int kStageBytes = kSub * kPairBytes;
+    static constexpr int kStages = 24576 / kStageBytes;       // 24 KB a warp, one block an SM
     static constexpr int kCols = 16;
     static constexpr int kRing = kWarps * kStages * kStageBytes;
-    static constexpr int kMeta = kWarps * kStages * 4 + 16;
-    static constexpr int kSmem = kRing + kMeta;
+    static constexpr int kBoxOff = kRing + kWarps * kStages * kSub * 4 + 16;
+    static_assert(kBoxOff % 16 == 0, "mailbox alignment");
+    static constexpr int kSmem = kBoxOff + static_cast<int>(sizeof(Mailbox<D, kCols>));
     // merge buffers reuse the ring
-    static_assert((kWarps * kCols * (D + 4 + 2) + kCols * (D + 2)) * 4 <= kRing, "merge buffers");
+    static_assert(kWarps * kCols * (D + 4 + 2) * 4 <= kRing, "merge buffers");
     static_assert(kStages >= 3 && kSmem <= 227 * 1024, "ring");
 };
 
 template <int D, int NT, bool kFp8>
 __global__ void __launch_bounds__(kSelThreads, 1) decode_selected_kernel(const SelParams p) {
     using Cf = SelCfg<D, kFp8>;
+    constexpr int J = Cf::kSub;
     extern __shared__ __align__(128) uint8_t smem[];
     int* nvs_all = reinterpret_cast<int*>(smem + Cf::kRing);
-    int* bad_flag = nvs_all + kWarps * Cf::kStages;
+    int* bad_flag = nvs_all + kWarps * Cf::kStages * J;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gid = lane >> 2, tig = lane & 3, r8 = lane & 7;
@@ -237,6 +259,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) decode_selected_kernel(const S
     const int ncol = min(16, p.G - 16 * cg);
     const int hq0 = g * p.G + 16 * cg;
     if (threadIdx.x == 0) *bad_flag = 0;
+    if (p.C > 1) cluster_arrive();  // (waited for before the states are sent)
     __syncthreads();
     wait_primary();
     allow_dependents();
@@ -245,58 +268,24 @@ __global__ void __launch_bounds__(kSelThreads, 1) decode_selected_kernel(const S
     const bool bad_len = N < 0 || N > p.S;
     if (bad_len) N = 0;
     SlabList list(p, b, g, N, blockIdx.x * kWarps + warp, p.C * kWarps);
-    const int n_it = list.count();
+    const int n_slab = list.count(), n_it = (n_slab + J - 1) / J;
     int e_next = list.entry(0);
 
     // q fragments (B operand of S^T = K Q^T): column n of n-tile t is query head
-    // hq0 + 8 t + n.  BF16 caches: as it is.  E4M3: FP16, times the power of two
-    // that brings the largest |q| of the group into [2^14, 2^15), in the channel
-    // order of the key bytes (k-step kk of lane tig: channels 32 tig + 4 kk ..).
+    // hq0 + 8 t + n, in the channel order of the key bytes for E4M3 caches (k-step kk
+    // of lane tig: channels 32 tig + 4 kk ..).
     uint32_t qb[NT][D / 16][2];
-    float sl2 = p.scale_log2, vscale = 1.f;
-    {
-        const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(p.q) + (static_cast<size_t>(b) * p.Hq + hq0) * D;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int c = nt * 8 + gid;
-            const bool on = c < ncol;
-            const __nv_bfloat16* qh = q0 + (on ? c : 0) * D;
+    for (int nt = 0; nt < NT; ++nt) {
+        const int c = nt * 8 + gid;
+        const bool on = c < ncol;
+        const __nv_bfloat16* qh =
+            static_cast<const __nv_bfloat16*>(p.q) + (static_cast<size_t>(b) * p.Hq + hq0 + (on ? c : 0)) * D;
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t* w = reinterpret_cast<const uint32_t*>(qh + (kFp8 ? 32 * tig + 4 * kk : 16 * kk + 2 * tig));
-                qb[nt][kk][0] = on ? w[0] : 0u;
-                qb[nt][kk][1] = on ? w[kFp8 ? 1 : 4] : 0u;
-            }
-        }
-        if constexpr (kFp8) {
-            auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
-            auto hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
-            float amax = 0.f;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        amax = fmaxf(amax, fmaxf(fabsf(lo(qb[nt][kk][i])), fabsf(hi(qb[nt][kk][i]))));
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-            int qexp = 0;
-            if (amax > 0.f && amax < INFINITY) {
-                int e;
-                frexpf(amax, &e);
-                qexp = max(-100, min(100, 15 - e));
-            }
-            const float qs = ldexpf(1.f, qexp);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        qb[nt][kk][i] = half2_bits(__floats2half2_rn(lo(qb[nt][kk][i]) * qs, hi(qb[nt][kk][i]) * qs));
-            sl2 *= __ldg(p.k_scale + g) / qs;
-            vscale = __ldg(p.v_scale + g) / kPScale;
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(qh + (kFp8 ? 32 * tig + 4 * kk : 16 * kk + 2 * tig));
+            qb[nt][kk][0] = on ? w[0] : 0u;
+            qb[nt][kk][1] = on ? w[kFp8 ? 1 : 4] : 0u;
         }
     }
 
@@ -311,25 +300,30 @@ __global__ void __launch_bounds__(kSelThreads, 1) decode_selected_kernel(const S
     }
 
     const uint32_t ring = smem_u32(smem) + warp * Cf::kStages * Cf::kStageBytes;
-    volatile int* nvs = nvs_all + warp * Cf::kStages;
+    volatile int* nvs = nvs_all + warp * Cf::kStages * J;
     SlabWindow win = list.place(0, e_next), win_next = win;
     const uint8_t* kbytes = static_cast<const uint8_t*>(p.k);
     const uint8_t* vbytes = static_cast<const uint8_t*>(p.v);
     const int es = kFp8 ? 1 : 2;
 
-    // Start the copies of the warp's slab i into stage i % kStages (one group).
+    // Start the copies of the warp's slabs i J .. into stage i % kStages (one group).
     auto issue = [&](int i) {
-        if (i < n_it) {
-            const int j = i & 31;
-            if (j == 0 && i > 0) win = win_next;
-            if (j == 0) e_next = list.entry(i + 32);
-            if (j == 16) win_next = list.place(i - 16 + 32, e_next);
+#pragma unroll
+        for (int sub = 0; sub < J; ++sub) {
+            const int s = i * J + sub, slot = (i % Cf::kStages) * J + sub;
+            if (s >= n_slab) {
+                if (lane == 0) nvs[slot] = 0;
+                continue;
+            }
+            const int j = s & 31;
+            if (j == 0 && s > 0) win = win_next;
+            if (j == 0) e_next = list.entry(s + 32);
+            if (j == 16) win_next = list.place(s + 16, e_next);
             const int nv = __shfl_sync(0xffffffffu, win.nv, j);
             const int64_t off = __shfl_sync(0xffffffffu, win.off, j) * es;
-            const int s = i % Cf::kStages;
-            if (lane == 0) nvs[s] = nv;
+            if (lane == 0) nvs[slot] = nv;
             if (nv > 0) {
-                const uint32_t dst = ring + s * Cf::kStageBytes;
+                const uint32_t dst = ring + slot * Cf::kPairBytes;
 #pragma unroll
                 for (int x = 0; x < kSlab * Cf::kChunks / 32; ++x) {
                     const int idx = x * 32 + lane, r = idx / Cf::kChunks, c = idx % Cf::kChunks;
@@ -352,56 +346,109 @@ __global__ void __launch_bounds__(kSelThreads, 1) decode_selected_kernel(const S
 
 #pragma unroll
     for (int i = 0; i < Cf::kStages - 1; ++i) issue(i);
+
+    // E4M3 caches: q as FP16, times the power of two that brings the largest |q| of
+    // the group into [2^14, 2^15) (exact; folded back into the logit scale), while
+    // the first keys are on their way.
+    float sl2 = p.scale_log2, vscale = 1.f;
+    if constexpr (kFp8) {
+        auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
+        auto hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
+        float amax = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    amax = fmaxf(amax, fmaxf(fabsf(lo(qb[nt][kk][i])), fabsf(hi(qb[nt][kk][i]))));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+        int qexp = 0;
+        if (amax > 0.f && amax < INFINITY) {
+            int e;
+            frexpf(amax, &e);
+            qexp = max(-100, min(100, 15 - e));
+        }
+        const float qs = ldexpf(1.f, qexp);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    qb[nt][kk][i] = half2_bits(__floats2half2_rn(lo(qb[nt][kk][i]) * qs, hi(qb[nt][kk][i]) * qs));
+        sl2 *= __ldg(p.k_scale + g) / qs;
+        vscale = __ldg(p.v_scale + g) / kPScale;
+    }
+
     for (int it = 0; it < n_it; ++it) {
         cp_async_wait<Cf::kStages - 2>();
         __syncwarp();  // the slab is in shared memory for every lane; every lane is done with the one before
         issue(it + Cf::kStages - 1);
-        const int s = it % Cf::kStages;
-        const int nv = nvs[s];
-        if (nv <= 0) continue;
-        const uint32_t kbase = ring + s * Cf::kStageBytes, vbase = kbase + Cf::kSlabBytes;
+        int nv[J];
+        uint32_t kbase[J];
+        bool any = false;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int slot = (it % Cf::kStages) * J + j;
+            nv[j] = nvs[slot];
+            kbase[j] = ring + slot * Cf::kPairBytes;
+            any |= nv[j] > 0;
+        }
+        if (!any) continue;  // (a slab without tokens beside one with some: masked below)
 
-        // S^T[16 tokens x columns] = K Q^T, two accumulators per n-tile
-        float sacc[2][NT][4];
+        // S^T[16 tokens x columns] = K Q^T per slab, two accumulators per n-tile
+        float sacc[J][2][NT][4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int j = 0; j < J; ++j) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sacc[u][nt][e] = 0.f;
-        if constexpr (kFp8) {
-            const uint32_t ra = kbase + gid * 128, rb = ra + 8 * 128;
-            const int c0 = ((2 * tig) ^ gid) << 4, c1 = ((2 * tig + 1) ^ gid) << 4;
-            const uint4 ka0 = lds128(ra + c0), ka1 = lds128(ra + c1), kb0 = lds128(rb + c0), kb1 = lds128(rb + c1);
-            const uint32_t wa[8] = {ka0.x, ka0.y, ka0.z, ka0.w, ka1.x, ka1.y, ka1.z, ka1.w};
-            const uint32_t wb[8] = {kb0.x, kb0.y, kb0.z, kb0.w, kb1.x, kb1.y, kb1.z, kb1.w};
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t a[4] = {e4m3x2_to_f16x2(wa[kk] & 0xffffu), e4m3x2_to_f16x2(wb[kk] & 0xffffu),
-                                       e4m3x2_to_f16x2(wa[kk] >> 16), e4m3x2_to_f16x2(wb[kk] >> 16)};
+                    for (int e = 0; e < 4; ++e) sacc[j][u][nt][e] = 0.f;
+            if constexpr (kFp8) {
+                const uint32_t ra = kbase[j] + gid * 128, rb = ra + 8 * 128;
+                const int c0 = ((2 * tig) ^ gid) << 4, c1 = ((2 * tig + 1) ^ gid) << 4;
+                const uint4 ka0 = lds128(ra + c0), ka1 = lds128(ra + c1), kb0 = lds128(rb + c0), kb1 = lds128(rb + c1);
+                const uint32_t wa[8] = {ka0.x, ka0.y, ka0.z, ka0.w, ka1.x, ka1.y, ka1.z, ka1.w};
+                const uint32_t wb[8] = {kb0.x, kb0.y, kb0.z, kb0.w, kb1.x, kb1.y, kb1.z, kb1.w};
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma_f16(sacc[kk & 1][nt], a, qb[nt][kk][0], qb[nt][kk][1]);
-            }
-        } else {
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t a[4] = {e4m3x2_to_f16x2(wa[kk] & 0xffffu), e4m3x2_to_f16x2(wb[kk] & 0xffffu),
+                                           e4m3x2_to_f16x2(wa[kk] >> 16), e4m3x2_to_f16x2(wb[kk] >> 16)};
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                uint32_t a[4];
-                ldsm_x4(a, kbase + k_lane + (((2 * kk + k_chi) ^ r8) << 4));
+                    for (int nt = 0; nt < NT; ++nt) mma_f16(sacc[j][kk & 1][nt], a, qb[nt][kk][0], qb[nt][kk][1]);
+                }
+            } else {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma_bf16(sacc[kk & 1][nt], a, qb[nt][kk][0], qb[nt][kk][1]);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    uint32_t a[4];
+                    ldsm_x4(a, kbase[j] + k_lane + (((2 * kk + k_chi) ^ r8) << 4));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_bf16(sacc[j][kk & 1][nt], a, qb[nt][kk][0], qb[nt][kk][1]);
+                }
             }
         }
-        // online softmax per column; P^T as B fragments in two parts
-        uint32_t bh[NT][2], bl[NT][2];
+        // Online softmax per column.  P^T as B fragments: the weights as the sum of three
+        // BF16 numbers (all 24 bits; two leave 2^-17, which showed: 2.4e-6 of the output's
+        // norm over 16384 tokens against 3.6e-7 in FP32), or two FP16 ones (22 bits).
+        uint32_t bh[J][NT][2], bl[J][NT][2], bt[J][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float s0 = (sacc[0][nt][0] + sacc[1][nt][0]) * sl2, s1 = (sacc[0][nt][1] + sacc[1][nt][1]) * sl2;
-            float s2 = (sacc[0][nt][2] + sacc[1][nt][2]) * sl2, s3 = (sacc[0][nt][3] + sacc[1][nt][3]) * sl2;
-            if (nv < kSlab) {
-                if (gid >= nv) s0 = s1 = -INFINITY;
-                if (gid + 8 >= nv) s2 = s3 = -INFINITY;
+            float sc[J][4], bm0 = -INFINITY, bm1 = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[j][e] = (sacc[j][0][nt][e] + sacc[j][1][nt][e]) * sl2;
+                if (nv[j] < kSlab) {
+                    if (gid >= nv[j]) sc[j][0] = sc[j][1] = -INFINITY;
+                    if (gid + 8 >= nv[j]) sc[j][2] = sc[j][3] = -INFINITY;
+                }
+                bm0 = fmaxf(bm0, fmaxf(sc[j][0], sc[j][2]));
+                bm1 = fmaxf(bm1, fmaxf(sc[j][1], sc[j][3]));
             }
-            float bm0 = fmaxf(s0, s2), bm1 = fmaxf(s1, s3);
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
                 bm0 = fmaxf(bm0, __shfl_xor_sync(0xffffffffu, bm0, off));
@@ -410,9 +457,37 @@ __global__ void __launch_bounds__(kSelThreads, 1) decode_selected_kernel(const S
             const float mn0 = fmaxf(m[nt][0], bm0), mn1 = fmaxf(m[nt][1], bm1);
             const float ms0 = (mn0 == -INFINITY) ? 0.f : mn0, ms1 = (mn1 == -INFINITY) ? 0.f : mn1;
             const float al0 = ex2(m[nt][0] - ms0), al1 = ex2(m[nt][1] - ms1);
-            const float p0 = ex2(s0 - ms0), p1 = ex2(s1 - ms1), p2 = ex2(s2 - ms0), p3 = ex2(s3 - ms1);
-            l[nt][0] = l[nt][0] * al0 + (p0 + p2);
-            l[nt][1] = l[nt][1] * al1 + (p1 + p3);
+            float ps0 = 0.f, ps1 = 0.f;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const float p0 = ex2(sc[j][0] - ms0), p1 = ex2(sc[j][1] - ms1);
+                const float p2 = ex2(sc[j][2] - ms0), p3 = ex2(sc[j][3] - ms1);
+                ps0 += p0 + p2;
+                ps1 += p1 + p3;
+                if constexpr (kFp8) {
+                    const float q0 = p0 * kPScale, q1 = p1 * kPScale, q2 = p2 * kPScale, q3 = p3 * kPScale;
+                    const __half2 h01 = __floats2half2_rn(q0, q1), h23 = __floats2half2_rn(q2, q3);
+                    const float2 f01 = __half22float2(h01), f23 = __half22float2(h23);
+                    bh[j][nt][0] = movtrans(half2_bits(h01));
+                    bh[j][nt][1] = movtrans(half2_bits(h23));
+                    bl[j][nt][0] = movtrans(half2_bits(__floats2half2_rn(q0 - f01.x, q1 - f01.y)));
+                    bl[j][nt][1] = movtrans(half2_bits(__floats2half2_rn(q2 - f23.x, q3 - f23.y)));
+                } else {
+                    const __nv_bfloat162 h01 = __floats2bfloat162_rn(p0, p1), h23 = __floats2bfloat162_rn(p2, p3);
+                    const float2 f01 = __bfloat1622float2(h01), f23 = __bfloat1622float2(h23);
+                    bh[j][nt][0] = movtrans(bf16x2_bits(h01));
+                    bh[j][nt][1] = movtrans(bf16x2_bits(h23));
+                    const float d0 = p0 - f01.x, d1 = p1 - f01.y, d2 = p2 - f23.x, d3 = p3 - f23.y;
+                    const __nv_bfloat162 l01 = __floats2bfloat162_rn(d0, d1), l23 = __floats2bfloat162_rn(d2, d3);
+                    const float2 g01 = __bfloat1622float2(l01), g23 = __bfloat1622float2(l23);
+                    bl[j][nt][0] = movtrans(bf16x2_bits(l01));
+                    bl[j][nt][1] = movtrans(bf16x2_bits(l23));
+                    bt[j][nt][0] = movtrans(bf16x2_bits(__floats2bfloat162_rn(d0 - g01.x, d1 - g01.y)));
+                    bt[j][nt][1] = movtrans(bf16x2_bits(__floats2bfloat162_rn(d2 - g23.x, d3 - g23.y)));
+                }
+            }
+            l[nt][0] = l[nt][0] * al0 + ps0;
+            l[nt][1] = l[nt][1] * al1 + ps1;
             m[nt][0] = mn0;
             m[nt][1] = mn1;
             if (__any_sync(0xffffffffu, (al0 != 1.f) || (al1 != 1.f))) {
@@ -424,55 +499,45 @@ __global__ void __launch_bounds__(kSelThreads, 1) decode_selected_kernel(const S
                     oacc[nt][mt][3] *= al1;
                 }
             }
-            if constexpr (kFp8) {
-                const float q0 = p0 * kPScale, q1 = p1 * kPScale, q2 = p2 * kPScale, q3 = p3 * kPScale;
-                const __half2 h01 = __floats2half2_rn(q0, q1), h23 = __floats2half2_rn(q2, q3);
-                const float2 f01 = __half22float2(h01), f23 = __half22float2(h23);
-                bh[nt][0] = movtrans(half2_bits(h01));
-                bh[nt][1] = movtrans(half2_bits(h23));
-                bl[nt][0] = movtrans(half2_bits(__floats2half2_rn(q0 - f01.x, q1 - f01.y)));
-                bl[nt][1] = movtrans(half2_bits(__floats2half2_rn(q2 - f23.x, q3 - f23.y)));
-            } else {
-                const __nv_bfloat162 h01 = __floats2bfloat162_rn(p0, p1), h23 = __floats2bfloat162_rn(p2, p3);
-                const float2 f01 = __bfloat1622float2(h01), f23 = __bfloat1622float2(h23);
-                bh[nt][0] = movtrans(bf16x2_bits(h01));
-                bh[nt][1] = movtrans(bf16x2_bits(h23));
-                bl[nt][0] = movtrans(bf16x2_bits(__floats2bfloat162_rn(p0 - f01.x, p1 - f01.y)));
-                bl[nt][1] = movtrans(bf16x2_bits(__floats2bfloat162_rn(p2 - f23.x, p3 - f23.y)));
-            }
         }
         // O^T += V^T P^T (rows past the length were zero-filled)
-        if constexpr (kFp8) {
-            const int t0 = 2 * tig;  // rows t0, t0 + 1, t0 + 8, t0 + 9; channels 16 gid ..
-            const uint32_t c0 = (gid ^ t0) << 4, c1 = (gid ^ (t0 + 1)) << 4;
-            const uint4 va = lds128(vbase + t0 * 128 + c0), vb = lds128(vbase + (t0 + 1) * 128 + c1);
-            const uint4 vc = lds128(vbase + (t0 + 8) * 128 + c0), vd = lds128(vbase + (t0 + 9) * 128 + c1);
-            const uint32_t xa[4] = {va.x, va.y, va.z, va.w}, xb[4] = {vb.x, vb.y, vb.z, vb.w};
-            const uint32_t xc[4] = {vc.x, vc.y, vc.z, vc.w}, xd[4] = {vd.x, vd.y, vd.z, vd.w};
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
+        for (int j = 0; j < J; ++j) {
+            if (J > 1 && nv[j] <= 0) continue;  // its buffer may hold anything
+            const uint32_t vbase = kbase[j] + Cf::kSlabBytes;
+            if constexpr (kFp8) {
+                const int t0 = 2 * tig;  // rows t0, t0 + 1, t0 + 8, t0 + 9; channels 16 gid ..
+                const uint32_t c0 = (gid ^ t0) << 4, c1 = (gid ^ (t0 + 1)) << 4;
+                const uint4 va = lds128(vbase + t0 * 128 + c0), vb = lds128(vbase + (t0 + 1) * 128 + c1);
+                const uint4 vc = lds128(vbase + (t0 + 8) * 128 + c0), vd = lds128(vbase + (t0 + 9) * 128 + c1);
+                const uint32_t xa[4] = {va.x, va.y, va.z, va.w}, xb[4] = {vb.x, vb.y, vb.z, vb.w};
+                const uint32_t xc[4] = {vc.x, vc.y, vc.z, vc.w}, xd[4] = {vd.x, vd.y, vd.z, vd.w};
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t sel = half ? 0x7362u : 0x5140u;  // byte pairs of two token rows
-                    const uint32_t pa = prmt(xa[w], xb[w], sel), pc = prmt(xc[w], xd[w], sel);
-                    const uint32_t a[4] = {e4m3x2_to_f16x2(pa & 0xffffu), e4m3x2_to_f16x2(pa >> 16),
-                                           e4m3x2_to_f16x2(pc & 0xffffu), e4m3x2_to_f16x2(pc >> 16)};
+                for (int w = 0; w < 4; ++w) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_f16(oacc[nt][2 * w + half], a, bh[nt][0], bh[nt][1]);
-                        mma_f16(oacc[nt][2 * w + half], a, bl[nt][0], bl[nt][1]);
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t sel = half ? 0x7362u : 0x5140u;  // byte pairs of two token rows
+                        const uint32_t pa = prmt(xa[w], xb[w], sel), pc = prmt(xc[w], xd[w], sel);
+                        const uint32_t a[4] = {e4m3x2_to_f16x2(pa & 0xffffu), e4m3x2_to_f16x2(pa >> 16),
+                                               e4m3x2_to_f16x2(pc & 0xffffu), e4m3x2_to_f16x2(pc >> 16)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_f16(oacc[nt][2 * w + half], a, bh[j][nt][0], bh[j][nt][1]);
+                            mma_f16(oacc[nt][2 * w + half], a, bl[j][nt][0], bl[j][nt][1]);
+                        }
                     }
                 }
-            }
-        } else {
+            } else {
 #pragma unroll
-            for (int mt = 0; mt < D / 16; ++mt) {
-                uint32_t a[4];
-                ldsm_x4_t(a, vbase + v_lane + (((2 * mt + v_chi) ^ r8) << 4));
+                for (int mt = 0; mt < D / 16; ++mt) {
+                    uint32_t a[4];
+                    ldsm_x4_t(a, vbase + v_lane + (((2 * mt + v_chi) ^ r8) << 4));
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma_bf16(oacc[nt][mt], a, bh[nt][0], bh[nt][1]);
-                    mma_bf16(oacc[nt][mt], a, bl[nt][0], bl[nt][1]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_bf16(oacc[nt][mt], a, bh[j][nt][0], bh[j][nt][1]);
+                        mma_bf16(oacc[nt][mt], a, bl[j][nt][0], bl[j][nt][1]);
+                        mma_bf16(oacc[nt][mt], a, bt[j][nt][0], bt[j][nt][1]);
+                    }
                 }
             }
         }
@@ -493,9 +558,6 @@ __global__ void __launch_bounds__(kSelThreads, 1) decode_selected_kernel(const S
     float* mg_o = reinterpret_cast<float*>(smem);
     float* mg_m = mg_o + kWarps * kCols * MS;
     float* mg_l = mg_m + kWarps * kCols;
-    float* cs_o = mg_l + kWarps * kCols;
-    float* cs_m = cs_o + kCols * D;
-    float* cs_l = cs_m + kCols;
     float* mo = mg_o + warp * kCols * MS;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -515,7 +577,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) decode_selected_kernel(const S
         }
     }
     __syncthreads();
-    finish_list<D, kFp8>(p, b, hq0, ncol, kCols, vscale, mg_o, mg_m, mg_l, cs_o, cs_m, cs_l, bad_len || *bad_flag);
+    finish_list<D, kCols, kFp8>(p, b, hq0, ncol, vscale, mg_o, mg_m, mg_l,
+                                reinterpret_cast<Mailbox<D, kCols>*>(smem + Cf::kBoxOff), bad_len || *bad_flag);
 }
 
 // -------------------------------------------------------------- FP32 caches
@@ -529,12 +592,13 @@ __global__ void __launch_bounds__(kSelThreads) decode_selected_f32_kernel(const 
     __shared__ __align__(16) float qs[GC][D];
     __shared__ __align__(16) float mg_o[kWarps * GC * MS];
     __shared__ float mg_m[kWarps * GC], mg_l[kWarps * GC];
-    __shared__ float cs_o[GC * D], cs_m[GC], cs_l[GC];
+    __shared__ Mailbox<D, GC> box;
     __shared__ int bad_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l8 = lane & 7, tok = lane >> 3;
     const int g = blockIdx.y / p.ngroups, cg = blockIdx.y - g * p.ngroups, b = blockIdx.z;
     const int ncol = min(GC, p.G - GC * cg);
     const int hq0 = g * p.G + GC * cg;
+    if (p.C > 1) cluster_arrive();  // (waited for before the states are sent)
     wait_primary();
     allow_dependents();
     if (threadIdx.x == 0) bad_flag = 0;
@@ -636,7 +700,7 @@ __global__ void __launch_bounds__(kSelThreads) decode_selected_f32_kernel(const 
         }
     }
     __syncthreads();
-    finish_list<D, false>(p, b, hq0, ncol, GC, 1.f, mg_o, mg_m, mg_l, cs_o, cs_m, cs_l, bad_len || bad_flag);
+    finish_list<D, GC, false>(p, b, hq0, ncol, 1.f, mg_o, mg_m, mg_l, &box, bad_len || bad_flag);
 }
 
 // ---------------------------------------------------------------- host side
@@ -648,61 +712,55 @@ constexpr int kMaxDevices = 64;
 struct Instance {
     std::mutex mu;
     bool ready[kMaxDevices] = {};
-    int clusters[kMaxDevices][5];  // of 1, 2, 4, 8, 16 blocks
+    int clusters[kMaxDevices][kMaxCluster + 1];  // by blocks per cluster
 };
 
 template <typename Kernel>
-int prepare_instance(Kernel kernel, int smem, int device, Instance* inst, int* fit) {
+int prepare_instance(Kernel kernel, int smem, int device, Instance* inst) {
     std::lock_guard<std::mutex> lock(inst->mu);
-    if (!inst->ready[device]) {
-        if (smem > 0 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-            return TA_ERR_CUDA;
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-            return TA_ERR_CUDA;
-        for (int i = 0; i < 5; ++i) {
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3(1 << i, 1, 1);
-            cfg.blockDim = dim3(kSelThreads, 1, 1);
-            cfg.dynamicSmemBytes = smem;
-            cudaLaunchAttribute a = {};
-            a.id = cudaLaunchAttributeClusterDimension;
-            a.val.clusterDim.x = 1 << i;
-            a.val.clusterDim.y = a.val.clusterDim.z = 1;
-            cfg.attrs = &a;
-            cfg.numAttrs = 1;
-            int n = 0;
-            if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
-                (void)cudaGetLastError();  // size not available here
-                n = 0;
-            }
-            inst->clusters[device][i] = n;
+    if (inst->ready[device]) return TA_OK;
+    if (smem > 0 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return TA_ERR_CUDA;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return TA_ERR_CUDA;
+    for (int c = 1; c <= kMaxCluster; ++c) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(c, 1, 1);
+        cfg.blockDim = dim3(kSelThreads, 1, 1);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute a = {};
+        a.id = cudaLaunchAttributeClusterDimension;
+        a.val.clusterDim.x = c;
+        a.val.clusterDim.y = a.val.clusterDim.z = 1;
+        cfg.attrs = &a;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();  // size not available here
+            n = 0;
         }
-        inst->ready[device] = true;
+        inst->clusters[device][c] = n;
     }
-    std::copy(inst->clusters[device], inst->clusters[device] + 5, fit);
+    inst->ready[device] = true;
     return TA_OK;
 }
 
-// Blocks per list: the largest power of two that gives every warp at least one
-// slab and keeps all lists resident at once; one block when there are more
-// lists than that.
+// Blocks per list: the most that leave every warp a slab and keep all lists
+// resident at once (how many clusters of a size fit depends on the GPCs: on
+// GB300, with one block an SM, 36 of 4 blocks but only 15 of 7 or 8); one block
+// when there are more lists than that.
 int pick_cluster(int64_t lists, int64_t slabs, const int* fit) {
     int c = 1;
-    for (int i = 1; i < 5; ++i) {
-        const int n = 1 << i;
-        if (slabs < static_cast<int64_t>(n) * kWarps || lists > fit[i]) break;
-        c = n;
-    }
+    for (int n = 2; n <= kMaxCluster; ++n)
+        if (slabs >= static_cast<int64_t>(n) * kWarps && lists <= fit[n]) c = n;
     return c;
 }
 
 template <typename Kernel>
 int launch_selected(Kernel kernel, int smem, Instance* inst, int device, SelParams p, int batch, cudaStream_t stream) {
-    int fit[5];
-    const int rc = prepare_instance(kernel, smem, device, inst, fit);
+    const int rc = prepare_instance(kernel, smem, device, inst);
     if (rc != TA_OK) return rc;
     const int64_t lists = static_cast<int64_t>(batch) * p.Hkv * p.ngroups;
-    p.C = pick_cluster(lists, static_cast<int64_t>(p.num_select) << (p.page_shift - 4), fit);
+    p.C = pick_cluster(lists, static_cast<int64_t>(p.num_select) << (p.page_shift - 4), inst->clusters[device]);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.C, p.Hkv * p.ngroups, batch);
     cfg.blockDim = dim3(kSelThreads, 1, 1);
