@@ -429,21 +429,16 @@ __device__ __forceinline__ float unordered(uint32_t k) {
 // Sums over the block's warps of two warp-uniform values, and of those of the
 // warps before this one.
 __device__ __forceinline__ void warp_sums(int a, int b, int2* buf, int2* before, int2* all) {
-    const int warp = threadIdx.x >> 5;
+    static_assert(kPickWarps <= 32, "one lane per warp");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) buf[warp] = make_int2(a, b);
+    if (lane == 0) buf[warp] = make_int2(a, b);
     __syncthreads();
-    *before = *all = make_int2(0, 0);
-#pragma unroll
-    for (int w = 0; w < kPickWarps; ++w) {
-        const int2 c = buf[w];
-        if (w < warp) {
-            before->x += c.x;
-            before->y += c.y;
-        }
-        all->x += c.x;
-        all->y += c.y;
-    }
+    const int2 c = lane < kPickWarps ? buf[lane] : make_int2(0, 0);
+    before->x = __reduce_add_sync(0xffffffffu, lane < warp ? c.x : 0);
+    before->y = __reduce_add_sync(0xffffffffu, lane < warp ? c.y : 0);
+    all->x = __reduce_add_sync(0xffffffffu, c.x);
+    all->y = __reduce_add_sync(0xffffffffu, c.y);
 }
 
 // The `need`-th largest (need >= 1) of the keys that are not 0 (0: no key), n4 groups
@@ -562,15 +557,10 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
         mag = __reduce_max_sync(0xffffffffu, mag);
         if (lane == 0) range_w[warp] = make_uint4(kmin - 1, kmax, mag, 0u);
         __syncthreads();
-        kmin = 0xffffffffu;
-#pragma unroll
-        for (int w = 0; w < kPickWarps; ++w) {
-            const uint4 r = range_w[w];
-            kmin = min(kmin, r.x);
-            kmax = max(kmax, r.y);
-            mag = max(mag, r.z);
-        }
-        kmin += 1;
+        const uint4 r = lane < kPickWarps ? range_w[lane] : make_uint4(0xffffffffu, 0u, 0u, 0u);
+        kmin = __reduce_min_sync(0xffffffffu, r.x) + 1;
+        kmax = __reduce_max_sync(0xffffffffu, r.y);
+        mag = __reduce_max_sync(0xffffffffu, r.z);
         int above;
         const uint32_t last = radix_pick(n4, need, kmax, 32 - __clz(kmin ^ kmax), hist, found, key4, &above);
         // 2 eps, and the range around the last page that FP32 cannot tell apart
@@ -638,9 +628,12 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
                 __shared__ float2 few_s[32];
                 if (threadIdx.x == 0) few_n = 0;
                 __syncthreads();
-                for (int i = threadIdx.x; i < n; i += kPickThreads) {
-                    const uint32_t k = keys_kept[i];
-                    if (k <= top && k >= low) few[atomicAdd(&few_n, 1)] = i;
+                for (int i = threadIdx.x; i < n4; i += kPickThreads) {
+                    const uint4 q = key4(i);
+                    const uint32_t k[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (k[j] <= top && k[j] >= low) few[atomicAdd(&few_n, 1)] = 4 * i + j;
                 }
                 __syncthreads();
                 for (int j = warp; j < n_between; j += kPickWarps) {
@@ -695,28 +688,38 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
     }
     // every warp takes a run of consecutive pages, 32 at a time: count, sum, write in order
     __syncthreads();
-    const int per = (n + kPickThreads - 1) / kPickThreads * 32;
-    const int i0 = min(n, warp * per), i1 = min(n, i0 + per);
     const unsigned lower = (1u << lane) - 1u;
     int2 before, all;
-    if (T == 0 && T2 == 0) {  // one threshold tells them all apart
-        auto takes = [&](int i) {
-            return i < n && (i < lo || i >= hi || (need > 0 && key(i) >= low));
+    if (T == 0 && T2 == 0) {  // one threshold tells them all apart: four pages a lane
+        const int per = (n4 + kPickThreads - 1) / kPickThreads * 32;
+        const int i0 = min(n4, warp * per), i1 = min(n4, i0 + per);
+        auto takes = [&](int i, int x, uint32_t k) { return i + x < n && (i + x < lo || i + x >= hi || k >= low); };
+        auto flags = [&](int i4) -> unsigned {  // which of pages 4 i4 .. are taken
+            if (i4 >= i1) return 0u;
+            const uint4 k = need > 0 ? key4(i4) : make_uint4(0u, 0u, 0u, 0u);
+            const int i = 4 * i4;
+            return (takes(i, 0, k.x) ? 1u : 0u) | (takes(i, 1, k.y) ? 2u : 0u) | (takes(i, 2, k.z) ? 4u : 0u) |
+                   (takes(i, 3, k.w) ? 8u : 0u);
         };
         int taken = 0;
-#pragma unroll 4
-        for (int i = i0; i < i1; i += 32) taken += __popc(__ballot_sync(0xffffffffu, takes(i + lane)));
-        warp_sums(taken, 0, sums, &before, &all);
+#pragma unroll 2
+        for (int i = i0; i < i1; i += 32) taken += __popc(flags(i + lane));
+        warp_sums(__reduce_add_sync(0xffffffffu, taken), 0, sums, &before, &all);
         int at = before.x;
-#pragma unroll 4
+#pragma unroll 2
         for (int i = i0; i < i1; i += 32) {
-            const bool take = takes(i + lane);
-            const unsigned t = __ballot_sync(0xffffffffu, take);
-            if (take) sel[at + __popc(t & lower)] = i + lane;
-            at += __popc(t);
+            unsigned f = flags(i + lane);
+            const int c = __popc(f);  // 0 .. 4: its prefix sum from its three bits
+            const unsigned b0 = __ballot_sync(0xffffffffu, c & 1), b1 = __ballot_sync(0xffffffffu, c & 2),
+                           b2 = __ballot_sync(0xffffffffu, c & 4);
+            int to = at + __popc(b0 & lower) + 2 * __popc(b1 & lower) + 4 * __popc(b2 & lower);
+            for (; f != 0; f &= f - 1) sel[to++] = 4 * (i + lane) + __ffs(f) - 1;
+            at += __popc(b0) + 2 * __popc(b1) + 4 * __popc(b2);
         }
         return;
     }
+    const int per = (n + kPickThreads - 1) / kPickThreads * 32;
+    const int i0 = min(n, warp * per), i1 = min(n, i0 + per);
     auto kind = [&](int i) -> int {  // 2: taken, 1: a tie, 0: not taken
         if (i < lo || i >= hi) return i < n ? 2 : 0;
         const uint32_t k = key(i);
