@@ -44,19 +44,19 @@ FALLBACK_HBM_GBS = 6800.0
 NCU_TRAFFIC = {
     # warp-level tensor-core kernel, BF16 cache, 8B-shaped layer of 131072 tokens, 19 splits
     ("mma", "llama3.1-8b-decode-layer", 1): {
-        "bytes_per_launch": 537316608 + 2760192, "num_splits": 19,
-        "src_sha256": "59386695fba4fc9262837d650de324d47d9e706eacf4aa39fcf9eb83df155df7"},
+        "bytes_per_launch": 537349120 + 2781952, "num_splits": 19,
+        "src_sha256": "fabe09c7fc7fd0f9f4420c4d3e546adec36ce0456347c5c323a30b74167dd509"},
     # tcgen05 kernel, the same layer with 8 and 16 queries per row (32 and 64 columns per KV head)
     ("tc05", "llama3.1-8b-decode-layer", 8): {
-        "bytes_per_launch": 537053696 + 2923008, "num_splits": 19,
-        "src_sha256": "7b2271b50877b0922013af7bf995687381b9919b45172c56d16581a9ad887131"},
+        "bytes_per_launch": 537041152 + 2807296, "num_splits": 19,
+        "src_sha256": "4b30520dfbe8833e98e24e31fd99df4d8cd64c5336da4dbcb3f8cb0042c944e3"},
     ("tc05", "llama3.1-8b-decode-layer", 16): {
-        "bytes_per_launch": 537125632 + 3222016, "num_splits": 19,
-        "src_sha256": "7b2271b50877b0922013af7bf995687381b9919b45172c56d16581a9ad887131"},
+        "bytes_per_launch": 537189632 + 3212032, "num_splits": 19,
+        "src_sha256": "4b30520dfbe8833e98e24e31fd99df4d8cd64c5336da4dbcb3f8cb0042c944e3"},
     # tcgen05 FP8 kernel, the same layer's E4M3 cache with 8 queries per row (32 columns per KV head)
     ("fp8tc05", "llama3.1-8b-decode-layer", 8): {
-        "bytes_per_launch": 268646656 + 3003904, "num_splits": 19,
-        "src_sha256": "5e686e4a74a3e0766f61d2ad2a9009fcea89ac37da8bc5e2c0252ec89b010c34"},
+        "bytes_per_launch": 268612096 + 2792192, "num_splits": 19,
+        "src_sha256": "dfe2297c48880c3d45ba1cfd07fbf263ee900528c572e6cd5c9fed58e6f65f62"},
 }
 
 

@@ -349,3 +349,66 @@ def test_two_streams_do_not_share_anything():
         torch.cuda.synchronize()
         for a, b in zip(alone, got):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("distinct", [True, False])
+def test_select_pages_of_very_long_rows(distinct):
+    """More pages than the selection keeps in shared memory; with few physical pages behind a
+    long table most scores are equal, so ties decide."""
+    d, page, n = 64, 16, 40003
+    g = torch.Generator().manual_seed(21)
+    pages = n if distinct else 60
+    bounds = page_ranges(g, pages, 1, d, torch.bfloat16)
+    bt = (torch.randperm(n, generator=g) if distinct else torch.randint(0, pages, (n,), generator=g)).view(1, n).to(torch.int32)
+    q = torch.randn(1, 3, d, generator=g).to(torch.bfloat16)
+    lens = torch.tensor([n * page - 5], dtype=torch.int32)
+    for nsel, first, last in ((1, 0, 0), (700, 3, 5), (30000, 0, 1)):
+        sel = ta.tree_attn_select_pages(q.cuda(), bounds.cuda(), bt.cuda(), lens.cuda(), page, nsel, first, last)
+        assert torch.equal(sel.cpu(), ref.select_pages(q, bounds, bt, lens, page, nsel, first, last)), nsel
+    assert ta.tree_attn_get_device_error() == 0
+
+
+def test_pools_past_32_bit_offsets():
+    """Bounds, selection and decode on pages whose element and byte offsets pass 2^32 (one 4.4 GB
+    E4M3 pool for keys and values)."""
+    page, hkv, d = 64, 8, 128
+    pages = (2 ** 32) // (page * hkv * d) + 600
+    k = torch.zeros(pages, page, hkv, d, dtype=torch.uint8, device="cuda")
+    far = torch.tensor([0, 1, 65535, 65536, pages - 1, pages - 2, pages - 300], dtype=torch.int64)
+    g = torch.Generator().manual_seed(1)
+    for p in far.tolist():
+        k[p] = (torch.randn(page, hkv, d, generator=g) * 50).to(FP8).view(torch.uint8).cuda()
+    k = k.view(FP8)
+    bt = far.view(1, 7).to(torch.int32)
+    lens = torch.tensor([7 * page - 9], dtype=torch.int32)
+    bounds = ta.tree_attn_page_bounds(k, bt.cuda(), lens.cuda())
+    small = k.view(torch.uint8)[far.cuda()].cpu().view(FP8)
+    near = torch.arange(7, dtype=torch.int32).view(1, 7)
+    want = ref.page_bounds(small, near, lens, torch.zeros(7, hkv, 2, d, dtype=torch.float64))
+    assert torch.equal(bounds[far.cuda()].cpu().double(), want)
+    q = torch.randn(1, 32, d, generator=g).to(torch.bfloat16)
+    sel = ta.tree_attn_select_pages(q.cuda(), bounds, bt.cuda(), lens.cuda(), page, 4, 1, 1)
+    assert torch.equal(sel.cpu(), ref.select_pages(q, want.to(torch.bfloat16), near, lens, page, 4, 1, 1))
+    sc = torch.full((hkv,), 0.02)
+    out, lse = ta.tree_attn_decode_selected(q.cuda(), k, k, bt.cuda(), lens.cuda(), sel, k_scale=sc.cuda(), v_scale=sc.cuda())
+    w, wl = ref.decode_selected(q, small, small, near, lens, sel.cpu(), k_scale=sc, v_scale=sc)
+    assert (out.cpu().double() - w).abs().max() <= 1e-3 and (lse.cpu().double() - wl).abs().max() <= 2e-4
+    assert ta.tree_attn_get_device_error() == 0
+
+
+def test_stream_handles_and_empty_rows():
+    g = torch.Generator().manual_seed(3)
+    page, hkv, d, B = 16, 1, 64, 3
+    k = pool(g, torch.bfloat16, 9, page, hkv, d, "NHD").cuda()
+    bt = table(g, B, 3, 9).cuda()
+    lens = torch.zeros(B, dtype=torch.int32).cuda()
+    q = torch.randn(B, 2, d, generator=g).to(torch.bfloat16).cuda()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    for stream in (None, 0, st, st.cuda_stream):
+        b = ta.tree_attn_page_bounds(k, bt, lens, stream=stream)
+        sel = ta.tree_attn_select_pages(q, b, bt, lens, page, 2, stream=stream)
+        out, lse = ta.tree_attn_decode_selected(q, k, k, bt, lens, sel, stream=stream)
+        torch.cuda.synchronize()
+        assert (b == 0).all() and (sel == -1).all() and (out == 0).all() and (lse == -math.inf).all()
+    assert ta.tree_attn_get_device_error() == 0
