@@ -432,9 +432,10 @@ __global__ void __launch_bounds__(kSelThreads, 1) decode_selected_kernel(const S
             }
         }
         // Online softmax per column.  P^T as B fragments: the weights as the sum of three
-        // BF16 numbers (all 24 bits; two leave 2^-17, which showed: 2.4e-6 of the output's
-        // norm over 16384 tokens against 3.6e-7 in FP32), or two FP16 ones (22 bits).
+        // BF16 numbers (all 24 bits; two leave 2^-18, which shows in FP32 outputs), or two
+        // FP16 ones (22 bits).
         uint32_t bh[J][NT][2], bl[J][NT][2], bt[J][NT][2];
+        float alpha[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float sc[J][4], bm0 = -INFINITY, bm1 = -INFINITY;
@@ -490,54 +491,75 @@ __global__ void __launch_bounds__(kSelThreads, 1) decode_selected_kernel(const S
             l[nt][1] = l[nt][1] * al1 + ps1;
             m[nt][0] = mn0;
             m[nt][1] = mn1;
-            if (__any_sync(0xffffffffu, (al0 != 1.f) || (al1 != 1.f))) {
-#pragma unroll
-                for (int mt = 0; mt < D / 16; ++mt) {
-                    oacc[nt][mt][0] *= al0;
-                    oacc[nt][mt][1] *= al1;
-                    oacc[nt][mt][2] *= al0;
-                    oacc[nt][mt][3] *= al1;
-                }
-            }
+            alpha[nt][0] = al0;
+            alpha[nt][1] = al1;
         }
-        // O^T += V^T P^T (rows past the length were zero-filled)
+        // O^T = alpha O^T + V^T P^T (rows past the length were zero-filled).  The products of
+        // one step are summed on their own and added in FP32: the tensor cores cut off
+        // what they add to a running sum (toward zero), which over 512 tokens a warp was
+        // 2e-6 of the output.
+        auto add = [&](int nt, int mt, const float (&f)[4]) {
+            oacc[nt][mt][0] = fmaf(oacc[nt][mt][0], alpha[nt][0], f[0]);
+            oacc[nt][mt][1] = fmaf(oacc[nt][mt][1], alpha[nt][1], f[1]);
+            oacc[nt][mt][2] = fmaf(oacc[nt][mt][2], alpha[nt][0], f[2]);
+            oacc[nt][mt][3] = fmaf(oacc[nt][mt][3], alpha[nt][1], f[3]);
+        };
+        if constexpr (kFp8) {
+            const int t0 = 2 * tig;  // rows t0, t0 + 1, t0 + 8, t0 + 9; channels 16 gid ..
+            const uint32_t c0 = (gid ^ t0) << 4, c1 = (gid ^ (t0 + 1)) << 4;
+            uint32_t xa[J][4], xb[J][4], xc[J][4], xd[J][4];
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            if (J > 1 && nv[j] <= 0) continue;  // its buffer may hold anything
-            const uint32_t vbase = kbase[j] + Cf::kSlabBytes;
-            if constexpr (kFp8) {
-                const int t0 = 2 * tig;  // rows t0, t0 + 1, t0 + 8, t0 + 9; channels 16 gid ..
-                const uint32_t c0 = (gid ^ t0) << 4, c1 = (gid ^ (t0 + 1)) << 4;
-                const uint4 va = lds128(vbase + t0 * 128 + c0), vb = lds128(vbase + (t0 + 1) * 128 + c1);
-                const uint4 vc = lds128(vbase + (t0 + 8) * 128 + c0), vd = lds128(vbase + (t0 + 9) * 128 + c1);
-                const uint32_t xa[4] = {va.x, va.y, va.z, va.w}, xb[4] = {vb.x, vb.y, vb.z, vb.w};
-                const uint32_t xc[4] = {vc.x, vc.y, vc.z, vc.w}, xd[4] = {vd.x, vd.y, vd.z, vd.w};
+            for (int j = 0; j < J; ++j) {
+                const uint32_t vbase = kbase[j] + Cf::kSlabBytes;
+                uint4 va, vb, vc, vd;
+                va = vb = vc = vd = make_uint4(0u, 0u, 0u, 0u);
+                if (nv[j] > 0) {  // (else its buffer may hold anything)
+                    va = lds128(vbase + t0 * 128 + c0);
+                    vb = lds128(vbase + (t0 + 1) * 128 + c1);
+                    vc = lds128(vbase + (t0 + 8) * 128 + c0);
+                    vd = lds128(vbase + (t0 + 9) * 128 + c1);
+                }
+                xa[j][0] = va.x, xa[j][1] = va.y, xa[j][2] = va.z, xa[j][3] = va.w;
+                xb[j][0] = vb.x, xb[j][1] = vb.y, xb[j][2] = vb.z, xb[j][3] = vb.w;
+                xc[j][0] = vc.x, xc[j][1] = vc.y, xc[j][2] = vc.z, xc[j][3] = vc.w;
+                xd[j][0] = vd.x, xd[j][1] = vd.y, xd[j][2] = vd.z, xd[j][3] = vd.w;
+            }
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
+            for (int w = 0; w < 4; ++w) {
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint32_t sel = half ? 0x7362u : 0x5140u;  // byte pairs of two token rows
-                        const uint32_t pa = prmt(xa[w], xb[w], sel), pc = prmt(xc[w], xd[w], sel);
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t sel = half ? 0x7362u : 0x5140u;  // byte pairs of two token rows
+                    float f[NT][4];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) f[nt][0] = f[nt][1] = f[nt][2] = f[nt][3] = 0.f;
+#pragma unroll
+                    for (int j = 0; j < J; ++j) {
+                        const uint32_t pa = prmt(xa[j][w], xb[j][w], sel), pc = prmt(xc[j][w], xd[j][w], sel);
                         const uint32_t a[4] = {e4m3x2_to_f16x2(pa & 0xffffu), e4m3x2_to_f16x2(pa >> 16),
                                                e4m3x2_to_f16x2(pc & 0xffffu), e4m3x2_to_f16x2(pc >> 16)};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma_f16(oacc[nt][2 * w + half], a, bh[j][nt][0], bh[j][nt][1]);
-                            mma_f16(oacc[nt][2 * w + half], a, bl[j][nt][0], bl[j][nt][1]);
+                            mma_f16(f[nt], a, bh[j][nt][0], bh[j][nt][1]);
+                            mma_f16(f[nt], a, bl[j][nt][0], bl[j][nt][1]);
                         }
                     }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) add(nt, 2 * w + half, f[nt]);
                 }
-            } else {
+            }
+        } else {
+            const uint32_t vbase = kbase[0] + Cf::kSlabBytes;
 #pragma unroll
-                for (int mt = 0; mt < D / 16; ++mt) {
-                    uint32_t a[4];
-                    ldsm_x4_t(a, vbase + v_lane + (((2 * mt + v_chi) ^ r8) << 4));
+            for (int mt = 0; mt < D / 16; ++mt) {
+                uint32_t a[4];
+                ldsm_x4_t(a, vbase + v_lane + (((2 * mt + v_chi) ^ r8) << 4));
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_bf16(oacc[nt][mt], a, bh[j][nt][0], bh[j][nt][1]);
-                        mma_bf16(oacc[nt][mt], a, bl[j][nt][0], bl[j][nt][1]);
-                        mma_bf16(oacc[nt][mt], a, bt[j][nt][0], bt[j][nt][1]);
-                    }
+                for (int nt = 0; nt < NT; ++nt) {
+                    float f[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma_bf16(f, a, bh[0][nt][0], bh[0][nt][1]);
+                    mma_bf16(f, a, bl[0][nt][0], bl[0][nt][1]);
+                    mma_bf16(f, a, bt[0][nt][0], bt[0][nt][1]);
+                    add(nt, mt, f);
                 }
             }
         }

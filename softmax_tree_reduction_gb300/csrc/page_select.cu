@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
         int above;
         const uint32_t last = radix_pick(n4, need, kmax, 32 - __clz(kmin ^ kmax), hist, found, key4, &above);
         // 2 eps, and the range around the last page that FP32 cannot tell apart
-        const float t = unordered(last), e2 = fmaf(__uint_as_float(mag), 40.f * 5.9604645e-8f, 1e-42f);
+        const float t = unordered(last), e2 = fmaf(__uint_as_float(mag), 40.f * 5.9604645e-8f, 1e-40f);
         const float tu = t + e2, tl = t - e2;
         top = tu == tu ? ordered(tu) : 0xffffffffu;
         low = tl == tl ? ordered(tl) : 1u;
