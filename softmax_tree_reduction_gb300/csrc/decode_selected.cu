@@ -166,6 +166,7 @@ __device__ void finish_list(const SelParams& p, int b, int hq0, int ncol, float 
     const int C = p.C, items = ncol * D, share = (items + C - 1) / C;
     const int rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
     if (C > 1) cluster_wait();  // every block of the cluster has started
+#pragma unroll 2
     for (int idx = tid; idx < items; idx += kSelThreads) {
         const int h = idx / D, dd = idx - h * D;
         const int pos = kFp8 ? (dd % 16) * 8 + dd / 16 : dd;
@@ -206,15 +207,22 @@ __device__ void finish_list(const SelParams& p, int b, int hq0, int ncol, float 
     const int n = min(share, items - rank * share);
     for (int i = tid; i < n; i += kSelThreads) {
         const int idx = rank * share + i, h = idx / D, dd = idx - h * D;
-        float M = -INFINITY;
-        for (int c = 0; c < C; ++c) M = fmaxf(M, box->ml[c][h].x);
+        float2 ml[kMaxCluster];
+        float o[kMaxCluster], M = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {  // all loads in flight at once
+            ml[c] = c < C ? box->ml[c][h] : make_float2(-INFINITY, 0.f);
+            o[c] = c < C ? box->o[c * share + i] : 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) M = fmaxf(M, ml[c].x);
         const float Ms = (M == -INFINITY) ? 0.f : M;
         float L = 0.f, O = 0.f;
-        for (int c = 0; c < C; ++c) {
-            const float2 ml = box->ml[c][h];
-            const float w = (ml.x == -INFINITY) ? 0.f : ex2(ml.x - Ms);
-            L = fmaf(w, ml.y, L);
-            O = fmaf(w, box->o[c * share + i], O);
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+            const float w = (ml[c].x == -INFINITY) ? 0.f : ex2(ml[c].x - Ms);
+            L = fmaf(w, ml[c].y, L);
+            O = fmaf(w, o[c], O);
         }
         p.out[(row0 + h) * D + dd] = (L == 0.f) ? 0.f : O / L;  // NaN of a poisoned block propagates
         if (dd == 0 && p.lse) p.lse[row0 + h] = (L == 0.f) ? -INFINITY : (M + log2f(L)) * kLn2;

@@ -27,7 +27,7 @@
 //
 // Selection.  One block per (row, KV head): scores are kept in shared memory as
 // order-preserving integers, whose common leading bits are skipped, and the
-// last page's is found digit by digit (8 bits a pass, counted with integer
+// last page's is found digit by digit (11 bits a pass, counted with integer
 // atomics in shared memory: their order cannot change the counts).  Ties go to
 // the lowest pages.
 //
@@ -339,17 +339,14 @@ __global__ void __launch_bounds__(kScoreThreads, std::is_same<TB, float>::value 
     allow_dependents();
     const int g = blockIdx.y, b = blockIdx.z;
     const int N = p.seqlens[b];
-    if (N < 0 || N > p.S) return;                     // the selection reports it
-    const int n = static_cast<int>((static_cast<int64_t>(N) + (1 << p.page_shift) - 1) >> p.page_shift);
-    const int p0 = blockIdx.x * p.per_block, p1 = min(n, p0 + p.per_block);
-    if (n <= p.num_select || p0 >= n) return;         // every page is taken, or no page here
+    const int p0 = blockIdx.x * p.per_block, pmax = min(p.pages, p0 + p.per_block);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.max_pages;
     float* scores = p.scores + (static_cast<int64_t>(b) * p.Hkv + g) * p.stride;
     float* mags = p.mags + (static_cast<int64_t>(b) * p.Hkv + g) * (p.stride / 8);
     const TB* bounds = static_cast<const TB*>(p.bounds) + static_cast<int64_t>(g) * 2 * D + lane * E;
-    auto lookup = [&](int q0) { return (lane < 8 && q0 + lane < p1) ? __ldg(table + q0 + lane) : -1; };
-    // the first pages' numbers are on their way while the coefficients are summed
+    auto lookup = [&](int q0) { return (lane < 8 && q0 + lane < pmax) ? __ldg(table + q0 + lane) : -1; };
+    // the length and the first pages' numbers are on their way while the coefficients are summed
     int q0 = p0 + warp * 8;
     int phys = lookup(q0);
     for (int i = threadIdx.x; i < 2 * D; i += kScoreThreads) {
@@ -357,6 +354,10 @@ __global__ void __launch_bounds__(kScoreThreads, std::is_same<TB, float>::value 
         coef[i] = __fadd_rn(c.x, c.y);
         if (blockIdx.x == 0) p.coef[(static_cast<int64_t>(b) * p.Hkv + g) * 2 * D + i] = c;
     }
+    if (N < 0 || N > p.S) return;                     // the selection reports it
+    const int n = static_cast<int>((static_cast<int64_t>(N) + (1 << p.page_shift) - 1) >> p.page_shift);
+    const int p1 = min(n, pmax);
+    if (n <= p.num_select || p0 >= n) return;         // every page is taken, or no page here
     __syncthreads();
     float c[E];
 #pragma unroll
@@ -415,6 +416,7 @@ __global__ void __launch_bounds__(kScoreThreads, std::is_same<TB, float>::value 
 // ---------------------------------------------------------------- selection
 constexpr int kPickThreads = 512;
 constexpr int kPickWarps = kPickThreads / 32;
+constexpr int kDigitBits = 11, kDigits = 1 << kDigitBits;
 constexpr int kPickKeep = 24576;  // scores kept in shared memory; longer rows read them again
 
 // Order-preserving integer of a float (no NaN), and back.
@@ -443,15 +445,19 @@ __device__ __forceinline__ void warp_sums(int a, int b, int2* buf, int2* before,
 
 // The `need`-th largest (need >= 1) of the keys that are not 0 (0: no key), n4 groups
 // of four that key4(i) gives, where all keys agree with `first` above their `bits`
-// low bits; *above: how many are larger.
+// low bits; *above: how many are larger.  Digits of 11 bits: scores of a row lie in a
+// narrow range, and with 8 bits the first pass's counters were contended (1500
+// against 700 cycles a pass).
 template <typename Key4>
-__device__ uint32_t radix_pick(int n4, int need, uint32_t first, int bits, int* hist, int* found, Key4&& key4, int* above) {
+__device__ uint32_t radix_pick(int n4, int need, uint32_t first, int bits, int* hist, int* tot, int* found, Key4&& key4, int* above) {
+    static_assert(kPickThreads * 4 == kDigits && kPickWarps <= 32, "four counters a thread");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t prefix = bits < 32 ? first >> bits : 0;
     int left = need;
     while (bits > 0) {
-        const int width = min(8, bits), shift = bits - width;
+        const int width = min(kDigitBits, bits), shift = bits - width;
         const uint32_t mask = (1u << width) - 1;
-        if (threadIdx.x < 256) hist[threadIdx.x] = 0;
+        reinterpret_cast<int4*>(hist)[threadIdx.x] = make_int4(0, 0, 0, 0);
         __syncthreads();
 #pragma unroll 2
         for (int i = threadIdx.x; i < n4; i += kPickThreads) {
@@ -462,28 +468,28 @@ __device__ uint32_t radix_pick(int n4, int need, uint32_t first, int bits, int* 
                 if (k[j] != 0 && (bits == 32 || (k[j] >> bits) == prefix)) atomicAdd(&hist[(k[j] >> shift) & mask], 1);
         }
         __syncthreads();
-        if (threadIdx.x < 32) {  // the largest digit with at least `left` keys at or above it
-            const int lane = threadIdx.x;
-            const int4 u = reinterpret_cast<const int4*>(hist)[63 - 2 * lane], v = reinterpret_cast<const int4*>(hist)[62 - 2 * lane];
-            const int c[8] = {u.w, u.z, u.y, u.x, v.w, v.z, v.y, v.x};  // digits 255 - 8 lane downwards
-            int sum[8];
-            sum[0] = c[0];
+        // the largest digit with at least `left` keys at or above it: digits downwards, four a thread
+        const int base = kPickThreads - 1 - static_cast<int>(threadIdx.x);
+        const int4 u = reinterpret_cast<const int4*>(hist)[base];
+        const int c[4] = {u.w, u.z, u.y, u.x};
+        const int sum = c[0] + c[1] + c[2] + c[3];
+        int x = sum;
 #pragma unroll
-            for (int j = 1; j < 8; ++j) sum[j] = sum[j - 1] + c[j];
-            int x = sum[7];
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, off);
+            if (lane >= off) x += y;
+        }
+        if (lane == 31) tot[warp] = x;
+        __syncthreads();
+        int b0 = __reduce_add_sync(0xffffffffu, lane < warp ? tot[lane] : 0) + x - sum;
+        if (b0 < left && left <= b0 + sum) {
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, off);
-                if (lane >= off) x += y;
-            }
-            const int before = x - sum[7];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int b0 = before + sum[j] - c[j];
+            for (int j = 0; j < 4; ++j) {
                 if (b0 < left && left <= b0 + c[j]) {
-                    found[0] = 255 - (lane * 8 + j);
+                    found[0] = 4 * base + 3 - j;
                     found[1] = left - b0;
                 }
+                b0 += c[j];
             }
         }
         __syncthreads();
@@ -499,8 +505,8 @@ template <int D, typename TQ, typename TB>
 __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const SelectParams p) {
     using PB = PageBounds<D, TB>;
     extern __shared__ __align__(16) uint32_t keys_kept[];
-    __shared__ __align__(16) int hist[256];
-    __shared__ int found[2];
+    __shared__ __align__(16) int hist[kDigits];
+    __shared__ int found[2], tot[kPickWarps];
     __shared__ int2 sums[kPickWarps];
     __shared__ uint4 range_w[kPickWarps];
     wait_primary();
@@ -508,7 +514,13 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
     const int g = blockIdx.x, b = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t* sel = p.selected + (static_cast<int64_t>(b) * p.Hkv + g) * p.num_select;
+    const int64_t row = static_cast<int64_t>(b) * p.Hkv + g;
+    const float* sc = p.scores + row * p.stride;
     const int N = p.seqlens[b];
+    // (the first scores do not wait for the length: past the row's pages they are ignored)
+    float4 ahead = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.pages > p.num_select && static_cast<int>(threadIdx.x) * 4 < p.stride)
+        ahead = __ldcg(reinterpret_cast<const float4*>(sc) + threadIdx.x);
     const bool bad = N < 0 || N > p.S;
     if (bad && threadIdx.x == 0) atomicOr(p.err, kErrBadSeqlen);
     const int n = bad ? 0 : static_cast<int>((static_cast<int64_t>(N) + (1 << p.page_shift) - 1) >> p.page_shift);
@@ -516,8 +528,6 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
         for (int i = threadIdx.x; i < p.num_select; i += kPickThreads) sel[i] = i < n ? i : -1;
         return;
     }
-    const int64_t row = static_cast<int64_t>(b) * p.Hkv + g;
-    const float* sc = p.scores + row * p.stride;
     float2* exact = p.exact + row * p.pages;
     const int lo = p.first, hi = n - p.last;             // the pages that compete
     const int need = p.num_select - p.first - p.last;    // places for them; fewer than hi - lo
@@ -528,7 +538,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
     int ties = 0;                                        // pages at (T, T2) to take, lowest first
     // four pages' keys (0: the page does not compete)
     auto scored4 = [&](int i) {
-        const float4 s = __ldcg(reinterpret_cast<const float4*>(sc) + i);
+        const float4 s = i == static_cast<int>(threadIdx.x) ? ahead : __ldcg(reinterpret_cast<const float4*>(sc) + i);
         const int q = 4 * i;
         uint4 k;
         k.x = q >= lo && q < hi ? ordered(s.x) : 0u;
@@ -562,7 +572,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
         kmax = __reduce_max_sync(0xffffffffu, r.y);
         mag = __reduce_max_sync(0xffffffffu, r.z);
         int above;
-        const uint32_t last = radix_pick(n4, need, kmax, 32 - __clz(kmin ^ kmax), hist, found, key4, &above);
+        const uint32_t last = radix_pick(n4, need, kmax, 32 - __clz(kmin ^ kmax), hist, tot, found, key4, &above);
         // 2 eps, and the range around the last page that FP32 cannot tell apart
         const float t = unordered(last), e2 = fmaf(__uint_as_float(mag), 40.f * 5.9604645e-8f, 1e-40f);
         const float tu = t + e2, tl = t - e2;
@@ -675,9 +685,9 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
                     return r;
                 };
                 int above1, above2;
-                T = radix_pick(n4, places, 0u, 32, hist, found,
+                T = radix_pick(n4, places, 0u, 32, hist, tot, found,
                                [&](int i) { return four(i, [&](int j) { return ordered(exact[j].x); }); }, &above1);
-                T2 = radix_pick(n4, places - above1, 0u, 32, hist, found,
+                T2 = radix_pick(n4, places - above1, 0u, 32, hist, tot, found,
                                 [&](int i) {
                                     return four(i, [&](int j) { return ordered(exact[j].x) == T ? ordered(exact[j].y) : 0u; });
                                 },
