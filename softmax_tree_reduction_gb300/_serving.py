@@ -175,12 +175,12 @@ def tree_attn_select_pages(q: torch.Tensor, bounds: torch.Tensor, block_table: t
     tree_attn_select_workspace_bytes bytes (allocated when not passed).
     """
     calls = _calls or _open()
-    if stream is not None or selected is None or workspace is None:
+    if stream is not None or selected is None:
         stream, ctx = _on(stream, q)
         with ctx:
             if selected is None:
                 selected = torch.empty((block_table.shape[0], bounds.shape[1], max(0, int(num_select))), dtype=torch.int32, device=q.device)
-            if workspace is None:
+            if workspace is None and stream is not None:   # (on the current stream the extension allocates it)
                 workspace = torch.empty(max(16, calls.select_workspace_bytes(bounds, block_table, page_size, max_seqlen)), dtype=torch.uint8,
                                         device=q.device)
     rc = calls.select_pages(q, bounds, block_table, seqlens, page_size, num_select, first_pages, last_pages, selected, workspace, max_seqlen, stream)

@@ -166,7 +166,7 @@ __device__ void finish_list(const SelParams& p, int b, int hq0, int ncol, float 
     const int C = p.C, items = ncol * D, share = (items + C - 1) / C;
     const int rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
     if (C > 1) cluster_wait();  // every block of the cluster has started
-#pragma unroll 2
+#pragma unroll 1
     for (int idx = tid; idx < items; idx += kSelThreads) {
         const int h = idx / D, dd = idx - h * D;
         const int pos = kFp8 ? (dd % 16) * 8 + dd / 16 : dd;

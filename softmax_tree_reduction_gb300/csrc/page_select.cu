@@ -15,9 +15,9 @@
 // Precision.  The list must not depend on the order of summation, yet FP32
 // scores of a few hundred terms differ from the real ones by more than some
 // neighbouring pages do.  So the score kernel sums in FP32 and also returns
-// mag = sum_i |A[i] hi[i]| + |B[i] lo[i]|: coefficients are rounded once, a lane
-// chains at most 8 products and 5 levels join the lanes, so a score is off by
-// less than 16 u mag (u = 2^-24), taken as eps = 20 u max(mag).  With t the
+// mag = sum_i |A[i] hi[i]| + |B[i] lo[i]|: a coefficient has G roundings (G heads), a
+// lane chains at most 8 products and 5 levels join the lanes, so a score is off by
+// less than (G + 14) u mag (u = 2^-24), taken as eps = (G + 20) u max(mag).  With t the
 // FP32 score of the last page to be taken, pages above t + 2 eps are in and those
 // below t - 2 eps are out whatever the rounding; usually nothing but that page
 // lies between.  Otherwise the pages between are scored again as unevaluated sums
@@ -31,9 +31,8 @@
 // atomics in shared memory: their order cannot change the counts).  Ties go to
 // the lowest pages.
 //
-// Measured (GB300, cold L2): the two-FP32-number sum for every page cost 135
-// instructions a page and bound the score kernel by issue (28 us for 131072
-// page scores of 512 bytes, 10 us of HBM time).
+// Summing every page as two FP32 numbers cost 135 instructions a page (28 us for
+// the same 131072 scores).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -255,13 +254,12 @@ struct SelectParams {
     float* scores;              // [B][Hkv][stride]: FP32 scores
     float* mags;                // [B][Hkv][stride / 8]: largest sum of term magnitudes of 8 pages
     float2* exact;              // [B][Hkv][pages]: the pages FP32 cannot rank, as two FP32 numbers
-    float2* coef;               // [B][Hkv][2 d]: the coefficients, as two FP32 numbers
     int* err;
     int B, Hq, Hkv, G, S, pages;  // pages: most pages a row can have
     int stride;                 // pages rounded up to 32
     int num_select, first, last;
     int max_pages, page_shift, num_pages;
-    int per_block;              // pages a block scores
+    int per_block, hb;          // pages a block scores, KV heads it does so for
 };
 
 constexpr int kScoreThreads = 256;
@@ -275,30 +273,53 @@ __device__ __forceinline__ void two_sum(float a, float b, float* s, float* e) {
     *s = t;
 }
 
-template <typename TQ>
-__device__ __forceinline__ float q_value(const void* q, size_t i) {
-    if constexpr (std::is_same<TQ, float>::value)
-        return static_cast<const float*>(q)[i];
-    else
-        return __bfloat162float(static_cast<const __nv_bfloat16*>(q)[i]);
-}
-
 // Coefficient i of (row b, KV head g) as the sum of two FP32 numbers: i < D for
 // the minima, then for the maxima.
 template <int D, typename TQ>
 __device__ __forceinline__ float2 coefficient(const SelectParams& p, int b, int g, int i) {
     const bool up = i >= D;
-    const size_t at = (static_cast<size_t>(b) * p.Hq + g * p.G) * D + (up ? i - D : i);
+    const TQ* q = static_cast<const TQ*>(p.q) + (static_cast<size_t>(b) * p.Hq + g * p.G) * D + (up ? i - D : i);
     float s = 0.f, e = 0.f;
 #pragma unroll 4
     for (int h = 0; h < p.G; ++h) {
-        const float x = q_value<TQ>(p.q, at + static_cast<size_t>(h) * D);
+        const float x = static_cast<float>(q[static_cast<size_t>(h) * D]);
         float err;
         // (a NaN must stay one: fmaxf and fminf would drop it)
         two_sum(s, (up ? x > 0.f : x < 0.f) || x != x ? x : 0.f, &s, &err);
         e = __fadd_rn(e, err);
     }
     return make_float2(s, e);
+}
+
+// A lane's coefficients in FP32, G roundings each: lanes 0 .. 15 those of the minima,
+// the others those of the maxima, E = D / 16 channels each.  (Short on purpose: this
+// runs once per warp, and instruction fetches of a longer version cost 3.6 us.)
+template <int D, typename TQ>
+__device__ __forceinline__ void coefficients(const SelectParams& p, int b, int g, int lane, float (&c)[D / 16]) {
+    constexpr int E = D / 16;
+    const float sign = lane >= 16 ? 1.f : -1.f;
+    const TQ* q = static_cast<const TQ*>(p.q) + (static_cast<size_t>(b) * p.Hq + g * p.G) * D + (lane & 15) * E;
+#pragma unroll
+    for (int i = 0; i < E; ++i) c[i] = 0.f;
+#pragma unroll 4
+    for (int h = 0; h < p.G; ++h) {
+#pragma unroll
+        for (int i = 0; i < E; i += 4) {
+            float x[4];
+            if constexpr (std::is_same<TQ, float>::value) {
+                const float4 v = *reinterpret_cast<const float4*>(q + h * D + i);
+                x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+            } else {
+                const uint2 v = *reinterpret_cast<const uint2*>(q + h * D + i);
+                x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xffff0000u);
+                x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xffff0000u);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) c[i + k] += Range<float>::fmax_nan(sign * x[k], 0.f);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) c[i] *= sign;
 }
 
 // A lane's share of one page's bounds.
@@ -320,6 +341,18 @@ struct PageBounds {
             }
         }
     }
+    __device__ __forceinline__ void take(const uint8_t* smem) {  // from shared memory
+        if constexpr (W == 2) {
+            const uint2 v = *reinterpret_cast<const uint2*>(smem);
+            w[0] = v.x; w[1] = v.y;
+        } else {
+#pragma unroll
+            for (int x = 0; x < W / 4; ++x) {
+                const uint4 v = reinterpret_cast<const uint4*>(smem)[x];
+                w[4 * x] = v.x; w[4 * x + 1] = v.y; w[4 * x + 2] = v.z; w[4 * x + 3] = v.w;
+            }
+        }
+    }
     __device__ __forceinline__ float operator[](int i) const {
         if constexpr (kF32)
             return __uint_as_float(w[i]);
@@ -328,62 +361,107 @@ struct PageBounds {
     }
 };
 
-// Pages [blockIdx.x * per_block, ..) of (KV head blockIdx.y, row blockIdx.z).  A warp
-// takes 8 pages at a time; a lane holds the coefficients of its channels.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+    if constexpr (BYTES == 8) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < BYTES; i += 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst) + i),
+                         "l"(static_cast<const uint8_t*>(src) + i)
+                         : "memory");
+    }
+}
+
+// A warp's ring of page groups (8 pages of bounds each) in shared memory.
+template <int D, typename TB>
+struct ScoreRing {
+    static constexpr int kLane = PageBounds<D, TB>::E * static_cast<int>(sizeof(TB));  // bytes a lane: 8, 16 or 32
+    static constexpr int kGroup = 8 * 32 * kLane;
+    static constexpr int kStages = 2;
+    static constexpr int kSmem = kScoreWarps * kStages * kGroup;  // 32, 64 or 128 KB
+    static constexpr int kBlocks = kLane == 32 ? 1 : 3;           // an SM
+};
+
+// Pages [blockIdx.x * per_block, ..) of row blockIdx.z for HB KV heads: warp w takes
+// head blockIdx.y HB + w % HB, 8 pages at a time.  The bounds arrive by cp.async a
+// group ahead; each lane reads only what it copied, so waiting for its own copies is
+// enough, and there is no barrier at all.  Issue and HBM bind it about equally:
+// some 60 instructions a page and head, 13.5 us for 131072 page scores (67 MB, 9.9 us
+// at the copy rate; the ring against loads into registers: 14.3).
 template <int D, typename TQ, typename TB>
-__global__ void __launch_bounds__(kScoreThreads, std::is_same<TB, float>::value ? 2 : 4) page_score_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kScoreThreads, ScoreRing<D, TB>::kBlocks) page_score_kernel(const SelectParams p) {
     using PB = PageBounds<D, TB>;
-    constexpr int E = PB::E;
-    __shared__ float coef[2 * D];
+    using Ring = ScoreRing<D, TB>;
+    constexpr int E = PB::E, kStages = Ring::kStages;
+    extern __shared__ __align__(16) uint8_t ring_all[];
     wait_primary();
     allow_dependents();
-    const int g = blockIdx.y, b = blockIdx.z;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = blockIdx.y * p.hb + warp % p.hb, b = blockIdx.z;
+    if (g >= p.Hkv) return;
     const int N = p.seqlens[b];
     const int p0 = blockIdx.x * p.per_block, pmax = min(p.pages, p0 + p.per_block);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.max_pages;
     float* scores = p.scores + (static_cast<int64_t>(b) * p.Hkv + g) * p.stride;
     float* mags = p.mags + (static_cast<int64_t>(b) * p.Hkv + g) * (p.stride / 8);
     const TB* bounds = static_cast<const TB*>(p.bounds) + static_cast<int64_t>(g) * 2 * D + lane * E;
-    auto lookup = [&](int q0) { return (lane < 8 && q0 + lane < pmax) ? __ldg(table + q0 + lane) : -1; };
-    // the length and the first pages' numbers are on their way while the coefficients are summed
-    int q0 = p0 + warp * 8;
-    int phys = lookup(q0);
-    for (int i = threadIdx.x; i < 2 * D; i += kScoreThreads) {
-        const float2 c = coefficient<D, TQ>(p, b, g, i);
-        coef[i] = __fadd_rn(c.x, c.y);
-        if (blockIdx.x == 0) p.coef[(static_cast<int64_t>(b) * p.Hkv + g) * 2 * D + i] = c;
-    }
-    if (N < 0 || N > p.S) return;                     // the selection reports it
-    const int n = static_cast<int>((static_cast<int64_t>(N) + (1 << p.page_shift) - 1) >> p.page_shift);
-    const int p1 = min(n, pmax);
-    if (n <= p.num_select || p0 >= n) return;         // every page is taken, or no page here
-    __syncthreads();
-    float c[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) c[i] = coef[lane * E + i];
-    while (q0 < p1) {
+    uint8_t* ring = ring_all + warp * kStages * Ring::kGroup + lane * Ring::kLane;
+    const int kStep = kScoreWarps / p.hb * 8;
+    auto lookup = [&](int q) { return (lane < 8 && q + lane < pmax) ? __ldg(table + q + lane) : -1; };
+    // start the copies of one group into `stage`; which of its pages are in the pool
+    auto issue = [&](int phys, int stage) -> unsigned {
         const unsigned ok = __ballot_sync(0xffffffffu, phys >= 0 && phys < p.num_pages);
-        PB x[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int ph = __shfl_sync(0xffffffffu, phys, j);
-            x[j].load(bounds + (((ok >> j) & 1u) ? static_cast<int64_t>(ph) * p.Hkv * 2 * D : 0));
+            if ((ok >> j) & 1u)
+                copy_async<Ring::kLane>(ring + stage * Ring::kGroup + j * 32 * Ring::kLane,
+                                        bounds + static_cast<int64_t>(ph) * p.Hkv * 2 * D);
         }
-        const int next = q0 + kScoreWarps * 8;
-        phys = lookup(next);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        return ok;
+    };
+    // the first groups are on their way while the length arrives and the coefficients are summed
+    int q0 = p0 + warp / p.hb * 8;
+    unsigned ok[kStages] = {};
+    {
+        int phys[kStages - 1];
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) phys[i] = lookup(q0 + i * kStep);
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) ok[i] = issue(phys[i], i);
+    }
+    int phys = lookup(q0 + (kStages - 1) * kStep);
+    float c[E];
+    coefficients<D, TQ>(p, b, g, lane, c);
+    const bool bad = N < 0 || N > p.S;                // the selection reports it
+    const int n = bad ? 0 : static_cast<int>((static_cast<int64_t>(N) + (1 << p.page_shift) - 1) >> p.page_shift);
+    const int p1 = n <= p.num_select ? 0 : min(n, pmax);  // 0: every page is taken
+    for (int stage = 0; q0 < p1; q0 += kStep) {
+        const int into = stage == 0 ? kStages - 1 : stage - 1;
+        ok[kStages - 1] = issue(phys, into);          // the stage read in the last step
+        phys = lookup(q0 + kStages * kStep);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        const unsigned here = ok[0];
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) ok[i] = ok[i + 1];
         float s[8], m[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
+            PB x;
+            x.take(ring + stage * Ring::kGroup + j * 32 * Ring::kLane);
             s[j] = 0.f;
             m[j] = 0.f;
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                const float v = x[j][i];
+                const float v = x[i];
                 s[j] = fmaf(c[i], v, s[j]);
                 m[j] = fmaf(fabsf(c[i]), fabsf(v), m[j]);
             }
         }
+        stage = stage == kStages - 1 ? 0 : stage + 1;
         // 8 pages over 32 lanes: halve the pages held three times, then the lanes
 #pragma unroll
         for (int st = 0; st < 3; ++st) {
@@ -404,13 +482,14 @@ __global__ void __launch_bounds__(kScoreThreads, std::is_same<TB, float>::value 
         }
         const int mine = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
         const bool mine_in = q0 + mine < p1;
-        const bool fin = ((ok >> mine) & 1u) && fabsf(s[0]) < INFINITY;
+        // (a page outside the pool: its sums are of whatever the ring held, and are not used)
+        const bool fin = ((here >> mine) & 1u) && fabsf(s[0]) < INFINITY;
         if ((lane & 3) == 0 && mine_in) scores[q0 + mine] = fin ? s[0] + 0.f : INFINITY;  // + 0: one zero
         // (magnitudes are not negative, so their bits are ordered; NaN last)
         const uint32_t big = __reduce_max_sync(0xffffffffu, mine_in && fin ? __float_as_uint(m[0]) : 0u);
         if (lane == 0) mags[q0 >> 3] = __uint_as_float(big);
-        q0 = next;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");  // no copy outlives the block
 }
 
 // ---------------------------------------------------------------- selection
@@ -459,7 +538,7 @@ __device__ uint32_t radix_pick(int n4, int need, uint32_t first, int bits, int* 
         const uint32_t mask = (1u << width) - 1;
         reinterpret_cast<int4*>(hist)[threadIdx.x] = make_int4(0, 0, 0, 0);
         __syncthreads();
-#pragma unroll 2
+#pragma unroll 1
         for (int i = threadIdx.x; i < n4; i += kPickThreads) {
             const uint4 q = key4(i);
             const uint32_t k[4] = {q.x, q.y, q.z, q.w};
@@ -552,7 +631,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
     auto key = [&](int i) { return kept ? keys_kept[i] : (i >= lo && i < hi ? ordered(__ldcg(sc + i)) : 0u); };
     if (need > 0) {
         uint32_t kmin = 0xffffffffu, kmax = 0, mag = 0;
-#pragma unroll 2
+#pragma unroll 1
         for (int i = threadIdx.x; i < n4; i += kPickThreads) {
             const uint4 k = scored4(i);
             if (kept) reinterpret_cast<uint4*>(keys_kept)[i] = k;
@@ -574,12 +653,12 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
         int above;
         const uint32_t last = radix_pick(n4, need, kmax, 32 - __clz(kmin ^ kmax), hist, tot, found, key4, &above);
         // 2 eps, and the range around the last page that FP32 cannot tell apart
-        const float t = unordered(last), e2 = fmaf(__uint_as_float(mag), 40.f * 5.9604645e-8f, 1e-40f);
+        const float t = unordered(last), e2 = fmaf(__uint_as_float(mag), (2 * p.G + 40) * 5.9604645e-8f, 1e-40f);
         const float tu = t + e2, tl = t - e2;
         top = tu == tu ? ordered(tu) : 0xffffffffu;
         low = tl == tl ? ordered(tl) : 1u;
         int over = 0, between = 0;
-#pragma unroll 2
+#pragma unroll 1
         for (int i = threadIdx.x; i < n4; i += kPickThreads) {
             const uint4 k = key4(i);
             over += (k.x > top) + (k.y > top) + (k.z > top) + (k.w > top);
@@ -590,10 +669,13 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
         const int n_over = all.x, n_between = all.y - all.x;
         if (need - n_over < n_between) {
             // Score the pages between again, a warp a page.
+            __shared__ float2 coef[2 * D];
+            if (threadIdx.x < 2 * D) coef[threadIdx.x] = coefficient<D, TQ>(p, b, g, threadIdx.x);
+            __syncthreads();
             float2 c[PB::E];
 #pragma unroll
             for (int j = 0; j < PB::E; ++j) {
-                c[j] = p.coef[row * 2 * D + lane * PB::E + j];
+                c[j] = coef[lane * PB::E + j];
                 if constexpr (!PB::kF32) {
                     const float cut = __uint_as_float(__float_as_uint(c[j].x) & 0xffffff00u);
                     c[j] = make_float2(cut, __fadd_rn(__fsub_rn(c[j].x, cut), c[j].y));
@@ -712,11 +794,11 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
                    (takes(i, 3, k.w) ? 8u : 0u);
         };
         int taken = 0;
-#pragma unroll 2
+#pragma unroll 1
         for (int i = i0; i < i1; i += 32) taken += __popc(flags(i + lane));
         warp_sums(__reduce_add_sync(0xffffffffu, taken), 0, sums, &before, &all);
         int at = before.x;
-#pragma unroll 2
+#pragma unroll 1
         for (int i = i0; i < i1; i += 32) {
             unsigned f = flags(i + lane);
             const int c = __popc(f);  // 0 .. 4: its prefix sum from its three bits
@@ -765,14 +847,14 @@ int pages_of(const ta_shape* s, int page_shift) {
     return static_cast<int>((static_cast<int64_t>(s->max_seqlen) + (int64_t(1) << page_shift) - 1) >> page_shift);
 }
 
-// Workspace: scores [rows][stride], magnitudes [rows][stride / 8], exact sums
-// [rows][pages] and coefficients [rows][2 d], rows = B * Hkv.
+// Workspace: scores [rows][stride], magnitudes [rows][stride / 8] and exact sums
+// [rows][pages], rows = B * Hkv.
 int score_stride(int pages) { return (pages + 31) / 32 * 32; }
 
 size_t select_bytes(const ta_shape* s, int page_shift) {
     const size_t rows = static_cast<size_t>(s->batch) * s->num_kv_heads, pages = pages_of(s, page_shift);
     const size_t stride = (pages + 31) / 32 * 32;
-    return rows * (stride * sizeof(float) + stride / 8 * sizeof(float) + (pages + 2 * s->head_dim) * sizeof(float2));
+    return rows * (stride * sizeof(float) + stride / 8 * sizeof(float) + pages * sizeof(float2));
 }
 
 template <typename Kernel, typename Params>
@@ -793,13 +875,18 @@ int launch_select(SelectParams p, const DeviceInfo& dev, cudaStream_t s) {
     static std::atomic<unsigned long long> configured{0};
     if (set_smem_once(page_pick_kernel<D, TQ, TB>, kPickKeep * 4, configured) != cudaSuccess) return TA_ERR_CUDA;
     if (p.pages > p.num_select) {  // else every page is listed
-        // a block's 8 warps take 8 pages each at a time; one wave of four blocks an SM
-        const int64_t all = static_cast<int64_t>(p.B) * p.Hkv * p.pages, wave = 4 * static_cast<int64_t>(dev.num_sms);
-        const int step = kScoreWarps * 8;
-        const int per = static_cast<int>(std::max<int64_t>(1, (all + wave * step - 1) / (wave * step))) * step;
-        p.per_block = per;
-        const dim3 grid((p.pages + per - 1) / per, p.Hkv, p.B);
-        if (launch(page_score_kernel<D, TQ, TB>, grid, kScoreThreads, 0, p, s) != cudaSuccess) return TA_ERR_CUDA;
+        // the blocks of all rows fill the device once, 8 pages a warp each at least
+        using Ring = ScoreRing<D, TB>;
+        static std::atomic<unsigned long long> score_configured{0};
+        if (set_smem_once(page_score_kernel<D, TQ, TB>, Ring::kSmem, score_configured) != cudaSuccess) return TA_ERR_CUDA;
+        p.hb = p.Hkv >= 8 ? 8 : (p.Hkv >= 4 ? 4 : (p.Hkv >= 2 ? 2 : 1));
+        const int step = kScoreWarps / p.hb * 8;
+        const int64_t rows = static_cast<int64_t>(p.B) * ((p.Hkv + p.hb - 1) / p.hb);
+        const int64_t per_row = std::max<int64_t>(1, Ring::kBlocks * static_cast<int64_t>(dev.num_sms) / rows);
+        const int64_t per = std::max<int64_t>(step, ((p.pages + per_row - 1) / per_row + 7) / 8 * 8);
+        p.per_block = static_cast<int>(std::min<int64_t>(per, (static_cast<int64_t>(p.pages) + 7) / 8 * 8));
+        const dim3 grid((p.pages + p.per_block - 1) / p.per_block, (p.Hkv + p.hb - 1) / p.hb, p.B);
+        if (launch(page_score_kernel<D, TQ, TB>, grid, kScoreThreads, Ring::kSmem, p, s) != cudaSuccess) return TA_ERR_CUDA;
     }
     const int smem = p.pages > p.num_select ? std::min(p.stride, kPickKeep) * 4 : 0;
     return launch(page_pick_kernel<D, TQ, TB>, dim3(p.Hkv, p.B, 1), kPickThreads, smem, p, s) == cudaSuccess ? TA_OK : TA_ERR_CUDA;
@@ -908,7 +995,6 @@ extern "C" int tree_attn_select_pages(const ta_shape* shape, const ta_paged_kv* 
     p.scores = static_cast<float*>(workspace);
     p.mags = p.scores + rows * p.stride;
     p.exact = reinterpret_cast<float2*>(p.mags + rows * (p.stride / 8));
-    p.coef = p.exact + rows * p.pages;
     p.num_select = num_select;
     p.first = first_pages;
     p.last = last_pages;

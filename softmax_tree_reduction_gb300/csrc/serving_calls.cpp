@@ -10,11 +10,13 @@
 // TypeError for arguments the descriptors cannot express, and returns the C
 // call's status.  C++ exceptions stop at the boundary.
 #include <Python.h>
+#include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstring>
 #include <stdexcept>
 #include <string>
@@ -430,9 +432,10 @@ PyObject* select_workspace_bytes(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* select_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 12, [&] {
         const Tensor &q = need(a[0], "q"), &b = need(a[1], "bounds"), &bt = need(a[2], "block_table"), &len = need(a[3], "seqlens"),
-                     &sel = need(a[8], "selected"), &ws = need(a[9], "workspace");
+                     &sel = need(a[8], "selected");
+        const Tensor* given = opt(a[9], "workspace");
         Device dev;
-        for (const Tensor* t : {&q, &b, &bt, &len, &sel, &ws}) dev.add(t);
+        for (const Tensor* t : {&q, &b, &bt, &len, &sel, given}) dev.add(t);
         ta_shape s;
         ta_paged_kv pg;
         select_shape(b, bt, a[4], a[10], &s, &pg);
@@ -443,9 +446,14 @@ PyObject* select_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (sel.scalar_type() != at::kInt || sel.dim() != 3 || sel.size(0) != s.batch || sel.size(1) != s.num_kv_heads || sel.size(2) != ns ||
             !sel.is_contiguous())
             throw BadValue("selected must be a contiguous int32 [B, Hkv, num_select] tensor");
-        if (!ws.is_contiguous()) throw BadValue("workspace must be contiguous");
         const int32_t* pl = ints(&len, "seqlens", s.batch);
         void* st = dev.stream(a[11]);
+        if (given && !given->is_contiguous()) throw BadValue("workspace must be contiguous");
+        if (!given && a[11] != Py_None) throw BadValue("a workspace is needed with a stream");
+        // (from torch's allocator for the current stream, which the call runs on)
+        const Tensor ws = given ? *given
+                                : at::empty({static_cast<int64_t>(std::max<size_t>(16, p_select_workspace_bytes(&s, &pg)))},
+                                            q.options().dtype(at::kByte));
         return enqueue([&] {
             return p_select_pages(&s, &pg, q.data_ptr(), b.data_ptr(), pl, ns, first, last, static_cast<int32_t*>(sel.data_ptr()), ws.data_ptr(),
                                   ws.nbytes(), st);

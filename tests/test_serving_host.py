@@ -111,7 +111,7 @@ def test_page_call_refusals(ta):
     assert select(first=2**31 - 1, last=2**31 - 1) == -3
     assert select(ws=None) == -6 and select(ws=0x4008) == -2
     need = lib.tree_attn_select_workspace_bytes(ref_of(shape(ta)), ref_of(pg))
-    assert need == 2 * 2 * (32 * 4 + 4 * 4 + (16 + 2 * 128) * 8) and select(wsb=need - 1) == -6
+    assert need == 2 * 2 * (32 * 4 + 4 * 4 + 16 * 8) and select(wsb=need - 1) == -6
     assert ta.tree_attn_select_workspace_bytes(2, 2, 16) == need
     assert lib.tree_attn_select_workspace_bytes(ref_of(shape(ta, head_dim=32)), ref_of(pg)) == 0
     assert select(s=shape(ta, q_dtype=2)) == -4
