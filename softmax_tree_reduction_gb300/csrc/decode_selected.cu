@@ -35,8 +35,6 @@
 namespace ta {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kSelThreads = 32 * kWarps;
 constexpr int kMaxCluster = 16;
 constexpr int kSlab = 16;           // tokens
 constexpr float kPScale = 16384.f;  // 2^14: P's FP16 hi + lo parts keep small weights (E4M3 caches)
@@ -133,6 +131,16 @@ struct SlabList {
     }
 };
 
+// Pairwise sum of N values.
+template <int N>
+__device__ __forceinline__ float sum_of(const float* v) {
+    if constexpr (N == 1) {
+        return v[0];
+    } else {
+        return sum_of<N / 2>(v) + sum_of<N - N / 2>(v + N / 2);
+    }
+}
+
 // Mailbox of a block: what the cluster's blocks have sent it of their merged
 // states.  Not part of the rings: a block may still be streaming when another
 // sends.
@@ -156,10 +164,10 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // reads a peer's memory.  The caller has arrived once at the cluster's barrier
 // when it started.  kFp8: numerators of channel c sit at (c % 16) * 8 + c / 16 and
 // still lack V's scale.
-template <int D, int kCols, bool kFp8>
+template <int D, int kWarps, int kCols, bool kFp8>
 __device__ void finish_list(const SelParams& p, int b, int hq0, int ncol, float vscale, const float* mg_o,
                             const float* mg_m, const float* mg_l, Mailbox<D, kCols>* box, bool poison) {
-    constexpr int MS = D + 4;
+    constexpr int MS = D + 4, kThreads = 32 * kWarps;
     const int tid = threadIdx.x;
     const float nan = __int_as_float(0x7fc00000);
     const size_t row0 = static_cast<size_t>(b) * p.Hq + hq0;
@@ -167,7 +175,7 @@ __device__ void finish_list(const SelParams& p, int b, int hq0, int ncol, float 
     const int rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
     if (C > 1) cluster_wait();  // every block of the cluster has started
 #pragma unroll 1
-    for (int idx = tid; idx < items; idx += kSelThreads) {
+    for (int idx = tid; idx < items; idx += kThreads) {
         const int h = idx / D, dd = idx - h * D;
         const int pos = kFp8 ? (dd % 16) * 8 + dd / 16 : dd;
         float mw[kWarps], M = -INFINITY;
@@ -184,8 +192,8 @@ __device__ void finish_list(const SelParams& p, int b, int hq0, int ncol, float 
             ow[w] = wt * mg_o[(w * kCols + h) * MS + pos];
             lw[w] = wt * mg_l[w * kCols + h];
         }
-        float o = tree_sum<kWarps>(ow);
-        float l = tree_sum<kWarps>(lw);
+        float o = sum_of<kWarps>(ow);
+        float l = sum_of<kWarps>(lw);
         if (kFp8) o *= vscale;
         if (poison) o = l = M = nan;
         if (C > 1) {
@@ -205,7 +213,7 @@ __device__ void finish_list(const SelParams& p, int b, int hq0, int ncol, float 
     cluster_arrive();
     cluster_wait();
     const int n = min(share, items - rank * share);
-    for (int i = tid; i < n; i += kSelThreads) {
+    for (int i = tid; i < n; i += kThreads) {
         const int idx = rank * share + i, h = idx / D, dd = idx - h * D;
         float2 ml[kMaxCluster];
         float o[kMaxCluster], M = -INFINITY;
@@ -230,7 +238,7 @@ __device__ void finish_list(const SelParams& p, int b, int hq0, int ncol, float 
 }
 
 // ------------------------------------------------------------ tensor cores
-template <int D, bool kFp8>
+template <int D, bool kFp8, int W>
 struct SelCfg {
     static constexpr int kRowBytes = kFp8 ? D : 2 * D;
     static constexpr int kChunks = kRowBytes / 16;            // 16-byte chunks per row
@@ -242,7 +250,9 @@ struct SelCfg {
     static constexpr int kSub = kFp8 ? 2 : 1;
     static constexpr int kPairBytes = 2 * kSlabBytes;         // keys, values
     static constexpr int kStageBytes = kSub * kPairBytes;
-    static constexpr int kStages = 24576 / kStageBytes;       // 24 KB a warp, one block an SM
+    static constexpr int kWarps = W;  // 192 KB of rings, one block an SM
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kStages = 196608 / kWarps / kStageBytes;
     static constexpr int kCols = 16;
     static constexpr int kRing = kWarps * kStages * kStageBytes;
     static constexpr int kBoxOff = kRing + kWarps * kStages * kSub * 4 + 16;
@@ -250,13 +260,13 @@ struct SelCfg {
     static constexpr int kSmem = kBoxOff + static_cast<int>(sizeof(Mailbox<D, kCols>));
     // merge buffers reuse the ring
     static_assert(kWarps * kCols * (D + 4 + 2) * 4 <= kRing, "merge buffers");
-    static_assert(kStages >= 3 && kSmem <= 227 * 1024, "ring");
+    static_assert(kStages >= 2 && kSmem <= 227 * 1024, "ring");
 };
 
-template <int D, int NT, bool kFp8>
-__global__ void __launch_bounds__(kSelThreads, 1) decode_selected_kernel(const SelParams p) {
-    using Cf = SelCfg<D, kFp8>;
-    constexpr int J = Cf::kSub;
+template <int D, int NT, bool kFp8, int W>
+__global__ void __launch_bounds__(SelCfg<D, kFp8, W>::kThreads, 1) decode_selected_kernel(const SelParams p) {
+    using Cf = SelCfg<D, kFp8, W>;
+    constexpr int J = Cf::kSub, kWarps = W;
     extern __shared__ __align__(128) uint8_t smem[];
     int* nvs_all = reinterpret_cast<int*>(smem + Cf::kRing);
     int* bad_flag = nvs_all + kWarps * Cf::kStages * J;
@@ -607,7 +617,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) decode_selected_kernel(const S
         }
     }
     __syncthreads();
-    finish_list<D, kCols, kFp8>(p, b, hq0, ncol, vscale, mg_o, mg_m, mg_l,
+    finish_list<D, kWarps, kCols, kFp8>(p, b, hq0, ncol, vscale, mg_o, mg_m, mg_l,
                                 reinterpret_cast<Mailbox<D, kCols>*>(smem + Cf::kBoxOff), bad_len || *bad_flag);
 }
 
@@ -615,8 +625,11 @@ __global__ void __launch_bounds__(kSelThreads, 1) decode_selected_kernel(const S
 // CUDA cores (BF16 operands would lose the FP32 tolerance).  Eight lanes hold
 // a token's channels, four tokens a warp step, straight from global memory;
 // each eight-lane group keeps a running state for GC query heads.
+constexpr int kF32Warps = 8;
+
 template <int D, int GC>
-__global__ void __launch_bounds__(kSelThreads) decode_selected_f32_kernel(const SelParams p) {
+__global__ void __launch_bounds__(32 * kF32Warps) decode_selected_f32_kernel(const SelParams p) {
+    constexpr int kWarps = kF32Warps;
     constexpr int J = D / 32;  // float4 per lane: channels 4 (l8 + 8 j) ..
     constexpr int MS = D + 4;
     __shared__ __align__(16) float qs[GC][D];
@@ -632,7 +645,7 @@ __global__ void __launch_bounds__(kSelThreads) decode_selected_f32_kernel(const 
     wait_primary();
     allow_dependents();
     if (threadIdx.x == 0) bad_flag = 0;
-    for (int i = threadIdx.x; i < GC * D; i += kSelThreads)
+    for (int i = threadIdx.x; i < GC * D; i += 32 * kWarps)
         qs[i / D][i % D] = i / D < ncol
                                ? static_cast<const float*>(p.q)[(static_cast<size_t>(b) * p.Hq + hq0) * D + i] * p.scale_log2
                                : 0.f;
@@ -730,7 +743,7 @@ __global__ void __launch_bounds__(kSelThreads) decode_selected_f32_kernel(const 
         }
     }
     __syncthreads();
-    finish_list<D, GC, false>(p, b, hq0, ncol, 1.f, mg_o, mg_m, mg_l, &box, bad_len || bad_flag);
+    finish_list<D, kWarps, GC, false>(p, b, hq0, ncol, 1.f, mg_o, mg_m, mg_l, &box, bad_len || bad_flag);
 }
 
 // ---------------------------------------------------------------- host side
@@ -746,7 +759,7 @@ struct Instance {
 };
 
 template <typename Kernel>
-int prepare_instance(Kernel kernel, int smem, int device, Instance* inst) {
+int prepare_instance(Kernel kernel, int warps, int smem, int device, Instance* inst) {
     std::lock_guard<std::mutex> lock(inst->mu);
     if (inst->ready[device]) return TA_OK;
     if (smem > 0 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
@@ -755,7 +768,7 @@ int prepare_instance(Kernel kernel, int smem, int device, Instance* inst) {
     for (int c = 1; c <= kMaxCluster; ++c) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(c, 1, 1);
-        cfg.blockDim = dim3(kSelThreads, 1, 1);
+        cfg.blockDim = dim3(32 * warps, 1, 1);
         cfg.dynamicSmemBytes = smem;
         cudaLaunchAttribute a = {};
         a.id = cudaLaunchAttributeClusterDimension;
@@ -778,22 +791,22 @@ int prepare_instance(Kernel kernel, int smem, int device, Instance* inst) {
 // resident at once (how many clusters of a size fit depends on the GPCs: on
 // GB300, with one block an SM, 36 of 4 blocks but only 15 of 7 or 8); one block
 // when there are more lists than that.
-int pick_cluster(int64_t lists, int64_t slabs, const int* fit) {
+int pick_cluster(int64_t lists, int64_t slabs, int warps, const int* fit) {
     int c = 1;
     for (int n = 2; n <= kMaxCluster; ++n)
-        if (slabs >= static_cast<int64_t>(n) * kWarps && lists <= fit[n]) c = n;
+        if (slabs >= static_cast<int64_t>(n) * warps && lists <= fit[n]) c = n;
     return c;
 }
 
 template <typename Kernel>
-int launch_selected(Kernel kernel, int smem, Instance* inst, int device, SelParams p, int batch, cudaStream_t stream) {
-    const int rc = prepare_instance(kernel, smem, device, inst);
+int launch_selected(Kernel kernel, int warps, int smem, Instance* inst, int device, SelParams p, int batch, cudaStream_t stream) {
+    const int rc = prepare_instance(kernel, warps, smem, device, inst);
     if (rc != TA_OK) return rc;
     const int64_t lists = static_cast<int64_t>(batch) * p.Hkv * p.ngroups;
-    p.C = pick_cluster(lists, static_cast<int64_t>(p.num_select) << (p.page_shift - 4), inst->clusters[device]);
+    p.C = pick_cluster(lists, static_cast<int64_t>(p.num_select) << (p.page_shift - 4), warps, inst->clusters[device]);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.C, p.Hkv * p.ngroups, batch);
-    cfg.blockDim = dim3(kSelThreads, 1, 1);
+    cfg.blockDim = dim3(32 * warps, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -807,16 +820,30 @@ int launch_selected(Kernel kernel, int smem, Instance* inst, int device, SelPara
     return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? TA_OK : TA_ERR_CUDA;
 }
 
-template <int D, int NT, bool kFp8>
-int launch_mma(int device, const SelParams& p, int batch, cudaStream_t s) {
+template <int D, int NT, bool kFp8, int W>
+int launch_mma_warps(int device, const SelParams& p, int batch, cudaStream_t s) {
     static Instance inst;
-    return launch_selected(decode_selected_kernel<D, NT, kFp8>, SelCfg<D, kFp8>::kSmem, &inst, device, p, batch, s);
+    return launch_selected(decode_selected_kernel<D, NT, kFp8, W>, W, SelCfg<D, kFp8, W>::kSmem, &inst, device, p, batch, s);
+}
+
+// BF16: 12 warps with two stages each hide more of each other's chains than 8 with
+// three once every warp of the device has some 8 slabs (256 pages of 64 tokens in 32
+// lists: 44.6 against 46.3 us; 2048: 299 against 315), but short lists pay for merging
+// more states (16 pages in 8 lists: 7.0 against 6.1 us).  E4M3 slabs come in pairs with
+// a longer chain and want the third stage (64 pages in 8 lists: 7.1 against 7.4 us).
+template <int D, int NT, bool kFp8>
+int launch_mma(const DeviceInfo& dev, const SelParams& p, int batch, cudaStream_t s) {
+    if constexpr (!kFp8) {
+        const int64_t slabs = static_cast<int64_t>(batch) * p.Hkv * p.ngroups * p.num_select << (p.page_shift - 4);
+        if (slabs >= 12 * 8 * static_cast<int64_t>(dev.num_sms)) return launch_mma_warps<D, NT, kFp8, 12>(dev.device, p, batch, s);
+    }
+    return launch_mma_warps<D, NT, kFp8, 8>(dev.device, p, batch, s);
 }
 
 template <int D, int GC>
 int launch_f32(int device, const SelParams& p, int batch, cudaStream_t s) {
     static Instance inst;
-    return launch_selected(decode_selected_f32_kernel<D, GC>, 0, &inst, device, p, batch, s);
+    return launch_selected(decode_selected_f32_kernel<D, GC>, kF32Warps, 0, &inst, device, p, batch, s);
 }
 
 }  // namespace
@@ -877,16 +904,16 @@ extern "C" int tree_attn_decode_selected(const ta_shape* shape, const ta_paged_k
     const float scale = shape->scale > 0.f ? shape->scale : 1.0f / std::sqrt(static_cast<float>(shape->head_dim));
     p.scale_log2 = scale * kLog2e;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int B = shape->batch, d = dev.device;
+    const int B = shape->batch;
     const bool two = G > 8, d128 = shape->head_dim == 128;
-    if (fp8) return two ? launch_mma<128, 2, true>(d, p, B, s) : launch_mma<128, 1, true>(d, p, B, s);
+    if (fp8) return two ? launch_mma<128, 2, true>(dev, p, B, s) : launch_mma<128, 1, true>(dev, p, B, s);
     if (!f32) {
-        if (d128) return two ? launch_mma<128, 2, false>(d, p, B, s) : launch_mma<128, 1, false>(d, p, B, s);
-        return two ? launch_mma<64, 2, false>(d, p, B, s) : launch_mma<64, 1, false>(d, p, B, s);
+        if (d128) return two ? launch_mma<128, 2, false>(dev, p, B, s) : launch_mma<128, 1, false>(dev, p, B, s);
+        return two ? launch_mma<64, 2, false>(dev, p, B, s) : launch_mma<64, 1, false>(dev, p, B, s);
     }
     switch (cols) {
-        case 1: return d128 ? launch_f32<128, 1>(d, p, B, s) : launch_f32<64, 1>(d, p, B, s);
-        case 2: return d128 ? launch_f32<128, 2>(d, p, B, s) : launch_f32<64, 2>(d, p, B, s);
-        default: return d128 ? launch_f32<128, 4>(d, p, B, s) : launch_f32<64, 4>(d, p, B, s);
+        case 1: return d128 ? launch_f32<128, 1>(dev.device, p, B, s) : launch_f32<64, 1>(dev.device, p, B, s);
+        case 2: return d128 ? launch_f32<128, 2>(dev.device, p, B, s) : launch_f32<64, 2>(dev.device, p, B, s);
+        default: return d128 ? launch_f32<128, 4>(dev.device, p, B, s) : launch_f32<64, 4>(dev.device, p, B, s);
     }
 }

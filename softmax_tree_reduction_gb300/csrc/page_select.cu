@@ -59,7 +59,7 @@ struct BoundsParams {
     int max_pages, page_shift, num_pages;
 };
 
-constexpr int kBoundsThreads = 256;
+constexpr int kBoundsThreads = 128;
 
 struct E4m3 {};  // cache type tag
 
@@ -193,13 +193,15 @@ struct Range<E4m3> {
 
 // One warp per (row, page, KV head), heads fastest: a token's heads are
 // neighbours in token-major pools.  16 bytes a lane, the lanes of a warp
-// covering 32 / LT tokens at a time.
-template <int D, typename T>
+// covering 32 / LT tokens at a time, F of its loads in flight.  Few pages (a decode
+// step) are a matter of latency: F = 8 (3.1 us for 128 E4M3 pages, 3.5 with 4); many
+// are read faster with F = 4 and more warps (16384 BF16 pages of 64 tokens, 268 MB:
+// 43.5 us against 45.0; 39.6 at the copy rate).
+template <int D, typename T, int F>
 __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const BoundsParams p) {
     constexpr int E = Range<T>::kElems;
     constexpr int LT = D / E;          // lanes per token: 4 .. 32
     constexpr int TW = 32 / LT;        // tokens per warp step
-    constexpr int kFlight = 8;         // loads in flight per lane
     constexpr int es = std::is_same<T, E4m3>::value ? 1 : static_cast<int>(sizeof(T));
     wait_primary();
     allow_dependents();
@@ -230,12 +232,12 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
     Range<T> r;
     r.init();
     int t = tok;
-    for (; t + (kFlight - 1) * TW < nv; t += kFlight * TW) {
-        uint4 x[kFlight];
+    for (; t + (F - 1) * TW < nv; t += F * TW) {
+        uint4 x[F];
 #pragma unroll
-        for (int j = 0; j < kFlight; ++j) x[j] = __ldg(reinterpret_cast<const uint4*>(base + (t + j * TW) * p.st * es));
+        for (int j = 0; j < F; ++j) x[j] = __ldg(reinterpret_cast<const uint4*>(base + (t + j * TW) * p.st * es));
 #pragma unroll
-        for (int j = 0; j < kFlight; ++j) r.add(x[j]);
+        for (int j = 0; j < F; ++j) r.add(x[j]);
     }
     for (; t < nv; t += TW) r.add(__ldg(reinterpret_cast<const uint4*>(base + t * p.st * es)));
     __syncwarp();
@@ -870,6 +872,16 @@ cudaError_t launch(Kernel kernel, dim3 grid, int threads, int smem, const Params
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+template <typename T>
+cudaError_t launch_bounds(int head_dim, bool many, unsigned blocks, const BoundsParams& p, cudaStream_t s) {
+    const dim3 grid(blocks, 1, 1);
+    if (head_dim == 128)
+        return many ? launch(page_bounds_kernel<128, T, 4>, grid, kBoundsThreads, 0, p, s)
+                    : launch(page_bounds_kernel<128, T, 8>, grid, kBoundsThreads, 0, p, s);
+    return many ? launch(page_bounds_kernel<64, T, 4>, grid, kBoundsThreads, 0, p, s)
+                : launch(page_bounds_kernel<64, T, 8>, grid, kBoundsThreads, 0, p, s);
+}
+
 template <int D, typename TQ, typename TB>
 int launch_select(SelectParams p, const DeviceInfo& dev, cudaStream_t s) {
     static std::atomic<unsigned long long> configured{0};
@@ -932,18 +944,15 @@ extern "C" int tree_attn_page_bounds(const ta_shape* shape, const ta_paged_kv* p
     if ((rc = device_info(&dev)) != TA_OK) return rc;
     p.err = dev.err;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const dim3 grid(static_cast<unsigned>(blocks), 1, 1);
-    const bool d128 = shape->head_dim == 128;
+    const bool many = items > 32 * static_cast<int64_t>(dev.num_sms);
+    const unsigned grid = static_cast<unsigned>(blocks);
     cudaError_t e;
     if (shape->kv_dtype == TA_BF16)
-        e = d128 ? launch(page_bounds_kernel<128, __nv_bfloat16>, grid, kBoundsThreads, 0, p, s)
-                 : launch(page_bounds_kernel<64, __nv_bfloat16>, grid, kBoundsThreads, 0, p, s);
+        e = launch_bounds<__nv_bfloat16>(shape->head_dim, many, grid, p, s);
     else if (shape->kv_dtype == TA_E4M3)
-        e = d128 ? launch(page_bounds_kernel<128, E4m3>, grid, kBoundsThreads, 0, p, s)
-                 : launch(page_bounds_kernel<64, E4m3>, grid, kBoundsThreads, 0, p, s);
+        e = launch_bounds<E4m3>(shape->head_dim, many, grid, p, s);
     else
-        e = d128 ? launch(page_bounds_kernel<128, float>, grid, kBoundsThreads, 0, p, s)
-                 : launch(page_bounds_kernel<64, float>, grid, kBoundsThreads, 0, p, s);
+        e = launch_bounds<float>(shape->head_dim, many, grid, p, s);
     return e == cudaSuccess ? TA_OK : TA_ERR_CUDA;
 }
 

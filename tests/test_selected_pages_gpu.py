@@ -412,3 +412,23 @@ def test_stream_handles_and_empty_rows():
         torch.cuda.synchronize()
         assert (b == 0).all() and (sel == -1).all() and (out == 0).all() and (lse == -math.inf).all()
     assert ta.tree_attn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("kv,d,G", [(torch.bfloat16, 64, 3), (torch.bfloat16, 64, 16), (torch.bfloat16, 128, 9), (FP8, 128, 4), (torch.float32, 64, 2)])
+def test_decode_selected_much_work(kv, d, G):
+    """Enough tokens for the wide blocks (BF16), a page size of four slabs, lists in any order."""
+    g = torch.Generator().manual_seed(d + G)
+    page, hkv, B, per, nsel = 64, 2, 4, 520, 500
+    lens = torch.tensor([page * per, page * 400 + 9, page * per - 1, 17], dtype=torch.int32)
+    pages = B * per
+    k, v = (pool(g, kv, pages, page, hkv, d, "HND") for _ in range(2))
+    bt = table(g, B, per, pages)
+    q = torch.randn(B, hkv * G, d, generator=g).to(torch.float32 if kv == torch.float32 else torch.bfloat16)
+    sel = lists(g, B, hkv, nsel, -(-lens // page), "mixed")
+    sc = torch.full((hkv,), 0.015) if kv == FP8 else None
+    kw = dict(k_scale=sc.cuda(), v_scale=sc.cuda()) if kv == FP8 else {}
+    out, lse = ta.tree_attn_decode_selected(q.cuda(), k.cuda(), v.cuda(), bt.cuda(), lens.cuda(), sel.cuda(), **kw)
+    want, wl = ref.decode_selected(q, k, v, bt, lens, sel, k_scale=sc, v_scale=sc)
+    to, tl = TOL[kv]
+    assert (out.cpu().double() - want).abs().max() <= to and (lse.cpu().double() - wl).abs().max() <= tl
+    assert ta.tree_attn_get_device_error() == 0
