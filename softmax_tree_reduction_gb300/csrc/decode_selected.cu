@@ -322,7 +322,11 @@ __global__ void __launch_bounds__(SelCfg<D, kFp8, W>::kThreads, 1) decode_select
     SlabWindow win = list.place(0, e_next), win_next = win;
     const uint8_t* kbytes = static_cast<const uint8_t*>(p.k);
     const uint8_t* vbytes = static_cast<const uint8_t*>(p.v);
-    const int es = kFp8 ? 1 : 2;
+    constexpr int es = kFp8 ? 1 : 2;
+    // this lane's share of a slab's copies: chunk c_chunk of rows c_row, c_row + kRowsAtOnce, ..
+    constexpr int kRowsAtOnce = 32 / Cf::kChunks;
+    const int c_row = lane / Cf::kChunks, c_chunk = lane % Cf::kChunks;
+    const int64_t src_lane = c_row * p.st * es + c_chunk * 16, row_step = kRowsAtOnce * p.st * es;
 
     // Start the copies of the warp's slabs i J .. into stage i % kStages (one group).
     auto issue = [&](int i) {
@@ -341,13 +345,15 @@ __global__ void __launch_bounds__(SelCfg<D, kFp8, W>::kThreads, 1) decode_select
             const int64_t off = __shfl_sync(0xffffffffu, win.off, j) * es;
             if (lane == 0) nvs[slot] = nv;
             if (nv > 0) {
-                const uint32_t dst = ring + slot * Cf::kPairBytes;
+                // rows past the length are zero-filled (a slab's 16 rows lie in its page)
+                const uint32_t dst = ring + slot * Cf::kPairBytes + c_row * Cf::kRowBytes;
+                const int64_t src = off + src_lane;
 #pragma unroll
-                for (int x = 0; x < kSlab * Cf::kChunks / 32; ++x) {
-                    const int idx = x * 32 + lane, r = idx / Cf::kChunks, c = idx % Cf::kChunks;
+                for (int x = 0; x < kSlab / kRowsAtOnce; ++x) {
+                    const int r = x * kRowsAtOnce + c_row;
                     const int bytes = r < nv ? 16 : 0;
-                    const int64_t o = off + (r < nv ? r : 0) * p.st * es + c * 16;
-                    const uint32_t d = dst + r * Cf::kRowBytes + ((c ^ (r & 7)) << 4);
+                    const int64_t o = src + x * row_step;
+                    const uint32_t d = dst + x * kRowsAtOnce * Cf::kRowBytes + ((c_chunk ^ (r & 7)) << 4);
                     cp_async16(d, kbytes + o, bytes);
                     cp_async16(d + Cf::kSlabBytes, vbytes + o, bytes);
                 }
@@ -382,13 +388,10 @@ __global__ void __launch_bounds__(SelCfg<D, kFp8, W>::kThreads, 1) decode_select
                     amax = fmaxf(amax, fmaxf(fabsf(lo(qb[nt][kk][i])), fabsf(hi(qb[nt][kk][i]))));
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-        int qexp = 0;
-        if (amax > 0.f && amax < INFINITY) {
-            int e;
-            frexpf(amax, &e);
-            qexp = max(-100, min(100, 15 - e));
-        }
-        const float qs = ldexpf(1.f, qexp);
+        // amax = f 2^e with f in [0.5, 1); powers of two are made from their exponent bits
+        const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 126;
+        const int qexp = amax > 0.f && amax < INFINITY ? max(-100, min(100, 15 - e)) : 0;
+        const float qs = __uint_as_float(static_cast<uint32_t>(127 + qexp) << 23);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -396,8 +399,8 @@ __global__ void __launch_bounds__(SelCfg<D, kFp8, W>::kThreads, 1) decode_select
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     qb[nt][kk][i] = half2_bits(__floats2half2_rn(lo(qb[nt][kk][i]) * qs, hi(qb[nt][kk][i]) * qs));
-        sl2 *= __ldg(p.k_scale + g) / qs;
-        vscale = __ldg(p.v_scale + g) / kPScale;
+        sl2 *= __ldg(p.k_scale + g) * __uint_as_float(static_cast<uint32_t>(127 - qexp) << 23);
+        vscale = __ldg(p.v_scale + g) * (1.f / kPScale);
     }
 
     for (int it = 0; it < n_it; ++it) {

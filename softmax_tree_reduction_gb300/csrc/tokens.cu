@@ -12,11 +12,12 @@
 // accesses and eight shuffles a vector to bring partners together; the runs need half
 // the cosines and registers too: 152 -> 131 us for 32768 tokens of 32 + 16 BF16
 // heads, 806 MB, 119 us at the copy rate.)  Blocks of 128 threads: with 256 the last
-// ones of a long list leave SMs idle (145 us).
+// ones of a long list leave SMs idle (145 us).  Register limits of 7 (BF16) and 5
+// (FP32) blocks an SM: 4052 tokens of 54 heads 20.9 -> 14.6 us, the others as without.
 //
-// With few tokens a token's heads are spread over several groups instead
-// (heads_per_group): then the call is bound by the latency of one load, the
-// angles and one store, and recomputing the angles costs nothing.
+// Long lists are bound by HBM; with few tokens a token's heads are spread over warps
+// and blocks, and the call is bound by the latency of one load, the angles and one
+// store.
 //
 // Rotation angles.  The angle p * f of position p is needed modulo 2 pi.  The
 // frequency is turned into a 64-bit binary fraction of a full turn per
@@ -40,7 +41,9 @@ namespace ta {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kFlight = 4;  // vectors a group keeps in flight
+constexpr int kFlight = 4;        // vectors a group keeps in flight
+constexpr int kWarpsWanted = 32;  // an SM, before a tile's heads stay in one block
+constexpr int kTilesWhole = 24;   // an SM, from which on a warp takes whole tiles
 
 struct Vectors {
     void* data;
@@ -331,36 +334,70 @@ __device__ __forceinline__ int64_t cache_place(const TokenParams& p, int t, int 
     return -1;
 }
 
-// Which of a token's vectors a group takes.  False: nothing to do.
+// Which of a token's vectors a group of the reading kernel takes.  False: nothing to
+// do.  A warp's groups take the same share of neighbouring tokens, so that they walk
+// keys and values together.
 template <int L>
 __device__ __forceinline__ bool group_work(const TokenParams& p, int heads, int* t, int* h0, int* h1) {
-    const int64_t g = static_cast<int64_t>(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
-    *t = static_cast<int>(g / p.chunks);
-    if (*t >= p.T) return false;
-    *h0 = static_cast<int>(g - static_cast<int64_t>(*t) * p.chunks) * p.hpg;
+    constexpr int kGroups = 32 / L;
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t first = w / p.chunks;
+    *h0 = static_cast<int>(w - first * p.chunks) * p.hpg;
     *h1 = min(heads, *h0 + p.hpg);
-    return true;
+    const int64_t token = first * kGroups + (threadIdx.x & 31) / L;
+    *t = static_cast<int>(token);
+    return token < p.T;
 }
 
 // Heads of a token: [0, Hq) queries, [Hq, Hq + Hkv) keys, then (with a cache)
-// the values.  TC void: keys go to ko and there are no values.
+// the values.  TC void: keys go to ko and there are no values.  A tile is the 32 / L
+// tokens that a warp holds vectors of at a time (a warp's lanes always are at the same
+// head: groups at different heads of one token diverge between queries, keys and
+// values, 18.8 against 13.8 us for 6653 tokens of 16 + 4 heads of 64 channels).
+//  many tiles (chunks = 0)  a warp takes all heads of a tile and computes its tokens'
+//                           angles itself, four a lane;
+//  few                      `chunks` blocks to a tile, whose threads compute one angle
+//                           each for all of them and whose warps take hpg heads each.
+// Each form is the faster one on its side: 700 tokens of 40 heads 4.9 against 6.8 us,
+// 32768 of 48 130.6 against 144.
 template <int D, typename T, typename TC>
-__global__ void __launch_bounds__(kThreads) token_write_kernel(const TokenParams p) {
-    constexpr int L = D / 8;
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 5) token_write_kernel(const TokenParams p) {
+    constexpr int L = D / 8, kGroups = 32 / L;
     constexpr bool kCache = !std::is_void<TC>::value;
+    static_assert(kGroups * (D / 2) == kThreads, "one angle a thread");
+    __shared__ __align__(16) float cos_s[kThreads], sin_s[kThreads];
     wait_primary();
     allow_dependents();
-    int t, h0, h1;
-    if (!group_work<L>(p, p.Hq + p.Hkv + (kCache ? p.Hkv : 0), &t, &h0, &h1)) return;
+    const int heads = p.Hq + p.Hkv + (kCache ? p.Hkv : 0), kend = p.Hq + p.Hkv;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int64_t tile = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + warp;
+    int h0 = 0, h1 = heads;
+    if (p.chunks > 0) {
+        tile = blockIdx.x / p.chunks;
+        h0 = (static_cast<int>(blockIdx.x - tile * p.chunks) * (kThreads / 32) + warp) * p.hpg;
+        h1 = min(heads, h0 + p.hpg);
+        if (p.rot) {
+            const int j = threadIdx.x % (D / 2);
+            const int64_t mine = tile * kGroups + threadIdx.x / (D / 2);
+            if (2 * j < p.rot && mine < p.T)
+                turn(p.positions[mine], __ldg(p.inv_freq + j), &cos_s[threadIdx.x], &sin_s[threadIdx.x]);
+            __syncthreads();
+        }
+    }
+    if (tile * kGroups + lane / L >= p.T || h0 >= heads) return;
+    const int t = static_cast<int>(tile) * kGroups + lane / L;
     const int pos = p.positions[t];
     const int row = !kCache || !p.rows ? t : p.rows[t];
     if (pos < 0 || row < 0) return;  // a padding token
-    const int lane = threadIdx.x & 31;
     const unsigned mask = ((1u << L) - 1u) << (lane & ~(L - 1));
     const Lane c = make_lane(p, lane % L);
-    const int kend = p.Hq + p.Hkv;
     float cs[4], sn[4];
-    if (c.on && h0 < kend) {
+    if (c.on && p.chunks > 0) {
+        const int at = lane / L * (D / 2) + 4 * (lane % L);
+        const float4 u = *reinterpret_cast<const float4*>(cos_s + at), v = *reinterpret_cast<const float4*>(sin_s + at);
+        cs[0] = u.x, cs[1] = u.y, cs[2] = u.z, cs[3] = u.w;
+        sn[0] = v.x, sn[1] = v.y, sn[2] = v.z, sn[3] = v.w;
+    } else if (c.on) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) turn(pos, __ldg(p.inv_freq + 4 * (lane % L) + i), &cs[i], &sn[i]);
     }
@@ -442,9 +479,9 @@ __global__ void __launch_bounds__(kThreads) token_read_kernel(const TokenParams 
 }
 
 // ---------------------------------------------------------------- host side
-// Heads per group: all of a token's vectors while the tokens alone fill the
-// device (1024 threads an SM), else the token's heads in even shares, each of a
-// few kFlight vectors, down to one vector a group.
+// Heads a group takes (hpg) and how many groups to a token (chunks): all of a token's
+// vectors in one while the tokens alone fill the device (1024 threads an SM), else
+// even shares, down to one vector a group.
 void plan_groups(TokenParams* p, int heads, int lanes, int num_sms) {
     const int64_t want = static_cast<int64_t>(num_sms) * 1024 / lanes;
     int64_t hpg = (static_cast<int64_t>(p->T) * heads + want - 1) / want;
@@ -455,10 +492,30 @@ void plan_groups(TokenParams* p, int heads, int lanes, int num_sms) {
     p->chunks = (heads + p->hpg - 1) / p->hpg;
 }
 
+// The writing kernel's: warps take whole tiles (chunks = 0, returned as 1 warp a tile)
+// from kTilesWhole tiles an SM on; below, a tile gets blocks of four warps, more
+// of them while the device has room.
+int64_t plan_tiles(TokenParams* p, int heads, int lanes, int num_sms) {
+    constexpr int kWarps = kThreads / 32;
+    const int64_t tiles = (static_cast<int64_t>(p->T) * lanes + 31) / 32;
+    if (tiles >= static_cast<int64_t>(kTilesWhole) * num_sms) {
+        p->chunks = 0;
+        p->hpg = heads;
+        return 1;
+    }
+    const int64_t room = static_cast<int64_t>(kWarpsWanted) * num_sms / (kWarps * tiles);
+    const int64_t chunks = std::max<int64_t>(1, std::min<int64_t>((heads + kWarps - 1) / kWarps, room));
+    p->hpg = static_cast<int>((heads + kWarps * chunks - 1) / (kWarps * chunks));
+    p->chunks = (heads + kWarps * p->hpg - 1) / (kWarps * p->hpg);
+    return static_cast<int64_t>(p->chunks) * kWarps;
+}
+
+// warps_a_tile: warps to the 32 / L tokens of a tile.
 template <typename Kernel>
-cudaError_t launch(Kernel kernel, const TokenParams& p, int d, cudaStream_t stream) {
-    const int64_t per_block = kThreads / (d / 8);
-    const int64_t blocks = (static_cast<int64_t>(p.T) * p.chunks + per_block - 1) / per_block;
+cudaError_t launch(Kernel kernel, const TokenParams& p, int d, int64_t warps_a_tile, cudaStream_t stream) {
+    const int groups = 32 / (d / 8);  // tokens of a tile
+    const int64_t warps = (static_cast<int64_t>(p.T) + groups - 1) / groups * warps_a_tile;
+    const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
@@ -471,21 +528,21 @@ cudaError_t launch(Kernel kernel, const TokenParams& p, int d, cudaStream_t stre
 }
 
 template <int D, typename T>
-cudaError_t launch_write(int cache, const TokenParams& p, cudaStream_t s) {
+cudaError_t launch_write(int cache, const TokenParams& p, int64_t tile, cudaStream_t s) {
     switch (cache) {
-        case TA_F32: return launch(token_write_kernel<D, T, float>, p, D, s);
-        case TA_BF16: return launch(token_write_kernel<D, T, __nv_bfloat16>, p, D, s);
-        case TA_E4M3: return launch(token_write_kernel<D, T, __nv_fp8_e4m3>, p, D, s);
-        default: return launch(token_write_kernel<D, T, void>, p, D, s);
+        case TA_F32: return launch(token_write_kernel<D, T, float>, p, D, tile, s);
+        case TA_BF16: return launch(token_write_kernel<D, T, __nv_bfloat16>, p, D, tile, s);
+        case TA_E4M3: return launch(token_write_kernel<D, T, __nv_fp8_e4m3>, p, D, tile, s);
+        default: return launch(token_write_kernel<D, T, void>, p, D, tile, s);
     }
 }
 
 template <int D, typename T>
 cudaError_t launch_read(int cache, const TokenParams& p, cudaStream_t s) {
     switch (cache) {
-        case TA_F32: return launch(token_read_kernel<D, T, float>, p, D, s);
-        case TA_BF16: return launch(token_read_kernel<D, T, __nv_bfloat16>, p, D, s);
-        default: return launch(token_read_kernel<D, T, __nv_fp8_e4m3>, p, D, s);
+        case TA_F32: return launch(token_read_kernel<D, T, float>, p, D, p.chunks, s);
+        case TA_BF16: return launch(token_read_kernel<D, T, __nv_bfloat16>, p, D, p.chunks, s);
+        default: return launch(token_read_kernel<D, T, __nv_fp8_e4m3>, p, D, p.chunks, s);
     }
 }
 
@@ -576,7 +633,11 @@ int enqueue(const ta_shape* shape, TokenParams* p, int heads, int cache, bool re
     const int rc = device_info(&dev);
     if (rc != TA_OK) return rc;
     p->err = dev.err;
-    plan_groups(p, heads, shape->head_dim / 8, dev.num_sms);
+    int64_t tile = 0;  // warps to a tile
+    if (read)
+        plan_groups(p, heads, shape->head_dim / 8, dev.num_sms);
+    else
+        tile = plan_tiles(p, heads, shape->head_dim / 8, dev.num_sms);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool d128 = shape->head_dim == 128, bf16 = shape->q_dtype == TA_BF16;
     cudaError_t e;
@@ -584,8 +645,8 @@ int enqueue(const ta_shape* shape, TokenParams* p, int heads, int cache, bool re
         e = d128 ? (bf16 ? launch_read<128, __nv_bfloat16>(cache, *p, s) : launch_read<128, float>(cache, *p, s))
                  : (bf16 ? launch_read<64, __nv_bfloat16>(cache, *p, s) : launch_read<64, float>(cache, *p, s));
     else
-        e = d128 ? (bf16 ? launch_write<128, __nv_bfloat16>(cache, *p, s) : launch_write<128, float>(cache, *p, s))
-                 : (bf16 ? launch_write<64, __nv_bfloat16>(cache, *p, s) : launch_write<64, float>(cache, *p, s));
+        e = d128 ? (bf16 ? launch_write<128, __nv_bfloat16>(cache, *p, tile, s) : launch_write<128, float>(cache, *p, tile, s))
+                 : (bf16 ? launch_write<64, __nv_bfloat16>(cache, *p, tile, s) : launch_write<64, float>(cache, *p, tile, s));
     return e == cudaSuccess ? TA_OK : TA_ERR_CUDA;
 }
 
