@@ -164,10 +164,10 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // reads a peer's memory.  The caller has arrived once at the cluster's barrier
 // when it started.  kFp8: numerators of channel c sit at (c % 16) * 8 + c / 16 and
 // still lack V's scale.
-template <int D, int kWarps, int kCols, bool kFp8>
+template <int D, int kWarps, int kCols, bool kFp8, int kThreads = 32 * kWarps>
 __device__ void finish_list(const SelParams& p, int b, int hq0, int ncol, float vscale, const float* mg_o,
                             const float* mg_m, const float* mg_l, Mailbox<D, kCols>* box, bool poison) {
-    constexpr int MS = D + 4, kThreads = 32 * kWarps;
+    constexpr int MS = D + 4;
     const int tid = threadIdx.x;
     const float nan = __int_as_float(0x7fc00000);
     const size_t row0 = static_cast<size_t>(b) * p.Hq + hq0;
@@ -625,98 +625,215 @@ __global__ void __launch_bounds__(SelCfg<D, kFp8, W>::kThreads, 1) decode_select
 }
 
 // -------------------------------------------------------------- FP32 caches
-// CUDA cores (BF16 operands would lose the FP32 tolerance).  Eight lanes hold
-// a token's channels, four tokens a warp step, straight from global memory;
-// each eight-lane group keeps a running state for GC query heads.
-constexpr int kF32Warps = 8;
+// CUDA cores (BF16 operands would lose the FP32 tolerance), with the lists and rings
+// of the tensor-core kernel.  Eight lanes hold a token's channels and a warp's four
+// groups take every fourth token of a slab; each group keeps a running state for GC
+// query heads, updated once per slab (its four tokens), so that the four share a load
+// of q, the rescaling and the wait for the exponentials.  From 3 heads of a KV head on,
+// P = 2 warps share a ring: both copy half of a slab's rows and each takes GC of the
+// heads, so that the cache is read once for 8 heads and neither warp needs more
+// registers than it has (one warp with 8 heads' states spilled: 169 us for 4 x 8 lists
+// of 16384 tokens at 8 heads of 128 channels, where this takes 101; 4 heads as one warp
+// with 4: 86, as 2 x 2: 82; one head: 81; floor 79).  Reading
+// the cache straight into registers, a token at a time and again for every 4 heads,
+// took 252, 136 and 84 us.  At 8 heads the bound is the chain of a slab (products, sums
+// over 8 lanes, maxima, exponentials) with three warps a scheduler to hide it.
+// Two products and sums of FP32 in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmov.b64 z, {%6, %7};\n"
+        "fma.rn.f32x2 z, x, y, z;\nmov.b64 {%0, %1}, z;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n.reg .b64 x, y;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\n"
+        "mul.rn.f32x2 x, x, y;\nmov.b64 {%0, %1}, x;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 
-template <int D, int GC>
-__global__ void __launch_bounds__(32 * kF32Warps) decode_selected_f32_kernel(const SelParams p) {
-    constexpr int kWarps = kF32Warps;
+template <int D, int P>
+struct F32Cfg {
+    static constexpr int kRowBytes = 4 * D;
+    static constexpr int kChunks = kRowBytes / 16;
+    static constexpr int kSlabBytes = kSlab * kRowBytes;
+    static constexpr int kStageBytes = 2 * kSlabBytes;           // keys, values: 8 or 16 KB
+    static constexpr int kRings = D == 64 && P == 1 ? 12 : 6;    // 192 KB together
+    static constexpr int kStages = 196608 / kRings / kStageBytes;
+    static constexpr int kWarps = P * kRings;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kRing = kRings * kStages * kStageBytes;
+    static_assert(kStages >= 2 && kRings * 8 * (D + 4 + 2) * 4 <= kRing, "ring, merge buffers");
+};
+
+template <int D, int GC, int P>
+__global__ void __launch_bounds__(F32Cfg<D, P>::kThreads, 1) decode_selected_f32_kernel(const SelParams p) {
+    using Cf = F32Cfg<D, P>;
+    constexpr int kRings = Cf::kRings, kStages = Cf::kStages;
+    constexpr int kCols = P * GC;
     constexpr int J = D / 32;  // float4 per lane: channels 4 (l8 + 8 j) ..
     constexpr int MS = D + 4;
-    __shared__ __align__(16) float qs[GC][D];
-    __shared__ __align__(16) float mg_o[kWarps * GC * MS];
-    __shared__ float mg_m[kWarps * GC], mg_l[kWarps * GC];
-    __shared__ Mailbox<D, GC> box;
+    constexpr int kSteps = kSlab / 4;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(16) float q_all[kCols][D];
+    __shared__ Mailbox<D, kCols> box;
+    __shared__ int nvs_all[Cf::kWarps * kStages];
     __shared__ int bad_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l8 = lane & 7, tok = lane >> 3;
     const int g = blockIdx.y / p.ngroups, cg = blockIdx.y - g * p.ngroups, b = blockIdx.z;
-    const int ncol = min(GC, p.G - GC * cg);
-    const int hq0 = g * p.G + GC * cg;
+    const int ncol = min(kCols, p.G - kCols * cg);
+    const int hq0 = g * p.G + kCols * cg;
+    const int r = warp / P, part = warp - r * P;  // ring, and which GC columns of it
     if (p.C > 1) cluster_arrive();  // (waited for before the states are sent)
+    if (threadIdx.x == 0) bad_flag = 0;
     wait_primary();
     allow_dependents();
-    if (threadIdx.x == 0) bad_flag = 0;
-    for (int i = threadIdx.x; i < GC * D; i += 32 * kWarps)
-        qs[i / D][i % D] = i / D < ncol
-                               ? static_cast<const float*>(p.q)[(static_cast<size_t>(b) * p.Hq + hq0) * D + i] * p.scale_log2
-                               : 0.f;
-    __syncthreads();
     int N = p.seqlens[b];
     const bool bad_len = N < 0 || N > p.S;
     if (bad_len) N = 0;
-    SlabList list(p, b, g, N, blockIdx.x * kWarps + warp, p.C * kWarps);
+    SlabList list(p, b, g, N, blockIdx.x * kRings + r, p.C * kRings);
     const int n_it = list.count();
+    int e_next = list.entry(0);
+    for (int i = threadIdx.x; i < kCols * D; i += Cf::kThreads)
+        q_all[i / D][i % D] = i / D < ncol
+                               ? static_cast<const float*>(p.q)[(static_cast<size_t>(b) * p.Hq + hq0) * D + i] * p.scale_log2
+                               : 0.f;
+    const uint32_t ring = smem_u32(smem) + r * kStages * Cf::kStageBytes;
+    const uint8_t* ring_ptr = smem + r * kStages * Cf::kStageBytes;
+    volatile int* nvs = nvs_all + warp * kStages;
+    const float(*qs)[D] = q_all + part * GC;
+    // every lane of the ring's warps
+    auto ring_sync = [&] {
+        if constexpr (P == 1)
+            __syncwarp();
+        else
+            asm volatile("bar.sync %0, %1;" ::"r"(r + 1), "n"(32 * P) : "memory");
+    };
+    SlabWindow win = list.place(0, e_next), win_next = win;
+    const uint8_t* kbytes = static_cast<const uint8_t*>(p.k);
+    const uint8_t* vbytes = static_cast<const uint8_t*>(p.v);
+    constexpr int kRowsAtOnce = 32 / Cf::kChunks;  // rows a copy instruction of the warp covers
+    const int c_row = part * kRowsAtOnce + lane / Cf::kChunks, c_chunk = lane % Cf::kChunks;
+    const int64_t src_lane = c_row * p.st * 4 + c_chunk * 16, row_step = P * kRowsAtOnce * p.st * 4;
+
+    // Start the warp's copies of the ring's slab i into stage i % kStages (one group).
+    auto issue = [&](int i) {
+        if (i < n_it) {
+            const int j = i & 31, s = i % kStages;
+            if (j == 0 && i > 0) win = win_next;
+            if (j == 0) e_next = list.entry(i + 32);
+            if (j == 16) win_next = list.place(i + 16, e_next);
+            const int nv = __shfl_sync(0xffffffffu, win.nv, j);
+            const int64_t src = __shfl_sync(0xffffffffu, win.off, j) * 4 + src_lane;
+            if (lane == 0) nvs[s] = nv;
+            if (nv > 0) {  // rows past the length are zero-filled (a slab's 16 rows lie in its page)
+                const uint32_t dst = ring + s * Cf::kStageBytes + c_row * Cf::kRowBytes + c_chunk * 16;
+#pragma unroll
+                for (int x = 0; x < kSlab / (P * kRowsAtOnce); ++x) {
+                    const int bytes = x * P * kRowsAtOnce + c_row < nv ? 16 : 0;
+                    const uint32_t d = dst + x * P * kRowsAtOnce * Cf::kRowBytes;
+                    cp_async16(d, kbytes + src + x * row_step, bytes);
+                    cp_async16(d + Cf::kSlabBytes, vbytes + src + x * row_step, bytes);
+                }
+            }
+        }
+        cp_async_commit();
+    };
+
     float m[GC], l[GC];
-    float4 o[GC][J];
+    float2 o[GC][2 * J];
 #pragma unroll
     for (int h = 0; h < GC; ++h) {
         m[h] = -INFINITY;
         l[h] = 0.f;
 #pragma unroll
-        for (int j = 0; j < J; ++j) o[h][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < 2 * J; ++j) o[h][j] = make_float2(0.f, 0.f);
     }
-    const float* kp = static_cast<const float*>(p.k);
-    const float* vp = static_cast<const float*>(p.v);
-    SlabWindow win;
-    win.off = 0;
-    win.nv = 0;
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+    __syncthreads();  // q is in shared memory
     for (int it = 0; it < n_it; ++it) {
-        if ((it & 31) == 0) win = list.place(it, list.entry(it));
-        const int nv = __shfl_sync(0xffffffffu, win.nv, it & 31);
-        const int64_t off = __shfl_sync(0xffffffffu, win.off, it & 31);
-#pragma unroll 1
-        for (int t = 0; t < nv; t += 4) {
-            const int r = t + tok;
-            const bool on = r < nv;
-            const int64_t at = off + (on ? r : 0) * p.st + 4 * l8;
-            float4 k4[J], v4[J];
+        ring_sync();  // every lane is done with the slab before
+        issue(it + kStages - 1);
+        cp_async_wait<kStages - 1>();
+        ring_sync();  // the slab is in shared memory for every lane
+        const int s = it % kStages;
+        const int nv = nvs[s];
+        if (nv <= 0) continue;
+        const float* ks = reinterpret_cast<const float*>(ring_ptr + s * Cf::kStageBytes) + tok * D + 4 * l8;
+        const float* vs = ks + Cf::kSlabBytes / 4;
+        float sc[GC][kSteps];  // tokens 4 t + tok
+        {
+            float2 z[GC][kSteps];
 #pragma unroll
-            for (int j = 0; j < J; ++j) k4[j] = __ldg(reinterpret_cast<const float4*>(kp + at + 32 * j));
+            for (int j = 0; j < J; ++j) {
+                float4 k4[kSteps];
 #pragma unroll
-            for (int j = 0; j < J; ++j)
-                v4[j] = on ? __ldg(reinterpret_cast<const float4*>(vp + at + 32 * j)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int t = 0; t < kSteps; ++t) k4[t] = *reinterpret_cast<const float4*>(ks + 4 * t * D + 32 * j);
 #pragma unroll
-            for (int h = 0; h < GC; ++h) {
-                float s = 0.f;
-#pragma unroll
-                for (int j = 0; j < J; ++j) {
+                for (int h = 0; h < GC; ++h) {
                     const float4 q4 = *reinterpret_cast<const float4*>(&qs[h][4 * l8 + 32 * j]);
-                    s = fmaf(q4.x, k4[j].x, s);
-                    s = fmaf(q4.y, k4[j].y, s);
-                    s = fmaf(q4.z, k4[j].z, s);
-                    s = fmaf(q4.w, k4[j].w, s);
+#pragma unroll
+                    for (int t = 0; t < kSteps; ++t) {
+                        z[h][t] = fma2(make_float2(q4.x, q4.y), make_float2(k4[t].x, k4[t].y),
+                                       j ? z[h][t] : make_float2(0.f, 0.f));
+                        z[h][t] = fma2(make_float2(q4.z, q4.w), make_float2(k4[t].z, k4[t].w), z[h][t]);
+                    }
                 }
+            }
 #pragma unroll
-                for (int x = 4; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-                if (!on) s = -INFINITY;
-                const float mn = fmaxf(m[h], s), ms = (mn == -INFINITY) ? 0.f : mn;
-                const float al = ex2(m[h] - ms), w = ex2(s - ms);
-                m[h] = mn;
-                l[h] = fmaf(l[h], al, w);
+            for (int h = 0; h < GC; ++h)
 #pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    o[h][j].x = fmaf(o[h][j].x, al, w * v4[j].x);
-                    o[h][j].y = fmaf(o[h][j].y, al, w * v4[j].y);
-                    o[h][j].z = fmaf(o[h][j].z, al, w * v4[j].z);
-                    o[h][j].w = fmaf(o[h][j].w, al, w * v4[j].w);
+                for (int t = 0; t < kSteps; ++t) {
+                    float y = z[h][t].x + z[h][t].y;
+#pragma unroll
+                    for (int x = 4; x > 0; x >>= 1) y += __shfl_xor_sync(0xffffffffu, y, x);
+                    sc[h][t] = 4 * t + tok < nv ? y : -INFINITY;
+                }
+        }
+#pragma unroll
+        for (int h = 0; h < GC; ++h) {
+            float mn = m[h];
+#pragma unroll
+            for (int t = 0; t < kSteps; ++t) mn = fmaxf(mn, sc[h][t]);
+            const float ms = (mn == -INFINITY) ? 0.f : mn;
+            const float al = ex2(m[h] - ms);
+            float sum = 0.f;
+#pragma unroll
+            for (int t = 0; t < kSteps; ++t) {
+                sc[h][t] = ex2(sc[h][t] - ms);
+                sum += sc[h][t];
+            }
+            m[h] = mn;
+            l[h] = fmaf(l[h], al, sum);
+#pragma unroll
+            for (int j = 0; j < 2 * J; ++j) o[h][j] = mul2(o[h][j], make_float2(al, al));
+        }
+#pragma unroll
+        for (int t = 0; t < kSteps; ++t) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const float4 v4 = *reinterpret_cast<const float4*>(vs + 4 * t * D + 32 * j);
+#pragma unroll
+                for (int h = 0; h < GC; ++h) {
+                    const float2 w = make_float2(sc[h][t], sc[h][t]);
+                    o[h][2 * j] = fma2(w, make_float2(v4.x, v4.y), o[h][2 * j]);
+                    o[h][2 * j + 1] = fma2(w, make_float2(v4.z, v4.w), o[h][2 * j + 1]);
                 }
             }
         }
     }
+    cp_async_wait<0>();
     if (list.bad) bad_flag = 1;
     if (list.bad || (bad_len && threadIdx.x == 0)) atomicOr(p.err, kErrBadSeqlen);
+    __syncthreads();  // every warp is done with its ring
+    float* mg_o = reinterpret_cast<float*>(smem);
+    float* mg_m = mg_o + kRings * kCols * MS;
+    float* mg_l = mg_m + kRings * kCols;
     // the warp's four token groups, then its state into shared memory
 #pragma unroll
     for (int h = 0; h < GC; ++h) {
@@ -727,18 +844,17 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_selected_f32_kernel(con
             const float a = ex2(m[h] - ms), c = ex2(mo - ms);
             l[h] = l[h] * a + __shfl_xor_sync(0xffffffffu, l[h], x) * c;
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
+            for (int j = 0; j < 2 * J; ++j) {
                 o[h][j].x = o[h][j].x * a + __shfl_xor_sync(0xffffffffu, o[h][j].x, x) * c;
                 o[h][j].y = o[h][j].y * a + __shfl_xor_sync(0xffffffffu, o[h][j].y, x) * c;
-                o[h][j].z = o[h][j].z * a + __shfl_xor_sync(0xffffffffu, o[h][j].z, x) * c;
-                o[h][j].w = o[h][j].w * a + __shfl_xor_sync(0xffffffffu, o[h][j].w, x) * c;
             }
             m[h] = mn;
         }
         if (tok == 0) {
 #pragma unroll
             for (int j = 0; j < J; ++j)
-                *reinterpret_cast<float4*>(&mg_o[(warp * GC + h) * MS + 4 * l8 + 32 * j]) = o[h][j];
+                *reinterpret_cast<float4*>(&mg_o[(warp * GC + h) * MS + 4 * l8 + 32 * j]) =
+                    make_float4(o[h][2 * j].x, o[h][2 * j].y, o[h][2 * j + 1].x, o[h][2 * j + 1].y);
             if (l8 == 0) {
                 mg_m[warp * GC + h] = m[h];
                 mg_l[warp * GC + h] = l[h];
@@ -746,7 +862,7 @@ __global__ void __launch_bounds__(32 * kF32Warps) decode_selected_f32_kernel(con
         }
     }
     __syncthreads();
-    finish_list<D, kWarps, GC, false>(p, b, hq0, ncol, 1.f, mg_o, mg_m, mg_l, &box, bad_len || bad_flag);
+    finish_list<D, kRings, kCols, false, Cf::kThreads>(p, b, hq0, ncol, 1.f, mg_o, mg_m, mg_l, &box, bad_len || bad_flag);
 }
 
 // ---------------------------------------------------------------- host side
@@ -762,7 +878,7 @@ struct Instance {
 };
 
 template <typename Kernel>
-int prepare_instance(Kernel kernel, int warps, int smem, int device, Instance* inst) {
+int prepare_instance(Kernel kernel, int threads, int smem, int device, Instance* inst) {
     std::lock_guard<std::mutex> lock(inst->mu);
     if (inst->ready[device]) return TA_OK;
     if (smem > 0 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
@@ -771,7 +887,7 @@ int prepare_instance(Kernel kernel, int warps, int smem, int device, Instance* i
     for (int c = 1; c <= kMaxCluster; ++c) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(c, 1, 1);
-        cfg.blockDim = dim3(32 * warps, 1, 1);
+        cfg.blockDim = dim3(threads, 1, 1);
         cfg.dynamicSmemBytes = smem;
         cudaLaunchAttribute a = {};
         a.id = cudaLaunchAttributeClusterDimension;
@@ -790,26 +906,28 @@ int prepare_instance(Kernel kernel, int warps, int smem, int device, Instance* i
     return TA_OK;
 }
 
-// Blocks per list: the most that leave every warp a slab and keep all lists
+// Blocks per list: the most that leave every ring a slab and keep all lists
 // resident at once (how many clusters of a size fit depends on the GPCs: on
 // GB300, with one block an SM, 36 of 4 blocks but only 15 of 7 or 8); one block
 // when there are more lists than that.
-int pick_cluster(int64_t lists, int64_t slabs, int warps, const int* fit) {
+int pick_cluster(int64_t lists, int64_t slabs, int rings, const int* fit) {
     int c = 1;
     for (int n = 2; n <= kMaxCluster; ++n)
-        if (slabs >= static_cast<int64_t>(n) * warps && lists <= fit[n]) c = n;
+        if (slabs >= static_cast<int64_t>(n) * rings && lists <= fit[n]) c = n;
     return c;
 }
 
 template <typename Kernel>
-int launch_selected(Kernel kernel, int warps, int smem, Instance* inst, int device, SelParams p, int batch, cudaStream_t stream) {
-    const int rc = prepare_instance(kernel, warps, smem, device, inst);
+int launch_selected(Kernel kernel, int rings, int warps_per_ring, int smem, Instance* inst, int device, SelParams p,
+                    int batch, cudaStream_t stream) {
+    const int threads = 32 * rings * warps_per_ring;
+    const int rc = prepare_instance(kernel, threads, smem, device, inst);
     if (rc != TA_OK) return rc;
     const int64_t lists = static_cast<int64_t>(batch) * p.Hkv * p.ngroups;
-    p.C = pick_cluster(lists, static_cast<int64_t>(p.num_select) << (p.page_shift - 4), warps, inst->clusters[device]);
+    p.C = pick_cluster(lists, static_cast<int64_t>(p.num_select) << (p.page_shift - 4), rings, inst->clusters[device]);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.C, p.Hkv * p.ngroups, batch);
-    cfg.blockDim = dim3(32 * warps, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -826,7 +944,7 @@ int launch_selected(Kernel kernel, int warps, int smem, Instance* inst, int devi
 template <int D, int NT, bool kFp8, int W>
 int launch_mma_warps(int device, const SelParams& p, int batch, cudaStream_t s) {
     static Instance inst;
-    return launch_selected(decode_selected_kernel<D, NT, kFp8, W>, W, SelCfg<D, kFp8, W>::kSmem, &inst, device, p, batch, s);
+    return launch_selected(decode_selected_kernel<D, NT, kFp8, W>, W, 1, SelCfg<D, kFp8, W>::kSmem, &inst, device, p, batch, s);
 }
 
 // BF16: 12 warps with two stages each hide more of each other's chains than 8 with
@@ -843,10 +961,10 @@ int launch_mma(const DeviceInfo& dev, const SelParams& p, int batch, cudaStream_
     return launch_mma_warps<D, NT, kFp8, 8>(dev.device, p, batch, s);
 }
 
-template <int D, int GC>
+template <int D, int GC, int P>
 int launch_f32(int device, const SelParams& p, int batch, cudaStream_t s) {
     static Instance inst;
-    return launch_selected(decode_selected_f32_kernel<D, GC>, kF32Warps, 0, &inst, device, p, batch, s);
+    return launch_selected(decode_selected_f32_kernel<D, GC, P>, F32Cfg<D, P>::kRings, P, F32Cfg<D, P>::kRing, &inst, device, p, batch, s);
 }
 
 }  // namespace
@@ -875,7 +993,7 @@ extern "C" int tree_attn_decode_selected(const ta_shape* shape, const ta_paged_k
         return TA_ERR_DTYPE;
     }
     const int G = shape->num_q_heads / shape->num_kv_heads;
-    const int cols = f32 ? (G >= 3 ? 4 : G) : 16;  // columns a block serves
+    const int cols = f32 ? (G > 4 ? 8 : (G > 2 ? 4 : G)) : 16;  // columns a block serves
     SelParams p;
     std::memset(&p, 0, sizeof p);
     p.ngroups = (G + cols - 1) / cols;
@@ -915,8 +1033,9 @@ extern "C" int tree_attn_decode_selected(const ta_shape* shape, const ta_paged_k
         return two ? launch_mma<64, 2, false>(dev, p, B, s) : launch_mma<64, 1, false>(dev, p, B, s);
     }
     switch (cols) {
-        case 1: return d128 ? launch_f32<128, 1>(dev.device, p, B, s) : launch_f32<64, 1>(dev.device, p, B, s);
-        case 2: return d128 ? launch_f32<128, 2>(dev.device, p, B, s) : launch_f32<64, 2>(dev.device, p, B, s);
-        default: return d128 ? launch_f32<128, 4>(dev.device, p, B, s) : launch_f32<64, 4>(dev.device, p, B, s);
+        case 1: return d128 ? launch_f32<128, 1, 1>(dev.device, p, B, s) : launch_f32<64, 1, 1>(dev.device, p, B, s);
+        case 2: return d128 ? launch_f32<128, 2, 1>(dev.device, p, B, s) : launch_f32<64, 2, 1>(dev.device, p, B, s);
+        case 4: return d128 ? launch_f32<128, 2, 2>(dev.device, p, B, s) : launch_f32<64, 2, 2>(dev.device, p, B, s);
+        default: return d128 ? launch_f32<128, 4, 2>(dev.device, p, B, s) : launch_f32<64, 4, 2>(dev.device, p, B, s);
     }
 }

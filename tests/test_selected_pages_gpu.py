@@ -156,8 +156,9 @@ def lists(g, B, hkv, nsel, pages_of_row, order, fill=1.0):
 @pytest.mark.parametrize("layout", ["NHD", "HND"])
 @pytest.mark.parametrize("nsel,order,fill", [(1, "up", 1.0), (3, "mixed", 0.7), (40, "up", 1.0), (65, "mixed", 0.5), (200, "up", 1.0)])
 @pytest.mark.parametrize("kv,d,hkv,G,page", [(torch.bfloat16, 128, 2, 4, 64), (torch.bfloat16, 128, 1, 12, 16), (torch.bfloat16, 64, 3, 1, 32),
-                                             (torch.bfloat16, 64, 1, 40, 16), (FP8, 128, 2, 8, 16), (FP8, 128, 1, 24, 128),
-                                             (torch.float32, 128, 2, 1, 16), (torch.float32, 64, 2, 8, 64), (torch.float32, 128, 1, 6, 32)])
+                                             (torch.bfloat16, 64, 1, 40, 16), (FP8, 128, 2, 8, 16), (FP8, 128, 1, 20, 128),
+                                             (torch.float32, 128, 2, 1, 16), (torch.float32, 64, 2, 8, 64), (torch.float32, 128, 1, 6, 32),
+                                             (torch.float32, 128, 1, 2, 64), (torch.float32, 64, 2, 3, 16), (torch.float32, 64, 1, 11, 32), (torch.float32, 128, 1, 16, 128)])
 def test_decode_selected(kv, d, hkv, G, page, nsel, order, fill, layout):
     g = torch.Generator().manual_seed(d + G + nsel)
     lens = torch.tensor([0, 1, 17, page * 40 + 5, page * 60], dtype=torch.int32)
