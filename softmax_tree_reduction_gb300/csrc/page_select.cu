@@ -524,6 +524,38 @@ __device__ __forceinline__ void warp_sums(int a, int b, int2* buf, int2* before,
     all->y = __reduce_add_sync(0xffffffffu, c.y);
 }
 
+// The largest digit with at least `left` counted keys at or above it: found[0], with
+// found[1] of its found[2] keys still to take.  Digits downwards, four a thread.
+__device__ __forceinline__ void find_digit(const int* hist, int left, int* tot, int* found) {
+    static_assert(kPickThreads * 4 == kDigits && kPickWarps <= 32, "four counters a thread");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int base = kPickThreads - 1 - static_cast<int>(threadIdx.x);
+    const int4 u = reinterpret_cast<const int4*>(hist)[base];
+    const int c[4] = {u.w, u.z, u.y, u.x};
+    const int sum = c[0] + c[1] + c[2] + c[3];
+    int x = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+    }
+    if (lane == 31) tot[warp] = x;
+    __syncthreads();
+    int b0 = __reduce_add_sync(0xffffffffu, lane < warp ? tot[lane] : 0) + x - sum;
+    if (b0 < left && left <= b0 + sum) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (b0 < left && left <= b0 + c[j]) {
+                found[0] = 4 * base + 3 - j;
+                found[1] = left - b0;
+                found[2] = c[j];
+            }
+            b0 += c[j];
+        }
+    }
+    __syncthreads();
+}
+
 // The `need`-th largest (need >= 1) of the keys that are not 0 (0: no key), n4 groups
 // of four that key4(i) gives, where all keys agree with `first` above their `bits`
 // low bits; *above: how many are larger.  Digits of 11 bits: scores of a row lie in a
@@ -531,8 +563,6 @@ __device__ __forceinline__ void warp_sums(int a, int b, int2* buf, int2* before,
 // against 700 cycles a pass).
 template <typename Key4>
 __device__ uint32_t radix_pick(int n4, int need, uint32_t first, int bits, int* hist, int* tot, int* found, Key4&& key4, int* above) {
-    static_assert(kPickThreads * 4 == kDigits && kPickWarps <= 32, "four counters a thread");
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t prefix = bits < 32 ? first >> bits : 0;
     int left = need;
     while (bits > 0) {
@@ -549,31 +579,7 @@ __device__ uint32_t radix_pick(int n4, int need, uint32_t first, int bits, int* 
                 if (k[j] != 0 && (bits == 32 || (k[j] >> bits) == prefix)) atomicAdd(&hist[(k[j] >> shift) & mask], 1);
         }
         __syncthreads();
-        // the largest digit with at least `left` keys at or above it: digits downwards, four a thread
-        const int base = kPickThreads - 1 - static_cast<int>(threadIdx.x);
-        const int4 u = reinterpret_cast<const int4*>(hist)[base];
-        const int c[4] = {u.w, u.z, u.y, u.x};
-        const int sum = c[0] + c[1] + c[2] + c[3];
-        int x = sum;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, off);
-            if (lane >= off) x += y;
-        }
-        if (lane == 31) tot[warp] = x;
-        __syncthreads();
-        int b0 = __reduce_add_sync(0xffffffffu, lane < warp ? tot[lane] : 0) + x - sum;
-        if (b0 < left && left <= b0 + sum) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (b0 < left && left <= b0 + c[j]) {
-                    found[0] = 4 * base + 3 - j;
-                    found[1] = left - b0;
-                }
-                b0 += c[j];
-            }
-        }
-        __syncthreads();
+        find_digit(hist, left, tot, found);
         prefix = (prefix << width) | static_cast<uint32_t>(found[0]);
         left = found[1];
         bits = shift;
@@ -582,31 +588,43 @@ __device__ uint32_t radix_pick(int n4, int need, uint32_t first, int bits, int* 
     return prefix;
 }
 
+// Scores are finite or +inf (page_score_kernel); -inf here marks a page that does not
+// compete.  The block's passes over the scores are bound by instructions (four warps a
+// scheduler, one or two groups of four scores a thread), so they compare the scores
+// themselves, at two to four instructions a score.
 template <int D, typename TQ, typename TB>
 __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const SelectParams p) {
     using PB = PageBounds<D, TB>;
-    extern __shared__ __align__(16) uint32_t keys_kept[];
+    extern __shared__ __align__(16) float scores_kept[];
     __shared__ __align__(16) int hist[kDigits];
-    __shared__ int found[2], tot[kPickWarps];
+    __shared__ int found[3], tot[kPickWarps], list_n;
+    __shared__ __align__(16) float list_s[32];
+    __shared__ int list_i[32];
     __shared__ int2 sums[kPickWarps];
     __shared__ uint4 range_w[kPickWarps];
     wait_primary();
     allow_dependents();
     const int g = blockIdx.x, b = blockIdx.y;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    const float none = -INFINITY;
     int32_t* sel = p.selected + (static_cast<int64_t>(b) * p.Hkv + g) * p.num_select;
     const int64_t row = static_cast<int64_t>(b) * p.Hkv + g;
     const float* sc = p.scores + row * p.stride;
+    const float* mags = p.mags + row * (p.stride / 8);
     const int N = p.seqlens[b];
-    // (the first scores do not wait for the length: past the row's pages they are ignored)
-    float4 ahead = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (p.pages > p.num_select && static_cast<int>(threadIdx.x) * 4 < p.stride)
-        ahead = __ldcg(reinterpret_cast<const float4*>(sc) + threadIdx.x);
+    // (the first loads do not wait for the length: past the row's pages they are ignored)
+    float4 ahead[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    float mag_ahead = 0.f;
+    if (p.pages > p.num_select) {
+        if (4 * tid < p.stride) ahead[0] = __ldcg(reinterpret_cast<const float4*>(sc) + tid);
+        if (4 * (tid + kPickThreads) < p.stride) ahead[1] = __ldcg(reinterpret_cast<const float4*>(sc) + tid + kPickThreads);
+        if (8 * tid < p.stride) mag_ahead = __ldcg(mags + tid);
+    }
     const bool bad = N < 0 || N > p.S;
-    if (bad && threadIdx.x == 0) atomicOr(p.err, kErrBadSeqlen);
+    if (bad && tid == 0) atomicOr(p.err, kErrBadSeqlen);
     const int n = bad ? 0 : static_cast<int>((static_cast<int64_t>(N) + (1 << p.page_shift) - 1) >> p.page_shift);
     if (n <= p.num_select) {
-        for (int i = threadIdx.x; i < p.num_select; i += kPickThreads) sel[i] = i < n ? i : -1;
+        for (int i = tid; i < p.num_select; i += kPickThreads) sel[i] = i < n ? i : -1;
         return;
     }
     float2* exact = p.exact + row * p.pages;
@@ -614,61 +632,137 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
     const int need = p.num_select - p.first - p.last;    // places for them; fewer than hi - lo
     const int n4 = (n + 3) / 4;
     // Pages above `top` are taken, pages below `low` are not; those between are
-    // taken where (T, T2) says so.
-    uint32_t top = 0xffffffffu, low = 0xffffffffu, T = 0, T2 = 0;
+    // taken, or, once `ranked`, where their exact sums (T, T2) say so.
+    float top = INFINITY, low = INFINITY;
+    uint32_t T = 0, T2 = 0;
     int ties = 0;                                        // pages at (T, T2) to take, lowest first
-    // four pages' keys (0: the page does not compete)
+    bool ranked = false;
+    auto competing = [&](int i, float s) { return i >= lo && i < hi ? s : none; };
     auto scored4 = [&](int i) {
-        const float4 s = i == static_cast<int>(threadIdx.x) ? ahead : __ldcg(reinterpret_cast<const float4*>(sc) + i);
-        const int q = 4 * i;
-        uint4 k;
-        k.x = q >= lo && q < hi ? ordered(s.x) : 0u;
-        k.y = q + 1 >= lo && q + 1 < hi ? ordered(s.y) : 0u;
-        k.z = q + 2 >= lo && q + 2 < hi ? ordered(s.z) : 0u;
-        k.w = q + 3 >= lo && q + 3 < hi ? ordered(s.w) : 0u;
-        return k;
+        const float4 s = i == tid ? ahead[0] : (i == tid + kPickThreads ? ahead[1] : __ldcg(reinterpret_cast<const float4*>(sc) + i));
+        return make_float4(competing(4 * i, s.x), competing(4 * i + 1, s.y), competing(4 * i + 2, s.z), competing(4 * i + 3, s.w));
     };
     const bool kept = n <= kPickKeep;
-    auto key4 = [&](int i) { return kept ? reinterpret_cast<const uint4*>(keys_kept)[i] : scored4(i); };
-    auto key = [&](int i) { return kept ? keys_kept[i] : (i >= lo && i < hi ? ordered(__ldcg(sc + i)) : 0u); };
+    auto four = [&](int i) { return kept ? reinterpret_cast<const float4*>(scores_kept)[i] : scored4(i); };
+    auto one = [&](int i) { return kept ? scores_kept[i] : competing(i, __ldcg(sc + i)); };
     if (need > 0) {
-        uint32_t kmin = 0xffffffffu, kmax = 0, mag = 0;
+        float smin = INFINITY, smax = none;
+        uint32_t mag = 0;
+        reinterpret_cast<int4*>(hist)[tid] = make_int4(0, 0, 0, 0);
+        if (tid < 32) list_s[tid] = none;
+        if (tid == 0) list_n = 0;
 #pragma unroll 1
-        for (int i = threadIdx.x; i < n4; i += kPickThreads) {
-            const uint4 k = scored4(i);
-            if (kept) reinterpret_cast<uint4*>(keys_kept)[i] = k;
-            // (k - 1: no key becomes the largest)
-            kmin = min(min(min(kmin, k.x - 1), k.y - 1), min(k.z - 1, k.w - 1));
-            kmax = max(max(max(kmax, k.x), k.y), max(k.z, k.w));
+        for (int i = tid; i < n4; i += kPickThreads) {
+            const float4 s = scored4(i);
+            if (kept) reinterpret_cast<float4*>(scores_kept)[i] = s;
+            smax = fmaxf(fmaxf(fmaxf(smax, s.x), s.y), fmaxf(s.z, s.w));
+            smin = fminf(fminf(fminf(smin, s.x == none ? INFINITY : s.x), s.y == none ? INFINITY : s.y),
+                         fminf(s.z == none ? INFINITY : s.z, s.w == none ? INFINITY : s.w));
         }
-        for (int i = threadIdx.x; i < (n + 7) / 8; i += kPickThreads)
-            mag = max(mag, __float_as_uint(__ldcg(p.mags + row * (p.stride / 8) + i)));
-        kmin = __reduce_min_sync(0xffffffffu, kmin) + 1;
-        kmax = __reduce_max_sync(0xffffffffu, kmax);
+        // (magnitudes are not negative, so their bits are ordered; NaN last)
+        if (8 * tid < n) mag = __float_as_uint(mag_ahead);
+        for (int i = tid + kPickThreads; i < (n + 7) / 8; i += kPickThreads) mag = max(mag, __float_as_uint(__ldcg(mags + i)));
+        uint32_t kmin = __reduce_min_sync(0xffffffffu, ordered(smin));
+        uint32_t kmax = __reduce_max_sync(0xffffffffu, ordered(smax));
         mag = __reduce_max_sync(0xffffffffu, mag);
-        if (lane == 0) range_w[warp] = make_uint4(kmin - 1, kmax, mag, 0u);
+        if (lane == 0) range_w[warp] = make_uint4(kmin, kmax, mag, 0u);
         __syncthreads();
         const uint4 r = lane < kPickWarps ? range_w[lane] : make_uint4(0xffffffffu, 0u, 0u, 0u);
-        kmin = __reduce_min_sync(0xffffffffu, r.x) + 1;
+        kmin = __reduce_min_sync(0xffffffffu, r.x);
         kmax = __reduce_max_sync(0xffffffffu, r.y);
         mag = __reduce_max_sync(0xffffffffu, r.z);
-        int above;
-        const uint32_t last = radix_pick(n4, need, kmax, 32 - __clz(kmin ^ kmax), hist, tot, found, key4, &above);
-        // 2 eps, and the range around the last page that FP32 cannot tell apart
-        const float t = unordered(last), e2 = fmaf(__uint_as_float(mag), (2 * p.G + 40) * 5.9604645e-8f, 1e-40f);
-        const float tu = t + e2, tl = t - e2;
-        top = tu == tu ? ordered(tu) : 0xffffffffu;
-        low = tl == tl ? ordered(tl) : 1u;
-        int over = 0, between = 0;
+        smin = unordered(kmin);
+        // Counters over equal steps of the scores' range: a few pages a step, so one pass
+        // usually leaves at most 32 to rank, one a lane (the roundings below are monotone,
+        // so a step holds a run of scores).  Scores that gather in one step, and ranges
+        // that FP32 does not hold, are told apart by their bits.
+        const float per_step = (kDigits - 1) / (unordered(kmax) - smin);
+        auto place = [&](float s) { return (s - smin) * per_step; };  // its step is the integer part; -inf: none
+        int listed = 0, over_list = 0;
+        float step = 0.f, mine = none, last = 0.f;       // (mine: a lane's listed score)
+        if (per_step > 0.f && per_step < INFINITY) {
 #pragma unroll 1
-        for (int i = threadIdx.x; i < n4; i += kPickThreads) {
-            const uint4 k = key4(i);
-            over += (k.x > top) + (k.y > top) + (k.z > top) + (k.w > top);
-            between += (k.x >= low) + (k.y >= low) + (k.z >= low) + (k.w >= low);
+            for (int i = tid; i < n4; i += kPickThreads) {
+                const float4 q = four(i);
+                const float s[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int at = static_cast<int>(place(s[j]));
+                    if (at >= 0) atomicAdd(&hist[min(at, kDigits - 1)], 1);
+                }
+            }
+            __syncthreads();
+            find_digit(hist, need, tot, found);
+            if (found[2] <= 32) {
+                const int left = found[1];
+                step = static_cast<float>(found[0]);
+                listed = found[2];
+                over_list = need - left;
+#pragma unroll 1
+                for (int i = tid; i < n4; i += kPickThreads) {
+                    const float4 q = four(i);
+                    const float s[4] = {q.x, q.y, q.z, q.w};
+                    unsigned in = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float at = place(s[j]);
+                        in |= at >= step && (at < step + 1.f || step == kDigits - 1) ? 1u << j : 0u;
+                    }
+                    for (; in != 0; in &= in - 1) {
+                        const int j = __ffs(in) - 1, to = atomicAdd(&list_n, 1);
+                        list_s[to] = j < 2 ? (j == 0 ? q.x : q.y) : (j == 2 ? q.z : q.w);
+                        list_i[to] = 4 * i + j;
+                    }
+                }
+                __syncthreads();
+                mine = list_s[lane];
+                int better = 0;
+                for (int j = 0; j < listed; j += 4) {
+                    const float4 o = *reinterpret_cast<const float4*>(list_s + j);
+                    better += (o.x > mine || (o.x == mine && j < lane)) + (o.y > mine || (o.y == mine && j + 1 < lane)) +
+                              (o.z > mine || (o.z == mine && j + 2 < lane)) + (o.w > mine || (o.w == mine && j + 3 < lane));
+                }
+                const unsigned at = __ballot_sync(0xffffffffu, lane < listed && better == left - 1);
+                last = __shfl_sync(0xffffffffu, mine, __ffs(at) - 1);
+            }
         }
-        int2 before, all;
-        warp_sums(__reduce_add_sync(0xffffffffu, over), __reduce_add_sync(0xffffffffu, between), sums, &before, &all);
-        const int n_over = all.x, n_between = all.y - all.x;
+        if (listed == 0) {
+            int above;
+            last = unordered(radix_pick(
+                n4, need, kmax, 32 - __clz(kmin ^ kmax), hist, tot, found,
+                [&](int i) {
+                    const float4 s = four(i);
+                    return make_uint4(s.x == none ? 0u : ordered(s.x), s.y == none ? 0u : ordered(s.y),
+                                      s.z == none ? 0u : ordered(s.z), s.w == none ? 0u : ordered(s.w));
+                },
+                &above));
+        }
+        // 2 eps, and the range around the last page that FP32 cannot tell apart (all pages,
+        // where that is NaN)
+        const float e2 = fmaf(__uint_as_float(mag), (2 * p.G + 40) * 5.9604645e-8f, 1e-40f);
+        top = last + e2;
+        low = fmaxf(last - e2, -3.402823466e38f);
+        if (!(top == top)) top = INFINITY;
+        // pages above the range and in it: from the listed ones, where they hold all of it
+        const bool in_list = listed > 0 && place(low) >= step && (place(top) < step + 1.f || step == kDigits - 1);
+        const unsigned doubtful = __ballot_sync(0xffffffffu, in_list && mine >= low && mine <= top);
+        int n_over, n_between;
+        if (in_list) {
+            n_over = over_list + __popc(__ballot_sync(0xffffffffu, mine > top));
+            n_between = __popc(doubtful);
+        } else {
+            int over = 0, between = 0;
+#pragma unroll 1
+            for (int i = tid; i < n4; i += kPickThreads) {
+                const float4 s = four(i);
+                over += (s.x > top) + (s.y > top) + (s.z > top) + (s.w > top);
+                between += (s.x >= low) + (s.y >= low) + (s.z >= low) + (s.w >= low);
+            }
+            int2 before, all;
+            warp_sums(__reduce_add_sync(0xffffffffu, over), __reduce_add_sync(0xffffffffu, between), sums, &before, &all);
+            n_over = all.x;
+            n_between = all.y - all.x;
+        }
         if (need - n_over < n_between) {
             // Score the pages between again, a warp a page.
             __shared__ float2 coef[2 * D];
@@ -717,17 +811,21 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
             const int places = need - n_over;
             if (kept && n_between <= 32) {
                 // the usual few: listed, scored a warp each and ranked by one warp; a taken page's
-                // key becomes the largest, another's 0
+                // score becomes the largest, another's the mark of those that do not compete
                 __shared__ int few[32], few_n;
                 __shared__ float2 few_s[32];
-                if (threadIdx.x == 0) few_n = 0;
-                __syncthreads();
-                for (int i = threadIdx.x; i < n4; i += kPickThreads) {
-                    const uint4 q = key4(i);
-                    const uint32_t k[4] = {q.x, q.y, q.z, q.w};
+                if (in_list) {
+                    if (warp == 0 && ((doubtful >> lane) & 1u)) few[__popc(doubtful & ((1u << lane) - 1u))] = list_i[lane];
+                } else {
+                    if (tid == 0) few_n = 0;
+                    __syncthreads();
+                    for (int i = tid; i < n4; i += kPickThreads) {
+                        const float4 q = four(i);
+                        const float s[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (k[j] <= top && k[j] >= low) few[atomicAdd(&few_n, 1)] = 4 * i + j;
+                        for (int j = 0; j < 4; ++j)
+                            if (s[j] <= top && s[j] >= low) few[atomicAdd(&few_n, 1)] = 4 * i + j;
+                    }
                 }
                 __syncthreads();
                 for (int j = warp; j < n_between; j += kPickWarps) {
@@ -743,14 +841,13 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
                         const uint32_t h2 = ordered(few_s[j].x), l2 = ordered(few_s[j].y);
                         better += h2 > h || (h2 == h && (l2 > l || (l2 == l && few[j] < i)));
                     }
-                    keys_kept[i] = better < places ? 0xffffffffu : 0u;  // above `top`, below `low`
+                    scores_kept[i] = better < places ? INFINITY : none;
                 }
-                __syncthreads();
-                low = max(low, 1u);
             } else {
+                ranked = true;
                 for (int i0 = warp * 32; i0 < n; i0 += kPickThreads) {
-                    const uint32_t k = i0 + lane < n ? key(i0 + lane) : 0u;
-                    unsigned todo = __ballot_sync(0xffffffffu, k != 0 && k <= top && k >= low);
+                    const float sx = i0 + lane < n ? one(i0 + lane) : none;
+                    unsigned todo = __ballot_sync(0xffffffffu, sx <= top && sx >= low);
                     while (todo) {
                         const int i = i0 + __ffs(todo) - 1;
                         todo &= todo - 1;
@@ -759,41 +856,40 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
                     }
                 }
                 __syncthreads();  // (the block's own writes to global memory are visible to it)
-                auto four = [&](int i, auto&& part) {
-                    const uint4 k = key4(i);
-                    uint4 r;
-                    r.x = k.x != 0 && k.x <= top && k.x >= low ? part(4 * i) : 0u;
-                    r.y = k.y != 0 && k.y <= top && k.y >= low ? part(4 * i + 1) : 0u;
-                    r.z = k.z != 0 && k.z <= top && k.z >= low ? part(4 * i + 2) : 0u;
-                    r.w = k.w != 0 && k.w <= top && k.w >= low ? part(4 * i + 3) : 0u;
-                    return r;
+                auto doubt4 = [&](int i, auto&& part) {
+                    const float4 s = four(i);
+                    uint4 r4;
+                    r4.x = s.x <= top && s.x >= low ? part(4 * i) : 0u;
+                    r4.y = s.y <= top && s.y >= low ? part(4 * i + 1) : 0u;
+                    r4.z = s.z <= top && s.z >= low ? part(4 * i + 2) : 0u;
+                    r4.w = s.w <= top && s.w >= low ? part(4 * i + 3) : 0u;
+                    return r4;
                 };
                 int above1, above2;
                 T = radix_pick(n4, places, 0u, 32, hist, tot, found,
-                               [&](int i) { return four(i, [&](int j) { return ordered(exact[j].x); }); }, &above1);
+                               [&](int i) { return doubt4(i, [&](int j) { return ordered(exact[j].x); }); }, &above1);
                 T2 = radix_pick(n4, places - above1, 0u, 32, hist, tot, found,
                                 [&](int i) {
-                                    return four(i, [&](int j) { return ordered(exact[j].x) == T ? ordered(exact[j].y) : 0u; });
+                                    return doubt4(i, [&](int j) { return ordered(exact[j].x) == T ? ordered(exact[j].y) : 0u; });
                                 },
                                 &above2);
                 ties = places - above1 - above2;
             }
         }
     }
-    // every warp takes a run of consecutive pages, 32 at a time: count, sum, write in order
+    // every warp takes a run of consecutive pages: count, sum, write in order
     __syncthreads();
     const unsigned lower = (1u << lane) - 1u;
     int2 before, all;
-    if (T == 0 && T2 == 0) {  // one threshold tells them all apart: four pages a lane
+    if (kept && need > 0 && !ranked) {  // one threshold tells them all apart: four pages a lane
+        for (int i = tid; i < p.first; i += kPickThreads) scores_kept[i] = INFINITY;
+        for (int i = tid; i < p.last; i += kPickThreads) scores_kept[n - 1 - i] = INFINITY;
+        __syncthreads();
         const int per = (n4 + kPickThreads - 1) / kPickThreads * 32;
         const int i0 = min(n4, warp * per), i1 = min(n4, i0 + per);
-        auto takes = [&](int i, int x, uint32_t k) { return i + x < n && (i + x < lo || i + x >= hi || k >= low); };
         auto flags = [&](int i4) -> unsigned {  // which of pages 4 i4 .. are taken
-            if (i4 >= i1) return 0u;
-            const uint4 k = need > 0 ? key4(i4) : make_uint4(0u, 0u, 0u, 0u);
-            const int i = 4 * i4;
-            return (takes(i, 0, k.x) ? 1u : 0u) | (takes(i, 1, k.y) ? 2u : 0u) | (takes(i, 2, k.z) ? 4u : 0u) |
-                   (takes(i, 3, k.w) ? 8u : 0u);
+            const float4 s = i4 < i1 ? reinterpret_cast<const float4*>(scores_kept)[i4] : make_float4(none, none, none, none);
+            return (s.x >= low ? 1u : 0u) | (s.y >= low ? 2u : 0u) | (s.z >= low ? 4u : 0u) | (s.w >= low ? 8u : 0u);
         };
         int taken = 0;
 #pragma unroll 1
@@ -816,9 +912,11 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
     const int i0 = min(n, warp * per), i1 = min(n, i0 + per);
     auto kind = [&](int i) -> int {  // 2: taken, 1: a tie, 0: not taken
         if (i < lo || i >= hi) return i < n ? 2 : 0;
-        const uint32_t k = key(i);
-        if (k > top) return 2;
-        if (k < low) return 0;
+        if (need == 0) return 0;
+        const float sx = one(i);
+        if (sx > top) return 2;
+        if (sx < low) return 0;
+        if (!ranked) return 2;
         const float2 s = exact[i];
         const uint32_t h = ordered(s.x);
         if (h != T) return h > T ? 2 : 0;
