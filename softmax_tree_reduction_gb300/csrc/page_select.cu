@@ -588,10 +588,11 @@ __device__ uint32_t radix_pick(int n4, int need, uint32_t first, int bits, int* 
     return prefix;
 }
 
-// Scores are finite or +inf (page_score_kernel); -inf here marks a page that does not
-// compete.  The block's passes over the scores are bound by instructions (four warps a
-// scheduler, one or two groups of four scores a thread), so they compare the scores
-// themselves, at two to four instructions a score.
+// Here the scores of the pages that compete are finite (the score kernel's +inf, a page
+// to take before any other, becomes FLT_MAX), +inf marks pages that are taken in any case
+// and -inf those that are not there.  The block is bound by the latencies of its short
+// passes and by the instructions of 16 warps that do the same, so the passes are few and
+// compare the scores themselves, at two to four instructions a score.
 template <int D, typename TQ, typename TB>
 __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const SelectParams p) {
     using PB = PageBounds<D, TB>;
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
     allow_dependents();
     const int g = blockIdx.x, b = blockIdx.y;
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
-    const float none = -INFINITY;
+    constexpr float none = -INFINITY, always = INFINITY, most = 3.402823466e38f;
     int32_t* sel = p.selected + (static_cast<int64_t>(b) * p.Hkv + g) * p.num_select;
     const int64_t row = static_cast<int64_t>(b) * p.Hkv + g;
     const float* sc = p.scores + row * p.stride;
@@ -633,32 +634,38 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
     const int n4 = (n + 3) / 4;
     // Pages above `top` are taken, pages below `low` are not; those between are
     // taken, or, once `ranked`, where their exact sums (T, T2) say so.
-    float top = INFINITY, low = INFINITY;
+    float top = always, low = always;
     uint32_t T = 0, T2 = 0;
     int ties = 0;                                        // pages at (T, T2) to take, lowest first
     bool ranked = false;
-    auto competing = [&](int i, float s) { return i >= lo && i < hi ? s : none; };
+    auto marked = [&](int i, float s) { return i >= lo && i < hi ? fminf(s, most) : (i < n ? always : none); };
     auto scored4 = [&](int i) {
         const float4 s = i == tid ? ahead[0] : (i == tid + kPickThreads ? ahead[1] : __ldcg(reinterpret_cast<const float4*>(sc) + i));
-        return make_float4(competing(4 * i, s.x), competing(4 * i + 1, s.y), competing(4 * i + 2, s.z), competing(4 * i + 3, s.w));
+        return make_float4(marked(4 * i, s.x), marked(4 * i + 1, s.y), marked(4 * i + 2, s.z), marked(4 * i + 3, s.w));
     };
     const bool kept = n <= kPickKeep;
     auto four = [&](int i) { return kept ? reinterpret_cast<const float4*>(scores_kept)[i] : scored4(i); };
-    auto one = [&](int i) { return kept ? scores_kept[i] : competing(i, __ldcg(sc + i)); };
-    if (need > 0) {
-        float smin = INFINITY, smax = none;
-        uint32_t mag = 0;
-        reinterpret_cast<int4*>(hist)[tid] = make_int4(0, 0, 0, 0);
-        if (tid < 32) list_s[tid] = none;
-        if (tid == 0) list_n = 0;
+    auto one = [&](int i) { return kept ? scores_kept[i] : marked(i, __ldcg(sc + i)); };
+    // Every warp takes a run of consecutive pages, [4 i0, 4 i1), to count and to write.
+    const int run = (n4 + kPickThreads - 1) / kPickThreads * 32, i0 = min(n4, warp * run), i1 = min(n4, i0 + run);
+    int taken_before = -1;                               // pages taken in the runs before this one (-1: not counted)
+    float smin = always, smax = none;
+    reinterpret_cast<int4*>(hist)[tid] = make_int4(0, 0, 0, 0);
+    if (tid < 32) list_s[tid] = none;
+    if (tid == 0) list_n = 0;
+    if (kept || need > 0) {
 #pragma unroll 1
         for (int i = tid; i < n4; i += kPickThreads) {
             const float4 s = scored4(i);
             if (kept) reinterpret_cast<float4*>(scores_kept)[i] = s;
-            smax = fmaxf(fmaxf(fmaxf(smax, s.x), s.y), fmaxf(s.z, s.w));
-            smin = fminf(fminf(fminf(smin, s.x == none ? INFINITY : s.x), s.y == none ? INFINITY : s.y),
-                         fminf(s.z == none ? INFINITY : s.z, s.w == none ? INFINITY : s.w));
+            auto high = [&](float x) { return x == always ? none : x; };
+            auto least = [&](float x) { return x == none ? always : x; };
+            smax = fmaxf(fmaxf(fmaxf(smax, high(s.x)), high(s.y)), fmaxf(high(s.z), high(s.w)));
+            smin = fminf(fminf(fminf(smin, least(s.x)), least(s.y)), fminf(least(s.z), least(s.w)));
         }
+    }
+    if (need > 0) {
+        uint32_t mag = 0;
         // (magnitudes are not negative, so their bits are ordered; NaN last)
         if (8 * tid < n) mag = __float_as_uint(mag_ahead);
         for (int i = tid + kPickThreads; i < (n + 7) / 8; i += kPickThreads) mag = max(mag, __float_as_uint(__ldcg(mags + i)));
@@ -677,7 +684,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
         // so a step holds a run of scores).  Scores that gather in one step, and ranges
         // that FP32 does not hold, are told apart by their bits.
         const float per_step = (kDigits - 1) / (unordered(kmax) - smin);
-        auto place = [&](float s) { return (s - smin) * per_step; };  // its step is the integer part; -inf: none
+        auto place = [&](float s) { return (s - smin) * per_step; };  // its step is the integer part, below kDigits
         int listed = 0, over_list = 0;
         float step = 0.f, mine = none, last = 0.f;       // (mine: a lane's listed score)
         if (per_step > 0.f && per_step < INFINITY) {
@@ -688,7 +695,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int at = static_cast<int>(place(s[j]));
-                    if (at >= 0) atomicAdd(&hist[min(at, kDigits - 1)], 1);
+                    if (static_cast<unsigned>(at) < kDigits) atomicAdd(&hist[at], 1);
                 }
             }
             __syncthreads();
@@ -698,15 +705,17 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
                 step = static_cast<float>(found[0]);
                 listed = found[2];
                 over_list = need - left;
+                int sure = 0;                            // pages of the run in the steps above
 #pragma unroll 1
-                for (int i = tid; i < n4; i += kPickThreads) {
+                for (int i = i0 + lane; i < i1; i += 32) {
                     const float4 q = four(i);
                     const float s[4] = {q.x, q.y, q.z, q.w};
                     unsigned in = 0;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float at = place(s[j]);
-                        in |= at >= step && (at < step + 1.f || step == kDigits - 1) ? 1u << j : 0u;
+                        sure += at >= step + 1.f;
+                        in |= at >= step && at < step + 1.f ? 1u << j : 0u;
                     }
                     for (; in != 0; in &= in - 1) {
                         const int j = __ffs(in) - 1, to = atomicAdd(&list_n, 1);
@@ -714,6 +723,8 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
                         list_i[to] = 4 * i + j;
                     }
                 }
+                sure = __reduce_add_sync(0xffffffffu, sure);
+                if (lane == 0) sums[warp].x = sure;
                 __syncthreads();
                 mine = list_s[lane];
                 int better = 0;
@@ -732,19 +743,18 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
                 n4, need, kmax, 32 - __clz(kmin ^ kmax), hist, tot, found,
                 [&](int i) {
                     const float4 s = four(i);
-                    return make_uint4(s.x == none ? 0u : ordered(s.x), s.y == none ? 0u : ordered(s.y),
-                                      s.z == none ? 0u : ordered(s.z), s.w == none ? 0u : ordered(s.w));
+                    auto bits = [&](float x) { return fabsf(x) == always ? 0u : ordered(x); };
+                    return make_uint4(bits(s.x), bits(s.y), bits(s.z), bits(s.w));
                 },
                 &above));
         }
         // 2 eps, and the range around the last page that FP32 cannot tell apart (all pages,
         // where that is NaN)
         const float e2 = fmaf(__uint_as_float(mag), (2 * p.G + 40) * 5.9604645e-8f, 1e-40f);
-        top = last + e2;
-        low = fmaxf(last - e2, -3.402823466e38f);
-        if (!(top == top)) top = INFINITY;
+        top = fminf(last + e2, most);
+        low = fmaxf(last - e2, -most);
         // pages above the range and in it: from the listed ones, where they hold all of it
-        const bool in_list = listed > 0 && place(low) >= step && (place(top) < step + 1.f || step == kDigits - 1);
+        const bool in_list = listed > 0 && place(low) >= step && place(top) < step + 1.f;
         const unsigned doubtful = __ballot_sync(0xffffffffu, in_list && mine >= low && mine <= top);
         int n_over, n_between;
         if (in_list) {
@@ -755,13 +765,14 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
 #pragma unroll 1
             for (int i = tid; i < n4; i += kPickThreads) {
                 const float4 s = four(i);
+                auto in = [&](float x) { return x >= low && x <= top; };
                 over += (s.x > top) + (s.y > top) + (s.z > top) + (s.w > top);
-                between += (s.x >= low) + (s.y >= low) + (s.z >= low) + (s.w >= low);
+                between += in(s.x) + in(s.y) + in(s.z) + in(s.w);
             }
             int2 before, all;
             warp_sums(__reduce_add_sync(0xffffffffu, over), __reduce_add_sync(0xffffffffu, between), sums, &before, &all);
-            n_over = all.x;
-            n_between = all.y - all.x;
+            n_over = all.x - p.first - p.last;
+            n_between = all.y;
         }
         if (need - n_over < n_between) {
             // Score the pages between again, a warp a page.
@@ -841,7 +852,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
                         const uint32_t h2 = ordered(few_s[j].x), l2 = ordered(few_s[j].y);
                         better += h2 > h || (h2 == h && (l2 > l || (l2 == l && few[j] < i)));
                     }
-                    scores_kept[i] = better < places ? INFINITY : none;
+                    scores_kept[i] = better < places ? always : none;
                 }
             } else {
                 ranked = true;
@@ -875,27 +886,27 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
                                 &above2);
                 ties = places - above1 - above2;
             }
+        } else if (in_list) {  // the steps above, and the listed pages that are taken
+            taken_before = __reduce_add_sync(0xffffffffu, lane < warp ? sums[lane].x : 0) +
+                           __popc(__ballot_sync(0xffffffffu, mine >= low && list_i[lane] < 4 * i0));
         }
     }
-    // every warp takes a run of consecutive pages: count, sum, write in order
-    __syncthreads();
     const unsigned lower = (1u << lane) - 1u;
     int2 before, all;
-    if (kept && need > 0 && !ranked) {  // one threshold tells them all apart: four pages a lane
-        for (int i = tid; i < p.first; i += kPickThreads) scores_kept[i] = INFINITY;
-        for (int i = tid; i < p.last; i += kPickThreads) scores_kept[n - 1 - i] = INFINITY;
-        __syncthreads();
-        const int per = (n4 + kPickThreads - 1) / kPickThreads * 32;
-        const int i0 = min(n4, warp * per), i1 = min(n4, i0 + per);
-        auto flags = [&](int i4) -> unsigned {  // which of pages 4 i4 .. are taken
-            const float4 s = i4 < i1 ? reinterpret_cast<const float4*>(scores_kept)[i4] : make_float4(none, none, none, none);
+    if (kept && !ranked) {  // one threshold tells them all apart: four pages a lane
+        auto flags = [&](int i) -> unsigned {  // which of pages 4 i .. are taken
+            const float4 s = i < i1 ? reinterpret_cast<const float4*>(scores_kept)[i] : make_float4(none, none, none, none);
             return (s.x >= low ? 1u : 0u) | (s.y >= low ? 2u : 0u) | (s.z >= low ? 4u : 0u) | (s.w >= low ? 8u : 0u);
         };
-        int taken = 0;
+        if (taken_before < 0) {
+            __syncthreads();
+            int taken = 0;
 #pragma unroll 1
-        for (int i = i0; i < i1; i += 32) taken += __popc(flags(i + lane));
-        warp_sums(__reduce_add_sync(0xffffffffu, taken), 0, sums, &before, &all);
-        int at = before.x;
+            for (int i = i0; i < i1; i += 32) taken += __popc(flags(i + lane));
+            warp_sums(__reduce_add_sync(0xffffffffu, taken), 0, sums, &before, &all);
+            taken_before = before.x;
+        }
+        int at = taken_before;
 #pragma unroll 1
         for (int i = i0; i < i1; i += 32) {
             unsigned f = flags(i + lane);
@@ -908,11 +919,10 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
         }
         return;
     }
-    const int per = (n + kPickThreads - 1) / kPickThreads * 32;
-    const int i0 = min(n, warp * per), i1 = min(n, i0 + per);
+    __syncthreads();
+    const int j0 = min(n, 4 * i0), j1 = min(n, 4 * i1);
     auto kind = [&](int i) -> int {  // 2: taken, 1: a tie, 0: not taken
-        if (i < lo || i >= hi) return i < n ? 2 : 0;
-        if (need == 0) return 0;
+        if (i >= j1) return 0;
         const float sx = one(i);
         if (sx > top) return 2;
         if (sx < low) return 0;
@@ -924,14 +934,14 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
         return l > T2 ? 2 : (l == T2 ? 1 : 0);
     };
     int taken = 0, equal = 0;
-    for (int i = i0; i < i1; i += 32) {
+    for (int i = j0; i < j1; i += 32) {
         const int k = kind(i + lane);
         taken += __popc(__ballot_sync(0xffffffffu, k == 2));
         equal += __popc(__ballot_sync(0xffffffffu, k == 1));
     }
     warp_sums(taken, equal, sums, &before, &all);
     int eq = before.y, at = before.x + min(before.y, ties);  // ties and places before this warp
-    for (int i = i0; i < i1; i += 32) {
+    for (int i = j0; i < j1; i += 32) {
         const int k = kind(i + lane);
         const unsigned eqs = __ballot_sync(0xffffffffu, k == 1);
         const bool take = k == 2 || (k == 1 && eq + __popc(eqs & lower) < ties);
