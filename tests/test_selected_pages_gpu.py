@@ -433,3 +433,28 @@ def test_decode_selected_much_work(kv, d, G):
     to, tl = TOL[kv]
     assert (out.cpu().double() - want).abs().max() <= to and (lse.cpu().double() - wl).abs().max() <= tl
     assert ta.tree_attn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("bdt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("alike", [1, 2, 31, 32, 33, 200])
+def test_select_pages_outliers_and_pages_alike(bdt, alike):
+    """The last places fall among `alike` equal pages, at the numbers where the ways of telling
+    pages apart change over; pages far above the others, forced or not, stretch the range."""
+    d, page, n, nsel = 128, 16, 2011, 300
+    g = torch.Generator().manual_seed(alike)
+    q = torch.randn(1, 4, d, generator=g).to(bdt)
+    lens = torch.tensor([n * page - 3], dtype=torch.int32)
+    base = page_ranges(g, n, 1, d, bdt)
+    for scaled, by in (([], 1.0), ([0, n - 1], 3.0e4), ([0, 700, n - 1], 3.0e4), ([700], 1.0e34), ([3, 1500], 1.0e37), (list(range(n)), 1.0e-30)):
+        bounds = base.clone()
+        bounds[scaled] = (bounds[scaled].float() * by).to(bdt)
+        bt = torch.arange(n).view(1, n)
+        scores = ref.page_scores(q[0], bounds, bt[0], 0, 4)
+        edge = scores.argsort(descending=True)[nsel - 20]    # one of the last to be listed
+        same = torch.randperm(n - 1000, generator=g)[:alike - 1] + 900    # pages that repeat one of the listed
+        bt[0, same] = edge
+        bt = bt.to(torch.int32)
+        for first, last in ((1, 1), (0, 0), (2, 40), (150, 150)):
+            sel = ta.tree_attn_select_pages(q.cuda(), bounds.cuda(), bt.cuda(), lens.cuda(), page, nsel, first, last)
+            assert torch.equal(sel.cpu(), ref.select_pages(q, bounds, bt, lens, page, nsel, first, last)), (scaled, first, last)
+    assert ta.tree_attn_get_device_error() == 0
