@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
     if (tid < 32) list_s[tid] = none;
     if (tid == 0) list_n = 0;
     if (kept || need > 0) {
-#pragma unroll 1
+#pragma unroll 4
         for (int i = tid; i < n4; i += kPickThreads) {
             const float4 s = scored4(i);
             if (kept) reinterpret_cast<float4*>(scores_kept)[i] = s;
