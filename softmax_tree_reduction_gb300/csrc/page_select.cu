@@ -297,14 +297,14 @@ __device__ __forceinline__ float2 coefficient(const SelectParams& p, int b, int 
     return make_float2(s, e);
 }
 
-// A lane's coefficients in FP32, G roundings each: lanes 0 .. 15 those of the minima,
-// the others those of the maxima, E = D / 16 channels each.  (Short on purpose: this
+// A lane's coefficients in FP32, G roundings each: of the 2 D / E lanes that share a page
+// the first half those of the minima, the others those of the maxima, E channels each.  (Short on purpose: this
 // runs once per warp, and instruction fetches of a longer version cost 3.6 us.)
-template <int D, typename TQ>
-__device__ __forceinline__ void coefficients(const SelectParams& p, int b, int g, int lane, float (&c)[D / 16]) {
-    constexpr int E = D / 16;
-    const float sign = lane >= 16 ? 1.f : -1.f;
-    const TQ* q = static_cast<const TQ*>(p.q) + (static_cast<size_t>(b) * p.Hq + g * p.G) * D + (lane & 15) * E;
+template <int D, typename TQ, int E>
+__device__ __forceinline__ void coefficients(const SelectParams& p, int b, int g, int lane, float (&c)[E]) {
+    constexpr int kHalf = D / E;
+    const float sign = (lane & kHalf) ? 1.f : -1.f;
+    const TQ* q = static_cast<const TQ*>(p.q) + (static_cast<size_t>(b) * p.Hq + g * p.G) * D + (lane & (kHalf - 1)) * E;
 #pragma unroll
     for (int i = 0; i < E; ++i) c[i] = 0.f;
 #pragma unroll 4
@@ -380,31 +380,36 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src) {
     }
 }
 
-// A warp's ring of page groups (8 pages of bounds each) in shared memory.
+// A warp's ring of page groups in shared memory: 8 pages of bounds, or 16 where those of one
+// are 256 bytes, which 16 lanes hold.  (With all lanes at every page, 64 channels took 42.9 us for
+// 16 rows x 8 heads x 4096 pages, with 16 lanes 31.3: the sums over the lanes cost as much as at 128.)
 template <int D, typename TB>
 struct ScoreRing {
-    static constexpr int kLane = PageBounds<D, TB>::E * static_cast<int>(sizeof(TB));  // bytes a lane: 8, 16 or 32
+    static constexpr int kPages = 2 * D * sizeof(TB) == 256 ? 2 : 1;  // side by side in a warp
+    using Bounds = PageBounds<kPages * D, TB>;                           // a lane's share
+    static constexpr int kGroupPages = 8 * kPages;
+    static constexpr int kLane = Bounds::E * static_cast<int>(sizeof(TB));  // bytes: 16 or 32
     static constexpr int kGroup = 8 * 32 * kLane;
     static constexpr int kStages = 2;
-    static constexpr int kSmem = kScoreWarps * kStages * kGroup;  // 32, 64 or 128 KB
+    static constexpr int kSmem = kScoreWarps * kStages * kGroup;  // 64 or 128 KB
     static constexpr int kBlocks = kLane == 32 ? 1 : 3;           // an SM
 };
 
 // Pages [blockIdx.x * per_block, ..) of row blockIdx.z for HB KV heads: warp w takes
-// head blockIdx.y HB + w % HB, 8 pages at a time.  The bounds arrive by cp.async a
+// head blockIdx.y HB + w % HB, 8 or 16 pages at a time.  The bounds arrive by cp.async a
 // group ahead; each lane reads only what it copied, so waiting for its own copies is
 // enough, and there is no barrier at all.  Issue and HBM bind it about equally:
 // some 60 instructions a page and head, 13.5 us for 131072 page scores (67 MB, 9.9 us
 // at the copy rate; the ring against loads into registers: 14.3).
 template <int D, typename TQ, typename TB>
 __global__ void __launch_bounds__(kScoreThreads, ScoreRing<D, TB>::kBlocks) page_score_kernel(const SelectParams p) {
-    using PB = PageBounds<D, TB>;
     using Ring = ScoreRing<D, TB>;
-    constexpr int E = PB::E, kStages = Ring::kStages;
+    using PB = typename Ring::Bounds;
+    constexpr int E = PB::E, kStages = Ring::kStages, H = Ring::kPages, W = 32 / H;  // W lanes hold a page
     extern __shared__ __align__(16) uint8_t ring_all[];
     wait_primary();
     allow_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ll = lane % W, side = lane / W;
     const int g = blockIdx.y * p.hb + warp % p.hb, b = blockIdx.z;
     if (g >= p.Hkv) return;
     const int N = p.seqlens[b];
@@ -412,17 +417,17 @@ __global__ void __launch_bounds__(kScoreThreads, ScoreRing<D, TB>::kBlocks) page
     const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.max_pages;
     float* scores = p.scores + (static_cast<int64_t>(b) * p.Hkv + g) * p.stride;
     float* mags = p.mags + (static_cast<int64_t>(b) * p.Hkv + g) * (p.stride / 8);
-    const TB* bounds = static_cast<const TB*>(p.bounds) + static_cast<int64_t>(g) * 2 * D + lane * E;
+    const TB* bounds = static_cast<const TB*>(p.bounds) + static_cast<int64_t>(g) * 2 * D + ll * E;
     uint8_t* ring = ring_all + warp * kStages * Ring::kGroup + lane * Ring::kLane;
-    const int kStep = kScoreWarps / p.hb * 8;
-    auto lookup = [&](int q) { return (lane < 8 && q + lane < pmax) ? __ldg(table + q + lane) : -1; };
+    const int kStep = kScoreWarps / p.hb * Ring::kGroupPages;
+    auto lookup = [&](int q) { return (lane < Ring::kGroupPages && q + lane < pmax) ? __ldg(table + q + lane) : -1; };
     // start the copies of one group into `stage`; which of its pages are in the pool
     auto issue = [&](int phys, int stage) -> unsigned {
         const unsigned ok = __ballot_sync(0xffffffffu, phys >= 0 && phys < p.num_pages);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int ph = __shfl_sync(0xffffffffu, phys, j);
-            if ((ok >> j) & 1u)
+            const int ph = __shfl_sync(0xffffffffu, phys, j * H + side);
+            if ((ok >> (j * H + side)) & 1u)
                 copy_async<Ring::kLane>(ring + stage * Ring::kGroup + j * 32 * Ring::kLane,
                                         bounds + static_cast<int64_t>(ph) * p.Hkv * 2 * D);
         }
@@ -430,7 +435,7 @@ __global__ void __launch_bounds__(kScoreThreads, ScoreRing<D, TB>::kBlocks) page
         return ok;
     };
     // the first groups are on their way while the length arrives and the coefficients are summed
-    int q0 = p0 + warp / p.hb * 8;
+    int q0 = p0 + warp / p.hb * Ring::kGroupPages;
     unsigned ok[kStages] = {};
     {
         int phys[kStages - 1];
@@ -441,7 +446,7 @@ __global__ void __launch_bounds__(kScoreThreads, ScoreRing<D, TB>::kBlocks) page
     }
     int phys = lookup(q0 + (kStages - 1) * kStep);
     float c[E];
-    coefficients<D, TQ>(p, b, g, lane, c);
+    coefficients<D, TQ, E>(p, b, g, lane, c);
     const bool bad = N < 0 || N > p.S;                // the selection reports it
     const int n = bad ? 0 : static_cast<int>((static_cast<int64_t>(N) + (1 << p.page_shift) - 1) >> p.page_shift);
     const int p1 = n <= p.num_select ? 0 : min(n, pmax);  // 0: every page is taken
@@ -468,10 +473,10 @@ __global__ void __launch_bounds__(kScoreThreads, ScoreRing<D, TB>::kBlocks) page
             }
         }
         stage = stage == kStages - 1 ? 0 : stage + 1;
-        // 8 pages over 32 lanes: halve the pages held three times, then the lanes
+        // 8 pages over W lanes: halve the pages held three times, then the lanes
 #pragma unroll
         for (int st = 0; st < 3; ++st) {
-            const int off = 16 >> st, half = 4 >> st;
+            const int off = (W / 2) >> st, half = 4 >> st;
             const bool up = (lane & off) != 0;
 #pragma unroll
             for (int j = 0; j < half; ++j) {
@@ -482,20 +487,20 @@ __global__ void __launch_bounds__(kScoreThreads, ScoreRing<D, TB>::kBlocks) page
             }
         }
 #pragma unroll
-        for (int off = 2; off > 0; off >>= 1) {
+        for (int off = W / 16; off > 0; off >>= 1) {
             s[0] += __shfl_xor_sync(0xffffffffu, s[0], off);
             m[0] += __shfl_xor_sync(0xffffffffu, m[0], off);
         }
-        const int mine = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
+        const int mine = ll / (W / 8) * H + side;
         const bool mine_in = q0 + mine < p1;
         // (a page outside the pool: its sums are of whatever the ring held, and are not used)
         const bool fin = ((here >> mine) & 1u) && fabsf(s[0]) < INFINITY;
-        if ((lane & 3) == 0 && mine_in) scores[q0 + mine] = fin ? s[0] + 0.f : INFINITY;  // + 0: one zero
+        if (ll % (W / 8) == 0 && mine_in) scores[q0 + mine] = fin ? s[0] + 0.f : INFINITY;  // + 0: one zero
         // (magnitudes are not negative, so their bits are ordered; NaN last.  Pages that are taken
         // in any case do not count: keys of a first page are often far larger than the others)
         const bool competes = q0 + mine >= p.first && q0 + mine < min(p1, n - p.last);
         const uint32_t big = __reduce_max_sync(0xffffffffu, competes && fin ? __float_as_uint(m[0]) : 0u);
-        if (lane == 0) mags[q0 >> 3] = __uint_as_float(big);
+        if (lane < H && q0 + 8 * lane < p1) mags[(q0 >> 3) + lane] = __uint_as_float(big);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");  // no copy outlives the block
 }
@@ -1006,11 +1011,11 @@ int launch_select(SelectParams p, const DeviceInfo& dev, cudaStream_t s) {
         static std::atomic<unsigned long long> score_configured{0};
         if (set_smem_once(page_score_kernel<D, TQ, TB>, Ring::kSmem, score_configured) != cudaSuccess) return TA_ERR_CUDA;
         p.hb = p.Hkv >= 8 ? 8 : (p.Hkv >= 4 ? 4 : (p.Hkv >= 2 ? 2 : 1));
-        const int step = kScoreWarps / p.hb * 8;
+        const int step = kScoreWarps / p.hb * Ring::kGroupPages;
         const int64_t rows = static_cast<int64_t>(p.B) * ((p.Hkv + p.hb - 1) / p.hb);
         const int64_t per_row = std::max<int64_t>(1, Ring::kBlocks * static_cast<int64_t>(dev.num_sms) / rows);
-        const int64_t per = std::max<int64_t>(step, ((p.pages + per_row - 1) / per_row + 7) / 8 * 8);
-        p.per_block = static_cast<int>(std::min<int64_t>(per, (static_cast<int64_t>(p.pages) + 7) / 8 * 8));
+        const int64_t per = std::max<int64_t>(step, ((p.pages + per_row - 1) / per_row + Ring::kGroupPages - 1) / Ring::kGroupPages * Ring::kGroupPages);
+        p.per_block = static_cast<int>(std::min<int64_t>(per, (static_cast<int64_t>(p.pages) + Ring::kGroupPages - 1) / Ring::kGroupPages * Ring::kGroupPages));
         const dim3 grid((p.pages + p.per_block - 1) / p.per_block, (p.Hkv + p.hb - 1) / p.hb, p.B);
         if (launch(page_score_kernel<D, TQ, TB>, grid, kScoreThreads, Ring::kSmem, p, s) != cudaSuccess) return TA_ERR_CUDA;
     }
