@@ -1010,7 +1010,10 @@ int launch_select(SelectParams p, const DeviceInfo& dev, cudaStream_t s) {
         using Ring = ScoreRing<D, TB>;
         static std::atomic<unsigned long long> score_configured{0};
         if (set_smem_once(page_score_kernel<D, TQ, TB>, Ring::kSmem, score_configured) != cudaSuccess) return TA_ERR_CUDA;
-        p.hb = p.Hkv >= 8 ? 8 : (p.Hkv >= 4 ? 4 : (p.Hkv >= 2 ? 2 : 1));
+        // heads of a page side by side in a block (their bounds are), as many as leave at most a
+        // fifth of its warps without one (9 heads, 4096 pages: 10.6 us against 12.1 as 2 x 8)
+        p.hb = 8;
+        while (p.hb > 1 && 5 * p.Hkv < 4 * ((p.Hkv + p.hb - 1) / p.hb * p.hb)) p.hb >>= 1;
         const int step = kScoreWarps / p.hb * Ring::kGroupPages;
         const int64_t rows = static_cast<int64_t>(p.B) * ((p.Hkv + p.hb - 1) / p.hb);
         const int64_t per_row = std::max<int64_t>(1, Ring::kBlocks * static_cast<int64_t>(dev.num_sms) / rows);
