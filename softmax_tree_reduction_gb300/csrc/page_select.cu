@@ -198,9 +198,12 @@ struct Range<E4m3> {
 // One warp per (row, page, KV head), heads fastest: a token's heads are
 // neighbours in token-major pools.  16 bytes a lane, the lanes of a warp
 // covering 32 / LT tokens at a time, F of its loads in flight.  Few pages (a decode
-// step) are a matter of latency: F = 8 (3.1 us for 128 E4M3 pages, 3.5 with 4); many
+// step) are a matter of latency: F = 8, and the rest of a page four loads at a time, the
+// last token again in place of those behind it (which changes no minimum or maximum):
+// 128 partly filled E4M3 pages of 64 tokens take 3.5 us, one load after the other 4.2.  Many
 // are read faster with F = 4 and more warps (16384 BF16 pages of 64 tokens, 268 MB:
-// 43.5 us against 45.0; 39.6 at the copy rate).
+// 43.5 us against 45.0; 39.6 at the copy rate), of BF16 and FP32 caches with a plain loop
+// (45.5 with repeated tokens), of E4M3 ones not (26.7 against 28.4).
 template <int D, typename T, int F>
 __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const BoundsParams p) {
     constexpr int E = Range<T>::kElems;
@@ -235,15 +238,34 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
     const uint8_t* base = static_cast<const uint8_t*>(p.k) + (phys * p.sb + g * p.sh + ch) * es;
     Range<T> r;
     r.init();
-    int t = tok;
-    for (; t + (F - 1) * TW < nv; t += F * TW) {
-        uint4 x[F];
+    auto load = [&](int i) { return __ldg(reinterpret_cast<const uint4*>(base + i * p.st * es)); };
+    if constexpr (F == 4 && es > 1) {
+        int t = tok;
+        for (; t + (F - 1) * TW < nv; t += F * TW) {
+            uint4 x[F];
 #pragma unroll
-        for (int j = 0; j < F; ++j) x[j] = __ldg(reinterpret_cast<const uint4*>(base + (t + j * TW) * p.st * es));
+            for (int j = 0; j < F; ++j) x[j] = load(t + j * TW);
 #pragma unroll
-        for (int j = 0; j < F; ++j) r.add(x[j]);
+            for (int j = 0; j < F; ++j) r.add(x[j]);
+        }
+        for (; t < nv; t += TW) r.add(load(t));
+    } else {
+        int t = 0;
+        for (; F > 4 && t + F * TW <= nv; t += F * TW) {
+            uint4 x[F];
+#pragma unroll
+            for (int j = 0; j < F; ++j) x[j] = load(t + tok + j * TW);
+#pragma unroll
+            for (int j = 0; j < F; ++j) r.add(x[j]);
+        }
+        for (; t < nv; t += 4 * TW) {
+            uint4 x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = load(min(t + tok + j * TW, nv - 1));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r.add(x[j]);
+        }
     }
-    for (; t < nv; t += TW) r.add(__ldg(reinterpret_cast<const uint4*>(base + t * p.st * es)));
     __syncwarp();
 #pragma unroll
     for (int off = LT; off < 32; off <<= 1) r.merge(off);
