@@ -170,8 +170,13 @@ ta_rope rope_of(int64_t d, const Tensor* inv_freq, const Tensor* qw, const Tenso
     return r;
 }
 
-// A stride of a cache axis; an axis of one entry may carry any, so it gets a valid one.
-int64_t cache_stride(const Tensor& t, int axis) { return t.size(axis) > 1 ? t.stride(axis) : 128; }
+// A stride of a cache axis; an axis of one entry may carry any, so it gets a valid one.  (Strides
+// of 0 on every axis would mean a dense cache to the C call, whatever memory is behind the view.)
+int64_t cache_stride(const Tensor& t, int axis) {
+    if (t.size(axis) <= 1) return 128;
+    if (t.stride(axis) == 0) throw BadValue("a cache's entries must not share memory: an axis of several has stride 0");
+    return t.stride(axis);
+}
 
 void check_table(const Tensor& bt) {
     if (bt.scalar_type() != at::kInt || bt.dim() != 2 || !bt.is_contiguous())
@@ -325,8 +330,6 @@ PyObject* cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (!q != !qo) throw BadValue("q and q_out go together");
         if (q && !turned) throw BadValue("q needs a norm or a rotation");
         if (!norm && (qw || kw)) throw BadValue("norm weights need norm=True");
-        Device dev;
-        for (const Tensor* t : {&k, &v, &kc, &vc, &pos, rows, bt, ks, vs, q, qo, f, qw, kw}) dev.add(t);
         like(k, v, "k and v");
         CacheCall c(kc, vc, pos, rows, bt, a[17], k);
         const ta_heads hk = heads(k, "k"), hv = heads(v, "v");
@@ -342,6 +345,8 @@ PyObject* cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
         ta_rope r;
         if (turned) r = rope_of(k.size(2), f, qw, kw, norm, real(a[15]), truth(a[16]));
         const float *pks = scales(ks, "k_scale", c.shape.num_kv_heads), *pvs = scales(vs, "v_scale", c.shape.num_kv_heads);
+        Device dev;
+        for (const Tensor* t : {&k, &v, &kc, &vc, &pos, rows, bt, ks, vs, q, qo, f, qw, kw}) dev.add(t);
         void* st = dev.stream(a[18]);
         return enqueue([&] {
             return p_cache_write(&c.shape, c.pages, &c.tokens, turned ? &r : nullptr, q ? &hq : nullptr, q ? &hqo : nullptr, &hk, &hv,
@@ -356,12 +361,12 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Tensor &kc = need(a[0], "k_cache"), &vc = need(a[1], "v_cache"), &pos = need(a[2], "positions"), &ko = need(a[7], "k_out"),
                      &vo = need(a[8], "v_out");
         const Tensor *rows = opt(a[3], "rows"), *bt = opt(a[4], "block_table"), *ks = opt(a[5], "k_scale"), *vs = opt(a[6], "v_scale");
-        Device dev;
-        for (const Tensor* t : {&kc, &vc, &pos, &ko, &vo, rows, bt, ks, vs}) dev.add(t);
         like(ko, vo, "k_out and v_out");
         CacheCall c(kc, vc, pos, rows, bt, a[9], ko);
         const ta_heads hk = heads(ko, "k_out", true), hv = heads(vo, "v_out", true);
         const float *pks = scales(ks, "k_scale", c.shape.num_kv_heads), *pvs = scales(vs, "v_scale", c.shape.num_kv_heads);
+        Device dev;
+        for (const Tensor* t : {&kc, &vc, &pos, &ko, &vo, rows, bt, ks, vs}) dev.add(t);
         void* st = dev.stream(a[10]);
         return enqueue([&] { return p_cache_read(&c.shape, c.pages, &c.tokens, kc.data_ptr(), vc.data_ptr(), &hk, &hv, pks, pvs, st); });
     });
@@ -377,8 +382,6 @@ void check_bounds(const Tensor& b, int64_t pages, int64_t hkv, int64_t d, bool f
 PyObject* page_bounds(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 7, [&] {
         const Tensor &k = need(a[0], "k_pages"), &bt = need(a[1], "block_table"), &len = need(a[2], "seqlens"), &b = need(a[3], "bounds");
-        Device dev;
-        for (const Tensor* t : {&k, &bt, &len, &b}) dev.add(t);
         ta_shape s;
         ta_paged_kv pg;
         std::memset(&s, 0, sizeof s);
@@ -388,6 +391,8 @@ PyObject* page_bounds(PyObject*, PyObject* const* a, Py_ssize_t n) {
         check_bounds(b, pg.num_pages, s.num_kv_heads, s.head_dim, s.kv_dtype == TA_F32);
         const int32_t* pl = ints(&len, "seqlens", s.batch);
         const int nt = static_cast<int>(std::min<long long>(std::max<long long>(integer(a[4]), 0), 0x7fffffff));
+        Device dev;
+        for (const Tensor* t : {&k, &bt, &len, &b}) dev.add(t);
         void* st = dev.stream(a[6]);
         return enqueue([&] { return p_page_bounds(&s, &pg, k.data_ptr(), pl, nt, b.data_ptr(), st); });
     });
@@ -467,8 +472,6 @@ PyObject* decode_selected(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Tensor &q = need(a[0], "q"), &k = need(a[1], "k_pages"), &v = need(a[2], "v_pages"), &bt = need(a[3], "block_table"),
                      &len = need(a[4], "seqlens"), &sel = need(a[5], "selected"), &out = need(a[6], "out");
         const Tensor *lse = opt(a[7], "lse"), *ks = opt(a[10], "k_scale"), *vs = opt(a[11], "v_scale");
-        Device dev;
-        for (const Tensor* t : {&q, &k, &v, &bt, &len, &sel, &out, lse, ks, vs}) dev.add(t);
         ta_shape s;
         ta_paged_kv pg;
         std::memset(&s, 0, sizeof s);
@@ -489,6 +492,8 @@ PyObject* decode_selected(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const float *pks = scales(ks, "k_scale", s.num_kv_heads), *pvs = scales(vs, "v_scale", s.num_kv_heads);
         const int32_t* pl = ints(&len, "seqlens", s.batch);
         const int ns = size32(sel.size(2), "selected");
+        Device dev;
+        for (const Tensor* t : {&q, &k, &v, &bt, &len, &sel, &out, lse, ks, vs}) dev.add(t);
         void* st = dev.stream(a[12]);
         return enqueue([&] {
             return p_decode_selected(&s, &pg, q.data_ptr(), k.data_ptr(), v.data_ptr(), pl, sel.const_data_ptr<int32_t>(), ns,

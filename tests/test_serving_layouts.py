@@ -1,0 +1,55 @@
+"""Cache and vector layouts that the calls around the decode step refuse, and limits that they
+apply, without a GPU: layouts are looked at before the tensors' device, so host tensors show
+which check answers."""
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def ta():
+    from softmax_tree_reduction_gb300 import build
+    build.build()
+    import softmax_tree_reduction_gb300 as mod
+    mod.load()
+    return mod
+
+
+BF16 = torch.bfloat16
+
+
+def page_calls(ta, pool):
+    """Every call that takes a page pool, on host tensors that are otherwise valid."""
+    hkv, d = pool.shape[2], pool.shape[3]
+    k, pos = torch.zeros(3, hkv, d, dtype=BF16), torch.zeros(3, dtype=torch.int32)
+    bt, sl = torch.zeros(3, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    q = torch.zeros(3, 2 * hkv, d, dtype=BF16)
+    return (lambda: ta.tree_attn_cache_write(k, k, pool, pool, pos, block_table=bt),
+            lambda: ta.tree_attn_cache_read(pool, pool, pos, block_table=bt),
+            lambda: ta.tree_attn_page_bounds(pool, bt, sl),
+            lambda: ta.tree_attn_decode_selected(q, pool, pool, bt, sl, torch.zeros(3, hkv, 4, dtype=torch.int32)))
+
+
+def dense_calls(ta, cache):
+    B, hkv, _, d = cache.shape
+    k, pos = torch.zeros(B, hkv, d, dtype=BF16), torch.zeros(B, dtype=torch.int32)
+    return (lambda: ta.tree_attn_cache_write(k, k, cache, cache, pos), lambda: ta.tree_attn_cache_read(cache, cache, pos))
+
+
+def test_caches_whose_entries_share_memory(ta):
+    """A cache expanded along an axis: along all of them its strides would read as "dense" in
+    the C call, which then stores far past the view's memory."""
+    one = torch.zeros(1, 1, 1, 128, dtype=BF16)
+    row = torch.zeros(1, 2, 32, 128, dtype=BF16)
+    for cache in (one.expand(4, 2, 32, 128), row.expand(4, 2, 32, 128), row[:, :1].expand(1, 2, 32, 128), row[:, :, :1].expand(1, 2, 32, 128)):
+        for call in dense_calls(ta, cache):
+            with pytest.raises(ValueError, match="share memory"):
+                call()
+    page = torch.zeros(1, 16, 2, 128, dtype=BF16)
+    for pool in (one.expand(8, 16, 2, 128), page.expand(8, 16, 2, 128), page[:, :1].expand(1, 16, 2, 128), page[:, :, :1].expand(1, 16, 2, 128)):
+        for call in page_calls(ta, pool):
+            with pytest.raises(ValueError, match="share memory"):
+                call()
+    # an axis of one entry may carry any stride
+    for call in (*dense_calls(ta, one.expand(1, 1, 1, 128)), *page_calls(ta, page[:, :, :1].as_strided((1, 16, 1, 128), (0, 256, 0, 1)))):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
