@@ -185,6 +185,14 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _cache_strides(cache: torch.Tensor):
+    """Strides of a cache's first three axes.  Entries that share memory are refused: strides of 0
+    on every axis would mean a dense cache to the library, which then reads past the view."""
+    if any(n > 1 and st == 0 for n, st in zip(cache.shape[:3], cache.stride()[:3])):
+        raise ValueError("a cache's entries must not share memory: an axis of several has stride 0")
+    return cache.stride()[:3]
+
+
 def make_shape(q: torch.Tensor, k_cache: torch.Tensor, scale: Optional[float] = None) -> TaShape:
     """Shape descriptor for q [B, Hq, d] and a K/V cache viewed as [B, Hkv, S, d]
     (any strides with a unit channel stride)."""
@@ -196,7 +204,7 @@ def make_shape(q: torch.Tensor, k_cache: torch.Tensor, scale: Optional[float] = 
         raise ValueError("q and k_cache disagree on batch or head_dim")
     if k_cache.stride(3) != 1:
         raise ValueError("k_cache channels must be contiguous")
-    sb, sh, st, _ = k_cache.stride()
+    sb, sh, st = _cache_strides(k_cache)
     dense = k_cache.is_contiguous()
     return TaShape(B, Hq, Hkv, d, S, _dtype_code(q.dtype), _dtype_code(k_cache.dtype),
                    float(scale or 0.0), 0 if dense else sb, 0 if dense else sh, 0 if dense else st)
@@ -433,7 +441,7 @@ def tree_attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
     if dq != d or block_table.shape[0] != B:
         raise ValueError("q, pages and block_table disagree")
     S = int(max_seqlen) if max_seqlen is not None else block_table.shape[1] * page_size
-    sp, st, sh, _ = k_pages.stride()
+    sp, st, sh = _cache_strides(k_pages)
     shape = TaShape(B, Hq, Hkv, d, S, _dtype_code(q.dtype), _dtype_code(k_pages.dtype),
                     float(scale or 0.0), sp, sh, st)
     paged = TaPagedKV(block_table.data_ptr(), block_table.shape[1], page_size, num_pages, 0)
@@ -493,7 +501,7 @@ def tree_attn_decode_multi(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
             raise ValueError("block_table must be a contiguous int32 tensor")
         num_pages, page_size, Hkv, _ = k_cache.shape
         S = int(max_seqlen) if max_seqlen is not None else block_table.shape[1] * page_size
-        sp, st, sh, _ = k_cache.stride()
+        sp, st, sh = _cache_strides(k_cache)
         base = TaShape(B, Hq, Hkv, d, S, _dtype_code(q.dtype), _dtype_code(k_cache.dtype),
                        float(scale or 0.0), sp, sh, st)
         paged = TaPagedKV(block_table.data_ptr(), block_table.shape[1], page_size, num_pages, 0)

@@ -53,3 +53,21 @@ def test_caches_whose_entries_share_memory(ta):
     for call in (*dense_calls(ta, one.expand(1, 1, 1, 128)), *page_calls(ta, page[:, :, :1].as_strided((1, 16, 1, 128), (0, 256, 0, 1)))):
         with pytest.raises(ValueError, match="CUDA device"):
             call()
+
+
+def test_decode_calls_refuse_caches_whose_entries_share_memory(ta, monkeypatch):
+    """The decode calls over the same caches (their device check is passed over: nothing is
+    launched, the layout is refused first)."""
+    from softmax_tree_reduction_gb300 import _binding
+    monkeypatch.setattr(_binding, "_check_cuda", lambda *ts: None)
+    one = torch.zeros(1, 1, 1, 128, dtype=BF16)
+    q, sl, bt = torch.zeros(4, 4, 128, dtype=BF16), torch.zeros(4, dtype=torch.int32), torch.zeros(4, 4, dtype=torch.int32)
+    cache, pool = one.expand(4, 2, 32, 128), one.expand(8, 16, 2, 128)
+    for call in (lambda: ta.make_shape(q, cache), lambda: ta.tree_attn_decode(q, cache, cache, sl), lambda: ta.tree_attn_decode_paged(q, pool, pool, bt, sl),
+                 lambda: ta.tree_attn_decode_multi(q[:, :, None].contiguous(), cache, cache, sl),
+                 lambda: ta.tree_attn_decode_multi(q[:, :, None].contiguous(), pool, pool, sl, block_table=bt),
+                 lambda: ta.tree_attn_decode_noalloc(q, cache, cache, sl, torch.zeros(4, 4, 128))):
+        with pytest.raises(ValueError, match="share memory"):
+            call()
+    shape = ta.make_shape(q[:1], torch.zeros(1, 1, 32, 128, dtype=BF16).expand(1, 1, 32, 128))
+    assert shape.kv_stride_t in (0, 128)
