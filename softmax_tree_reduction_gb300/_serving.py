@@ -95,7 +95,8 @@ def tree_attn_cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tenso
     pools [num_pages, page_size, Hkv, d] with ``block_table``, of any cache type (E4M3 with
     ``k_scale``/``v_scale``: codes are e4m3(x / scale), saturating); positions: int32 [T]
     (negative: padding, nothing is stored); rows: int32 [T] batch rows (None: token t
-    is row t's).  With ``inv_freq`` or ``norm`` the keys are rotated or normed first, and so
+    is row t's); max_seqlen: positions from it on are out of range (default: all that the cache
+    or the block table holds).  With ``inv_freq`` or ``norm`` the keys are rotated or normed first, and so
     are the queries ``q`` [T, Hq, d] when given (into ``q_out``, which may be q), all in one
     kernel.  Returns q_out (None without q).
     """

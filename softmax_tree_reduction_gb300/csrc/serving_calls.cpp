@@ -226,6 +226,11 @@ struct CacheCall {
             shape.batch = size32(kc.size(0), "a cache");
             shape.num_kv_heads = size32(kc.size(1), "a cache");
             shape.max_seqlen = size32(kc.size(2), "a cache");
+            if (max_seqlen != Py_None) {
+                const int most = int32(max_seqlen, "max_seqlen");
+                if (most < 1 || most > shape.max_seqlen) throw BadValue("max_seqlen must be at least 1 and at most the cache's tokens");
+                shape.max_seqlen = most;
+            }
             shape.head_dim = size32(kc.size(3), "a cache");
             shape.kv_dtype = dtype_code(kc);
             shape.kv_stride_b = cache_stride(kc, 0);

@@ -71,3 +71,14 @@ def test_decode_calls_refuse_caches_whose_entries_share_memory(ta, monkeypatch):
             call()
     shape = ta.make_shape(q[:1], torch.zeros(1, 1, 32, 128, dtype=BF16).expand(1, 1, 32, 128))
     assert shape.kv_stride_t in (0, 128)
+
+
+def test_dense_caches_and_max_seqlen(ta):
+    """A limit above the cache's tokens (or below one) is refused; one within it is not."""
+    cache = torch.zeros(4, 2, 32, 128, dtype=BF16)
+    k, pos = torch.zeros(4, 2, 128, dtype=BF16), torch.zeros(4, dtype=torch.int32)
+    for limit, why in ((33, "max_seqlen"), (0, "max_seqlen"), (-1, "max_seqlen"), (2 ** 31, "max_seqlen"), (32, "CUDA device"), (1, "CUDA device")):
+        for call in (lambda: ta.tree_attn_cache_write(k, k, cache, cache, pos, max_seqlen=limit),
+                     lambda: ta.tree_attn_cache_read(cache, cache, pos, max_seqlen=limit)):
+            with pytest.raises(ValueError, match=why):
+                call()

@@ -1,0 +1,37 @@
+"""Limits and failures of the calls around the decode step on the GPU: what is outside them
+is left alone and reported."""
+import pytest
+import torch
+
+import softmax_tree_reduction_gb300 as ta
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+@pytest.mark.parametrize("layout", ["HND", "NHD"])
+def test_dense_cache_calls_apply_max_seqlen(layout):
+    """Positions from max_seqlen on: not stored, read as NaN, reported; the others as without it."""
+    B, hkv, S, d, limit = 3, 2, 40, 64, 33
+    shape = (B, hkv, S, d) if layout == "HND" else (B, S, hkv, d)
+    kc, vc = (torch.full(shape, 7.0, dtype=BF16, device="cuda") for _ in range(2))
+    kc, vc = (c if layout == "HND" else c.transpose(1, 2) for c in (kc, vc))
+    g = torch.Generator().manual_seed(limit)
+    k, v = (torch.randn(5, hkv, d, generator=g).to(BF16).cuda() for _ in range(2))
+    rows = torch.tensor([0, 1, 2, 2, 0], dtype=torch.int32).cuda()
+    pos = torch.tensor([limit - 1, limit, S - 1, 0, 5], dtype=torch.int32).cuda()
+    ta.tree_attn_cache_write(k, v, kc, vc, pos, rows=rows, max_seqlen=limit)
+    assert ta.tree_attn_get_device_error() == ta.TA_ERR_DEVICE_DATA
+    want_k, want_v = torch.full_like(kc, 7.0), torch.full_like(vc, 7.0)
+    for t, (r, p) in enumerate(zip(rows.tolist(), pos.tolist())):
+        if p < limit:
+            want_k[r, :, p], want_v[r, :, p] = k[t], v[t]
+    assert torch.equal(kc, want_k) and torch.equal(vc, want_v)
+    ko, vo = ta.tree_attn_cache_read(kc, vc, pos, rows=rows, max_seqlen=limit)
+    assert ta.tree_attn_get_device_error() == ta.TA_ERR_DEVICE_DATA
+    inside = pos < limit
+    assert torch.equal(ko[inside], k[inside]) and torch.equal(vo[inside], v[inside])
+    assert torch.isnan(ko[~inside]).all() and torch.isnan(vo[~inside]).all()
+    ta.tree_attn_cache_write(k, v, kc, vc, pos, rows=rows, max_seqlen=S)
+    assert ta.tree_attn_get_device_error() == 0 and torch.equal(kc[2, :, S - 1], k[2])
