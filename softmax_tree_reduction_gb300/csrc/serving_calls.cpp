@@ -117,6 +117,22 @@ struct Device {
     }
 };
 
+// Whether vectors of d elements, one for each (i, j) in [0, n) x [0, m) at i a + j b, overlap: two of them do
+// where |x a + y b| < d for some steps |x| < n, |y| < m, not both 0.
+bool overlapping(int64_t n, int64_t a, int64_t m, int64_t b, int64_t d) {
+    if (n <= 1) a = 0, n = 1;
+    if (m <= 1) b = 0, m = 1;
+    if (a < b) std::swap(a, b), std::swap(n, m);
+    // the usual layouts: the smaller step keeps vectors apart, and the larger one its whole runs
+    if ((m == 1 || b >= d) && (n == 1 || a >= (m - 1) * b + d)) return false;
+    if ((m > 1 && b < d) || (n > 1 && a < d)) return true;
+    for (int64_t y = 1; y < m; ++y) {  // (x and y of opposite signs; the x on either side of y b / a)
+        const int64_t x = y * b / a;
+        if ((x < n && y * b - x * a < d) || (x + 1 < n && (x + 1) * a - y * b < d)) return true;
+    }
+    return false;
+}
+
 // Head vectors [tokens, heads, head_dim]; `output`: they must not share memory.
 ta_heads heads(const Tensor& t, const char* name, bool output = false) {
     if (t.dim() != 3 || (t.stride(2) != 1 && t.size(2) > 1))
@@ -125,7 +141,7 @@ ta_heads heads(const Tensor& t, const char* name, bool output = false) {
     h.data = t.data_ptr();
     h.stride_t = t.size(0) > 1 ? t.stride(0) : 0;
     h.stride_h = t.size(1) > 1 ? t.stride(1) : 0;
-    if (output && ((t.size(0) > 1 && h.stride_t == 0) || (t.size(1) > 1 && h.stride_h == 0)))
+    if (output && overlapping(t.size(0), h.stride_t, t.size(1), h.stride_h, t.size(2)))
         throw BadValue(std::string(name) + " is written to: its vectors must not share memory");
     return h;
 }
@@ -294,8 +310,6 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (!q && !k) throw BadValue("q or k is needed");
         if (!q != !qo || !k != !ko) throw BadValue("an output without its input, or the other way round");
         if (!norm && !f) throw BadValue("nothing to do: no norm and no inv_freq");
-        Device dev;
-        for (const Tensor* t : {q, k, &pos, f, qw, kw, qo, ko}) dev.add(t);
         const Tensor& x = q ? *q : *k;
         ta_heads h[4];
         std::memset(h, 0, sizeof h);
@@ -315,6 +329,8 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         tok.num_tokens = size32(x.size(0), "the token list");
         tok.positions = ints(&pos, "positions", x.size(0));
         const ta_rope r = rope_of(x.size(2), f, qw, kw, norm, real(a[7]), truth(a[8]));
+        Device dev;
+        for (const Tensor* t : {q, k, &pos, f, qw, kw, qo, ko}) dev.add(t);
         void* st = dev.stream(a[11]);
         return enqueue([&] {
             return p_norm_rope(&s, &tok, &r, q ? &h[0] : nullptr, q ? &h[1] : nullptr, k ? &h[2] : nullptr, k ? &h[3] : nullptr, st);

@@ -82,3 +82,33 @@ def test_dense_caches_and_max_seqlen(ta):
                      lambda: ta.tree_attn_cache_read(cache, cache, pos, max_seqlen=limit)):
             with pytest.raises(ValueError, match=why):
                 call()
+
+
+def shared(T, H, st, sh, d):
+    """Whether any two of the T x H vectors of d elements share one (from the places themselves)."""
+    starts = sorted(t * st + h * sh for t in range(T) for h in range(H))
+    return any(b - a < d for a, b in zip(starts, starts[1:]))
+
+
+def test_output_vectors_that_overlap(ta):
+    """Outputs are refused exactly where two of their vectors share memory, whatever the strides."""
+    d = 64
+    buf = torch.zeros(60000)
+    seen = set()
+    for T, H in ((1, 1), (2, 1), (1, 3), (2, 2), (3, 2), (2, 5), (4, 3), (7, 4), (5, 7)):
+        x, pos = torch.zeros(T, H, d), torch.zeros(T, dtype=torch.int32)
+        for st in (0, 16, 48, 64, 80, 112, 128, 160, 192, 256, 320, 448, 1024):
+            for sh in (0, 32, 60, 64, 96, 128, 144, 176, 192, 208, 256, 512, 576, 2048):
+                out = buf.as_strided((T, H, d), (st, sh, 1))
+                bad = shared(T, H, st, sh, d)
+                seen.add(bad)
+                why = "share memory" if bad else "CUDA device"
+                with pytest.raises(ValueError, match=why):
+                    ta.tree_attn_norm_rope(x, None, pos, q_out=out)
+                if T == 3:                                       # (the other outputs take the same check)
+                    cache = torch.zeros(T, H, 4, d)
+                    with pytest.raises(ValueError, match=why):
+                        ta.tree_attn_cache_read(cache, cache, pos, k_out=out, v_out=torch.zeros(T, H, d))
+                    with pytest.raises(ValueError, match=why):
+                        ta.tree_attn_cache_write(x, x, cache, cache, pos, q=x, q_out=out, norm=True)
+    assert seen == {True, False}
