@@ -14,6 +14,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
@@ -284,6 +285,8 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, Fn&& fn) {
         if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, e.what());
     } catch (const BadType& e) {
         if (!PyErr_Occurred()) PyErr_SetString(PyExc_TypeError, e.what());
+    } catch (const c10::OutOfMemoryError& e) {  // (a workspace that torch's allocator could not provide)
+        if (!PyErr_Occurred()) PyErr_SetString(THPException_OutOfMemoryError, e.what_without_backtrace());
     } catch (const std::exception& e) {
         if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
     }

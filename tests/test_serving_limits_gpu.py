@@ -35,3 +35,26 @@ def test_dense_cache_calls_apply_max_seqlen(layout):
     assert torch.isnan(ko[~inside]).all() and torch.isnan(vo[~inside]).all()
     ta.tree_attn_cache_write(k, v, kc, vc, pos, rows=rows, max_seqlen=S)
     assert ta.tree_attn_get_device_error() == 0 and torch.equal(kc[2, :, S - 1], k[2])
+
+
+def test_select_pages_without_memory_for_its_workspace():
+    """torch's own out-of-memory error, as an output allocated by torch would raise it, and the
+    call works again once there is memory."""
+    B, hkv, per, page, d = 64, 8, 32768, 16, 64
+    bt = torch.zeros(B, per, dtype=torch.int32, device="cuda")
+    bounds = torch.zeros(1, hkv, 2, d, dtype=BF16, device="cuda")
+    lens = torch.full((B,), 5, dtype=torch.int32, device="cuda")
+    q = torch.zeros(B, hkv, d, dtype=BF16, device="cuda")
+    sel = torch.zeros(B, hkv, 4, dtype=torch.int32, device="cuda")
+    assert ta.tree_attn_select_workspace_bytes(B, hkv, per) > 200 << 20
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction(1e-4)      # 28 MB: the workspace does not fit
+    try:
+        with pytest.raises(torch.cuda.OutOfMemoryError):
+            ta.tree_attn_select_pages(q, bounds, bt, lens, page, 4, 1, 1, selected=sel)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    ta.tree_attn_select_pages(q, bounds, bt, lens, page, 4, 1, 1, selected=sel)
+    assert sel.cpu().tolist() == [[[0, -1, -1, -1]] * hkv] * B
+    assert ta.tree_attn_get_device_error() == 0
