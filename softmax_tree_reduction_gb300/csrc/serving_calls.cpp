@@ -14,7 +14,6 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
-#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
@@ -269,6 +268,15 @@ void like(const Tensor& a, const Tensor& b, const char* what) {
     if (!a.sizes().equals(b.sizes()) || a.scalar_type() != b.scalar_type()) throw BadValue(std::string(what) + " must agree on shape and type");
 }
 
+// torch.OutOfMemoryError (the class itself is not among libtorch_python's exported symbols).
+void set_out_of_memory(const char* what) {
+    PyObject* torch = PyImport_ImportModule("torch");
+    PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+    if (type) PyErr_SetString(type, what);
+    Py_XDECREF(type);
+    Py_XDECREF(torch);
+}
+
 template <typename Fn>
 PyObject* guarded(Py_ssize_t n, Py_ssize_t want, Fn&& fn) {
     if (n != want) {
@@ -286,7 +294,7 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, Fn&& fn) {
     } catch (const BadType& e) {
         if (!PyErr_Occurred()) PyErr_SetString(PyExc_TypeError, e.what());
     } catch (const c10::OutOfMemoryError& e) {  // (a workspace that torch's allocator could not provide)
-        if (!PyErr_Occurred()) PyErr_SetString(THPException_OutOfMemoryError, e.what_without_backtrace());
+        if (!PyErr_Occurred()) set_out_of_memory(e.what_without_backtrace());
     } catch (const std::exception& e) {
         if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
     }
