@@ -46,7 +46,7 @@ def test_select_pages_without_memory_for_its_workspace():
     lens = torch.full((B,), 5, dtype=torch.int32, device="cuda")
     q = torch.zeros(B, hkv, d, dtype=BF16, device="cuda")
     sel = torch.zeros(B, hkv, 4, dtype=torch.int32, device="cuda")
-    assert ta.tree_attn_select_workspace_bytes(B, hkv, per) > 200 << 20
+    assert ta.tree_attn_select_workspace_bytes(B, hkv, per) >= 200 << 20
     torch.cuda.synchronize()
     torch.cuda.empty_cache()
     torch.cuda.set_per_process_memory_fraction(1e-4)      # 28 MB: the workspace does not fit
