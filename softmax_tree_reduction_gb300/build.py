@@ -12,14 +12,18 @@ device error word (TA_ERR_DEVICE_BOUNDS).  Point the binding at it with the
 TREE_ATTN_LIBRARY environment variable.
 
 The argument marshalling of the calls around the decode step
-(csrc/serving_calls.cpp) is compiled with g++ against torch's headers into
-``softmax_tree_reduction_gb300/_serving_calls.so``.
+(csrc/serving_calls.cpp) is compiled with g++ against torch's and Python's
+headers into ``softmax_tree_reduction_gb300/_serving_calls.so``, for the torch
+and Python that run the build: with others it is built again.  The library
+itself needs nvcc alone; without torch (``python
+softmax_tree_reduction_gb300/build.py``) only it is built.
 
     python -m softmax_tree_reduction_gb300.build [--verbose-ptxas] [--force] [--debug]
 """
 from __future__ import annotations
 
 import os
+import platform
 import shutil
 import subprocess
 import sys
@@ -31,6 +35,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtreeattn.so")
 CALLS_SOURCE = os.path.join(CSRC, "serving_calls.cpp")
 CALLS = os.path.join(HERE, "_serving_calls.so")
+CALLS_FOR = os.path.join(BUILD, "serving_calls.for")  # what CALLS was built for
 LIB_DEBUG = os.path.join(HERE, "libtreeattn_debug.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
@@ -48,9 +53,22 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _calls_command(out: str) -> list:
+def _torch():
+    """The torch that the marshalling module is built for, or None."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    return torch
+
+
+def _calls_for(torch) -> str:
+    """Torch and Python versions, whose ABIs the module's binary depends on."""
+    return f"torch {torch.__version__} {sysconfig.get_config_var('SOABI')} {platform.machine()}"
+
+
+def _calls_command(torch, out: str) -> list:
     """The compiler call that makes the marshalling module."""
-    import torch
     root = os.path.dirname(torch.__file__)
     lib = os.path.join(root, "lib")
     cuda = os.path.dirname(os.path.dirname(nvcc()))
@@ -60,53 +78,90 @@ def _calls_command(out: str) -> list:
             "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ldl", "-Wl,-rpath," + lib]
 
 
-def _deps_mtime() -> float:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "tree_attn.h"))
-    files.append(os.path.abspath(__file__))
-    return max(os.path.getmtime(f) for f in files)
+def _newer(out: str, sources: list) -> bool:
+    """Whether `out` exists and was made after every one of its sources."""
+    return os.path.exists(out) and os.path.getmtime(out) >= max(os.path.getmtime(f) for f in sources)
+
+
+def _common_sources() -> list:
+    return [os.path.join(INCLUDE, "tree_attn.h"), os.path.abspath(__file__)]
+
+
+def _lib_up_to_date(lib: str) -> bool:
+    own = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != os.path.basename(CALLS_SOURCE)]
+    return _newer(lib, own + _common_sources())
+
+
+def _calls_up_to_date(torch) -> bool:
+    if torch is None:  # nothing that could use it
+        return True
+    if not _newer(CALLS, [CALLS_SOURCE] + _common_sources()) or not os.path.exists(CALLS_FOR):
+        return False
+    with open(CALLS_FOR) as fh:
+        return fh.read() == _calls_for(torch)
 
 
 def up_to_date(lib: str = LIB) -> bool:
-    return all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (lib, CALLS))
+    return _lib_up_to_date(lib) and _calls_up_to_date(_torch())
+
+
+def _start(cmd: list) -> subprocess.Popen:
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True, debug: bool = False) -> str:
     lib = LIB_DEBUG if debug else LIB
     build_dir = BUILD + "_debug" if debug else BUILD
-    if not force and up_to_date(lib):
+    torch = _torch()
+    make_lib = force or not _lib_up_to_date(lib)
+    make_calls = torch is not None and (force or not _calls_up_to_date(torch))
+    if not make_lib and not make_calls:
         return lib
     os.makedirs(build_dir, exist_ok=True)
+    os.makedirs(BUILD, exist_ok=True)
+    # every command first: nothing is running yet when one cannot be made
     cc = nvcc()
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
     if debug:
         extra.append("-DTA_DEBUG_BOUNDS")
-    procs = []
-    objs = []
-    for src in SOURCES:
-        obj = os.path.join(build_dir, src.replace(".cu", ".o"))
-        objs.append(obj)
-        cmd = [cc, *ARCH, *FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
-        procs.append((src, cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
-                                                 text=True)))
-    cmd = _calls_command(CALLS + ".tmp")
-    procs.append((os.path.basename(CALLS_SOURCE), cmd,
-                  subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+    objs = [os.path.join(build_dir, src.replace(".cu", ".o")) for src in SOURCES]
+    commands = [(src, [cc, *ARCH, *FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj])
+                for src, obj in zip(SOURCES, objs)] if make_lib else []
+    calls_command = _calls_command(torch, CALLS + ".tmp") if make_calls else None
+    running = [(src, cmd, _start(cmd)) for src, cmd in commands]
+    calls_failed = ""
+    calls = None
+    if make_calls:
+        try:
+            calls = _start(calls_command)
+        except OSError as e:
+            calls_failed = str(e)
     failed = []
-    for src, cmd, pr in procs:
+    for src, cmd, pr in running:
         out, _ = pr.communicate()
         if pr.returncode != 0:
             failed.append((src, out))
         elif out and (verbose_ptxas or not quiet):
             sys.stdout.write(f"--- {src}\n{out}")
+    if calls is not None:
+        out, _ = calls.communicate()
+        if calls.returncode != 0:
+            calls_failed = out
+        else:
+            os.replace(CALLS + ".tmp", CALLS)
+            with open(CALLS_FOR, "w") as fh:
+                fh.write(_calls_for(torch))
     if failed:
         msg = "\n".join(f"--- {s}\n{o}" for s, o in failed)
         raise RuntimeError(f"nvcc failed:\n{msg}")
-    os.replace(CALLS + ".tmp", CALLS)
-    tmp = lib + ".tmp"
-    subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lrt",
-                    "-lpthread"], check=True)
-    os.replace(tmp, lib)
+    if make_lib:
+        tmp = lib + ".tmp"
+        subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lrt",
+                        "-lpthread"], check=True)
+        os.replace(tmp, lib)
+    if calls_failed:  # the library is complete all the same
+        raise RuntimeError(f"{calls_command[0]} failed on {os.path.basename(CALLS_SOURCE)} "
+                           f"({os.path.basename(lib)} is built):\n{calls_failed}")
     return lib
 
 
