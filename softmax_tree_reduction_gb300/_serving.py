@@ -192,7 +192,12 @@ def tree_attn_select_pages(q: torch.Tensor, bounds: torch.Tensor, block_table: t
 
 def tree_attn_select_workspace_bytes(batch: int, num_kv_heads: int, max_pages: int) -> int:
     """Bytes tree_attn_select_pages needs as workspace for rows of up to ``max_pages`` pages."""
-    shape = TaShape(batch, num_kv_heads, num_kv_heads, 128, max_pages * 16, TA_F32, TA_F32, 0.0, 0, 0, 0)
+    most = 2 ** 31 - 1                           # tokens of a row; more pages than they fill are not used
+    if max(batch, num_kv_heads, max_pages) > most:
+        raise ValueError("batch, num_kv_heads and max_pages must be below 2^31")
+    if min(batch, num_kv_heads, max_pages) < 1:
+        return 0
+    shape = TaShape(batch, num_kv_heads, num_kv_heads, 128, min(max_pages * 16, most), TA_F32, TA_F32, 0.0, 0, 0, 0)
     paged = TaPagedKV(16, max_pages, 16, 1, 0)   # (a table address is required, none is read)
     return int(load().tree_attn_select_workspace_bytes(ctypes.byref(shape), ctypes.byref(paged)))
 

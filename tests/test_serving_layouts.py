@@ -112,3 +112,16 @@ def test_output_vectors_that_overlap(ta):
                     with pytest.raises(ValueError, match=why):
                         ta.tree_attn_cache_write(x, x, cache, cache, pos, q=x, q_out=out, norm=True)
     assert seen == {True, False}
+
+
+def test_selection_workspace_of_the_longest_rows(ta):
+    """Scores, magnitudes of 8 pages and exact sums: 4 + 4 / 8 + 8 bytes a page, of the pages that the
+    2^31 - 1 tokens of a row can fill; sizes that do not fit 32 bits are not cut off."""
+    for pages in (32, 2 ** 20, 2 ** 27 - 32, 2 ** 27):
+        assert ta.tree_attn_select_workspace_bytes(3, 5, pages) == 15 * (pages * 4 + pages // 2 + pages * 8)
+    assert ta.tree_attn_select_workspace_bytes(3, 5, 2 ** 30) == ta.tree_attn_select_workspace_bytes(3, 5, 2 ** 27)
+    for none in ((0, 5, 32), (3, -1, 32), (3, 5, 0)):
+        assert ta.tree_attn_select_workspace_bytes(*none) == 0
+    for bad in ((3, 5, 2 ** 31), (2 ** 32 + 1, 5, 32)):
+        with pytest.raises(ValueError):
+            ta.tree_attn_select_workspace_bytes(*bad)
