@@ -369,16 +369,11 @@ struct PageBounds {
             }
         }
     }
-    __device__ __forceinline__ void take(const uint8_t* smem) {  // from shared memory
-        if constexpr (W == 2) {
-            const uint2 v = *reinterpret_cast<const uint2*>(smem);
-            w[0] = v.x; w[1] = v.y;
-        } else {
+    __device__ __forceinline__ void take(const uint8_t* smem) {  // from shared memory, 16 bytes at least
 #pragma unroll
-            for (int x = 0; x < W / 4; ++x) {
-                const uint4 v = reinterpret_cast<const uint4*>(smem)[x];
-                w[4 * x] = v.x; w[4 * x + 1] = v.y; w[4 * x + 2] = v.z; w[4 * x + 3] = v.w;
-            }
+        for (int x = 0; x < W / 4; ++x) {
+            const uint4 v = reinterpret_cast<const uint4*>(smem)[x];
+            w[4 * x] = v.x; w[4 * x + 1] = v.y; w[4 * x + 2] = v.z; w[4 * x + 3] = v.w;
         }
     }
     __device__ __forceinline__ float operator[](int i) const {
@@ -391,15 +386,12 @@ struct PageBounds {
 
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void* dst, const void* src) {
-    if constexpr (BYTES == 8) {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-    } else {
+    static_assert(BYTES % 16 == 0, "16 bytes a copy");
 #pragma unroll
-        for (int i = 0; i < BYTES; i += 16)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst) + i),
-                         "l"(static_cast<const uint8_t*>(src) + i)
-                         : "memory");
-    }
+    for (int i = 0; i < BYTES; i += 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst) + i),
+                     "l"(static_cast<const uint8_t*>(src) + i)
+                     : "memory");
 }
 
 // A warp's ring of page groups in shared memory: 8 pages of bounds, or 16 where those of one

@@ -96,7 +96,6 @@ struct Four<float> {
 template <>
 struct Four<__nv_fp8_e4m3> {
     uint32_t x;
-    __device__ __forceinline__ void load(const __nv_fp8_e4m3* p) { x = *reinterpret_cast<const uint32_t*>(p); }
     __device__ __forceinline__ void unpack(float* f) const {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
