@@ -56,6 +56,8 @@ struct SelParams {
     int max_pages, page_shift, num_pages;
     int C;                     // blocks per cluster
     float scale_log2;
+    // extents, for the bounds-checking build
+    size_t q_elems, cache_elems, list_elems, table_elems, out_elems, rows;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
@@ -77,6 +79,12 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     uint32_t d;
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
     return d;
+}
+
+// Whether a copy of `bytes` from byte o of the pools stays in them.
+template <int es>
+__device__ __forceinline__ bool copy_in(const SelParams& p, int64_t o, int bytes) {
+    return bytes == 0 || in_bounds(static_cast<size_t>(o) + bytes - 1, p.cache_elems * es, p.err);
 }
 
 // One list's slabs as seen by one warp: lane i of a window holds the place of
@@ -105,7 +113,8 @@ struct SlabList {
     // list entry of this lane's slab in the window starting at the warp's slab i0 (-1: none)
     __device__ __forceinline__ int entry(int i0) const {
         const int64_t u = gw + static_cast<int64_t>(i0 + lane) * W;
-        return u < U ? __ldg(sel + (u >> (p.page_shift - 4))) : -1;
+        const int64_t i = u >> (p.page_shift - 4);
+        return u < U && in_bounds(sel - p.selected + i, p.list_elems, p.err) ? __ldg(sel + i) : -1;
     }
     // its place, once the entry has arrived
     __device__ __forceinline__ SlabWindow place(int i0, int e) {
@@ -120,6 +129,7 @@ struct SlabList {
         const int sub = static_cast<int>(u & ((1 << (p.page_shift - 4)) - 1));
         const int64_t t0 = (static_cast<int64_t>(e) << p.page_shift) + sub * kSlab;
         if (e < 0 || t0 >= N) return w;
+        if (!in_bounds(table - p.block_table + e, p.table_elems, p.err)) return w;
         const int page = __ldg(table + e);
         if (page < 0 || page >= p.num_pages) {
             bad = 1;
@@ -198,6 +208,7 @@ __device__ void finish_list(const SelParams& p, int b, int hq0, int ncol, float 
         if (poison) o = l = M = nan;
         if (C > 1) {
             const int to = idx / share;
+            if (!in_bounds(rank * share + idx - to * share, kCols * D + kMaxCluster, p.err) || !in_bounds(to, C, p.err)) continue;
             st_dsmem(dsmem_addr(&box->o[rank * share + idx - to * share], to), o);
             if (dd < C) {  // the column's maximum and denominator, to block dd
                 const uint32_t at = dsmem_addr(&box->ml[rank][h], dd);
@@ -205,8 +216,8 @@ __device__ void finish_list(const SelParams& p, int b, int hq0, int ncol, float 
                 st_dsmem(at + 4, l);
             }
         } else {
-            p.out[(row0 + h) * D + dd] = l == 0.f ? 0.f : o / l;
-            if (dd == 0 && p.lse) p.lse[row0 + h] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+            if (in_bounds((row0 + h) * D + dd, p.out_elems, p.err)) p.out[(row0 + h) * D + dd] = l == 0.f ? 0.f : o / l;
+            if (dd == 0 && p.lse && in_bounds(row0 + h, p.rows, p.err)) p.lse[row0 + h] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
         }
     }
     if (C == 1) return;
@@ -232,8 +243,9 @@ __device__ void finish_list(const SelParams& p, int b, int hq0, int ncol, float 
             L = fmaf(w, ml[c].y, L);
             O = fmaf(w, o[c], O);
         }
-        p.out[(row0 + h) * D + dd] = (L == 0.f) ? 0.f : O / L;  // NaN of a poisoned block propagates
-        if (dd == 0 && p.lse) p.lse[row0 + h] = (L == 0.f) ? -INFINITY : (M + log2f(L)) * kLn2;
+        if (in_bounds((row0 + h) * D + dd, p.out_elems, p.err))
+            p.out[(row0 + h) * D + dd] = (L == 0.f) ? 0.f : O / L;  // NaN of a poisoned block propagates
+        if (dd == 0 && p.lse && in_bounds(row0 + h, p.rows, p.err)) p.lse[row0 + h] = (L == 0.f) ? -INFINITY : (M + log2f(L)) * kLn2;
     }
 }
 
@@ -296,7 +308,7 @@ __global__ void __launch_bounds__(SelCfg<D, kFp8, W>::kThreads, 1) decode_select
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int c = nt * 8 + gid;
-        const bool on = c < ncol;
+        const bool on = c < ncol && in_bounds((static_cast<size_t>(b) * p.Hq + hq0 + c + 1) * D - 1, p.q_elems, p.err);
         const __nv_bfloat16* qh =
             static_cast<const __nv_bfloat16*>(p.q) + (static_cast<size_t>(b) * p.Hq + hq0 + (on ? c : 0)) * D;
 #pragma unroll
@@ -334,7 +346,7 @@ __global__ void __launch_bounds__(SelCfg<D, kFp8, W>::kThreads, 1) decode_select
         for (int sub = 0; sub < J; ++sub) {
             const int s = i * J + sub, slot = (i % Cf::kStages) * J + sub;
             if (s >= n_slab) {
-                if (lane == 0) nvs[slot] = 0;
+                if (lane == 0 && in_bounds(slot, Cf::kStages * J, p.err)) nvs[slot] = 0;
                 continue;
             }
             const int j = s & 31;
@@ -343,7 +355,7 @@ __global__ void __launch_bounds__(SelCfg<D, kFp8, W>::kThreads, 1) decode_select
             if (j == 16) win_next = list.place(s + 16, e_next);
             const int nv = __shfl_sync(0xffffffffu, win.nv, j);
             const int64_t off = __shfl_sync(0xffffffffu, win.off, j) * es;
-            if (lane == 0) nvs[slot] = nv;
+            if (lane == 0 && in_bounds(slot, Cf::kStages * J, p.err)) nvs[slot] = nv;
             if (nv > 0) {
                 // rows past the length are zero-filled (a slab's 16 rows lie in its page)
                 const uint32_t dst = ring + slot * Cf::kPairBytes + c_row * Cf::kRowBytes;
@@ -354,6 +366,7 @@ __global__ void __launch_bounds__(SelCfg<D, kFp8, W>::kThreads, 1) decode_select
                     const int bytes = r < nv ? 16 : 0;
                     const int64_t o = src + x * row_step;
                     const uint32_t d = dst + x * kRowsAtOnce * Cf::kRowBytes + ((c_chunk ^ (r & 7)) << 4);
+                    if (!copy_in<es>(p, o, bytes) || !in_bounds(d + Cf::kSlabBytes + 15 - smem_u32(smem), Cf::kRing, p.err)) continue;
                     cp_async16(d, kbytes + o, bytes);
                     cp_async16(d + Cf::kSlabBytes, vbytes + o, bytes);
                 }
@@ -699,7 +712,7 @@ __global__ void __launch_bounds__(F32Cfg<D, P>::kThreads, 1) decode_selected_f32
     const int n_it = list.count();
     int e_next = list.entry(0);
     for (int i = threadIdx.x; i < kCols * D; i += Cf::kThreads)
-        q_all[i / D][i % D] = i / D < ncol
+        q_all[i / D][i % D] = i / D < ncol && in_bounds((static_cast<size_t>(b) * p.Hq + hq0) * D + i, p.q_elems, p.err)
                                ? static_cast<const float*>(p.q)[(static_cast<size_t>(b) * p.Hq + hq0) * D + i] * p.scale_log2
                                : 0.f;
     const uint32_t ring = smem_u32(smem) + r * kStages * Cf::kStageBytes;
@@ -736,6 +749,7 @@ __global__ void __launch_bounds__(F32Cfg<D, P>::kThreads, 1) decode_selected_f32
                 for (int x = 0; x < kSlab / (P * kRowsAtOnce); ++x) {
                     const int bytes = x * P * kRowsAtOnce + c_row < nv ? 16 : 0;
                     const uint32_t d = dst + x * P * kRowsAtOnce * Cf::kRowBytes;
+                    if (!copy_in<4>(p, src + x * row_step, bytes) || !in_bounds(d + Cf::kSlabBytes + 15 - smem_u32(smem), Cf::kRing, p.err)) continue;
                     cp_async16(d, kbytes + src + x * row_step, bytes);
                     cp_async16(d + Cf::kSlabBytes, vbytes + src + x * row_step, bytes);
                 }
@@ -1022,6 +1036,11 @@ extern "C" int tree_attn_decode_selected(const ta_shape* shape, const ta_paged_k
     p.max_pages = paged->max_pages_per_seq;
     p.page_shift = lay.page_shift;
     p.num_pages = paged->num_pages;
+    p.q_elems = p.out_elems = static_cast<size_t>(shape->batch) * p.Hq * shape->head_dim;
+    p.rows = static_cast<size_t>(shape->batch) * p.Hq;
+    p.list_elems = static_cast<size_t>(shape->batch) * p.Hkv * num_select;
+    p.table_elems = static_cast<size_t>(shape->batch) * p.max_pages;
+    p.cache_elems = static_cast<size_t>((p.num_pages - 1) * p.sb + (p.Hkv - 1) * p.sh + (paged->page_size - 1) * p.st + shape->head_dim);
     const float scale = shape->scale > 0.f ? shape->scale : 1.0f / std::sqrt(static_cast<float>(shape->head_dim));
     p.scale_log2 = scale * kLog2e;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

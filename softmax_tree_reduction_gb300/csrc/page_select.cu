@@ -61,6 +61,7 @@ struct BoundsParams {
     int64_t sb, sh, st;
     int B, Hkv, S, new_tokens, slots;  // slots: pages looked at per row
     int max_pages, page_shift, num_pages;
+    size_t cache_elems, table_elems, bounds_elems;  // extents, for the bounds-checking build
 };
 
 constexpr int kBoundsThreads = 128;
@@ -229,6 +230,7 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
     const int64_t t0 = page << p.page_shift;
     if (t0 >= N) return;
     const int nv = static_cast<int>(min(static_cast<int64_t>(1) << p.page_shift, N - t0));
+    if (!in_bounds(b * p.max_pages + page, p.table_elems, p.err)) return;
     const int phys = __ldg(p.block_table + b * p.max_pages + page);
     if (phys < 0 || phys >= p.num_pages) {
         if (lane == 0) atomicOr(p.err, kErrBadSeqlen);
@@ -238,7 +240,10 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
     const uint8_t* base = static_cast<const uint8_t*>(p.k) + (phys * p.sb + g * p.sh + ch) * es;
     Range<T> r;
     r.init();
-    auto load = [&](int i) { return __ldg(reinterpret_cast<const uint4*>(base + i * p.st * es)); };
+    auto load = [&](int i) {
+        if (!in_bounds(phys * p.sb + g * p.sh + i * p.st + ch + E - 1, p.cache_elems, p.err)) return make_uint4(0u, 0u, 0u, 0u);
+        return __ldg(reinterpret_cast<const uint4*>(base + i * p.st * es));
+    };
     if constexpr (F == 4 && es > 1) {
         int t = tok;
         for (; t + (F - 1) * TW < nv; t += F * TW) {
@@ -269,7 +274,8 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
     __syncwarp();
 #pragma unroll
     for (int off = LT; off < 32; off <<= 1) r.merge(off);
-    if (tok == 0) r.store(p.bounds, ((static_cast<int64_t>(phys) * p.Hkv + g) * 2) * D + ch, D);
+    const int64_t to = ((static_cast<int64_t>(phys) * p.Hkv + g) * 2) * D + ch;
+    if (tok == 0 && in_bounds(to + D + E - 1, p.bounds_elems, p.err)) r.store(p.bounds, to, D);
 }
 
 // ------------------------------------------------------------------- scores
@@ -288,6 +294,16 @@ struct SelectParams {
     int num_select, first, last;
     int max_pages, page_shift, num_pages;
     int per_block, hb;          // pages a block scores, KV heads it does so for
+    int kept;                   // scores that the pick's shared memory holds
+    size_t q_elems, table_elems, bounds_elems;  // extents, for the bounds-checking build
+
+    // Index of channel i of the page's bounds of head g, n of them to be read; whether they are in bounds.
+    __device__ __forceinline__ bool bounds_in(int phys, int g, int i, int n, int d) const {
+        return in_bounds((static_cast<size_t>(phys) * Hkv + g) * 2 * d + i + n - 1, bounds_elems, err);
+    }
+    __device__ __forceinline__ bool page_in(int b, int page) const {
+        return in_bounds(static_cast<size_t>(b) * max_pages + page, table_elems, err);
+    }
 };
 
 constexpr int kScoreThreads = 256;
@@ -306,7 +322,9 @@ __device__ __forceinline__ void two_sum(float a, float b, float* s, float* e) {
 template <int D, typename TQ>
 __device__ __forceinline__ float2 coefficient(const SelectParams& p, int b, int g, int i) {
     const bool up = i >= D;
-    const TQ* q = static_cast<const TQ*>(p.q) + (static_cast<size_t>(b) * p.Hq + g * p.G) * D + (up ? i - D : i);
+    const size_t q0 = (static_cast<size_t>(b) * p.Hq + g * p.G) * D + (up ? i - D : i);
+    if (!in_bounds(q0 + (p.G - 1) * D, p.q_elems, p.err)) return make_float2(0.f, 0.f);
+    const TQ* q = static_cast<const TQ*>(p.q) + q0;
     float s = 0.f, e = 0.f;
 #pragma unroll 4
     for (int h = 0; h < p.G; ++h) {
@@ -326,9 +344,11 @@ template <int D, typename TQ, int E>
 __device__ __forceinline__ void coefficients(const SelectParams& p, int b, int g, int lane, float (&c)[E]) {
     constexpr int kHalf = D / E;
     const float sign = (lane & kHalf) ? 1.f : -1.f;
-    const TQ* q = static_cast<const TQ*>(p.q) + (static_cast<size_t>(b) * p.Hq + g * p.G) * D + (lane & (kHalf - 1)) * E;
+    const size_t q0 = (static_cast<size_t>(b) * p.Hq + g * p.G) * D + (lane & (kHalf - 1)) * E;
+    const TQ* q = static_cast<const TQ*>(p.q) + q0;
 #pragma unroll
     for (int i = 0; i < E; ++i) c[i] = 0.f;
+    if (!in_bounds(q0 + (p.G - 1) * D + E - 1, p.q_elems, p.err)) return;
 #pragma unroll 4
     for (int h = 0; h < p.G; ++h) {
 #pragma unroll
@@ -434,14 +454,15 @@ __global__ void __launch_bounds__(kScoreThreads, ScoreRing<D, TB>::kBlocks) page
     const TB* bounds = static_cast<const TB*>(p.bounds) + static_cast<int64_t>(g) * 2 * D + ll * E;
     uint8_t* ring = ring_all + warp * kStages * Ring::kGroup + lane * Ring::kLane;
     const int kStep = kScoreWarps / p.hb * Ring::kGroupPages;
-    auto lookup = [&](int q) { return (lane < Ring::kGroupPages && q + lane < pmax) ? __ldg(table + q + lane) : -1; };
+    auto lookup = [&](int q) { return (lane < Ring::kGroupPages && q + lane < pmax && p.page_in(b, q + lane)) ? __ldg(table + q + lane) : -1; };
     // start the copies of one group into `stage`; which of its pages are in the pool
     auto issue = [&](int phys, int stage) -> unsigned {
         const unsigned ok = __ballot_sync(0xffffffffu, phys >= 0 && phys < p.num_pages);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int ph = __shfl_sync(0xffffffffu, phys, j * H + side);
-            if ((ok >> (j * H + side)) & 1u)
+            if (((ok >> (j * H + side)) & 1u) && p.bounds_in(ph, g, ll * E, E, D) &&
+                in_bounds(static_cast<size_t>(warp * kStages + stage) * Ring::kGroup + (j * 32 + lane + 1) * Ring::kLane - 1, Ring::kSmem, p.err))
                 copy_async<Ring::kLane>(ring + stage * Ring::kGroup + j * 32 * Ring::kLane,
                                         bounds + static_cast<int64_t>(ph) * p.Hkv * 2 * D);
         }
@@ -509,12 +530,12 @@ __global__ void __launch_bounds__(kScoreThreads, ScoreRing<D, TB>::kBlocks) page
         const bool mine_in = q0 + mine < p1;
         // (a page outside the pool: its sums are of whatever the ring held, and are not used)
         const bool fin = ((here >> mine) & 1u) && fabsf(s[0]) < INFINITY;
-        if (ll % (W / 8) == 0 && mine_in) scores[q0 + mine] = fin ? s[0] + 0.f : INFINITY;  // + 0: one zero
+        if (ll % (W / 8) == 0 && mine_in && in_bounds(q0 + mine, p.stride, p.err)) scores[q0 + mine] = fin ? s[0] + 0.f : INFINITY;  // + 0: one zero
         // (magnitudes are not negative, so their bits are ordered; NaN last.  Pages that are taken
         // in any case do not count: keys of a first page are often far larger than the others)
         const bool competes = q0 + mine >= p.first && q0 + mine < min(p1, n - p.last);
         const uint32_t big = __reduce_max_sync(0xffffffffu, competes && fin ? __float_as_uint(m[0]) : 0u);
-        if (lane < H && q0 + 8 * lane < p1) mags[(q0 >> 3) + lane] = __uint_as_float(big);
+        if (lane < H && q0 + 8 * lane < p1 && in_bounds((q0 >> 3) + lane, p.stride / 8, p.err)) mags[(q0 >> 3) + lane] = __uint_as_float(big);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");  // no copy outlives the block
 }
@@ -650,7 +671,8 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
     if (bad && tid == 0) atomicOr(p.err, kErrBadSeqlen);
     const int n = bad ? 0 : static_cast<int>((static_cast<int64_t>(N) + (1 << p.page_shift) - 1) >> p.page_shift);
     if (n <= p.num_select) {
-        for (int i = tid; i < p.num_select; i += kPickThreads) sel[i] = i < n ? i : -1;
+        for (int i = tid; i < p.num_select; i += kPickThreads)
+            if (in_bounds(i, p.num_select, p.err)) sel[i] = i < n ? i : -1;
         return;
     }
     float2* exact = p.exact + row * p.pages;
@@ -665,12 +687,14 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
     bool ranked = false;
     auto marked = [&](int i, float s) { return i >= lo && i < hi ? fminf(s, most) : (i < n ? always : none); };
     auto scored4 = [&](int i) {
+        if (!in_bounds(4 * i + 3, p.stride, p.err)) return make_float4(none, none, none, none);
         const float4 s = i == tid ? ahead[0] : (i == tid + kPickThreads ? ahead[1] : __ldcg(reinterpret_cast<const float4*>(sc) + i));
         return make_float4(marked(4 * i, s.x), marked(4 * i + 1, s.y), marked(4 * i + 2, s.z), marked(4 * i + 3, s.w));
     };
     const bool kept = n <= kPickKeep;
-    auto four = [&](int i) { return kept ? reinterpret_cast<const float4*>(scores_kept)[i] : scored4(i); };
-    auto one = [&](int i) { return kept ? scores_kept[i] : marked(i, __ldcg(sc + i)); };
+    auto kept_in = [&](int i, int m) { return in_bounds(i + m - 1, p.kept, p.err); };
+    auto four = [&](int i) { return kept && kept_in(4 * i, 4) ? reinterpret_cast<const float4*>(scores_kept)[i] : scored4(i); };
+    auto one = [&](int i) { return kept && kept_in(i, 1) ? scores_kept[i] : marked(i, __ldcg(sc + i)); };
     // Every warp takes a run of consecutive pages, [4 i0, 4 i1), to count and to write.
     const int run = (n4 + kPickThreads - 1) / kPickThreads * 32, i0 = min(n4, warp * run), i1 = min(n4, i0 + run);
     int taken_before = -1;                               // pages taken in the runs before this one (-1: not counted)
@@ -682,7 +706,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
 #pragma unroll 4
         for (int i = tid; i < n4; i += kPickThreads) {
             const float4 s = scored4(i);
-            if (kept) reinterpret_cast<float4*>(scores_kept)[i] = s;
+            if (kept && kept_in(4 * i, 4)) reinterpret_cast<float4*>(scores_kept)[i] = s;
             auto high = [&](float x) { return x == always ? none : x; };
             auto least = [&](float x) { return x == none ? always : x; };
             smax = fmaxf(fmaxf(fmaxf(smax, high(s.x)), high(s.y)), fmaxf(high(s.z), high(s.w)));
@@ -693,7 +717,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
         uint32_t mag = 0;
         // (magnitudes are not negative, so their bits are ordered; NaN last)
         if (8 * tid < n) mag = __float_as_uint(mag_ahead);
-        for (int i = tid + kPickThreads; i < (n + 7) / 8; i += kPickThreads) mag = max(mag, __float_as_uint(__ldcg(mags + i)));
+        for (int i = tid + kPickThreads; i < (n + 7) / 8 && in_bounds(i, p.stride / 8, p.err); i += kPickThreads) mag = max(mag, __float_as_uint(__ldcg(mags + i)));
         uint32_t kmin = __reduce_min_sync(0xffffffffu, ordered(smin));
         uint32_t kmax = __reduce_max_sync(0xffffffffu, ordered(smax));
         mag = __reduce_max_sync(0xffffffffu, mag);
@@ -744,6 +768,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
                     }
                     for (; in != 0; in &= in - 1) {
                         const int j = __ffs(in) - 1, to = atomicAdd(&list_n, 1);
+                        if (!in_bounds(to, 32, p.err)) continue;
                         list_s[to] = j < 2 ? (j == 0 ? q.x : q.y) : (j == 2 ? q.z : q.w);
                         list_i[to] = 4 * i + j;
                     }
@@ -816,9 +841,9 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
             const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.max_pages;
             const TB* bounds = static_cast<const TB*>(p.bounds) + static_cast<int64_t>(g) * 2 * D + lane * PB::E;
             auto again = [&](int i) -> float2 {
-                const int phys = __ldg(table + i);
+                const int phys = p.page_in(b, i) ? __ldg(table + i) : -1;
                 float s = 0.f, e = 0.f;
-                if (phys >= 0 && phys < p.num_pages) {
+                if (phys >= 0 && phys < p.num_pages && p.bounds_in(phys, g, lane * PB::E, PB::E, D)) {
                     PB x;
                     x.load(bounds + static_cast<int64_t>(phys) * p.Hkv * 2 * D);
 #pragma unroll
@@ -860,7 +885,10 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
                         const float s[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            if (s[j] <= top && s[j] >= low) few[atomicAdd(&few_n, 1)] = 4 * i + j;
+                            if (s[j] <= top && s[j] >= low) {
+                                const int to = atomicAdd(&few_n, 1);
+                                if (in_bounds(to, 32, p.err)) few[to] = 4 * i + j;
+                            }
                     }
                 }
                 __syncthreads();
@@ -877,7 +905,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
                         const uint32_t h2 = ordered(few_s[j].x), l2 = ordered(few_s[j].y);
                         better += h2 > h || (h2 == h && (l2 > l || (l2 == l && few[j] < i)));
                     }
-                    scores_kept[i] = better < places ? always : none;
+                    if (kept_in(i, 1)) scores_kept[i] = better < places ? always : none;
                 }
             } else {
                 ranked = true;
@@ -888,7 +916,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
                         const int i = i0 + __ffs(todo) - 1;
                         todo &= todo - 1;
                         const float2 s = again(i);
-                        if (lane == 0) exact[i] = s;
+                        if (lane == 0 && in_bounds(i, p.pages, p.err)) exact[i] = s;
                     }
                 }
                 __syncthreads();  // (the block's own writes to global memory are visible to it)
@@ -920,7 +948,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
     int2 before, all;
     if (kept && !ranked) {  // one threshold tells them all apart: four pages a lane
         auto flags = [&](int i) -> unsigned {  // which of pages 4 i .. are taken
-            const float4 s = i < i1 ? reinterpret_cast<const float4*>(scores_kept)[i] : make_float4(none, none, none, none);
+            const float4 s = i < i1 && kept_in(4 * i, 4) ? reinterpret_cast<const float4*>(scores_kept)[i] : make_float4(none, none, none, none);
             return (s.x >= low ? 1u : 0u) | (s.y >= low ? 2u : 0u) | (s.z >= low ? 4u : 0u) | (s.w >= low ? 8u : 0u);
         };
         if (taken_before < 0) {
@@ -939,7 +967,8 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
             const unsigned b0 = __ballot_sync(0xffffffffu, c & 1), b1 = __ballot_sync(0xffffffffu, c & 2),
                            b2 = __ballot_sync(0xffffffffu, c & 4);
             int to = at + __popc(b0 & lower) + 2 * __popc(b1 & lower) + 4 * __popc(b2 & lower);
-            for (; f != 0; f &= f - 1) sel[to++] = 4 * (i + lane) + __ffs(f) - 1;
+            for (; f != 0; f &= f - 1, ++to)
+                if (in_bounds(to, p.num_select, p.err)) sel[to] = 4 * (i + lane) + __ffs(f) - 1;
             at += __popc(b0) + 2 * __popc(b1) + 4 * __popc(b2);
         }
         return;
@@ -971,7 +1000,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) page_pick_kernel(const Select
         const unsigned eqs = __ballot_sync(0xffffffffu, k == 1);
         const bool take = k == 2 || (k == 1 && eq + __popc(eqs & lower) < ties);
         const unsigned t = __ballot_sync(0xffffffffu, take);
-        if (take) sel[at + __popc(t & lower)] = i + lane;
+        if (take && in_bounds(at + __popc(t & lower), p.num_select, p.err)) sel[at + __popc(t & lower)] = i + lane;
         at += __popc(t);
         eq += __popc(eqs);
     }
@@ -1036,8 +1065,8 @@ int launch_select(SelectParams p, const DeviceInfo& dev, cudaStream_t s) {
         const dim3 grid((p.pages + p.per_block - 1) / p.per_block, (p.Hkv + p.hb - 1) / p.hb, p.B);
         if (launch(page_score_kernel<D, TQ, TB>, grid, kScoreThreads, Ring::kSmem, p, s) != cudaSuccess) return TA_ERR_CUDA;
     }
-    const int smem = p.pages > p.num_select ? std::min(p.stride, kPickKeep) * 4 : 0;
-    return launch(page_pick_kernel<D, TQ, TB>, dim3(p.Hkv, p.B, 1), kPickThreads, smem, p, s) == cudaSuccess ? TA_OK : TA_ERR_CUDA;
+    p.kept = p.pages > p.num_select ? std::min(p.stride, kPickKeep) : 0;
+    return launch(page_pick_kernel<D, TQ, TB>, dim3(p.Hkv, p.B, 1), kPickThreads, p.kept * 4, p, s) == cudaSuccess ? TA_OK : TA_ERR_CUDA;
 }
 
 }  // namespace
@@ -1073,6 +1102,9 @@ extern "C" int tree_attn_page_bounds(const ta_shape* shape, const ta_paged_kv* p
     p.max_pages = paged->max_pages_per_seq;
     p.page_shift = lay.page_shift;
     p.num_pages = paged->num_pages;
+    p.cache_elems = static_cast<size_t>((p.num_pages - 1) * p.sb + (p.Hkv - 1) * p.sh + (paged->page_size - 1) * p.st + shape->head_dim);
+    p.table_elems = static_cast<size_t>(p.B) * p.max_pages;
+    p.bounds_elems = static_cast<size_t>(p.num_pages) * p.Hkv * 2 * shape->head_dim;
     const int64_t items = static_cast<int64_t>(p.B) * p.slots * p.Hkv;
     const int64_t blocks = (items + kBoundsThreads / 32 - 1) / (kBoundsThreads / 32);
     if (blocks > 0x7fffffff) return TA_ERR_SHAPE;
@@ -1146,6 +1178,9 @@ extern "C" int tree_attn_select_pages(const ta_shape* shape, const ta_paged_kv* 
     p.max_pages = paged->max_pages_per_seq;
     p.page_shift = lay.page_shift;
     p.num_pages = paged->num_pages;
+    p.q_elems = static_cast<size_t>(p.B) * p.Hq * shape->head_dim;
+    p.table_elems = static_cast<size_t>(p.B) * p.max_pages;
+    p.bounds_elems = static_cast<size_t>(p.num_pages) * p.Hkv * 2 * shape->head_dim;
     const bool d128 = shape->head_dim == 128, qb = shape->q_dtype == TA_BF16;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (f32) {

@@ -48,6 +48,7 @@ constexpr int kTilesWhole = 24;   // an SM, from which on a warp takes whole til
 struct Vectors {
     void* data;
     int64_t st, sh;  // elements between tokens, heads
+    size_t elems;    // up to the end of the last vector (bounds-checking build)
 };
 
 struct TokenParams {
@@ -69,7 +70,17 @@ struct TokenParams {
     int chunks, hpg;              // groups per token, heads per group
     int rot, interleaved, norm, w_bf16;
     float eps;
+    size_t cache_elems, table_elems;  // extents, for the bounds-checking build
 };
+
+// Whether channels [ch, ch + n) of token t, head h lie in the vectors' memory.
+__device__ __forceinline__ bool vector_in(const Vectors& v, int t, int h, int ch, int n, int* err) {
+    return in_bounds(static_cast<size_t>(t * v.st + h * v.sh + ch + n - 1), v.elems, err);
+}
+// The same of the cache, for the place that a token's vectors have in it.
+__device__ __forceinline__ bool cache_in(const TokenParams& p, int64_t place, int h, int ch, int n) {
+    return in_bounds(static_cast<size_t>(place + h * p.ch + ch + n - 1), p.cache_elems, p.err);
+}
 
 // Four channels of a vector in memory, and as FP32.
 template <typename T>
@@ -202,11 +213,12 @@ __device__ __forceinline__ Lane make_lane(const TokenParams& p, int l) {
     return c;
 }
 
-__device__ __forceinline__ void load_weight(const void* w, int bf16, const Lane& c, float (&f)[8]) {
-    if (w == nullptr) {
+template <int D>
+__device__ __forceinline__ void load_weight(const TokenParams& p, const void* w, const Lane& c, float (&f)[8]) {
+    if (w == nullptr || !in_bounds(c.a + 3, D, p.err) || !in_bounds(c.b + 3, D, p.err)) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = 1.f;
-    } else if (bf16) {
+    } else if (p.w_bf16) {
         Four<__nv_bfloat16> x, y;
         x.load(static_cast<const __nv_bfloat16*>(w) + c.a);
         y.load(static_cast<const __nv_bfloat16*>(w) + c.b);
@@ -277,14 +289,16 @@ struct Runs {
 };
 
 template <typename T, typename Use>
-__device__ __forceinline__ void walk_runs(const T* src, int64_t sh, const Lane& c, int h0, int h1, Use&& use) {
+__device__ __forceinline__ void walk_runs(const TokenParams& p, const Vectors& v, int t, const Lane& c, int h0, int h1, Use&& use) {
+    const T* src = static_cast<const T*>(v.data) + t * v.st;
     const T* sa = src + c.a;
     const T* sb = src + c.b;
     walk_heads<Runs<T>>(
         h0, h1,
         [&](Runs<T>& r, int h) {
-            r.x.load(sa + h * sh);
-            r.y.load(sb + h * sh);
+            if (!vector_in(v, t, h, c.a, 4, p.err) || !vector_in(v, t, h, c.b, 4, p.err)) return;
+            r.x.load(sa + h * v.sh);
+            r.y.load(sb + h * v.sh);
         },
         [&](const Runs<T>& r, int h) {
             float f[8];
@@ -294,11 +308,14 @@ __device__ __forceinline__ void walk_runs(const T* src, int64_t sh, const Lane& 
         });
 }
 
-// Whole vectors, the lane's eight channels from `src` on.
-template <typename T, typename Use>
-__device__ __forceinline__ void walk_whole(const T* src, int64_t sh, int h0, int h1, Use&& use) {
+// Whole vectors, the lane's eight channels from `src` on; in(h): whether head h's are in bounds.
+template <typename T, typename In, typename Use>
+__device__ __forceinline__ void walk_whole(const T* src, int64_t sh, int h0, int h1, In&& in, Use&& use) {
     walk_heads<Eight<T>>(
-        h0, h1, [&](Eight<T>& e, int h) { e.load(src + h * sh); },
+        h0, h1,
+        [&](Eight<T>& e, int h) {
+            if (in(h)) e.load(src + h * sh);
+        },
         [&](const Eight<T>& e, int h) {
             float f[8];
             e.unpack(f);
@@ -326,7 +343,8 @@ __device__ __forceinline__ void to_codes(const float* scale, int h, float (&f)[8
 __device__ __forceinline__ int64_t cache_place(const TokenParams& p, int t, int row, int pos) {
     if (row < p.B && pos < p.S) {
         if (!p.block_table) return row * p.cb + pos * p.ct;
-        const int page = __ldg(p.block_table + static_cast<int64_t>(row) * p.max_pages + (pos >> p.page_shift));
+        const int64_t e = static_cast<int64_t>(row) * p.max_pages + (pos >> p.page_shift);
+        const int page = in_bounds(e, p.table_elems, p.err) ? __ldg(p.block_table + e) : -1;
         if (page >= 0 && page < p.num_pages) return page * p.cb + (pos & ((1 << p.page_shift) - 1)) * p.ct;
     }
     atomicOr(p.err, kErrBadSeqlen);
@@ -393,19 +411,22 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 5) token_write_
     float cs[4], sn[4];
     if (c.on && p.chunks > 0) {
         const int at = lane / L * (D / 2) + 4 * (lane % L);
+        if (!in_bounds(at + 3, kThreads, p.err)) return;
         const float4 u = *reinterpret_cast<const float4*>(cos_s + at), v = *reinterpret_cast<const float4*>(sin_s + at);
         cs[0] = u.x, cs[1] = u.y, cs[2] = u.z, cs[3] = u.w;
         sn[0] = v.x, sn[1] = v.y, sn[2] = v.z, sn[3] = v.w;
     } else if (c.on) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) turn(pos, __ldg(p.inv_freq + 4 * (lane % L) + i), &cs[i], &sn[i]);
+        for (int i = 0; i < 4; ++i)
+            if (in_bounds(4 * (lane % L) + i, p.rot / 2, p.err)) turn(pos, __ldg(p.inv_freq + 4 * (lane % L) + i), &cs[i], &sn[i]);
     }
     if (h0 < p.Hq) {
         float w[8];
-        if (p.norm) load_weight(p.qw, p.w_bf16, c, w);
+        if (p.norm) load_weight<D>(p, p.qw, c, w);
         T* dst = static_cast<T*>(p.qo.data) + t * p.qo.st;
-        walk_runs(static_cast<const T*>(p.q.data) + t * p.q.st, p.q.sh, c, h0, min(h1, p.Hq), [&](int h, float (&f)[8]) {
+        walk_runs<T>(p, p.q, t, c, h0, min(h1, p.Hq), [&](int h, float (&f)[8]) {
             norm_rotate<L>(p, c, cs, sn, w, f, mask);
+            if (!vector_in(p.qo, t, h, c.a, 4, p.err) || !vector_in(p.qo, t, h, c.b, 4, p.err)) return;
             store_runs(dst + h * p.qo.sh, c, f);
         });
     }
@@ -417,26 +438,30 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 5) token_write_
     }
     if (h0 < kend) {
         float w[8];
-        if (p.norm) load_weight(p.kw, p.w_bf16, c, w);
-        walk_runs(static_cast<const T*>(p.k.data) + t * p.k.st, p.k.sh, c, max(h0 - p.Hq, 0), min(h1 - p.Hq, p.Hkv),
-                  [&](int h, float (&f)[8]) {
-                      norm_rotate<L>(p, c, cs, sn, w, f, mask);
-                      if constexpr (!kCache) {
-                          store_runs(static_cast<T*>(p.ko.data) + t * p.ko.st + h * p.ko.sh, c, f);
-                      } else {
-                          to_codes<TC>(p.ks, h, f);
-                          store_runs(static_cast<TC*>(p.kc) + place + h * p.ch, c, f);
-                      }
-                  });
+        if (p.norm) load_weight<D>(p, p.kw, c, w);
+        walk_runs<T>(p, p.k, t, c, max(h0 - p.Hq, 0), min(h1 - p.Hq, p.Hkv), [&](int h, float (&f)[8]) {
+            norm_rotate<L>(p, c, cs, sn, w, f, mask);
+            if constexpr (!kCache) {
+                if (!vector_in(p.ko, t, h, c.a, 4, p.err) || !vector_in(p.ko, t, h, c.b, 4, p.err)) return;
+                store_runs(static_cast<T*>(p.ko.data) + t * p.ko.st + h * p.ko.sh, c, f);
+            } else {
+                if (!cache_in(p, place, h, c.a, 4) || !cache_in(p, place, h, c.b, 4)) return;
+                to_codes<TC>(p.ks, h, f);
+                store_runs(static_cast<TC*>(p.kc) + place + h * p.ch, c, f);
+            }
+        });
     }
     if constexpr (kCache) {
         if (h1 <= kend) return;
         const int ch = 8 * (lane % L);
-        walk_whole(static_cast<const T*>(p.v.data) + t * p.v.st + ch, p.v.sh, max(h0 - kend, 0), h1 - kend,
-                   [&](int h, float (&f)[8]) {
-                       to_codes<TC>(p.vs, h, f);
-                       store8(static_cast<TC*>(p.vc) + place + h * p.ch + ch, f);
-                   });
+        walk_whole(
+            static_cast<const T*>(p.v.data) + t * p.v.st + ch, p.v.sh, max(h0 - kend, 0), h1 - kend,
+            [&](int h) { return vector_in(p.v, t, h, ch, 8, p.err); },
+            [&](int h, float (&f)[8]) {
+                if (!cache_in(p, place, h, ch, 8)) return;
+                to_codes<TC>(p.vs, h, f);
+                store8(static_cast<TC*>(p.vc) + place + h * p.ch + ch, f);
+            });
     }
 }
 
@@ -463,17 +488,20 @@ __global__ void __launch_bounds__(kThreads) token_read_kernel(const TokenParams 
         if (place < 0) {
             const float nan = __int_as_float(0x7fc00000);
             const float f[8] = {nan, nan, nan, nan, nan, nan, nan, nan};
-            for (int h = a; h < b; ++h) store8(dst + h * out.sh, f);
+            for (int h = a; h < b; ++h)
+                if (vector_in(out, t, h, ch, 8, p.err)) store8(dst + h * out.sh, f);
             continue;
         }
-        walk_whole(static_cast<const TC*>(kv ? p.vc : p.kc) + place + ch, p.ch, a, b, [&](int h, float (&f)[8]) {
-            if constexpr (std::is_same<TC, __nv_fp8_e4m3>::value) {
-                const float sc = __ldg(scale + h);
+        walk_whole(
+            static_cast<const TC*>(kv ? p.vc : p.kc) + place + ch, p.ch, a, b, [&](int h) { return cache_in(p, place, h, ch, 8); },
+            [&](int h, float (&f)[8]) {
+                if constexpr (std::is_same<TC, __nv_fp8_e4m3>::value) {
+                    const float sc = __ldg(scale + h);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] *= sc;
-            }
-            store8(dst + h * out.sh, f);
-        });
+                    for (int i = 0; i < 8; ++i) f[i] *= sc;
+                }
+                if (vector_in(out, t, h, ch, 8, p.err)) store8(dst + h * out.sh, f);
+            });
     }
 }
 
@@ -616,13 +644,21 @@ int check_cache_call(const ta_shape* shape, const ta_paged_kv* paged, const ta_t
     p->Hkv = shape->num_kv_heads;
     p->B = shape->batch;
     p->S = shape->max_seqlen;
+    p->cache_elems = static_cast<size_t>(((paged ? paged->num_pages : p->B) - 1) * lay.stride_b + (p->Hkv - 1) * lay.stride_h +
+                                         ((paged ? paged->page_size : p->S) - 1) * lay.stride_t + shape->head_dim);
     if (paged) {
+        p->table_elems = static_cast<size_t>(p->B) * paged->max_pages_per_seq;
         p->block_table = paged->block_table;
         p->max_pages = paged->max_pages_per_seq;
         p->page_shift = lay.page_shift;
         p->num_pages = paged->num_pages;
     }
     return TA_OK;
+}
+
+// Elements from the first of T x H vectors of d channels to the end of the last.
+size_t extent(int64_t T, int64_t H, int64_t st, int64_t sh, int64_t d) {
+    return T > 0 && H > 0 ? static_cast<size_t>((T - 1) * st + (H - 1) * sh + d) : 0;
 }
 
 // Enqueue a checked call.  `cache`: the cache's type, -1 without a cache.
@@ -632,6 +668,8 @@ int enqueue(const ta_shape* shape, TokenParams* p, int heads, int cache, bool re
     const int rc = device_info(&dev);
     if (rc != TA_OK) return rc;
     p->err = dev.err;
+    for (Vectors* v : {&p->q, &p->qo}) v->elems = extent(p->T, p->Hq, v->st, v->sh, shape->head_dim);
+    for (Vectors* v : {&p->k, &p->ko, &p->v, &p->vo}) v->elems = extent(p->T, p->Hkv, v->st, v->sh, shape->head_dim);
     int64_t tile = 0;  // warps to a tile
     if (read)
         plan_groups(p, heads, shape->head_dim / 8, dev.num_sms);
