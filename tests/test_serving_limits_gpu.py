@@ -58,3 +58,33 @@ def test_select_pages_without_memory_for_its_workspace():
     ta.tree_attn_select_pages(q, bounds, bt, lens, page, 4, 1, 1, selected=sel)
     assert sel.cpu().tolist() == [[[0, -1, -1, -1]] * hkv] * B
     assert ta.tree_attn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("kv", [torch.bfloat16, torch.float8_e4m3fn, torch.float32])
+def test_keys_and_values_of_one_pool(kv):
+    """Caches that are views of one [pages, 2, page, heads, channels] pool, heads padded at the end:
+    every call gives what it gives on pools of their own, and the padding stays."""
+    pages, page, hkv, d, B, per = 24, 16, 3, 128, 2, 11
+    g = torch.Generator().manual_seed(7)
+    dt = torch.float32 if kv == torch.float32 else BF16
+    pool = torch.full((pages, 2, page, hkv + 1, d), 3.0).to(kv).cuda()
+    own = [torch.full((pages, page, hkv, d), 3.0).to(kv).cuda() for _ in range(2)]
+    views = [pool[:, i, :, :hkv] for i in range(2)]
+    bt = torch.randperm(pages, generator=g)[:B * per].view(B, per).to(torch.int32).cuda()
+    lens = torch.tensor([per * page - 3, 100], dtype=torch.int32).cuda()
+    rows = torch.arange(B).repeat_interleave(lens.cpu().long()).to(torch.int32).cuda()
+    pos = torch.cat([torch.arange(int(n)) for n in lens]).to(torch.int32).cuda()
+    k, v = (torch.randn(rows.numel(), hkv, d, generator=g).to(dt).cuda() for _ in range(2))
+    q = torch.randn(B, 2 * hkv, d, generator=g).to(dt).cuda()
+    sc = dict(k_scale=torch.full((hkv,), 0.02).cuda(), v_scale=torch.full((hkv,), 0.03).cuda()) if kv == torch.float8_e4m3fn else {}
+    got = []
+    for kc, vc in (views, own):
+        ta.tree_attn_cache_write(k, v, kc, vc, pos, rows=rows, block_table=bt, **sc)
+        read = ta.tree_attn_cache_read(kc, vc, pos, rows=rows, block_table=bt, dtype=dt, **sc)
+        bounds = ta.tree_attn_page_bounds(kc, bt, lens)
+        sel = ta.tree_attn_select_pages(q, bounds, bt, lens, page, 5)
+        got.append((*read, bounds, sel, *ta.tree_attn_decode_selected(q, kc, vc, bt, lens, sel, **sc)))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    for view, o in zip(views, own):
+        assert torch.equal(view.float(), o.float())
+    assert bool((pool[:, :, :, hkv].float() == 3).all()) and ta.tree_attn_get_device_error() == 0
