@@ -37,6 +37,25 @@ def test_dense_cache_calls_apply_max_seqlen(layout):
     assert ta.tree_attn_get_device_error() == 0 and torch.equal(kc[2, :, S - 1], k[2])
 
 
+def test_queries_of_tokens_without_a_place():
+    """A token whose row, position or page is bad is not stored, but its query is normed and rotated."""
+    B, S, hkv, d, page = 2, 64, 1, 128, 16
+    g = torch.Generator().manual_seed(3)
+    q, k = torch.randn(5, 3, d, generator=g).to(BF16).cuda(), torch.randn(5, hkv, d, generator=g).to(BF16).cuda()
+    pool = torch.full((9, page, hkv, d), 5.0, dtype=BF16, device="cuda")
+    bt = torch.arange(8, dtype=torch.int32).view(B, 4).cuda()
+    bt[1, 1] = 9
+    rows, pos = torch.tensor([0, 2, 0, 1, -1], dtype=torch.int32).cuda(), torch.tensor([3, 3, S, 20, 9], dtype=torch.int32).cuda()
+    f = torch.rand(d // 2, generator=g).cuda()
+    qo = ta.tree_attn_cache_write(k, k, pool, pool.clone(), pos, rows=rows, block_table=bt, q=q, inv_freq=f, norm=True)
+    assert ta.tree_attn_get_device_error() == ta.TA_ERR_DEVICE_DATA
+    want, kn = ta.tree_attn_norm_rope(q, k, pos, f)
+    assert torch.equal(qo[:4], want[:4]) and bool((qo[4] == 0).all())        # (row -1: a padding token)
+    left = torch.full_like(pool, 5.0)
+    left[0, 3] = kn[0]
+    assert torch.equal(pool, left)
+
+
 def test_select_pages_without_memory_for_its_workspace():
     """torch's own out-of-memory error, as an output allocated by torch would raise it, and the
     call works again once there is memory."""
