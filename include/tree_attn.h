@@ -376,7 +376,8 @@ typedef struct {
  *             (a, b) -> (a cos - b sin, b cos + a sin); the pair is the channels
  *             (i, i + rot_dim/2), or (2i, 2i+1) with `interleaved`.  Channels from
  *             rot_dim on are not turned.  The angle is reduced modulo a full turn in
- *             64-bit fixed point, so far positions lose nothing. */
+ *             64-bit fixed point before it is rounded to FP32 (at most 2^-25 half
+ *             turns off), so far positions lose nothing that near ones keep. */
 typedef struct {
     const float *inv_freq;   /* device float [rot_dim/2]; NULL only when rot_dim is 0 */
     const void *q_weight;    /* device [head_dim] of weight_dtype, or NULL: ones (norm only) */
@@ -410,10 +411,11 @@ int tree_attn_norm_rope(const ta_shape *shape, const ta_tokens *tokens, const ta
  *               x / k_scale[g] (v_scale for values): device float [num_kv_heads],
  *               positive; both NULL for other caches
  * Positions not in the list keep what they hold.  A (row, position) should be in the
- * list once: of several vectors for one place, which is stored is not defined.
+ * list once: of several vectors for one place, what is stored is not defined (it may be
+ * parts of several).
  * A row outside [0, batch), a position outside [0, max_seqlen) or a block-table
- * entry outside the pool stores nothing for that token and sets the device
- * error word (TA_ERR_DEVICE_DATA). */
+ * entry outside the pool stores no key and value for that token and sets the device
+ * error word (TA_ERR_DEVICE_DATA); its query is normed and rotated all the same. */
 int tree_attn_cache_write(const ta_shape *shape, const ta_paged_kv *paged, const ta_tokens *tokens,
                           const ta_rope *rope, const ta_heads *q, const ta_heads *q_out,
                           const ta_heads *k, const ta_heads *v, void *k_cache, void *v_cache,

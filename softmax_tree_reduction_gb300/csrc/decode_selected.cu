@@ -466,8 +466,9 @@ __global__ void __launch_bounds__(SelCfg<D, kFp8, W>::kThreads, 1) decode_select
             }
         }
         // Online softmax per column.  P^T as B fragments: the weights as the sum of three
-        // BF16 numbers (all 24 bits; two leave 2^-18, which shows in FP32 outputs), or two
-        // FP16 ones (22 bits).
+        // BF16 numbers (all 24 bits; two leave 2^-17, which shows in FP32 outputs), or two
+        // FP16 ones (22 bits: at most four half steps of FP32, as much as ex2 is off by; a third
+        // would be half as many products again).
         uint32_t bh[J][NT][2], bl[J][NT][2], bt[J][NT][2];
         float alpha[NT][2];
 #pragma unroll

@@ -31,9 +31,10 @@
 // listed and ranked.  Where more than 32 share it, the last page's score is found
 // digit by digit instead (11 bits a pass of the scores as order-preserving integers, whose
 // common leading bits are skipped).  Ties go to the lowest pages.  Digits alone took
-// 8.3 us for 8 x 2048 pages and 21.6 for 32 x 4096, this takes 6.9 and 19.6 with the
-// scores; more than 32 pages within the error of each other cost up to 100 us more (all
-// 4096 alike: 184 us), as they are summed again.
+// 8.3 us for 8 x 2048 pages and 21.6 for 32 x 4096, this takes 6.9 to 7.8 and 19.6 to 20.5
+// with the scores, by the device.  Pages within the error of each other are summed again: 32
+// lists of 4096 pages take 16 us where FP32 ranks them, 61 where one page's scores of
+// 10^4 times the others' widen the error of all, 106 with half of the pages alike, 181 with all.
 //
 // Summing every page as two FP32 numbers cost 135 instructions a page (28 us for
 // the same 131072 scores).

@@ -17,14 +17,18 @@
 //
 // Long lists are bound by HBM; with few tokens a token's heads are spread over warps
 // and blocks, and the call is bound by the latency of one load, the angles and one
-// store.
+// store.  Writing a prompt into an E4M3 cache is bound by instructions: the codes are
+// those of the quotient x / scale, an IEEE division a channel (16384 tokens of 8 + 8 BF16
+// heads 28.5 us against 24 into a BF16 cache of twice the bytes).
 //
 // Rotation angles.  The angle p * f of position p is needed modulo 2 pi.  The
 // frequency is turned into a 64-bit binary fraction of a full turn per
 // position, u = f / (2 pi) * 2^64, by an integer product with 2^64 / (2 pi);
-// u * p in 64-bit wrap-around arithmetic is then the angle modulo one turn,
-// with an error of at most about p * 2^-63 turns whatever the position, and its
-// top bits go to sincospi.
+// u * p in 64-bit wrap-around arithmetic is then the angle modulo one turn.  Two
+// truncations leave an error of at most (1 + |f|) p 2^-64 turns: 2^-32 turns at p = 2^31
+// and |f| <= 1.  The angle then becomes one FP32 number of half turns for sincospi, off by
+// at most 2^-25 of them (9.4e-8 rad, at any position), which is the size of the
+// rounding of an FP32 result (6.0e-8).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
