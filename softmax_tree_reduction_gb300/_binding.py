@@ -188,9 +188,10 @@ def _stream(stream) -> int:
 def _cache_strides(cache: torch.Tensor):
     """Strides of a cache's first three axes.  Entries that share memory are refused: strides of 0
     on every axis would mean a dense cache to the library, which then reads past the view."""
-    if any(n > 1 and st == 0 for n, st in zip(cache.shape[:3], cache.stride()[:3])):
+    strides = cache.stride()[:3]
+    if 0 in strides and any(n > 1 and st == 0 for n, st in zip(cache.shape, strides)):
         raise ValueError("a cache's entries must not share memory: an axis of several has stride 0")
-    return cache.stride()[:3]
+    return strides
 
 
 def make_shape(q: torch.Tensor, k_cache: torch.Tensor, scale: Optional[float] = None) -> TaShape:

@@ -126,7 +126,7 @@ bool overlapping(int64_t n, int64_t a, int64_t m, int64_t b, int64_t d) {
     // the usual layouts: the smaller step keeps vectors apart, and the larger one its whole runs
     if ((m == 1 || b >= d) && (n == 1 || a >= (m - 1) * b + d)) return false;
     if ((m > 1 && b < d) || (n > 1 && a < d)) return true;
-    for (int64_t y = 1; y < m; ++y) {  // (x and y of opposite signs; the x on either side of y b / a)
+    for (int64_t y = 1; y < m && y * b < (n - 1) * a + d; ++y) {  // (x and y of opposite signs; the x on either side of y b / a)
         const int64_t x = y * b / a;
         if ((x < n && y * b - x * a < d) || (x + 1 < n && (x + 1) * a - y * b < d)) return true;
     }
