@@ -31,7 +31,7 @@
 // listed and ranked.  Where more than 32 share it, the last page's score is found
 // digit by digit instead (11 bits a pass of the scores as order-preserving integers, whose
 // common leading bits are skipped).  Ties go to the lowest pages.  Digits alone took
-// 8.3 us for 8 x 2048 pages and 21.6 for 32 x 4096, this takes 6.9 to 7.8 and 19.6 to 20.5
+// 8.3 us for 8 x 2048 pages and 21.6 for 32 x 4096, this takes 6.9 to 7.8 and 19.6 to 20.7
 // with the scores, by the device.  Pages within the error of each other are summed again: 32
 // lists of 4096 pages take 16 us where FP32 ranks them, 61 where one page's scores of
 // 10^4 times the others' widen the error of all, 106 with half of the pages alike, 181 with all.
