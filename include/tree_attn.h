@@ -72,10 +72,12 @@ typedef enum {
 typedef enum {
     TA_F32 = 0,   /* IEEE binary32 */
     TA_BF16 = 1,  /* bfloat16 (upper half of a binary32) */
-    TA_E4M3 = 2   /* FP8 E4M3 ("fn": no infinities), KV caches only; the element
+    TA_E4M3 = 2,  /* FP8 E4M3 ("fn": no infinities), KV caches only; the element
                      value is the code times a per-KV-head scale given in
                      ta_options (k_scale, v_scale).  Needs BF16 q, head_dim 128
                      and at most 16 query heads (x queries) per KV head. */
+    TA_INT4 = 3   /* 4-bit codes with a step for each 16 channels, KV caches of the
+                     _int4 calls only (see ta_int4_kv) */
 } ta_dtype;
 
 /* Largest accepted num_splits. */
@@ -498,6 +500,95 @@ int tree_attn_decode_selected(const ta_shape *shape, const ta_paged_kv *paged, c
                               const void *k_pages, const void *v_pages, const int32_t *seqlens,
                               const int32_t *selected, int num_select, float *out, float *lse,
                               const float *k_scale, const float *v_scale, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Caches held in 4 bits.
+ *
+ * A vector of head_dim channels is held as head_dim codes of 4 bits (two
+ * channels a byte, the even one in the low half) and an E4M3 step for each 16
+ * neighbouring channels: 72 bytes at head_dim 128, against 256 in BF16.
+ *      value = scale[g] * (step * (code - 8))
+ * with the product in brackets exact and one FP32 rounding after it; scale is
+ * an FP32 number for each KV head, 1 where none is given.
+ * `shape` is that of the other calls with kv_dtype TA_INT4 and its kv_stride_*
+ * 0; dense caches are [batch][num_kv_heads][max_seqlen], pools [num_pages]
+ * [page_size][num_kv_heads], followed by the vector's bytes, unless strides say
+ * otherwise.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    void *k_codes;           /* device, head_dim / 2 bytes a vector; 16-byte aligned */
+    void *v_codes;
+    void *k_steps;           /* device, head_dim / 16 bytes a vector, aligned to that many bytes */
+    void *v_steps;
+    int64_t code_stride_b;   /* bytes between rows or pages; multiples of 16; all three 0: the layout above */
+    int64_t code_stride_h;   /* between KV heads */
+    int64_t code_stride_t;   /* between tokens */
+    int64_t step_stride_b;   /* bytes; multiples of head_dim / 16; all three 0: the layout above */
+    int64_t step_stride_h;
+    int64_t step_stride_t;
+    const float *k_scale;    /* device float [num_kv_heads], positive; both or neither */
+    const float *v_scale;
+} ta_int4_kv;
+
+/* tree_attn_cache_write into a 4-bit cache.  y, the FP32 channels after the norm
+ * and the rotation, is stored as
+ *      z = y / scale[g]                                   (FP32 quotient; y without a scale)
+ *      step = E4M3(min(max(FP32(top / 7), 2^-9), 448)),   top = max |z| of the 16 channels
+ *      code = 8 + the whole number next to z / step (ties to even) in [-7, 7]
+ * so finite values beyond 7 * 448 scales saturate, as infinite ones do, and a NaN
+ * makes its 16 channels NaN.  Other arguments, padding, bad data and places that are
+ * listed twice as there. */
+int tree_attn_cache_write_int4(const ta_shape *shape, const ta_paged_kv *paged,
+                               const ta_tokens *tokens, const ta_rope *rope, const ta_heads *q,
+                               const ta_heads *q_out, const ta_heads *k, const ta_heads *v,
+                               const ta_int4_kv *cache, void *stream);
+
+/* tree_attn_cache_read from a 4-bit cache. */
+int tree_attn_cache_read_int4(const ta_shape *shape, const ta_paged_kv *paged,
+                              const ta_tokens *tokens, const ta_int4_kv *cache,
+                              const ta_heads *k_out, const ta_heads *v_out, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Attention to a window of the cache behind a few first tokens ("sinks").
+ *
+ * Query i of row b sits at position s = seqlens[b] - num_queries + i and sees the
+ * tokens t <= s with t > s - window or t < sinks (each once).  A window of
+ * max_seqlen or more leaves the causal mask alone.  Only tokens that some query of
+ * the row sees are read, and only their pages' block-table entries: pages that fell
+ * out of the window may be freed or reused, whatever their entries hold.
+ * Values of tokens that a query does not see take no part in its output, also when
+ * they are infinite or NaN.
+ * ------------------------------------------------------------------------ */
+
+/* Bytes of device workspace for the two calls below: 0 when a call of this shape
+ * needs none on the current device (and for invalid input).  kv_dtype TA_INT4 is
+ * tree_attn_decode_int4's. */
+size_t tree_attn_window_workspace_bytes(const ta_shape *shape, const ta_paged_kv *paged,
+                                        int num_queries, int window, int sinks);
+
+/* tree_attn_decode_multi (causal) within the window.
+ *  q    device [batch][num_q_heads][num_queries][head_dim], dense, q_dtype
+ *  out  device float32, as q; lse device float32 [batch][num_q_heads][num_queries] or NULL
+ *  num_queries in [1, 16], window >= 1, sinks >= 0
+ *  workspace  device, >= tree_attn_window_workspace_bytes, 16-byte aligned (NULL where that
+ *       is 0); contents on entry are ignored; calls sharing one must be ordered on the GPU
+ * Types as for tree_attn_decode_selected: BF16 q with a BF16 cache (up to 64 query heads a
+ * KV head) or an E4M3 cache (head_dim 128; k_scale, v_scale), FP32 q with an FP32 cache
+ * (up to 16).  A query that sees no token gives out = 0, lse = -inf.  A length
+ * outside [0, max_seqlen] makes the row NaN, a page outside the pool its (row, KV head), and the
+ * device error word is set.  Results are bitwise reproducible on one device model. */
+int tree_attn_decode_window(const ta_shape *shape, const ta_paged_kv *paged, int num_queries,
+                            int window, int sinks, const void *q, const void *k_cache,
+                            const void *v_cache, const int32_t *seqlens, float *out, float *lse,
+                            const float *k_scale, const float *v_scale, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* The same over a 4-bit cache; BF16 q, up to 64 query heads a KV head.  The logits and outputs
+ * are those of the cache's values (of ta_int4_kv's formula) in FP32. */
+int tree_attn_decode_int4(const ta_shape *shape, const ta_paged_kv *paged, int num_queries,
+                          int window, int sinks, const void *q, const ta_int4_kv *cache,
+                          const int32_t *seqlens, float *out, float *lse, void *workspace,
+                          size_t workspace_bytes, void *stream);
 
 /* Synchronise `stream`, then read and clear the current device's error word.
  * Returns TA_OK, TA_ERR_DEVICE_DATA, TA_ERR_DEVICE_TIMEOUT or (bounds-checking

@@ -24,7 +24,7 @@ TA_OK = 0
 TA_ERR_DEVICE_DATA = -8      # a length or page-table entry outside its range (rows are NaN)
 TA_ERR_DEVICE_TIMEOUT = -9   # a bounded on-chip wait gave up (outputs are NaN)
 TA_ERR_DEVICE_BOUNDS = -11   # bounds-checking build: an index outside its buffer was caught
-TA_F32, TA_BF16, TA_E4M3 = 0, 1, 2
+TA_F32, TA_BF16, TA_E4M3, TA_INT4 = 0, 1, 2, 3
 TA_KERNEL = {"auto": 0, "fma": 1, "mma": 2, "tc05": 3}
 TA_MAX_SPLITS = 4096
 TA_FLAG_DETERMINISTIC = 1
@@ -40,7 +40,9 @@ _EXPORTS = ["tree_attn_status_string", "tree_attn_version", "tree_attn_check_sha
             "tree_attn_decode_noalloc", "tree_attn_launch_count", "tree_attn_decode_paged",
             "tree_attn_decode_multi", "tree_attn_pick_splits_paged", "tree_attn_norm_rope",
             "tree_attn_cache_write", "tree_attn_cache_read", "tree_attn_page_bounds",
-            "tree_attn_select_workspace_bytes", "tree_attn_select_pages", "tree_attn_decode_selected"]
+            "tree_attn_select_workspace_bytes", "tree_attn_select_pages", "tree_attn_decode_selected",
+            "tree_attn_cache_write_int4", "tree_attn_cache_read_int4", "tree_attn_window_workspace_bytes",
+            "tree_attn_decode_window", "tree_attn_decode_int4"]
 
 
 class TaShape(ctypes.Structure):
@@ -77,6 +79,13 @@ class TaRope(ctypes.Structure):
     _fields_ = [("inv_freq", ctypes.c_void_p), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
                 ("weight_dtype", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
                 ("norm", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class TaInt4KV(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_steps", ctypes.c_void_p), ("v_steps", ctypes.c_void_p),
+                ("code_stride_b", ctypes.c_int64), ("code_stride_h", ctypes.c_int64), ("code_stride_t", ctypes.c_int64),
+                ("step_stride_b", ctypes.c_int64), ("step_stride_h", ctypes.c_int64), ("step_stride_t", ctypes.c_int64),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 
 class TreeAttnError(RuntimeError):
@@ -139,6 +148,15 @@ def load(path: str = LIB_PATH):
         lib.tree_attn_select_workspace_bytes.restype = SZ
         lib.tree_attn_select_pages.argtypes = [SP, GP, P, P, P, I32, I32, I32, P, P, SZ, P]
         lib.tree_attn_decode_selected.argtypes = [SP, GP, P, P, P, P, P, I32, P, P, P, P, P]
+        IP = ctypes.POINTER(TaInt4KV)
+        lib.tree_attn_cache_write_int4.argtypes = [SP, GP, TP, RP, HP, HP, HP, HP, IP, P]
+        lib.tree_attn_cache_read_int4.argtypes = [SP, GP, TP, IP, HP, HP, P]
+        lib.tree_attn_window_workspace_bytes.argtypes = [SP, GP, I32, I32, I32]
+        lib.tree_attn_window_workspace_bytes.restype = SZ
+        lib.tree_attn_decode_window.argtypes = [SP, GP, I32, I32, I32, P, P, P, P, P, P, P, P, P, SZ, P]
+        lib.tree_attn_decode_int4.argtypes = [SP, GP, I32, I32, I32, P, IP, P, P, P, P, SZ, P]
+        for name in ("cache_write_int4", "cache_read_int4", "decode_window", "decode_int4"):
+            getattr(lib, "tree_attn_" + name).restype = I32
         for name in ("norm_rope", "cache_write", "cache_read", "page_bounds", "select_pages", "decode_selected"):
             getattr(lib, "tree_attn_" + name).restype = I32
         lib.tree_attn_get_device_error.restype = I32

@@ -223,3 +223,127 @@ def tree_attn_decode_selected(q: torch.Tensor, k_pages: torch.Tensor, v_pages: t
     if rc:
         raise TreeAttnError(rc, "tree_attn_decode_selected")
     return out, lse
+
+
+def tree_attn_cache_write_int4(k: torch.Tensor, v: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor,
+                               k_steps: torch.Tensor, v_steps: torch.Tensor, positions: torch.Tensor,
+                               rows: Optional[torch.Tensor] = None, block_table: Optional[torch.Tensor] = None,
+                               k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                               q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                               inv_freq: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+                               k_weight: Optional[torch.Tensor] = None, norm: bool = False, eps: float = 1e-6,
+                               interleaved: bool = False, max_seqlen: Optional[int] = None, stream=None):
+    """Store the keys and values of a token list in a 4-bit cache.
+
+    The cache is codes, uint8 [B, Hkv, S, d / 2] or pools [num_pages, page_size, Hkv, d / 2] with
+    ``block_table`` (two channels a byte, the even one in the low half), and steps, float8_e4m3fn
+    [.., d / 16]; a channel's value is scale * step * (code - 8) with the FP32 scale of its KV head
+    (``k_scale``/``v_scale``, both or neither).  Each 16 channels get the step next to a seventh of
+    their largest magnitude and the codes next to their quotients by it.  The other arguments are
+    tree_attn_cache_write's.  Returns q_out (None without q).
+    """
+    if stream is not None or (q is not None and q_out is None):
+        stream, ctx = _on(stream, k)
+        if q is not None and q_out is None:
+            with ctx:
+                q_out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    rc = (_calls or _open()).cache_write_int4(k, v, k_codes, v_codes, k_steps, v_steps, positions, rows, block_table, k_scale, v_scale, q, q_out,
+                                              inv_freq, q_weight, k_weight, norm, eps, interleaved, max_seqlen, stream)
+    if rc:
+        raise TreeAttnError(rc, "tree_attn_cache_write_int4")
+    return q_out
+
+
+def tree_attn_cache_read_int4(k_codes: torch.Tensor, v_codes: torch.Tensor, k_steps: torch.Tensor, v_steps: torch.Tensor,
+                              positions: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                              block_table: Optional[torch.Tensor] = None, k_scale: Optional[torch.Tensor] = None,
+                              v_scale: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
+                              k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
+                              max_seqlen: Optional[int] = None, stream=None):
+    """Read the keys and values of a token list from a 4-bit cache (tree_attn_cache_write_int4).
+
+    Returns (k_out, v_out), [T, Hkv, d] of ``dtype`` (BF16 or FP32) unless passed; vectors of padding
+    tokens are left as they were (zeros in outputs allocated here).
+    """
+    if stream is not None or k_out is None or v_out is None:
+        if k_codes.dim() != 4:
+            raise ValueError("4-bit caches must be 4-D")
+        stream, ctx = _on(stream, k_codes)
+        like = k_out if k_out is not None else v_out
+        size = (positions.shape[0], k_codes.shape[1] if block_table is None else k_codes.shape[2], 2 * k_codes.shape[3])
+        with ctx:
+            dt = dtype if like is None else like.dtype
+            k_out = torch.zeros(size, dtype=dt, device=k_codes.device) if k_out is None else k_out
+            v_out = torch.zeros(size, dtype=dt, device=k_codes.device) if v_out is None else v_out
+    rc = (_calls or _open()).cache_read_int4(k_codes, v_codes, k_steps, v_steps, positions, rows, block_table, k_scale, v_scale, k_out, v_out,
+                                             max_seqlen, stream)
+    if rc:
+        raise TreeAttnError(rc, "tree_attn_cache_read_int4")
+    return k_out, v_out
+
+
+def _windowed_buffers(q, cache, block_table, window, sinks, max_seqlen, out, lse, want_lse, workspace, stream):
+    """Outputs that were not passed, and with an explicit stream the workspace too (else the extension makes it)."""
+    if stream is not None or out is None or (lse is None and want_lse):
+        calls = _calls or _open()
+        stream, ctx = _on(stream, q)
+        with ctx:
+            if out is None:
+                out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+            if lse is None and want_lse:
+                lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+            if workspace is None and stream is not None:
+                need = calls.window_workspace_bytes(cache, block_table, q, window, sinks, max_seqlen)
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    return out, lse, workspace, stream
+
+
+def tree_attn_decode_window(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, seqlens: torch.Tensor,
+                            window: int, sinks: int = 0, block_table: Optional[torch.Tensor] = None,
+                            out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                            scale: Optional[float] = None, max_seqlen: Optional[int] = None,
+                            k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None, want_lse: bool = True, stream=None):
+    """Decode attention to the last ``window`` tokens and the first ``sinks`` ones.
+
+    q: [B, Hq, d], or [B, Hq, nq, d] for several queries a row; query i sits at position
+    s = seqlens[b] - nq + i and sees the tokens t <= s with t > s - window or t < sinks.  Caches: dense
+    [B, Hkv, S, d] or pools [num_pages, page_size, Hkv, d] with ``block_table``, whose entries are read
+    only for pages that some query sees: those that fell out of the window may be freed.  BF16 q with a BF16 or
+    E4M3 cache (``k_scale``, ``v_scale``), FP32 q with an FP32 one.  ``workspace``: a CUDA tensor of at
+    least tree_attn_window_workspace_bytes bytes (allocated when not passed).
+    Returns (out fp32 of q's shape, lse fp32 without the channels, or None).
+    """
+    out, lse, workspace, stream = _windowed_buffers(q, k_cache, block_table, window, sinks, max_seqlen, out, lse, want_lse, workspace, stream)
+    rc = (_calls or _open()).decode_window(q, k_cache, v_cache, seqlens, window, sinks, block_table, out, lse, scale, max_seqlen, k_scale, v_scale,
+                                           workspace, stream)
+    if rc:
+        raise TreeAttnError(rc, "tree_attn_decode_window")
+    return out, lse
+
+
+def tree_attn_decode_int4(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor, k_steps: torch.Tensor,
+                          v_steps: torch.Tensor, seqlens: torch.Tensor, window: Optional[int] = None, sinks: int = 0,
+                          block_table: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                          lse: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                          max_seqlen: Optional[int] = None, k_scale: Optional[torch.Tensor] = None,
+                          v_scale: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                          want_lse: bool = True, stream=None):
+    """Decode attention over a 4-bit cache (tree_attn_cache_write_int4), to all of a row or a window of it.
+
+    q (BF16), outputs, window and sinks are tree_attn_decode_window's; ``window`` None: every token
+    up to the query's own position.
+    """
+    out, lse, workspace, stream = _windowed_buffers(q, k_codes, block_table, window, sinks, max_seqlen, out, lse, want_lse, workspace, stream)
+    rc = (_calls or _open()).decode_int4(q, k_codes, v_codes, k_steps, v_steps, seqlens, window, sinks, block_table, out, lse, scale, max_seqlen,
+                                         k_scale, v_scale, workspace, stream)
+    if rc:
+        raise TreeAttnError(rc, "tree_attn_decode_int4")
+    return out, lse
+
+
+def tree_attn_window_workspace_bytes(q: torch.Tensor, cache: torch.Tensor, window: Optional[int] = None, sinks: int = 0,
+                                     block_table: Optional[torch.Tensor] = None, max_seqlen: Optional[int] = None) -> int:
+    """Bytes of workspace that tree_attn_decode_window (``cache``: its keys) or tree_attn_decode_int4 (its key
+    codes) needs for these queries on the current device; 0: none."""
+    return int((_calls or _open()).window_workspace_bytes(cache, block_table, q, window, sinks, max_seqlen))

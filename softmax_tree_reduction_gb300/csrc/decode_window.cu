@@ -1,0 +1,1278 @@
+// Decode attention to a window of the cache behind a few first tokens (sinks), over BF16,
+// FP32, E4M3 and 4-bit caches, one or several queries a row.  Without a window: the causal
+// attention of a 4-bit cache.
+//
+// Query i of nq sits at position s_i = N - nq + i of its row of N tokens and sees the tokens t <= s_i
+// with t > s_i - window or t < sinks.  The tokens that some query sees are [0, sinks) and
+// [N - nq + 1 - window, N); they are cut into slabs of 16 (aligned to 16, so that a slab lies in
+// one page), sinks first, and the list's slabs are split evenly over its blocks.  Rows of
+// a slab that no query sees are zero-filled instead of read, and their pages are not looked up.
+// Masks are applied in the slabs at the window's ends only.
+//
+// The unit of work, the rings and the products are those of the decode over selected pages:
+// every warp copies its slabs itself into a ring of its own.  The blocks of a list merge
+// through a cluster's shared memory, or, where a list wants more blocks than a cluster holds,
+// through partial states in the workspace and a second kernel.
+//
+// 4-bit caches.  A channel's value is step * (code - 8) * scale.  Four products of bits turn a
+// word of eight codes into FP16 numbers: (w & 0x000f000f) | 0x64006400 is the pair
+// 1024 + code of channels 0 and 4, and one FMA with step / 8 and -1032 step / 8 makes step / 8 *
+// (code - 8) of it, exactly: both constants have at most 11 significant bits (1032 = 8 * 129, times
+// the 4 bits of an E4M3 number), and so has the result.  The odd codes come as 1024 + 16 code
+// (mask 0x00f000f0) with step / 128 and -72 step / 8.  So the tensor cores multiply exact values.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <mutex>
+
+#include "common.cuh"
+#include "host.h"
+#include "kernels.h"
+#include "slabs.cuh"
+#include "warp_mma.cuh"
+
+namespace ta {
+namespace {
+
+enum Cache { kBf16, kE4m3, kInt4, kF32 };
+
+struct SpanParams {
+    const void* q;             // [B][Hq][nq][d]
+    const uint8_t* k;          // keys, values; codes of 4-bit caches
+    const uint8_t* v;
+    const uint8_t* k_steps;    // 4-bit caches
+    const uint8_t* v_steps;
+    const int32_t* seqlens;
+    const int32_t* block_table;  // null: dense
+    const float* k_scale;      // E4M3; 4-bit (may be null: ones)
+    const float* v_scale;
+    float* out;
+    float* lse;
+    float* part_o;             // [rows][P][d], rows = B * Hq * nq; null: the blocks of a list merge in their cluster
+    float2* part_ml;           // [rows][P]: maximum (log2 units), denominator
+    int* err;
+    int64_t sb, sh, st;        // bytes between rows or pages, heads, tokens
+    int64_t tb, th, tt;        // the same of the steps
+    int Hq, Hkv, G, nq, cols, S, ngroups;  // cols = G * nq columns of a KV head, column = head * nq + query
+    int window, sinks;         // at most S
+    int max_pages, page_shift, num_pages;
+    int P, C;                  // blocks of a list, of a cluster (P, or 1 with partial states)
+    float scale_log2;
+    // extents, for the bounds-checking build
+    size_t q_elems, cache_bytes, step_bytes, table_elems, out_elems, rows;
+};
+
+// The tokens of a row that some query sees, as slabs: [0, head) and [first, last).
+struct Span {
+    int N, lo, head, first, count;
+    __device__ __forceinline__ Span(const SpanParams& p, int N_) : N(N_) {
+        lo = max(0, N - p.nq + 1 - p.window);
+        first = lo >> 4;
+        head = min((min(p.sinks, N) + 15) >> 4, first);
+        count = N > 0 ? head + ((N + 15) >> 4) - first : 0;
+    }
+    __device__ __forceinline__ int token(int u) const { return (u < head ? u : u - head + first) << 4; }
+};
+
+// Places of a warp's slabs, 32 at a time, one a lane: first token (-1: no slab) and byte offsets.
+struct Slab {
+    int64_t off, steps;
+    int t0;
+};
+
+struct SpanList {
+    const SpanParams& p;
+    const Span& span;
+    const int32_t* table;
+    int b, g, u, W, n;  // the warp's first slab, its stride, its number of slabs
+    int lane, bad;
+
+    __device__ __forceinline__ SpanList(const SpanParams& p_, const Span& s, int b_, int g_, int part, int warp, int W_)
+        : p(p_), span(s), b(b_), g(g_), W(W_), bad(0) {
+        lane = threadIdx.x & 31;
+        table = p.block_table ? p.block_table + static_cast<int64_t>(b) * p.max_pages : nullptr;
+        const int u0 = static_cast<int>(static_cast<int64_t>(span.count) * part / p.P);
+        const int u1 = static_cast<int>(static_cast<int64_t>(span.count) * (part + 1) / p.P);
+        u = u0 + warp;
+        n = u1 > u ? (u1 - u + W - 1) / W : 0;
+    }
+    // page of this lane's slab in the window starting at the warp's slab i0 (-1: none)
+    __device__ __forceinline__ int entry(int i0) const {
+        const int i = i0 + lane;
+        if (i >= n) return -1;
+        if (!table) return b;
+        const int page = span.token(u + i * W) >> p.page_shift;
+        return in_bounds(table - p.block_table + page, p.table_elems, p.err) ? __ldg(table + page) : -1;
+    }
+    // its place, once the page has arrived
+    __device__ __forceinline__ Slab place(int i0, int page) {
+        Slab s;
+        s.off = s.steps = 0;
+        s.t0 = -1;
+        const int i = i0 + lane;
+        if (i >= n) return s;
+        if (table && (page < 0 || page >= p.num_pages)) {
+            bad = 1;
+            return s;
+        }
+        s.t0 = span.token(u + i * W);
+        const int64_t slot = table ? s.t0 & ((1 << p.page_shift) - 1) : s.t0;
+        s.off = page * p.sb + g * p.sh + slot * p.st;
+        s.steps = page * p.tb + g * p.th + slot * p.tt;
+        return s;
+    }
+    // whether some query sees token t of one of its slabs
+    __device__ __forceinline__ bool seen(int t) const { return t < span.N && (t >= span.lo || t < p.sinks); }
+    // whether every query sees all tokens of the slab
+    __device__ __forceinline__ bool whole(int t0) const {
+        return t0 + 15 <= span.N - p.nq && (t0 >= span.N - p.window || t0 + 15 < p.sinks);
+    }
+};
+
+// Whether the query at position s sees token t.
+__device__ __forceinline__ bool sees(const SpanParams& p, int s, int t) {
+    return t <= s && (t > s - p.window || t < p.sinks);
+}
+
+__device__ __forceinline__ bool bytes_in(int64_t o, int bytes, size_t extent, int* err) {
+    return bytes == 0 || in_bounds(static_cast<size_t>(o) + bytes - 1, extent, err);
+}
+
+// The merged state of a block, written as the partial state of rows row0 .. row0 + ncol.
+template <int D, int kWarps, int kCols, bool kFp8, int kThreads = 32 * kWarps>
+__device__ void store_partial(const SpanParams& p, size_t row0, int ncol, float vscale, const float* mg_o, const float* mg_m,
+                              const float* mg_l, bool poison) {
+    constexpr int MS = D + 4;
+    const float nan = __int_as_float(0x7fc00000);
+    for (int idx = threadIdx.x; idx < ncol * D; idx += kThreads) {
+        const int h = idx / D, dd = idx - h * D;
+        const int pos = kFp8 ? (dd % 16) * 8 + dd / 16 : dd;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mg_m[w * kCols + h]);
+        const float Ms = (M == -INFINITY) ? 0.f : M;
+        float ow[kWarps], lw[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float wt = ex2(mg_m[w * kCols + h] - Ms);
+            ow[w] = wt * mg_o[(w * kCols + h) * MS + pos];
+            lw[w] = wt * mg_l[w * kCols + h];
+        }
+        float o = sum_of<kWarps>(ow), l = sum_of<kWarps>(lw);
+        if (kFp8) o *= vscale;
+        if (poison) o = l = M = nan;
+        const size_t at = (row0 + h) * p.P + blockIdx.x;
+        if (!in_bounds(at, p.rows * p.P, p.err)) continue;
+        p.part_o[at * D + dd] = o;
+        if (dd == 0) p.part_ml[at] = make_float2(M, l);
+    }
+}
+
+// The partial states of a row become its outputs; one thread a channel.
+template <int D>
+__global__ void __launch_bounds__(D) span_combine_kernel(const SpanParams p) {
+    wait_primary();
+    const size_t row = blockIdx.x;
+    const float2* ml = p.part_ml + row * p.P;
+    const float* o = p.part_o + row * p.P * D + threadIdx.x;
+    float M = -INFINITY;
+    for (int i = 0; i < p.P; ++i) M = fmaxf(M, ml[i].x);
+    const float Ms = (M == -INFINITY) ? 0.f : M;
+    float L = 0.f, O = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < p.P; ++i) {
+        const float2 s = ml[i];
+        const float w = (s.x == -INFINITY) ? 0.f : ex2(s.x - Ms);
+        L = fmaf(w, s.y, L);
+        O = fmaf(w, o[static_cast<size_t>(i) * D], O);
+    }
+    if (in_bounds(row * D + threadIdx.x, p.out_elems, p.err)) p.out[row * D + threadIdx.x] = (L == 0.f) ? 0.f : O / L;
+    if (threadIdx.x == 0 && p.lse && in_bounds(row, p.rows, p.err)) p.lse[row] = (L == 0.f) ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+// ------------------------------------------------------------ tensor cores
+template <int D, int NT, int kCache, int W, int kStages_>
+struct SpanCfg {
+    static constexpr int kRowBytes = kCache == kInt4 ? D / 2 : (kCache == kE4m3 ? D : 2 * D);
+    static constexpr int kChunks = kRowBytes / 16;                                  // 16-byte chunks of a row
+    static constexpr int kVRow = kCache == kInt4 ? kRowBytes + 16 : kRowBytes;      // (4-bit values: rows apart in the banks)
+    static constexpr int kStepRow = kCache == kInt4 ? D / 16 : 0;
+    static constexpr int kVOff = kSlab * kRowBytes;
+    static constexpr int kKStep = kVOff + kSlab * kVRow;
+    static constexpr int kVStep = kKStep + kSlab * kStepRow;
+    static constexpr int kPairBytes = kVStep + kSlab * kStepRow;                    // keys, values and steps of a slab
+    static constexpr int kSub = kCache == kBf16 ? 1 : 2;                            // slabs that a warp takes together
+    static constexpr int kStageBytes = kSub * kPairBytes;
+    static constexpr int kWarps = W, kThreads = 32 * W, kStages = kStages_;
+    static constexpr int kCols = 8 * NT;
+    static constexpr int kRing = kWarps * kStages * kStageBytes;
+    static constexpr int kFlagOff = kRing + kWarps * kStages * kSub * 4;
+    static constexpr int kBoxOff = (kFlagOff + 4 + 15) / 16 * 16;
+    static constexpr int kSmem = kBoxOff + static_cast<int>(sizeof(Mailbox<D, kCols>));
+    static_assert(kWarps * kCols * (D + 4 + 2) * 4 <= kRing, "merge buffers reuse the ring");
+    static_assert(kStages >= 2 && kSmem <= 227 * 1024, "ring");
+};
+
+__device__ __forceinline__ uint32_t hfma2_bits(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// (w & mask) | magic
+__device__ __forceinline__ uint32_t pick_codes(uint32_t w, uint32_t mask) { return (w & mask) | 0x64006400u; }
+
+// Factors that turn pairs of codes into step / 8 * (code - 8), for a pair of steps (FP16).
+struct Unpack {
+    uint32_t lo, lo_add, hi, hi_add;  // codes in the low, high four bits of their byte
+    __device__ __forceinline__ explicit Unpack(uint32_t steps) {
+        lo = hmul2_bits(steps, 0x30003000u);          // 2^-3
+        lo_add = hmul2_bits(lo, 0xe408e408u);         // -1032
+        hi = hmul2_bits(steps, 0x20002000u);          // 2^-7
+        hi_add = hmul2_bits(lo, 0xd480d480u);         // -72
+    }
+    // channels i and i + 4 of eight (i = 0, 1) of the word's bytes; shift the word by 8 for i = 2, 3
+    __device__ __forceinline__ uint32_t even(uint32_t w) const { return hfma2_bits(pick_codes(w, 0x000f000fu), lo, lo_add); }
+    __device__ __forceinline__ uint32_t odd(uint32_t w) const { return hfma2_bits(pick_codes(w, 0x00f000f0u), hi, hi_add); }
+};
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+template <int N>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes) : "memory");
+}
+
+template <int D, int NT, int kCache, int W, int kStages_>
+__global__ void __launch_bounds__(32 * W) decode_span_kernel(const SpanParams p) {
+    using Cf = SpanCfg<D, NT, kCache, W, kStages_>;
+    constexpr int J = Cf::kSub, kWarps = W, kStages = Cf::kStages;
+    constexpr bool kTwo = kCache != kBf16;   // FP16 operands: weights in two parts
+    extern __shared__ __align__(128) uint8_t smem[];
+    int* t0s_all = reinterpret_cast<int*>(smem + Cf::kRing);
+    int* bad_flag = reinterpret_cast<int*>(smem + Cf::kFlagOff);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int gid = lane >> 2, tig = lane & 3, r8 = lane & 7;
+    const int g = blockIdx.y / p.ngroups, cg = blockIdx.y - g * p.ngroups, b = blockIdx.z;
+    const int c_first = Cf::kCols * cg;
+    const int ncol = min(Cf::kCols, p.cols - c_first);
+    const size_t row0 = static_cast<size_t>(b) * p.Hq * p.nq + static_cast<size_t>(g) * p.cols + c_first;
+    if (threadIdx.x == 0) *bad_flag = 0;
+    if (p.C > 1) cluster_arrive();  // (waited for before the states are sent)
+    __syncthreads();
+    wait_primary();
+    allow_dependents();
+
+    int N = p.seqlens[b];
+    const bool bad_len = N < 0 || N > p.S;
+    if (bad_len) N = 0;
+    const Span span(p, N);
+    SpanList list(p, span, b, g, blockIdx.x, warp, kWarps);
+    const int n_it = (list.n + J - 1) / J;
+    int e_next = list.entry(0);
+
+    // q fragments (B operand of S^T = K Q^T), as BF16 words: column n of n-tile t is column
+    // c_first + 8 t + n, in the channel order in which a lane holds the key's bytes
+    // (E4M3: k-step kk of lane tig is channels 32 tig + 4 kk ..; 4 bits: see below).
+    uint32_t qb[NT][D / 16][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int c = nt * 8 + gid;
+        const bool on = c < ncol && in_bounds((row0 + c + 1) * D - 1, p.q_elems, p.err);
+        const __nv_bfloat16* qh = static_cast<const __nv_bfloat16*>(p.q) + (row0 + (on ? c : 0)) * D;
+        if constexpr (kCache == kInt4) {
+            // word w of the lane's codes: channels c0 .. c0 + 7; k-step 2 w + h multiplies the pairs
+            // (2 h, 2 h + 4) and (2 h + 1, 2 h + 5) of them
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+                const uint4 x = on ? *reinterpret_cast<const uint4*>(qh + D / 4 * tig + 8 * w) : make_uint4(0u, 0u, 0u, 0u);
+                qb[nt][2 * w][0] = prmt(x.x, x.z, 0x5410u);
+                qb[nt][2 * w][1] = prmt(x.x, x.z, 0x7632u);
+                qb[nt][2 * w + 1][0] = prmt(x.y, x.w, 0x5410u);
+                qb[nt][2 * w + 1][1] = prmt(x.y, x.w, 0x7632u);
+            }
+        } else {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t* w = reinterpret_cast<const uint32_t*>(qh + (kCache == kE4m3 ? 32 * tig + 4 * kk : 16 * kk + 2 * tig));
+                qb[nt][kk][0] = on ? w[0] : 0u;
+                qb[nt][kk][1] = on ? w[kCache == kE4m3 ? 1 : 4] : 0u;
+            }
+        }
+    }
+
+    float m[NT][2], l[NT][2], oacc[NT][D / 16][4], sl2[NT][2];
+    int col_query[NT][2];  // queries of the lane's columns 2 tig, 2 tig + 1 (and 8 further for each n-tile)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            m[nt][i] = -INFINITY;
+            l[nt][i] = 0.f;
+            sl2[nt][i] = p.scale_log2;
+            col_query[nt][i] = (c_first + nt * 8 + 2 * tig + i) % p.nq;
+        }
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt)
+            oacc[nt][mt][0] = oacc[nt][mt][1] = oacc[nt][mt][2] = oacc[nt][mt][3] = 0.f;
+    }
+
+    const uint32_t ring = smem_u32(smem) + warp * kStages * Cf::kStageBytes;
+    volatile int* t0s = t0s_all + warp * kStages * J;
+    Slab win = list.place(0, e_next), win_next = win;
+    // this lane's share of a slab's copies: chunk c_chunk of rows c_row, c_row + kRowsAtOnce, ..
+    constexpr int kRowsAtOnce = 32 / Cf::kChunks;
+    const int c_row = lane / Cf::kChunks, c_chunk = lane % Cf::kChunks;
+
+    // Start the copies of the warp's slabs i J .. into stage i % kStages (one group).
+    auto issue = [&](int i) {
+#pragma unroll
+        for (int sub = 0; sub < J; ++sub) {
+            const int s = i * J + sub, slot = (i % kStages) * J + sub;
+            if (s >= list.n) {
+                if (lane == 0 && in_bounds(slot, kStages * J, p.err)) t0s[slot] = -1;
+                continue;
+            }
+            const int j = s & 31;
+            if (j == 0 && s > 0) win = win_next;
+            if (j == 0) e_next = list.entry(s + 32);
+            if (j == 16) win_next = list.place(s + 16, e_next);
+            const int t0 = __shfl_sync(0xffffffffu, win.t0, j);
+            const int64_t off = __shfl_sync(0xffffffffu, win.off, j);
+            if (lane == 0 && in_bounds(slot, kStages * J, p.err)) t0s[slot] = t0;
+            int64_t steps = 0;
+            if constexpr (kCache == kInt4) steps = __shfl_sync(0xffffffffu, win.steps, j);
+            if (t0 >= 0) {
+                const uint32_t base = ring + slot * Cf::kPairBytes;
+#pragma unroll
+                for (int x = 0; x < kSlab / kRowsAtOnce; ++x) {
+                    const int r = x * kRowsAtOnce + c_row;
+                    const int bytes = list.seen(t0 + r) ? 16 : 0;
+                    const int64_t o = off + r * p.st + c_chunk * 16;
+                    const int chunk = kCache == kInt4 ? c_chunk : c_chunk ^ (r & 7);  // (swizzled against bank conflicts)
+                    const uint32_t dk = base + r * Cf::kRowBytes + (chunk << 4), dv = base + Cf::kVOff + r * Cf::kVRow + (chunk << 4);
+                    if (!bytes_in(o, bytes, p.cache_bytes, p.err) || !in_bounds(dv + 15 - smem_u32(smem), Cf::kRing, p.err)) continue;
+                    cp_async16(dk, p.k + (bytes ? o : 0), bytes);
+                    cp_async16(dv, p.v + (bytes ? o : 0), bytes);
+                }
+                if constexpr (kCache == kInt4) {
+                    constexpr int SR = Cf::kStepRow;
+                    const int r = lane & 15;
+                    const int bytes = list.seen(t0 + r) ? SR : 0;
+                    const int64_t o = bytes ? steps + r * p.tt : 0;
+                    const uint32_t d = base + (lane < 16 ? Cf::kKStep : Cf::kVStep) + r * SR;
+                    if (bytes_in(o, bytes, p.step_bytes, p.err) && in_bounds(d + SR - 1 - smem_u32(smem), Cf::kRing, p.err))
+                        cp_async_small<SR>(d, (lane < 16 ? p.k_steps : p.v_steps) + o, bytes);
+                }
+            }
+        }
+        cp_async_commit();
+    };
+
+    // fragment addresses within a BF16 slab; chunk c of row r sits at chunk c ^ (r & 7)
+    const uint32_t k_lane = (r8 + 8 * ((lane >> 3) & 1)) * Cf::kRowBytes;
+    const int k_chi = lane >> 4;
+    const uint32_t v_lane = (r8 + 8 * (lane >> 4)) * Cf::kRowBytes;
+    const int v_chi = (lane >> 3) & 1;
+
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+
+    // E4M3 and 4-bit caches: q as FP16, each column times the power of two that brings its largest |q|
+    // into [2^14, 2^15) (exact; folded back into the column's logit scale), while
+    // the first keys are on their way.
+    float vscale = 1.f;
+    if constexpr (kTwo) {
+        auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
+        auto hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
+        const float ks = (p.k_scale ? __ldg(p.k_scale + g) : 1.f) * (kCache == kInt4 ? 8.f : 1.f);
+        vscale = (p.v_scale ? __ldg(p.v_scale + g) : 1.f) * ((kCache == kInt4 ? 8.f : 1.f) / kPScale);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float amax = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) amax = fmaxf(amax, fmaxf(fabsf(lo(qb[nt][kk][i])), fabsf(hi(qb[nt][kk][i]))));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // amax = f 2^e with f in [0.5, 1); powers of two are made from their exponent bits
+            const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 126;
+            const int qexp = amax > 0.f && amax < INFINITY ? max(-100, min(100, 15 - e)) : 0;
+            const float qs = __uint_as_float(static_cast<uint32_t>(127 + qexp) << 23);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    qb[nt][kk][i] = half2_bits(__floats2half2_rn(lo(qb[nt][kk][i]) * qs, hi(qb[nt][kk][i]) * qs));
+            const float back = __uint_as_float(static_cast<uint32_t>(127 - qexp) << 23);
+            sl2[nt][0] *= ks * __shfl_sync(0xffffffffu, back, 8 * tig);
+            sl2[nt][1] *= ks * __shfl_sync(0xffffffffu, back, 8 * tig + 4);
+        }
+    }
+
+    for (int it = 0; it < n_it; ++it) {
+        cp_async_wait<kStages - 2>();
+        __syncwarp();  // the slab is in shared memory for every lane; every lane is done with the one before
+        issue(it + kStages - 1);
+        int t0[J];
+        uint32_t kbase[J];
+        bool any = false, whole = true;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int slot = (it % kStages) * J + j;
+            t0[j] = t0s[slot];
+            kbase[j] = ring + slot * Cf::kPairBytes;
+            any |= t0[j] >= 0;
+            whole = whole && t0[j] >= 0 && list.whole(t0[j]);
+        }
+        if (!any) continue;  // (a missing slab beside one with tokens: masked below)
+
+        // S^T[16 tokens x columns] = K Q^T per slab, two accumulators per n-tile
+        float sacc[J][2][NT][4];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sacc[j][u][nt][e] = 0.f;
+            if constexpr (kCache == kInt4) {
+                const uint32_t ra = kbase[j] + gid * Cf::kRowBytes + tig * (D / 8), rb = ra + 8 * Cf::kRowBytes;
+                uint32_t wa[D / 32], wb[D / 32], sa, sb;
+                const uint32_t srow = kbase[j] + Cf::kKStep + gid * Cf::kStepRow;
+                if constexpr (D == 128) {
+                    const uint4 x = lds128(ra), y = lds128(rb);
+                    wa[0] = x.x, wa[1] = x.y, wa[2] = x.z, wa[3] = x.w;
+                    wb[0] = y.x, wb[1] = y.y, wb[2] = y.z, wb[3] = y.w;
+                    sa = e4m3x2_to_f16x2(lds16(srow + 2 * tig));
+                    sb = e4m3x2_to_f16x2(lds16(srow + 2 * tig + 8 * Cf::kStepRow));
+                } else {
+                    const uint2 x = lds64(ra), y = lds64(rb);
+                    wa[0] = x.x, wa[1] = x.y;
+                    wb[0] = y.x, wb[1] = y.y;
+                    sa = e4m3x2_to_f16x2(lds8(srow + tig));
+                    sb = e4m3x2_to_f16x2(lds8(srow + tig + 8 * Cf::kStepRow));
+                }
+#pragma unroll
+                for (int blk = 0; blk < D / 64; ++blk) {  // 16 channels: two words
+                    const uint32_t sel = blk ? 0x3232u : 0x1010u;
+                    const Unpack ua(prmt(sa, sa, sel)), ub(prmt(sb, sb, sel));
+#pragma unroll
+                    for (int w = 2 * blk; w < 2 * blk + 2; ++w)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t x = wa[w] >> (8 * h), y = wb[w] >> (8 * h);
+                            const uint32_t a[4] = {ua.even(x), ub.even(y), ua.odd(x), ub.odd(y)};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma_f16(sacc[j][h][nt], a, qb[nt][2 * w + h][0], qb[nt][2 * w + h][1]);
+                        }
+                }
+            } else if constexpr (kCache == kE4m3) {
+                const uint32_t ra = kbase[j] + gid * 128, rb = ra + 8 * 128;
+                const int c0 = ((2 * tig) ^ gid) << 4, c1 = ((2 * tig + 1) ^ gid) << 4;
+                const uint4 ka0 = lds128(ra + c0), ka1 = lds128(ra + c1), kb0 = lds128(rb + c0), kb1 = lds128(rb + c1);
+                const uint32_t wa[8] = {ka0.x, ka0.y, ka0.z, ka0.w, ka1.x, ka1.y, ka1.z, ka1.w};
+                const uint32_t wb[8] = {kb0.x, kb0.y, kb0.z, kb0.w, kb1.x, kb1.y, kb1.z, kb1.w};
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t a[4] = {e4m3x2_to_f16x2(wa[kk] & 0xffffu), e4m3x2_to_f16x2(wb[kk] & 0xffffu),
+                                           e4m3x2_to_f16x2(wa[kk] >> 16), e4m3x2_to_f16x2(wb[kk] >> 16)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f16(sacc[j][kk & 1][nt], a, qb[nt][kk][0], qb[nt][kk][1]);
+                }
+            } else {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    uint32_t a[4];
+                    ldsm_x4(a, kbase[j] + k_lane + (((2 * kk + k_chi) ^ r8) << 4));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_bf16(sacc[j][kk & 1][nt], a, qb[nt][kk][0], qb[nt][kk][1]);
+                }
+            }
+        }
+        // Online softmax per column, P^T as B fragments: three BF16 parts (all 24 bits) or two FP16
+        // ones (22 bits), as in the decode over selected pages.
+        uint32_t bh[J][NT][2], bl[J][NT][2], bt[J][NT][2];
+        float alpha[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float sc[J][4], bm0 = -INFINITY, bm1 = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    sc[j][e] = (sacc[j][0][nt][e] + sacc[j][1][nt][e]) * sl2[nt][e & 1];
+                    if (!whole) {
+                        const int t = t0[j] + gid + 8 * (e >> 1);
+                        if (t0[j] < 0 || !sees(p, N - p.nq + col_query[nt][e & 1], t)) sc[j][e] = -INFINITY;
+                    }
+                }
+                bm0 = fmaxf(bm0, fmaxf(sc[j][0], sc[j][2]));
+                bm1 = fmaxf(bm1, fmaxf(sc[j][1], sc[j][3]));
+            }
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) {
+                bm0 = fmaxf(bm0, __shfl_xor_sync(0xffffffffu, bm0, off));
+                bm1 = fmaxf(bm1, __shfl_xor_sync(0xffffffffu, bm1, off));
+            }
+            const float mn0 = fmaxf(m[nt][0], bm0), mn1 = fmaxf(m[nt][1], bm1);
+            const float ms0 = (mn0 == -INFINITY) ? 0.f : mn0, ms1 = (mn1 == -INFINITY) ? 0.f : mn1;
+            const float al0 = ex2(m[nt][0] - ms0), al1 = ex2(m[nt][1] - ms1);
+            float ps0 = 0.f, ps1 = 0.f;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const float p0 = ex2(sc[j][0] - ms0), p1 = ex2(sc[j][1] - ms1);
+                const float p2 = ex2(sc[j][2] - ms0), p3 = ex2(sc[j][3] - ms1);
+                ps0 += p0 + p2;
+                ps1 += p1 + p3;
+                if constexpr (kTwo) {
+                    const float q0 = p0 * kPScale, q1 = p1 * kPScale, q2 = p2 * kPScale, q3 = p3 * kPScale;
+                    const __half2 h01 = __floats2half2_rn(q0, q1), h23 = __floats2half2_rn(q2, q3);
+                    const float2 f01 = __half22float2(h01), f23 = __half22float2(h23);
+                    bh[j][nt][0] = movtrans(half2_bits(h01));
+                    bh[j][nt][1] = movtrans(half2_bits(h23));
+                    bl[j][nt][0] = movtrans(half2_bits(__floats2half2_rn(q0 - f01.x, q1 - f01.y)));
+                    bl[j][nt][1] = movtrans(half2_bits(__floats2half2_rn(q2 - f23.x, q3 - f23.y)));
+                } else {
+                    const __nv_bfloat162 h01 = __floats2bfloat162_rn(p0, p1), h23 = __floats2bfloat162_rn(p2, p3);
+                    const float2 f01 = __bfloat1622float2(h01), f23 = __bfloat1622float2(h23);
+                    bh[j][nt][0] = movtrans(bf16x2_bits(h01));
+                    bh[j][nt][1] = movtrans(bf16x2_bits(h23));
+                    const float d0 = p0 - f01.x, d1 = p1 - f01.y, d2 = p2 - f23.x, d3 = p3 - f23.y;
+                    const __nv_bfloat162 l01 = __floats2bfloat162_rn(d0, d1), l23 = __floats2bfloat162_rn(d2, d3);
+                    const float2 g01 = __bfloat1622float2(l01), g23 = __bfloat1622float2(l23);
+                    bl[j][nt][0] = movtrans(bf16x2_bits(l01));
+                    bl[j][nt][1] = movtrans(bf16x2_bits(l23));
+                    bt[j][nt][0] = movtrans(bf16x2_bits(__floats2bfloat162_rn(d0 - g01.x, d1 - g01.y)));
+                    bt[j][nt][1] = movtrans(bf16x2_bits(__floats2bfloat162_rn(d2 - g23.x, d3 - g23.y)));
+                }
+            }
+            l[nt][0] = l[nt][0] * al0 + ps0;
+            l[nt][1] = l[nt][1] * al1 + ps1;
+            m[nt][0] = mn0;
+            m[nt][1] = mn1;
+            alpha[nt][0] = al0;
+            alpha[nt][1] = al1;
+        }
+        // O^T = alpha O^T + V^T P^T.  The products of one step are summed on their own and added in
+        // FP32 (the tensor cores cut off what they add to a running sum).
+        // mine: which queries' columns take them (-1: all); masks: of the lane's token pairs (2 tig, 2 tig + 1) and 8 further.
+        auto values = [&](int mine, auto&& keep) {
+            auto add = [&](int nt, int mt, const float (&f)[4]) {
+                if (mine < 0 || col_query[nt][0] == mine) {
+                    oacc[nt][mt][0] = fmaf(oacc[nt][mt][0], alpha[nt][0], f[0]);
+                    oacc[nt][mt][2] = fmaf(oacc[nt][mt][2], alpha[nt][0], f[2]);
+                }
+                if (mine < 0 || col_query[nt][1] == mine) {
+                    oacc[nt][mt][1] = fmaf(oacc[nt][mt][1], alpha[nt][1], f[1]);
+                    oacc[nt][mt][3] = fmaf(oacc[nt][mt][3], alpha[nt][1], f[3]);
+                }
+            };
+            if constexpr (kCache == kInt4) {
+                uint32_t w[J][4][D / 64];  // rows 2 tig, 2 tig + 1, + 8, + 9; the lane's D / 8 channels from D / 8 gid on
+                uint32_t st[J][2];         // their steps as FP16 pairs
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const uint32_t vrow = kbase[j] + Cf::kVOff + 2 * tig * Cf::kVRow + gid * (D / 16);
+                    const uint32_t srow = kbase[j] + Cf::kVStep + 2 * tig * Cf::kStepRow + (gid * D / 8) / 16;
+                    const bool on = t0[j] >= 0;  // (else its buffer may hold anything)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = (r & 1) + 8 * (r >> 1);
+                        if constexpr (D == 128) {
+                            const uint2 x = on ? lds64(vrow + row * Cf::kVRow) : make_uint2(0u, 0u);
+                            w[j][r][0] = x.x, w[j][r][1] = x.y;
+                        } else {
+                            w[j][r][0] = on ? lds32(vrow + row * Cf::kVRow) : 0u;
+                        }
+                    }
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t x = on ? lds8(srow + 8 * half * Cf::kStepRow) : 0u, y = on ? lds8(srow + (8 * half + 1) * Cf::kStepRow) : 0u;
+                        st[j][half] = e4m3x2_to_f16x2(x | (y << 8));
+                    }
+                }
+#pragma unroll
+                for (int wd = 0; wd < D / 64; ++wd)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)      // channels 8 wd + 4 half ..
+#pragma unroll
+                        for (int pr = 0; pr < 2; ++pr) {       // + 2 pr and 2 pr + 1: one m-tile
+                            float f[NT][4];
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) f[nt][0] = f[nt][1] = f[nt][2] = f[nt][3] = 0.f;
+#pragma unroll
+                            for (int j = 0; j < J; ++j) {
+                                const Unpack ua(st[j][0]), ub(st[j][1]);
+                                const uint32_t sel = half ? 0x7632u : 0x5410u;
+                                const uint32_t x = prmt(w[j][0][wd], w[j][1][wd], sel) >> (8 * pr), y = prmt(w[j][2][wd], w[j][3][wd], sel) >> (8 * pr);
+                                uint32_t a[4] = {ua.even(x), ua.odd(x), ub.even(y), ub.odd(y)};
+                                keep(j, a);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    mma_f16(f[nt], a, bh[j][nt][0], bh[j][nt][1]);
+                                    mma_f16(f[nt], a, bl[j][nt][0], bl[j][nt][1]);
+                                }
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) add(nt, 4 * wd + 2 * half + pr, f[nt]);
+                        }
+            } else if constexpr (kCache == kE4m3) {
+                const int r0 = 2 * tig;  // rows r0, r0 + 1, r0 + 8, r0 + 9; channels 16 gid ..
+                const uint32_t c0 = (gid ^ r0) << 4, c1 = (gid ^ (r0 + 1)) << 4;
+                uint32_t xa[J][4], xb[J][4], xc[J][4], xd[J][4];
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const uint32_t vbase = kbase[j] + Cf::kVOff;
+                    uint4 va, vb, vc, vd;
+                    va = vb = vc = vd = make_uint4(0u, 0u, 0u, 0u);
+                    if (t0[j] >= 0) {  // (else its buffer may hold anything)
+                        va = lds128(vbase + r0 * 128 + c0);
+                        vb = lds128(vbase + (r0 + 1) * 128 + c1);
+                        vc = lds128(vbase + (r0 + 8) * 128 + c0);
+                        vd = lds128(vbase + (r0 + 9) * 128 + c1);
+                    }
+                    xa[j][0] = va.x, xa[j][1] = va.y, xa[j][2] = va.z, xa[j][3] = va.w;
+                    xb[j][0] = vb.x, xb[j][1] = vb.y, xb[j][2] = vb.z, xb[j][3] = vb.w;
+                    xc[j][0] = vc.x, xc[j][1] = vc.y, xc[j][2] = vc.z, xc[j][3] = vc.w;
+                    xd[j][0] = vd.x, xd[j][1] = vd.y, xd[j][2] = vd.z, xd[j][3] = vd.w;
+                }
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t sel = half ? 0x7362u : 0x5140u;  // byte pairs of two token rows
+                        float f[NT][4];
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) f[nt][0] = f[nt][1] = f[nt][2] = f[nt][3] = 0.f;
+#pragma unroll
+                        for (int j = 0; j < J; ++j) {
+                            const uint32_t pa = prmt(xa[j][w], xb[j][w], sel), pc = prmt(xc[j][w], xd[j][w], sel);
+                            uint32_t a[4] = {e4m3x2_to_f16x2(pa & 0xffffu), e4m3x2_to_f16x2(pa >> 16), e4m3x2_to_f16x2(pc & 0xffffu),
+                                             e4m3x2_to_f16x2(pc >> 16)};
+                            keep(j, a);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                mma_f16(f[nt], a, bh[j][nt][0], bh[j][nt][1]);
+                                mma_f16(f[nt], a, bl[j][nt][0], bl[j][nt][1]);
+                            }
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) add(nt, 2 * w + half, f[nt]);
+                    }
+                }
+            } else {
+                const uint32_t vbase = kbase[0] + Cf::kVOff;
+#pragma unroll
+                for (int mt = 0; mt < D / 16; ++mt) {
+                    uint32_t a[4];
+                    ldsm_x4_t(a, vbase + v_lane + (((2 * mt + v_chi) ^ r8) << 4));
+                    keep(0, a);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float f[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma_bf16(f, a, bh[0][nt][0], bh[0][nt][1]);
+                        mma_bf16(f, a, bl[0][nt][0], bl[0][nt][1]);
+                        mma_bf16(f, a, bt[0][nt][0], bt[0][nt][1]);
+                        add(nt, mt, f);
+                    }
+                }
+            }
+        };
+        if (whole || p.nq == 1) {
+            values(-1, [](int, uint32_t (&)[4]) {});  // (rows that no query sees were zero-filled)
+        } else {
+            // A token that one query sees and another does not may be infinite or NaN, and 0 times it is
+            // NaN: one query at a time, with the values that it does not see taken out.
+#pragma unroll 1
+            for (int qi = 0; qi < p.nq; ++qi) {
+                const int s = N - p.nq + qi;
+                uint32_t mask[J][2];
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int t = t0[j] + 2 * tig + 8 * half;
+                        mask[j][half] = (t0[j] >= 0 && sees(p, s, t) ? 0xffffu : 0u) | (t0[j] >= 0 && sees(p, s, t + 1) ? 0xffff0000u : 0u);
+                    }
+                values(qi, [&](int j, uint32_t (&a)[4]) {
+                    a[0] &= mask[j][0];
+                    a[1] &= mask[j][0];
+                    a[2] &= mask[j][1];
+                    a[3] &= mask[j][1];
+                });
+            }
+        }
+    }
+    cp_async_wait<0>();
+    if (list.bad) *bad_flag = 1;
+    if (list.bad || (bad_len && threadIdx.x == 0)) atomicOr(p.err, kErrBadSeqlen);
+
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+            l[nt][0] += __shfl_xor_sync(0xffffffffu, l[nt][0], off);
+            l[nt][1] += __shfl_xor_sync(0xffffffffu, l[nt][1], off);
+        }
+    __syncthreads();  // every warp is done with its ring
+    constexpr int kCols = Cf::kCols, MS = D + 4;
+    float* mg_o = reinterpret_cast<float*>(smem);
+    float* mg_m = mg_o + kWarps * kCols * MS;
+    float* mg_l = mg_m + kWarps * kCols;
+    float* mo = mg_o + warp * kCols * MS;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int c0 = nt * 8 + 2 * tig;
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt) {
+            // channels of rows gid and gid + 8 of m-tile mt
+            const int ca = kCache == kInt4 ? D / 8 * gid + 2 * mt : 16 * mt + gid, cb = kCache == kInt4 ? ca + 1 : ca + 8;
+            const float f = kCache == kInt4 ? vscale : 1.f;  // (E4M3: applied to the merged state)
+            mo[c0 * MS + ca] = oacc[nt][mt][0] * f;
+            mo[(c0 + 1) * MS + ca] = oacc[nt][mt][1] * f;
+            mo[c0 * MS + cb] = oacc[nt][mt][2] * f;
+            mo[(c0 + 1) * MS + cb] = oacc[nt][mt][3] * f;
+        }
+        if (gid == 0) {
+            mg_m[warp * kCols + c0] = m[nt][0];
+            mg_m[warp * kCols + c0 + 1] = m[nt][1];
+            mg_l[warp * kCols + c0] = l[nt][0];
+            mg_l[warp * kCols + c0 + 1] = l[nt][1];
+        }
+    }
+    __syncthreads();
+    const bool poison = bad_len || *bad_flag;
+    if (p.part_o)
+        store_partial<D, kWarps, kCols, kCache == kE4m3>(p, row0, ncol, vscale, mg_o, mg_m, mg_l, poison);
+    else
+        finish_list<D, kWarps, kCols, kCache == kE4m3>(p, row0, ncol, vscale, mg_o, mg_m, mg_l,
+                                                       reinterpret_cast<Mailbox<D, kCols>*>(smem + Cf::kBoxOff), poison);
+}
+
+// -------------------------------------------------------------- FP32 caches
+// CUDA cores, as in the decode over selected pages: eight lanes hold a token's channels and a
+// warp's four groups take every fourth token of a slab; from 3 columns of a KV head on two warps
+// share a ring and take half of the columns each.
+template <int D, int P, int kRings_>
+struct SpanF32Cfg {
+    static constexpr int kRowBytes = 4 * D;
+    static constexpr int kChunks = kRowBytes / 16;
+    static constexpr int kSlabBytes = kSlab * kRowBytes;
+    static constexpr int kStageBytes = 2 * kSlabBytes;           // keys, values: 8 or 16 KB
+    static constexpr int kRings = kRings_;
+    static constexpr int kStages = 196608 / kRings / kStageBytes;
+    static constexpr int kWarps = P * kRings;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kRing = kRings * kStages * kStageBytes;
+    static_assert(kStages >= 2 && kRings * 8 * (D + 4 + 2) * 4 <= kRing, "ring, merge buffers");
+};
+
+template <int D, int GC, int P>
+__global__ void __launch_bounds__(SpanF32Cfg<D, P, 6>::kThreads, 1) decode_span_f32_kernel(const SpanParams p) {
+    using Cf = SpanF32Cfg<D, P, 6>;
+    constexpr int kRings = Cf::kRings, kStages = Cf::kStages;
+    constexpr int kCols = P * GC;
+    constexpr int J = D / 32;  // float4 per lane: channels 4 (l8 + 8 j) ..
+    constexpr int MS = D + 4;
+    constexpr int kSteps = kSlab / 4;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(16) float q_all[kCols][D];
+    __shared__ Mailbox<D, kCols> box;
+    __shared__ int t0s_all[Cf::kWarps * kStages];
+    __shared__ int bad_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l8 = lane & 7, tok = lane >> 3;
+    const int g = blockIdx.y / p.ngroups, cg = blockIdx.y - g * p.ngroups, b = blockIdx.z;
+    const int c_first = kCols * cg;
+    const int ncol = min(kCols, p.cols - c_first);
+    const size_t row0 = static_cast<size_t>(b) * p.Hq * p.nq + static_cast<size_t>(g) * p.cols + c_first;
+    const int r = warp / P, part = warp - r * P;  // ring, and which GC columns of it
+    if (p.C > 1) cluster_arrive();  // (waited for before the states are sent)
+    if (threadIdx.x == 0) bad_flag = 0;
+    wait_primary();
+    allow_dependents();
+    int N = p.seqlens[b];
+    const bool bad_len = N < 0 || N > p.S;
+    if (bad_len) N = 0;
+    const Span span(p, N);
+    SpanList list(p, span, b, g, blockIdx.x, r, kRings);
+    const int n_it = list.n;
+    int e_next = list.entry(0);
+    for (int i = threadIdx.x; i < kCols * D; i += Cf::kThreads)
+        q_all[i / D][i % D] = i / D < ncol && in_bounds(row0 * D + i, p.q_elems, p.err)
+                               ? static_cast<const float*>(p.q)[row0 * D + i] * p.scale_log2
+                               : 0.f;
+    const uint32_t ring = smem_u32(smem) + r * kStages * Cf::kStageBytes;
+    const uint8_t* ring_ptr = smem + r * kStages * Cf::kStageBytes;
+    volatile int* t0s = t0s_all + warp * kStages;
+    const float(*qs)[D] = q_all + part * GC;
+    // every lane of the ring's warps
+    auto ring_sync = [&] {
+        if constexpr (P == 1)
+            __syncwarp();
+        else
+            asm volatile("bar.sync %0, %1;" ::"r"(r + 1), "n"(32 * P) : "memory");
+    };
+    Slab win = list.place(0, e_next), win_next = win;
+    constexpr int kRowsAtOnce = 32 / Cf::kChunks;  // rows a copy instruction of the warp covers
+    const int c_row = part * kRowsAtOnce + lane / Cf::kChunks, c_chunk = lane % Cf::kChunks;
+
+    // Start the warp's copies of the ring's slab i into stage i % kStages (one group).
+    auto issue = [&](int i) {
+        if (i < n_it) {
+            const int j = i & 31, s = i % kStages;
+            if (j == 0 && i > 0) win = win_next;
+            if (j == 0) e_next = list.entry(i + 32);
+            if (j == 16) win_next = list.place(i + 16, e_next);
+            const int t0 = __shfl_sync(0xffffffffu, win.t0, j);
+            const int64_t off = __shfl_sync(0xffffffffu, win.off, j);
+            if (lane == 0) t0s[s] = t0;
+            if (t0 >= 0) {
+#pragma unroll
+                for (int x = 0; x < kSlab / (P * kRowsAtOnce); ++x) {
+                    const int row = x * P * kRowsAtOnce + c_row;
+                    const int bytes = list.seen(t0 + row) ? 16 : 0;
+                    const int64_t o = bytes ? off + row * p.st + c_chunk * 16 : 0;
+                    const uint32_t d = ring + s * Cf::kStageBytes + row * Cf::kRowBytes + c_chunk * 16;
+                    if (!bytes_in(o, bytes, p.cache_bytes, p.err) || !in_bounds(d + Cf::kSlabBytes + 15 - smem_u32(smem), Cf::kRing, p.err)) continue;
+                    cp_async16(d, p.k + o, bytes);
+                    cp_async16(d + Cf::kSlabBytes, p.v + o, bytes);
+                }
+            }
+        }
+        cp_async_commit();
+    };
+
+    float m[GC], l[GC];
+    int pos[GC];
+    float2 o[GC][2 * J];
+#pragma unroll
+    for (int h = 0; h < GC; ++h) {
+        m[h] = -INFINITY;
+        l[h] = 0.f;
+        pos[h] = N - p.nq + (c_first + part * GC + h) % p.nq;
+#pragma unroll
+        for (int j = 0; j < 2 * J; ++j) o[h][j] = make_float2(0.f, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+    __syncthreads();  // q is in shared memory
+    for (int it = 0; it < n_it; ++it) {
+        ring_sync();  // every lane is done with the slab before
+        issue(it + kStages - 1);
+        cp_async_wait<kStages - 1>();
+        ring_sync();  // the slab is in shared memory for every lane
+        const int s = it % kStages;
+        const int t0 = t0s[s];
+        if (t0 < 0) continue;
+        const bool whole = list.whole(t0);
+        const float* ks = reinterpret_cast<const float*>(ring_ptr + s * Cf::kStageBytes) + tok * D + 4 * l8;
+        const float* vs = ks + Cf::kSlabBytes / 4;
+        float sc[GC][kSteps];  // tokens 4 t + tok
+        {
+            float2 z[GC][kSteps];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                float4 k4[kSteps];
+#pragma unroll
+                for (int t = 0; t < kSteps; ++t) k4[t] = *reinterpret_cast<const float4*>(ks + 4 * t * D + 32 * j);
+#pragma unroll
+                for (int h = 0; h < GC; ++h) {
+                    const float4 q4 = *reinterpret_cast<const float4*>(&qs[h][4 * l8 + 32 * j]);
+#pragma unroll
+                    for (int t = 0; t < kSteps; ++t) {
+                        z[h][t] = fma2(make_float2(q4.x, q4.y), make_float2(k4[t].x, k4[t].y),
+                                       j ? z[h][t] : make_float2(0.f, 0.f));
+                        z[h][t] = fma2(make_float2(q4.z, q4.w), make_float2(k4[t].z, k4[t].w), z[h][t]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < GC; ++h)
+#pragma unroll
+                for (int t = 0; t < kSteps; ++t) {
+                    float y = z[h][t].x + z[h][t].y;
+#pragma unroll
+                    for (int x = 4; x > 0; x >>= 1) y += __shfl_xor_sync(0xffffffffu, y, x);
+                    sc[h][t] = whole || sees(p, pos[h], t0 + 4 * t + tok) ? y : -INFINITY;
+                }
+        }
+#pragma unroll
+        for (int h = 0; h < GC; ++h) {
+            float mn = m[h];
+#pragma unroll
+            for (int t = 0; t < kSteps; ++t) mn = fmaxf(mn, sc[h][t]);
+            const float ms = (mn == -INFINITY) ? 0.f : mn;
+            const float al = ex2(m[h] - ms);
+            float sum = 0.f;
+#pragma unroll
+            for (int t = 0; t < kSteps; ++t) {
+                sc[h][t] = ex2(sc[h][t] - ms);
+                sum += sc[h][t];
+            }
+            m[h] = mn;
+            l[h] = fmaf(l[h], al, sum);
+#pragma unroll
+            for (int j = 0; j < 2 * J; ++j) o[h][j] = mul2(o[h][j], make_float2(al, al));
+        }
+        // (a value that one query sees and another does not may be infinite or NaN: taken out for the other)
+        auto values = [&](auto&& keep) {
+#pragma unroll
+            for (int t = 0; t < kSteps; ++t) {
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const float4 v4 = *reinterpret_cast<const float4*>(vs + 4 * t * D + 32 * j);
+#pragma unroll
+                    for (int h = 0; h < GC; ++h) {
+                        if (!keep(h, t)) continue;
+                        const float2 w = make_float2(sc[h][t], sc[h][t]);
+                        o[h][2 * j] = fma2(w, make_float2(v4.x, v4.y), o[h][2 * j]);
+                        o[h][2 * j + 1] = fma2(w, make_float2(v4.z, v4.w), o[h][2 * j + 1]);
+                    }
+                }
+            }
+        };
+        if (whole || p.nq == 1)
+            values([](int, int) { return true; });
+        else
+            values([&](int h, int t) { return sees(p, pos[h], t0 + 4 * t + tok); });
+    }
+    cp_async_wait<0>();
+    if (list.bad) bad_flag = 1;
+    if (list.bad || (bad_len && threadIdx.x == 0)) atomicOr(p.err, kErrBadSeqlen);
+    __syncthreads();  // every warp is done with its ring
+    float* mg_o = reinterpret_cast<float*>(smem);
+    float* mg_m = mg_o + kRings * kCols * MS;
+    float* mg_l = mg_m + kRings * kCols;
+    // the warp's four token groups, then its state into shared memory
+#pragma unroll
+    for (int h = 0; h < GC; ++h) {
+#pragma unroll
+        for (int x = 8; x < 32; x <<= 1) {
+            const float mo = __shfl_xor_sync(0xffffffffu, m[h], x);
+            const float mn = fmaxf(m[h], mo), ms = (mn == -INFINITY) ? 0.f : mn;
+            const float a = ex2(m[h] - ms), c = ex2(mo - ms);
+            l[h] = l[h] * a + __shfl_xor_sync(0xffffffffu, l[h], x) * c;
+#pragma unroll
+            for (int j = 0; j < 2 * J; ++j) {
+                o[h][j].x = o[h][j].x * a + __shfl_xor_sync(0xffffffffu, o[h][j].x, x) * c;
+                o[h][j].y = o[h][j].y * a + __shfl_xor_sync(0xffffffffu, o[h][j].y, x) * c;
+            }
+            m[h] = mn;
+        }
+        if (tok == 0) {
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                *reinterpret_cast<float4*>(&mg_o[(warp * GC + h) * MS + 4 * l8 + 32 * j]) =
+                    make_float4(o[h][2 * j].x, o[h][2 * j].y, o[h][2 * j + 1].x, o[h][2 * j + 1].y);
+            if (l8 == 0) {
+                mg_m[warp * GC + h] = m[h];
+                mg_l[warp * GC + h] = l[h];
+            }
+        }
+    }
+    __syncthreads();
+    const bool poison = bad_len || bad_flag;
+    if (p.part_o)
+        store_partial<D, kRings, kCols, false, Cf::kThreads>(p, row0, ncol, 1.f, mg_o, mg_m, mg_l, poison);
+    else
+        finish_list<D, kRings, kCols, false, Cf::kThreads>(p, row0, ncol, 1.f, mg_o, mg_m, mg_l, &box, poison);
+}
+
+// ---------------------------------------------------------------- host side
+// One kernel instance: what a launch needs to know of it.
+struct Kernel {
+    const void* fn;
+    int threads, smem, rings;   // rings: slabs that a block takes at a time
+    int cols;                   // columns a block serves
+    Instance* inst;
+    cudaError_t (*launch)(const cudaLaunchConfig_t*, const SpanParams&);
+};
+
+template <int D, int NT, int kCache, int W, int kStages>
+const Kernel* mma_kernel() {
+    using Cf = SpanCfg<D, NT, kCache, W, kStages>;
+    static Instance inst;
+    static const Kernel k = {reinterpret_cast<const void*>(decode_span_kernel<D, NT, kCache, W, kStages>), Cf::kThreads, Cf::kSmem, W * Cf::kSub,
+                             Cf::kCols, &inst, [](const cudaLaunchConfig_t* cfg, const SpanParams& p) {
+                                 return cudaLaunchKernelEx(cfg, decode_span_kernel<D, NT, kCache, W, kStages>, p);
+                             }};
+    return &k;
+}
+
+template <int D, int GC, int P>
+const Kernel* f32_kernel() {
+    using Cf = SpanF32Cfg<D, P, 6>;
+    static Instance inst;
+    static const Kernel k = {reinterpret_cast<const void*>(decode_span_f32_kernel<D, GC, P>), Cf::kThreads, Cf::kRing, Cf::kRings, GC * P, &inst,
+                             [](const cudaLaunchConfig_t* cfg, const SpanParams& p) { return cudaLaunchKernelEx(cfg, decode_span_f32_kernel<D, GC, P>, p); }};
+    return &k;
+}
+
+template <int D>
+const Kernel* pick_kernel(int cache, int cols) {
+    const bool two = cols > 8;
+    switch (cache) {
+        case kBf16: return two ? mma_kernel<D, 2, kBf16, 4, 3>() : mma_kernel<D, 1, kBf16, 4, 3>();
+        case kInt4: return two ? mma_kernel<D, 2, kInt4, 4, 4>() : mma_kernel<D, 1, kInt4, 4, 4>();
+        case kE4m3:
+            if constexpr (D == 128) return two ? mma_kernel<D, 2, kE4m3, 4, 3>() : mma_kernel<D, 1, kE4m3, 4, 3>();
+            return nullptr;
+        default:
+            if (cols <= 1) return f32_kernel<D, 1, 1>();
+            if (cols <= 2) return f32_kernel<D, 2, 1>();
+            if (cols <= 4) return f32_kernel<D, 2, 2>();
+            return f32_kernel<D, 4, 2>();
+    }
+}
+
+// How a call is laid out on the device.
+struct Plan {
+    const Kernel* kernel;
+    int ngroups, head_dim, P, C;
+    int64_t rows;  // of the outputs
+    // Where the partial states' maxima and denominators lie in the workspace (behind the numerators), and its bytes.
+    size_t partial_ml() const { return (static_cast<size_t>(rows) * P * head_dim * sizeof(float) + 255) / 256 * 256; }
+    size_t workspace() const { return C == P ? 0 : partial_ml() + static_cast<size_t>(rows) * P * sizeof(float2); }
+};
+
+// Blocks of a list (P).  A call takes about (waves of blocks) x (a block's start and end + its slabs);
+// a cluster of up to 16 blocks merges without a second kernel where all fit at once.
+void pick_blocks(Plan* plan, int64_t lists, int64_t slabs, int num_sms, int blocks_per_sm, const int* fit) {
+    const int64_t rounds = std::max<int64_t>(1, (slabs + plan->kernel->rings - 1) / plan->kernel->rings);  // of a block that has the list to itself
+    const int64_t slots = static_cast<int64_t>(num_sms) * blocks_per_sm;
+    constexpr double kStart = 4., kMerge = 3., kSecond = 6.;   // in rounds
+    double best = 0.;
+    for (int P = 1; P <= std::min<int64_t>(rounds, 512); ++P) {
+        const bool cluster = P == 1 || (P <= kMaxCluster && lists <= fit[P]);
+        const double waves = static_cast<double>((lists * P + slots - 1) / slots);
+        const double cost = waves * (kStart + static_cast<double>((rounds + P - 1) / P)) + (P == 1 ? 0. : (cluster ? kMerge : kSecond));
+        if (P == 1 || cost < best) {
+            best = cost;
+            plan->P = P;
+            plan->C = cluster ? P : 1;
+        }
+    }
+}
+
+struct Call {
+    SpanParams p;
+    Plan plan;
+    DeviceInfo dev;
+    int head_dim, batch;
+};
+
+// Sizes and types of a call.
+int check_sizes(const ta_shape* shape, int cache, int nq, int window, int sinks, Call* c) {
+    if (nq < 1 || nq > 16 || window < 1 || sinks < 0) return TA_ERR_SHAPE;
+    SpanParams& p = c->p;
+    std::memset(&p, 0, sizeof p);
+    p.Hq = shape->num_q_heads;
+    p.Hkv = shape->num_kv_heads;
+    p.G = p.Hq / p.Hkv;
+    if (cache == kF32 && p.G > 16) return TA_ERR_SHAPE;
+    if (shape->q_dtype != (cache == kF32 ? TA_F32 : TA_BF16) || (cache == kE4m3 && shape->head_dim != 128)) return TA_ERR_DTYPE;
+    p.nq = nq;
+    p.cols = p.G * nq;
+    p.S = shape->max_seqlen;
+    p.window = std::min(window, p.S);
+    p.sinks = std::min(sinks, p.S);
+    c->head_dim = shape->head_dim;
+    c->batch = shape->batch;
+    Plan& plan = c->plan;
+    plan.head_dim = shape->head_dim;
+    plan.kernel = shape->head_dim == 128 ? pick_kernel<128>(cache, p.cols) : pick_kernel<64>(cache, p.cols);
+    p.ngroups = plan.ngroups = (p.cols + plan.kernel->cols - 1) / plan.kernel->cols;
+    const int64_t lists = static_cast<int64_t>(p.Hkv) * p.ngroups;
+    plan.rows = static_cast<int64_t>(shape->batch) * p.Hq * nq;
+    if (shape->batch > 65535 || lists > 65535 || plan.rows > 0x7fffffff) return TA_ERR_SHAPE;
+    const float scale = shape->scale > 0.f ? shape->scale : 1.0f / std::sqrt(static_cast<float>(shape->head_dim));
+    p.scale_log2 = scale * kLog2e;
+    p.rows = static_cast<size_t>(plan.rows);
+    p.q_elems = p.out_elems = p.rows * shape->head_dim;
+    return TA_OK;
+}
+
+// Its blocks on the current device.
+int make_plan(Call* c) {
+    SpanParams& p = c->p;
+    const Kernel& k = *c->plan.kernel;
+    int rc = device_info(&c->dev);
+    if (rc != TA_OK) return rc;
+    if ((rc = prepare_instance(k.fn, k.threads, k.smem, c->dev.device, k.inst)) != TA_OK) return rc;
+    const int64_t seen = std::min<int64_t>(p.S, static_cast<int64_t>(p.window) + p.nq - 1 + p.sinks);
+    const int* fit = k.inst->clusters[c->dev.device];
+    pick_blocks(&c->plan, static_cast<int64_t>(c->batch) * p.Hkv * p.ngroups, seen / kSlab + 2, c->dev.num_sms, std::max(1, fit[1] / c->dev.num_sms), fit);
+    p.P = c->plan.P;
+    p.C = c->plan.C;
+    p.err = c->dev.err;
+    return TA_OK;
+}
+
+// The pages, and the pointers that both kinds of caches share.
+int set_common(const ta_shape* shape, const ta_paged_kv* paged, const void* q, const int32_t* seqlens, float* out, float* lse, int page_shift,
+               SpanParams* p) {
+    if (!q || !seqlens || !out) return TA_ERR_NULL;
+    if (!aligned_to(q, 16) || !aligned_to(out, 16) || !aligned_to(seqlens, 4) || !aligned_to(lse, 4)) return TA_ERR_ALIGN;
+    p->q = q;
+    p->seqlens = seqlens;
+    p->out = out;
+    p->lse = lse;
+    if (paged) {
+        p->block_table = paged->block_table;
+        p->max_pages = paged->max_pages_per_seq;
+        p->page_shift = page_shift;
+        p->num_pages = paged->num_pages;
+        p->table_elems = static_cast<size_t>(shape->batch) * paged->max_pages_per_seq;
+    }
+    return TA_OK;
+}
+
+int enqueue(Call* c, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    SpanParams& p = c->p;
+    const Plan& plan = c->plan;
+    const int rc = make_plan(c);
+    if (rc != TA_OK) return rc;
+    const size_t need = plan.workspace();
+    if (need) {
+        if (!workspace || workspace_bytes < need) return TA_ERR_WORKSPACE;
+        if (!aligned_to(workspace, 16)) return TA_ERR_ALIGN;
+        p.part_o = static_cast<float*>(workspace);
+        p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + plan.partial_ml());
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(plan.P, p.Hkv * p.ngroups, c->batch);
+    cfg.blockDim = dim3(plan.kernel->threads, 1, 1);
+    cfg.dynamicSmemBytes = plan.kernel->smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0] = programmatic_launch();
+    attr[1] = {};
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(plan.C);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = plan.C > 1 ? 2 : 1;
+    if (plan.kernel->launch(&cfg, p) != cudaSuccess) return TA_ERR_CUDA;
+    if (!need) return TA_OK;
+    cudaLaunchConfig_t end = {};
+    end.gridDim = dim3(static_cast<unsigned>(plan.rows), 1, 1);
+    end.blockDim = dim3(c->head_dim, 1, 1);
+    end.stream = stream;
+    end.attrs = attr;
+    end.numAttrs = 1;
+    const cudaError_t e = c->head_dim == 128 ? cudaLaunchKernelEx(&end, span_combine_kernel<128>, p) : cudaLaunchKernelEx(&end, span_combine_kernel<64>, p);
+    return e == cudaSuccess ? TA_OK : TA_ERR_CUDA;
+}
+
+int cache_kind(int dtype) {
+    return dtype == TA_F32 ? kF32 : (dtype == TA_BF16 ? kBf16 : (dtype == TA_E4M3 ? kE4m3 : kInt4));
+}
+
+}  // namespace
+}  // namespace ta
+
+extern "C" size_t tree_attn_window_workspace_bytes(const ta_shape* shape, const ta_paged_kv* paged, int num_queries, int window, int sinks) {
+    using namespace ta;
+    if (!shape) return 0;
+    ta_shape like = *shape;
+    if (like.kv_dtype == TA_INT4) like.kv_dtype = TA_BF16;
+    like.kv_stride_b = like.kv_stride_h = like.kv_stride_t = 0;
+    ta_paged_kv pages;
+    if (paged) {
+        pages = *paged;
+        if (!pages.block_table) pages.block_table = reinterpret_cast<const int32_t*>(16);  // (not read)
+    }
+    CacheLayout lay;
+    Call c;
+    if (cache_layout(&like, paged ? &pages : nullptr, &lay) != TA_OK ||
+        check_sizes(shape, cache_kind(shape->kv_dtype), num_queries, window, sinks, &c) != TA_OK || make_plan(&c) != TA_OK)
+        return 0;
+    return c.plan.workspace();
+}
+
+extern "C" int tree_attn_decode_window(const ta_shape* shape, const ta_paged_kv* paged, int num_queries, int window, int sinks, const void* q,
+                                       const void* k_cache, const void* v_cache, const int32_t* seqlens, float* out, float* lse,
+                                       const float* k_scale, const float* v_scale, void* workspace, size_t workspace_bytes, void* stream) {
+    using namespace ta;
+    CacheLayout lay;
+    int rc = cache_layout(shape, paged, &lay);
+    if (rc != TA_OK) return rc;
+    if (!k_cache || !v_cache) return TA_ERR_NULL;
+    if (!aligned_to(k_cache, 16) || !aligned_to(v_cache, 16)) return TA_ERR_ALIGN;
+    if (shape->kv_dtype == TA_E4M3) {
+        if (!k_scale || !v_scale) return TA_ERR_NULL;
+        if (!aligned_to(k_scale, 4) || !aligned_to(v_scale, 4)) return TA_ERR_ALIGN;
+    } else if (k_scale || v_scale) {
+        return TA_ERR_DTYPE;
+    }
+    Call c;
+    if ((rc = check_sizes(shape, cache_kind(shape->kv_dtype), num_queries, window, sinks, &c)) != TA_OK) return rc;
+    if ((rc = set_common(shape, paged, q, seqlens, out, lse, lay.page_shift, &c.p)) != TA_OK) return rc;
+    const int64_t es = lay.elem_bytes;
+    c.p.k = static_cast<const uint8_t*>(k_cache);
+    c.p.v = static_cast<const uint8_t*>(v_cache);
+    c.p.k_scale = k_scale;
+    c.p.v_scale = v_scale;
+    c.p.sb = lay.stride_b * es;
+    c.p.sh = lay.stride_h * es;
+    c.p.st = lay.stride_t * es;
+    c.p.cache_bytes = static_cast<size_t>(((paged ? paged->num_pages : shape->batch) - 1) * c.p.sb + (c.p.Hkv - 1) * c.p.sh +
+                                          ((paged ? paged->page_size : shape->max_seqlen) - 1) * c.p.st + shape->head_dim * es);
+    return enqueue(&c, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int tree_attn_decode_int4(const ta_shape* shape, const ta_paged_kv* paged, int num_queries, int window, int sinks, const void* q,
+                                     const ta_int4_kv* cache, const int32_t* seqlens, float* out, float* lse, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+    using namespace ta;
+    Int4Layout lay;
+    int rc = int4_layout(shape, paged, cache, &lay);
+    if (rc != TA_OK) return rc;
+    Call c;
+    if ((rc = check_sizes(shape, kInt4, num_queries, window, sinks, &c)) != TA_OK) return rc;
+    if ((rc = set_common(shape, paged, q, seqlens, out, lse, lay.page_shift, &c.p)) != TA_OK) return rc;
+    c.p.k = static_cast<const uint8_t*>(cache->k_codes);
+    c.p.v = static_cast<const uint8_t*>(cache->v_codes);
+    c.p.k_steps = static_cast<const uint8_t*>(cache->k_steps);
+    c.p.v_steps = static_cast<const uint8_t*>(cache->v_steps);
+    c.p.k_scale = cache->k_scale;
+    c.p.v_scale = cache->v_scale;
+    c.p.sb = lay.code_b;
+    c.p.sh = lay.code_h;
+    c.p.st = lay.code_t;
+    c.p.tb = lay.step_b;
+    c.p.th = lay.step_h;
+    c.p.tt = lay.step_t;
+    c.p.cache_bytes = lay.code_bytes;
+    c.p.step_bytes = lay.step_bytes;
+    return enqueue(&c, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}

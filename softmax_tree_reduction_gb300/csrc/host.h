@@ -28,6 +28,16 @@ struct CacheLayout {
 // Validate a cache's shape (and its pages, when given) and resolve its strides.
 int cache_layout(const ta_shape* shape, const ta_paged_kv* paged, CacheLayout* out);
 
+// A 4-bit cache's strides in bytes and the bytes up to the end of its last vector.
+struct Int4Layout {
+    int64_t code_b, code_h, code_t, step_b, step_h, step_t;
+    size_t code_bytes, step_bytes;
+    int page_shift;
+};
+
+// Validate a 4-bit cache and its shape, and resolve its strides.
+int int4_layout(const ta_shape* shape, const ta_paged_kv* paged, const ta_int4_kv* cache, Int4Layout* out);
+
 inline bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Launch attribute: the grid may start while the previous one on the stream

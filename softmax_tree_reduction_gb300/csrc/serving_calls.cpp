@@ -37,6 +37,11 @@ decltype(&tree_attn_page_bounds) p_page_bounds;
 decltype(&tree_attn_select_workspace_bytes) p_select_workspace_bytes;
 decltype(&tree_attn_select_pages) p_select_pages;
 decltype(&tree_attn_decode_selected) p_decode_selected;
+decltype(&tree_attn_cache_write_int4) p_cache_write_int4;
+decltype(&tree_attn_cache_read_int4) p_cache_read_int4;
+decltype(&tree_attn_window_workspace_bytes) p_window_workspace_bytes;
+decltype(&tree_attn_decode_window) p_decode_window;
+decltype(&tree_attn_decode_int4) p_decode_int4;
 
 using Tensor = at::Tensor;
 
@@ -199,17 +204,11 @@ void check_table(const Tensor& bt) {
         throw BadValue("block_table must be a contiguous int32 [B, max_pages] tensor");
 }
 
-// [pages, page, Hkv, d] pools
-void pool_shape(const Tensor& k, const Tensor& bt, PyObject* max_seqlen, ta_shape* s, ta_paged_kv* pg) {
-    if (k.dim() != 4 || k.stride(3) != 1) throw BadValue("page pools must be [num_pages, page_size, Hkv, d] with contiguous channels");
+// Rows, pages and lengths of pools [pages, page, Hkv, ..].
+void pool_places(const Tensor& k, const Tensor& bt, PyObject* max_seqlen, ta_shape* s, ta_paged_kv* pg) {
     check_table(bt);
     s->batch = size32(bt.size(0), "block_table");
     s->num_kv_heads = size32(k.size(2), "a cache");
-    s->head_dim = size32(k.size(3), "a cache");
-    s->kv_dtype = dtype_code(k);
-    s->kv_stride_b = cache_stride(k, 0);
-    s->kv_stride_t = cache_stride(k, 1);
-    s->kv_stride_h = cache_stride(k, 2);
     pg->block_table = bt.const_data_ptr<int32_t>();
     pg->max_pages_per_seq = size32(bt.size(1), "block_table");
     pg->page_size = size32(k.size(1), "a page");
@@ -217,11 +216,101 @@ void pool_shape(const Tensor& k, const Tensor& bt, PyObject* max_seqlen, ta_shap
     const int64_t all = bt.size(1) * k.size(1);
     s->max_seqlen = max_seqlen == Py_None ? static_cast<int32_t>(std::min<int64_t>(all, 0x7fffffff)) : int32(max_seqlen, "max_seqlen");
 }
+// The same of dense caches [B, Hkv, S, ..].
+void dense_places(const Tensor& k, PyObject* max_seqlen, ta_shape* s) {
+    s->batch = size32(k.size(0), "a cache");
+    s->num_kv_heads = size32(k.size(1), "a cache");
+    s->max_seqlen = size32(k.size(2), "a cache");
+    if (max_seqlen != Py_None) {
+        const int most = int32(max_seqlen, "max_seqlen");
+        if (most < 1 || most > s->max_seqlen) throw BadValue("max_seqlen must be at least 1 and at most the cache's tokens");
+        s->max_seqlen = most;
+    }
+}
+
+// [pages, page, Hkv, d] pools
+void pool_shape(const Tensor& k, const Tensor& bt, PyObject* max_seqlen, ta_shape* s, ta_paged_kv* pg) {
+    if (k.dim() != 4 || k.stride(3) != 1) throw BadValue("page pools must be [num_pages, page_size, Hkv, d] with contiguous channels");
+    pool_places(k, bt, max_seqlen, s, pg);
+    s->head_dim = size32(k.size(3), "a cache");
+    s->kv_dtype = dtype_code(k);
+    s->kv_stride_b = cache_stride(k, 0);
+    s->kv_stride_t = cache_stride(k, 1);
+    s->kv_stride_h = cache_stride(k, 2);
+}
+
+// [B, Hkv, S, d] caches
+void dense_shape(const Tensor& k, PyObject* max_seqlen, ta_shape* s) {
+    if (k.dim() != 4 || k.stride(3) != 1) throw BadValue("dense caches must be [B, Hkv, S, d] with contiguous channels");
+    dense_places(k, max_seqlen, s);
+    s->head_dim = size32(k.size(3), "a cache");
+    s->kv_dtype = dtype_code(k);
+    s->kv_stride_b = cache_stride(k, 0);
+    s->kv_stride_h = cache_stride(k, 1);
+    s->kv_stride_t = cache_stride(k, 2);
+}
 
 void same_cache(const Tensor& k, const Tensor& v) {
     if (!v.sizes().equals(k.sizes()) || !v.strides().equals(k.strides()) || v.scalar_type() != k.scalar_type())
         throw BadValue("the key and value caches must agree on shape, strides and type");
 }
+
+// The token list of a cache write or read of head vectors like `vec`, and their type.
+void tokens_of(const Tensor& pos, const Tensor* rows, const Tensor& vec, ta_shape* shape, ta_tokens* tokens) {
+    shape->num_q_heads = shape->num_kv_heads;
+    shape->q_dtype = vec_dtype(vec);
+    if (pos.dim() != 1) throw BadValue("positions must be a contiguous int32 tensor [tokens]");
+    tokens->num_tokens = size32(pos.size(0), "positions");
+    tokens->positions = ints(&pos, "positions", pos.size(0));
+    tokens->rows = ints(rows, "rows", pos.size(0));
+    if (vec.dim() != 3 || vec.size(0) != pos.size(0) || vec.size(1) != shape->num_kv_heads || vec.size(2) != shape->head_dim)
+        throw BadValue("head vectors must be [tokens, num_kv_heads, head_dim] of the cache and the positions");
+}
+
+// A 4-bit cache: codes [.., d / 2] and steps [.., d / 16] over the axes of the other caches.
+struct Int4Cache {
+    ta_shape shape;
+    ta_paged_kv paged;
+    ta_int4_kv cache;
+    const ta_paged_kv* pages = nullptr;
+    Int4Cache(const Tensor& kc, const Tensor& vc, const Tensor& kst, const Tensor& vst, const Tensor* bt, PyObject* max_seqlen, const Tensor* ks,
+              const Tensor* vs) {
+        std::memset(&shape, 0, sizeof shape);
+        std::memset(&paged, 0, sizeof paged);
+        std::memset(&cache, 0, sizeof cache);
+        same_cache(kc, vc);
+        same_cache(kst, vst);
+        if (kc.scalar_type() != at::kByte || kst.scalar_type() != at::ScalarType::Float8_e4m3fn)
+            throw BadType("4-bit caches are uint8 codes and float8_e4m3fn steps");
+        if (kc.dim() != 4 || kst.dim() != 4 || kc.stride(3) != 1 || kst.stride(3) != 1)
+            throw BadValue("4-bit caches must be 4-D, with contiguous codes [.., d / 2] and steps [.., d / 16]");
+        for (int i = 0; i < 3; ++i)
+            if (kc.size(i) != kst.size(i)) throw BadValue("codes and steps must agree on pages or rows, tokens and heads");
+        if (kc.size(3) != 8 * kst.size(3)) throw BadValue("there must be a step for every eight bytes of codes");
+        if (bt) {
+            pool_places(kc, *bt, max_seqlen, &shape, &paged);
+            pages = &paged;
+        } else {
+            dense_places(kc, max_seqlen, &shape);
+        }
+        shape.head_dim = size32(2 * kc.size(3), "a cache");
+        shape.kv_dtype = TA_INT4;
+        const int h = bt ? 2 : 1, t = bt ? 1 : 2;
+        cache.k_codes = kc.data_ptr();
+        cache.v_codes = vc.data_ptr();
+        cache.k_steps = kst.data_ptr();
+        cache.v_steps = vst.data_ptr();
+        cache.code_stride_b = cache_stride(kc, 0);
+        cache.code_stride_h = cache_stride(kc, h);
+        cache.code_stride_t = cache_stride(kc, t);
+        cache.step_stride_b = cache_stride(kst, 0);
+        cache.step_stride_h = cache_stride(kst, h);
+        cache.step_stride_t = cache_stride(kst, t);
+        if (!ks != !vs) throw BadValue("k_scale and v_scale go together");
+        cache.k_scale = scales(ks, "k_scale", shape.num_kv_heads);
+        cache.v_scale = scales(vs, "v_scale", shape.num_kv_heads);
+    }
+};
 
 // Shape, pages and tokens of a cache write or read of head vectors like `vec`.
 struct CacheCall {
@@ -238,29 +327,9 @@ struct CacheCall {
             pool_shape(kc, *bt, max_seqlen, &shape, &paged);
             pages = &paged;
         } else {
-            if (kc.dim() != 4 || kc.stride(3) != 1) throw BadValue("dense caches must be [B, Hkv, S, d] with contiguous channels");
-            shape.batch = size32(kc.size(0), "a cache");
-            shape.num_kv_heads = size32(kc.size(1), "a cache");
-            shape.max_seqlen = size32(kc.size(2), "a cache");
-            if (max_seqlen != Py_None) {
-                const int most = int32(max_seqlen, "max_seqlen");
-                if (most < 1 || most > shape.max_seqlen) throw BadValue("max_seqlen must be at least 1 and at most the cache's tokens");
-                shape.max_seqlen = most;
-            }
-            shape.head_dim = size32(kc.size(3), "a cache");
-            shape.kv_dtype = dtype_code(kc);
-            shape.kv_stride_b = cache_stride(kc, 0);
-            shape.kv_stride_h = cache_stride(kc, 1);
-            shape.kv_stride_t = cache_stride(kc, 2);
+            dense_shape(kc, max_seqlen, &shape);
         }
-        shape.num_q_heads = shape.num_kv_heads;
-        shape.q_dtype = vec_dtype(vec);
-        if (pos.dim() != 1) throw BadValue("positions must be a contiguous int32 tensor [tokens]");
-        tokens.num_tokens = size32(pos.size(0), "positions");
-        tokens.positions = ints(&pos, "positions", pos.size(0));
-        tokens.rows = ints(rows, "rows", pos.size(0));
-        if (vec.dim() != 3 || vec.size(0) != pos.size(0) || vec.size(1) != shape.num_kv_heads || vec.size(2) != shape.head_dim)
-            throw BadValue("head vectors must be [tokens, num_kv_heads, head_dim] of the cache and the positions");
+        tokens_of(pos, rows, vec, &shape, &tokens);
     }
 };
 
@@ -349,6 +418,35 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// Vectors, norm and rotation of a cache write: what the writes of both kinds of caches share.
+struct Written {
+    ta_heads hk, hv, hq, hqo;
+    ta_rope rope;
+    bool turned;
+    const Tensor* q;
+    // k, v, q, q_out, inv_freq, q_weight, k_weight, norm, eps, interleaved
+    Written(const Tensor& k, const Tensor& v, const Tensor* q_, const Tensor* qo, const Tensor* f, const Tensor* qw, const Tensor* kw, PyObject* norm_,
+            PyObject* eps, PyObject* interleaved, ta_shape* shape)
+        : q(q_) {
+        const bool norm = truth(norm_);
+        turned = norm || f;
+        if (!q != !qo) throw BadValue("q and q_out go together");
+        if (q && !turned) throw BadValue("q needs a norm or a rotation");
+        if (!norm && (qw || kw)) throw BadValue("norm weights need norm=True");
+        hk = heads(k, "k");
+        hv = heads(v, "v");
+        if (q) {
+            like(*q, *qo, "q and q_out");
+            hq = heads(*q, "q");
+            hqo = heads(*qo, "q_out", true);
+            if (q->size(0) != k.size(0) || q->size(2) != k.size(2) || q->scalar_type() != k.scalar_type())
+                throw BadValue("q and k must agree on tokens, head_dim and type");
+            shape->num_q_heads = size32(q->size(1), "q");
+        }
+        if (turned) rope = rope_of(k.size(2), f, qw, kw, norm, real(eps), truth(interleaved));
+    }
+};
+
 // k, v, k_cache, v_cache, positions, rows, block_table, k_scale, v_scale, q, q_out, inv_freq, q_weight, k_weight, norm, eps,
 // interleaved, max_seqlen, stream
 PyObject* cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -358,32 +456,61 @@ PyObject* cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Tensor *rows = opt(a[5], "rows"), *bt = opt(a[6], "block_table"), *ks = opt(a[7], "k_scale"), *vs = opt(a[8], "v_scale"),
                      *q = opt(a[9], "q"), *qo = opt(a[10], "q_out"), *f = opt(a[11], "inv_freq"), *qw = opt(a[12], "q_weight"),
                      *kw = opt(a[13], "k_weight");
-        const bool norm = truth(a[14]), turned = norm || f;
-        if (!q != !qo) throw BadValue("q and q_out go together");
-        if (q && !turned) throw BadValue("q needs a norm or a rotation");
-        if (!norm && (qw || kw)) throw BadValue("norm weights need norm=True");
         like(k, v, "k and v");
         CacheCall c(kc, vc, pos, rows, bt, a[17], k);
-        const ta_heads hk = heads(k, "k"), hv = heads(v, "v");
-        ta_heads hq, hqo;
-        if (q) {
-            like(*q, *qo, "q and q_out");
-            hq = heads(*q, "q");
-            hqo = heads(*qo, "q_out", true);
-            if (q->size(0) != k.size(0) || q->size(2) != k.size(2) || q->scalar_type() != k.scalar_type())
-                throw BadValue("q and k must agree on tokens, head_dim and type");
-            c.shape.num_q_heads = size32(q->size(1), "q");
-        }
-        ta_rope r;
-        if (turned) r = rope_of(k.size(2), f, qw, kw, norm, real(a[15]), truth(a[16]));
+        const Written w(k, v, q, qo, f, qw, kw, a[14], a[15], a[16], &c.shape);
         const float *pks = scales(ks, "k_scale", c.shape.num_kv_heads), *pvs = scales(vs, "v_scale", c.shape.num_kv_heads);
         Device dev;
         for (const Tensor* t : {&k, &v, &kc, &vc, &pos, rows, bt, ks, vs, q, qo, f, qw, kw}) dev.add(t);
         void* st = dev.stream(a[18]);
         return enqueue([&] {
-            return p_cache_write(&c.shape, c.pages, &c.tokens, turned ? &r : nullptr, q ? &hq : nullptr, q ? &hqo : nullptr, &hk, &hv,
+            return p_cache_write(&c.shape, c.pages, &c.tokens, w.turned ? &w.rope : nullptr, q ? &w.hq : nullptr, q ? &w.hqo : nullptr, &w.hk, &w.hv,
                                  kc.data_ptr(), vc.data_ptr(), pks, pvs, st);
         });
+    });
+}
+
+// k, v, k_codes, v_codes, k_steps, v_steps, positions, rows, block_table, k_scale, v_scale, q, q_out, inv_freq, q_weight, k_weight,
+// norm, eps, interleaved, max_seqlen, stream
+PyObject* cache_write_int4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 21, [&] {
+        const Tensor &k = need(a[0], "k"), &v = need(a[1], "v"), &kc = need(a[2], "k_codes"), &vc = need(a[3], "v_codes"),
+                     &kst = need(a[4], "k_steps"), &vst = need(a[5], "v_steps"), &pos = need(a[6], "positions");
+        const Tensor *rows = opt(a[7], "rows"), *bt = opt(a[8], "block_table"), *ks = opt(a[9], "k_scale"), *vs = opt(a[10], "v_scale"),
+                     *q = opt(a[11], "q"), *qo = opt(a[12], "q_out"), *f = opt(a[13], "inv_freq"), *qw = opt(a[14], "q_weight"),
+                     *kw = opt(a[15], "k_weight");
+        like(k, v, "k and v");
+        Int4Cache c(kc, vc, kst, vst, bt, a[19], ks, vs);
+        ta_tokens tokens;
+        std::memset(&tokens, 0, sizeof tokens);
+        tokens_of(pos, rows, k, &c.shape, &tokens);
+        const Written w(k, v, q, qo, f, qw, kw, a[16], a[17], a[18], &c.shape);
+        Device dev;
+        for (const Tensor* t : {&k, &v, &kc, &vc, &kst, &vst, &pos, rows, bt, ks, vs, q, qo, f, qw, kw}) dev.add(t);
+        void* st = dev.stream(a[20]);
+        return enqueue([&] {
+            return p_cache_write_int4(&c.shape, c.pages, &tokens, w.turned ? &w.rope : nullptr, q ? &w.hq : nullptr, q ? &w.hqo : nullptr, &w.hk,
+                                      &w.hv, &c.cache, st);
+        });
+    });
+}
+
+// k_codes, v_codes, k_steps, v_steps, positions, rows, block_table, k_scale, v_scale, k_out, v_out, max_seqlen, stream
+PyObject* cache_read_int4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 13, [&] {
+        const Tensor &kc = need(a[0], "k_codes"), &vc = need(a[1], "v_codes"), &kst = need(a[2], "k_steps"), &vst = need(a[3], "v_steps"),
+                     &pos = need(a[4], "positions"), &ko = need(a[9], "k_out"), &vo = need(a[10], "v_out");
+        const Tensor *rows = opt(a[5], "rows"), *bt = opt(a[6], "block_table"), *ks = opt(a[7], "k_scale"), *vs = opt(a[8], "v_scale");
+        like(ko, vo, "k_out and v_out");
+        Int4Cache c(kc, vc, kst, vst, bt, a[11], ks, vs);
+        ta_tokens tokens;
+        std::memset(&tokens, 0, sizeof tokens);
+        tokens_of(pos, rows, ko, &c.shape, &tokens);
+        const ta_heads hk = heads(ko, "k_out", true), hv = heads(vo, "v_out", true);
+        Device dev;
+        for (const Tensor* t : {&kc, &vc, &kst, &vst, &pos, &ko, &vo, rows, bt, ks, vs}) dev.add(t);
+        void* st = dev.stream(a[12]);
+        return enqueue([&] { return p_cache_read_int4(&c.shape, c.pages, &tokens, &c.cache, &hk, &hv, st); });
     });
 }
 
@@ -534,6 +661,113 @@ PyObject* decode_selected(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// Queries [B, Hq, d] or [B, Hq, queries, d], outputs, lengths and window of a call over a row's first and last tokens.
+struct Windowed {
+    int queries = 1, window, sinks;
+    const int32_t* lengths;
+    // q, seqlens, window, sinks, out, lse, scale
+    Windowed(const Tensor& q, const Tensor& len, PyObject* window_, PyObject* sinks_, const Tensor& out, const Tensor* lse, PyObject* scale, ta_shape* s) {
+        const int64_t d = q.dim();
+        if ((d != 3 && d != 4) || q.size(0) != s->batch || q.size(d - 1) != s->head_dim || !q.is_contiguous())
+            throw BadValue("q must be a contiguous [B, Hq, d] or [B, Hq, queries, d] tensor that agrees with the cache");
+        s->num_q_heads = size32(q.size(1), "q");
+        s->q_dtype = vec_dtype(q);
+        if (d == 4) queries = size32(q.size(2), "q");
+        s->scale = scale == Py_None ? 0.f : static_cast<float>(real(scale));
+        window = window_ == Py_None ? 0x7fffffff : int32(window_, "window");
+        sinks = int32(sinks_, "sinks");
+        lengths = ints(&len, "seqlens", s->batch);
+        if (out.scalar_type() != at::kFloat || !out.sizes().equals(q.sizes()) || !out.is_contiguous())
+            throw BadValue("out must be a contiguous float32 tensor of q's shape");
+        if (lse && (lse->scalar_type() != at::kFloat || lse->dim() != d - 1 || !lse->sizes().equals(q.sizes().slice(0, d - 1)) || !lse->is_contiguous()))
+            throw BadValue("lse must be a contiguous float32 tensor of q's shape without the channels");
+    }
+};
+
+// The workspace of a windowed call: the given one, or one from torch's allocator for the current stream.
+Tensor window_workspace(const Tensor* given, PyObject* stream, const ta_shape& s, const ta_paged_kv* pages, const Windowed& w, const Tensor& q) {
+    if (given) {
+        if (!given->is_contiguous()) throw BadValue("workspace must be contiguous");
+        return *given;
+    }
+    const size_t need = p_window_workspace_bytes(&s, pages, w.queries, w.window, w.sinks);
+    if (need && stream != Py_None) throw BadValue("a workspace is needed with a stream");
+    return need ? at::empty({static_cast<int64_t>(need)}, q.options().dtype(at::kByte)) : Tensor();
+}
+
+// cache shape: k_cache or k_codes, block_table, q, window, sinks, max_seqlen; bytes of workspace that the call needs
+PyObject* window_workspace_bytes(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 6, [&] {
+        const Tensor &k = need(a[0], "the cache"), &q = need(a[2], "q");
+        const Tensor* bt = opt(a[1], "block_table");
+        ta_shape s;
+        ta_paged_kv pg;
+        std::memset(&s, 0, sizeof s);
+        std::memset(&pg, 0, sizeof pg);
+        if (k.dim() != 4 || q.dim() < 3 || q.dim() > 4) throw BadValue("caches must be 4-D, and q 3-D or 4-D");
+        if (bt)
+            pool_places(k, *bt, a[5], &s, &pg);
+        else
+            dense_places(k, a[5], &s);
+        const bool codes = k.scalar_type() == at::kByte;
+        s.head_dim = size32(q.size(q.dim() - 1), "q");
+        s.kv_dtype = codes ? static_cast<int>(TA_INT4) : dtype_code(k);
+        s.num_q_heads = size32(q.size(1), "q");
+        s.q_dtype = vec_dtype(q);
+        return static_cast<long>(p_window_workspace_bytes(&s, bt ? &pg : nullptr, q.dim() == 4 ? size32(q.size(2), "q") : 1,
+                                                          a[3] == Py_None ? 0x7fffffff : int32(a[3], "window"), int32(a[4], "sinks")));
+    });
+}
+
+// q, k_cache, v_cache, seqlens, window, sinks, block_table, out, lse, scale, max_seqlen, k_scale, v_scale, workspace, stream
+PyObject* decode_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 15, [&] {
+        const Tensor &q = need(a[0], "q"), &k = need(a[1], "k_cache"), &v = need(a[2], "v_cache"), &len = need(a[3], "seqlens"), &out = need(a[7], "out");
+        const Tensor *bt = opt(a[6], "block_table"), *lse = opt(a[8], "lse"), *ks = opt(a[11], "k_scale"), *vs = opt(a[12], "v_scale"),
+                     *given = opt(a[13], "workspace");
+        ta_shape s;
+        ta_paged_kv pg;
+        std::memset(&s, 0, sizeof s);
+        std::memset(&pg, 0, sizeof pg);
+        same_cache(k, v);
+        if (bt)
+            pool_shape(k, *bt, a[10], &s, &pg);
+        else
+            dense_shape(k, a[10], &s);
+        const Windowed w(q, len, a[4], a[5], out, lse, a[9], &s);
+        const float *pks = scales(ks, "k_scale", s.num_kv_heads), *pvs = scales(vs, "v_scale", s.num_kv_heads);
+        Device dev;
+        for (const Tensor* t : {&q, &k, &v, bt, &len, &out, lse, ks, vs, given}) dev.add(t);
+        void* st = dev.stream(a[14]);
+        const Tensor ws = window_workspace(given, a[14], s, bt ? &pg : nullptr, w, q);
+        return enqueue([&] {
+            return p_decode_window(&s, bt ? &pg : nullptr, w.queries, w.window, w.sinks, q.data_ptr(), k.data_ptr(), v.data_ptr(), w.lengths,
+                                   out.data_ptr<float>(), lse ? lse->data_ptr<float>() : nullptr, pks, pvs, ws.defined() ? ws.data_ptr() : nullptr,
+                                   ws.defined() ? ws.nbytes() : 0, st);
+        });
+    });
+}
+
+// q, k_codes, v_codes, k_steps, v_steps, seqlens, window, sinks, block_table, out, lse, scale, max_seqlen, k_scale, v_scale, workspace, stream
+PyObject* decode_int4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 17, [&] {
+        const Tensor &q = need(a[0], "q"), &kc = need(a[1], "k_codes"), &vc = need(a[2], "v_codes"), &kst = need(a[3], "k_steps"),
+                     &vst = need(a[4], "v_steps"), &len = need(a[5], "seqlens"), &out = need(a[9], "out");
+        const Tensor *bt = opt(a[8], "block_table"), *lse = opt(a[10], "lse"), *ks = opt(a[13], "k_scale"), *vs = opt(a[14], "v_scale"),
+                     *given = opt(a[15], "workspace");
+        Int4Cache c(kc, vc, kst, vst, bt, a[12], ks, vs);
+        const Windowed w(q, len, a[6], a[7], out, lse, a[11], &c.shape);
+        Device dev;
+        for (const Tensor* t : {&q, &kc, &vc, &kst, &vst, bt, &len, &out, lse, ks, vs, given}) dev.add(t);
+        void* st = dev.stream(a[16]);
+        const Tensor ws = window_workspace(given, a[16], c.shape, c.pages, w, q);
+        return enqueue([&] {
+            return p_decode_int4(&c.shape, c.pages, w.queries, w.window, w.sinks, q.data_ptr(), &c.cache, w.lengths, out.data_ptr<float>(),
+                                 lse ? lse->data_ptr<float>() : nullptr, ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, st);
+        });
+    });
+}
+
 template <typename F>
 bool resolve(void* lib, const char* name, F* f) {
     *f = reinterpret_cast<F>(dlsym(lib, name));
@@ -549,6 +783,9 @@ PyObject* init(PyObject*, PyObject* path) {
         !resolve(lib, "tree_attn_page_bounds", &p_page_bounds) ||
         !resolve(lib, "tree_attn_select_workspace_bytes", &p_select_workspace_bytes) ||
         !resolve(lib, "tree_attn_select_pages", &p_select_pages) || !resolve(lib, "tree_attn_decode_selected", &p_decode_selected) ||
+        !resolve(lib, "tree_attn_cache_write_int4", &p_cache_write_int4) || !resolve(lib, "tree_attn_cache_read_int4", &p_cache_read_int4) ||
+        !resolve(lib, "tree_attn_window_workspace_bytes", &p_window_workspace_bytes) ||
+        !resolve(lib, "tree_attn_decode_window", &p_decode_window) || !resolve(lib, "tree_attn_decode_int4", &p_decode_int4) ||
         !resolve(lib, "tree_attn_norm_rope", &p_norm_rope)) {
         PyErr_Format(PyExc_RuntimeError, "%s lacks the serving entry points: build it again", p);
         return nullptr;
@@ -565,6 +802,11 @@ PyMethodDef g_methods[] = {{"init", init, METH_O, nullptr},
                            TA_METHOD(select_workspace_bytes),
                            TA_METHOD(select_pages),
                            TA_METHOD(decode_selected),
+                           TA_METHOD(cache_write_int4),
+                           TA_METHOD(cache_read_int4),
+                           TA_METHOD(window_workspace_bytes),
+                           TA_METHOD(decode_window),
+                           TA_METHOD(decode_int4),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_serving_calls", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

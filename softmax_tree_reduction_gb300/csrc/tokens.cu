@@ -75,7 +75,15 @@ struct TokenParams {
     int rot, interleaved, norm, w_bf16;
     float eps;
     size_t cache_elems, table_elems;  // extents, for the bounds-checking build
+    // 4-bit caches: kc, vc are the codes, with cb, ch, ct and cache_elems in bytes; the steps beside them
+    void* kst;
+    void* vst;
+    int64_t stb, sth, stt;
+    size_t step_bytes;
 };
+
+// The type of a 4-bit cache: codes, two channels a byte, and an E4M3 step for 16 channels.
+struct Int4 {};
 
 // Whether channels [ch, ch + n) of token t, head h lie in the vectors' memory.
 __device__ __forceinline__ bool vector_in(const Vectors& v, int t, int h, int ch, int n, int* err) {
@@ -84,6 +92,10 @@ __device__ __forceinline__ bool vector_in(const Vectors& v, int t, int h, int ch
 // The same of the cache, for the place that a token's vectors have in it.
 __device__ __forceinline__ bool cache_in(const TokenParams& p, int64_t place, int h, int ch, int n) {
     return in_bounds(static_cast<size_t>(place + h * p.ch + ch + n - 1), p.cache_elems, p.err);
+}
+
+__device__ __forceinline__ bool step_in(const TokenParams& p, int64_t place, int h, int ch) {
+    return in_bounds(static_cast<size_t>(place + h * p.sth + (ch >> 4)), p.step_bytes, p.err);
 }
 
 // Four channels of a vector in memory, and as FP32.
@@ -335,7 +347,8 @@ __device__ __forceinline__ void store_runs(T* dst, const Lane& c, const float (&
 
 template <typename TC>
 __device__ __forceinline__ void to_codes(const float* scale, int h, float (&f)[8]) {
-    if constexpr (std::is_same<TC, __nv_fp8_e4m3>::value) {
+    if constexpr (std::is_same<TC, __nv_fp8_e4m3>::value || std::is_same<TC, Int4>::value) {
+        if (std::is_same<TC, Int4>::value && !scale) return;
         const float sc = __ldg(scale + h);
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = f[i] / sc;
@@ -343,17 +356,116 @@ __device__ __forceinline__ void to_codes(const float* scale, int h, float (&f)[8
 }
 
 // Start of the token's place in the cache (elements), or -1 (bad data: the
-// error word is set).
-__device__ __forceinline__ int64_t cache_place(const TokenParams& p, int t, int row, int pos) {
+// error word is set).  `steps`: also that of its steps (4-bit caches, both in bytes).
+__device__ __forceinline__ int64_t cache_place(const TokenParams& p, int t, int row, int pos, int64_t* steps = nullptr) {
     if (row < p.B && pos < p.S) {
-        if (!p.block_table) return row * p.cb + pos * p.ct;
+        if (!p.block_table) {
+            if (steps) *steps = row * p.stb + pos * p.stt;
+            return row * p.cb + pos * p.ct;
+        }
         const int64_t e = static_cast<int64_t>(row) * p.max_pages + (pos >> p.page_shift);
         const int page = in_bounds(e, p.table_elems, p.err) ? __ldg(p.block_table + e) : -1;
-        if (page >= 0 && page < p.num_pages) return page * p.cb + (pos & ((1 << p.page_shift) - 1)) * p.ct;
+        if (page >= 0 && page < p.num_pages) {
+            const int slot = pos & ((1 << p.page_shift) - 1);
+            if (steps) *steps = page * p.stb + slot * p.stt;
+            return page * p.cb + slot * p.ct;
+        }
     }
     atomicOr(p.err, kErrBadSeqlen);
     return -1;
 }
+
+// ------------------------------------------------------------- 4-bit caches
+// The larger one, NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float top4(const float* f) {
+    return max_nan(max_nan(fabsf(f[0]), fabsf(f[1])), max_nan(fabsf(f[2]), fabsf(f[3])));
+}
+
+// The step of 16 channels whose largest magnitude is `top`.
+struct Step {
+    uint32_t code;
+    float c, r;  // its value and the reciprocal
+};
+__device__ __forceinline__ Step make_step(float top) {
+    Step s;
+    s.code = __nv_cvt_float_to_fp8(max_nan(top / 7.f, 0.001953125f), __NV_SATFINITE, __NV_E4M3);
+    s.c = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(s.code), __NV_E4M3)));
+    s.r = 1.f / s.c;
+    return s;
+}
+
+// Codes of four channels.  z r is z / step but for half a unit of FP32 twice, so the whole
+// number n next to it is the one next to z / step, except where that lies in the middle of two
+// or next to it; e = z - n step says so (it is exact: a multiple of z's last bit and no
+// longer than z, and of at most 24 bits therefore), and which of the two it should be.
+// (An FP32 number z / step that is not in the middle is at least half a unit from it.)
+// Channels that saturate take the last code whatever e is.
+__device__ __forceinline__ uint32_t int4_codes(const float* z, const Step& s) {
+    uint32_t out = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float n = fminf(fmaxf(rintf(z[i] * s.r), -8.f), 8.f);
+        const float e = fmaf(-n, s.c, z[i]), e2 = 2.f * fabsf(e);
+        if (e2 > s.c || (e2 == s.c && (static_cast<int>(n) & 1))) n += copysignf(1.f, e);
+        n = fminf(fmaxf(n, -7.f), 7.f);
+        out |= static_cast<uint32_t>(static_cast<int>(n) + 8) << (4 * i);
+    }
+    return out;
+}
+
+// Where the other eight channels of the 16 that a lane's runs belong to are held.
+struct Partner {
+    int la, lb;   // lanes of the group
+    bool ra, rb;  // in the lane's second run
+};
+__device__ __forceinline__ Partner make_partner(const TokenParams& p, const Lane& c) {
+    const int half = p.rot >> 1;
+    auto find = [&](int ch, int* lane, bool* run) {  // holder of channel ch
+        const bool split = ch < p.rot && !p.interleaved;
+        *run = split && ch >= half;
+        *lane = split ? (ch - (*run ? half : 0)) >> 2 : ch >> 3;
+    };
+    Partner q;
+    find((c.a & ~7) ^ 8, &q.la, &q.ra);
+    find((c.b & ~7) ^ 8, &q.lb, &q.rb);
+    return q;
+}
+
+// Store a lane's two runs; `codes`, `steps`: the vector's bytes.  Every lane of the group.
+template <int L>
+__device__ __forceinline__ void store_runs_int4(const TokenParams& p, const Lane& c, const Partner& q, const float (&f)[8], uint8_t* codes,
+                                                uint8_t* steps, unsigned mask) {
+    float ma = top4(f), mb = top4(f + 4);
+    const float xa = __shfl_xor_sync(mask, ma, 1), xb = __shfl_xor_sync(mask, mb, 1);
+    if (c.on && !p.interleaved) {  // a run's neighbour holds the rest of its eight channels
+        ma = max_nan(ma, xa);
+        mb = max_nan(mb, xb);
+    } else {
+        ma = mb = max_nan(ma, mb);
+    }
+    const float aa = __shfl_sync(mask, ma, q.la, L), ab = __shfl_sync(mask, mb, q.la, L);
+    const float ba = __shfl_sync(mask, ma, q.lb, L), bb = __shfl_sync(mask, mb, q.lb, L);
+    const Step sa = make_step(max_nan(ma, q.ra ? ab : aa)), sb = make_step(max_nan(mb, q.rb ? bb : ba));
+    *reinterpret_cast<uint16_t*>(codes + (c.a >> 1)) = static_cast<uint16_t>(int4_codes(f, sa));
+    *reinterpret_cast<uint16_t*>(codes + (c.b >> 1)) = static_cast<uint16_t>(int4_codes(f + 4, sb));
+    if ((c.a & 15) == 0) steps[c.a >> 4] = static_cast<uint8_t>(sa.code);
+    if ((c.b & 15) == 0) steps[c.b >> 4] = static_cast<uint8_t>(sb.code);
+}
+
+// Eight channels of a 4-bit vector: their codes and the step.
+struct Eight4 {
+    uint32_t codes, step;
+    __device__ __forceinline__ void unpack(float (&f)[8]) const {
+        const float c = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(step), __NV_E4M3)));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = c * static_cast<float>(static_cast<int>((codes >> (4 * i)) & 15u) - 8);
+    }
+};
 
 // Which of a token's vectors a group of the reading kernel takes.  False: nothing to
 // do.  A warp's groups take the same share of neighbouring tokens, so that they walk
@@ -384,7 +496,7 @@ __device__ __forceinline__ bool group_work(const TokenParams& p, int heads, int*
 template <int D, typename T, typename TC>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 5) token_write_kernel(const TokenParams p) {
     constexpr int L = D / 8, kGroups = 32 / L;
-    constexpr bool kCache = !std::is_void<TC>::value;
+    constexpr bool kCache = !std::is_void<TC>::value, kInt4 = std::is_same<TC, Int4>::value;
     static_assert(kGroups * (D / 2) == kThreads, "one angle a thread");
     __shared__ __align__(16) float cos_s[kThreads], sin_s[kThreads];
     wait_primary();
@@ -435,19 +547,25 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 5) token_write_
         });
     }
     if (h1 <= p.Hq) return;
-    int64_t place = 0;
+    int64_t place = 0, steps = 0;
     if constexpr (kCache) {
-        place = cache_place(p, t, row, pos);
+        place = cache_place(p, t, row, pos, kInt4 ? &steps : nullptr);
         if (place < 0) return;
     }
     if (h0 < kend) {
         float w[8];
         if (p.norm) load_weight<D>(p, p.kw, c, w);
+        Partner mate;
+        if constexpr (kInt4) mate = make_partner(p, c);
         walk_runs<T>(p, p.k, t, c, max(h0 - p.Hq, 0), min(h1 - p.Hq, p.Hkv), [&](int h, float (&f)[8]) {
             norm_rotate<L>(p, c, cs, sn, w, f, mask);
             if constexpr (!kCache) {
                 if (!vector_in(p.ko, t, h, c.a, 4, p.err) || !vector_in(p.ko, t, h, c.b, 4, p.err)) return;
                 store_runs(static_cast<T*>(p.ko.data) + t * p.ko.st + h * p.ko.sh, c, f);
+            } else if constexpr (kInt4) {
+                if (!cache_in(p, place, h, 0, D / 2) || !step_in(p, steps, h, D - 1)) return;
+                to_codes<TC>(p.ks, h, f);
+                store_runs_int4<L>(p, c, mate, f, static_cast<uint8_t*>(p.kc) + place + h * p.ch, static_cast<uint8_t*>(p.kst) + steps + h * p.sth, mask);
             } else {
                 if (!cache_in(p, place, h, c.a, 4) || !cache_in(p, place, h, c.b, 4)) return;
                 to_codes<TC>(p.ks, h, f);
@@ -462,9 +580,18 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 5) token_write_
             static_cast<const T*>(p.v.data) + t * p.v.st + ch, p.v.sh, max(h0 - kend, 0), h1 - kend,
             [&](int h) { return vector_in(p.v, t, h, ch, 8, p.err); },
             [&](int h, float (&f)[8]) {
-                if (!cache_in(p, place, h, ch, 8)) return;
-                to_codes<TC>(p.vs, h, f);
-                store8(static_cast<TC*>(p.vc) + place + h * p.ch + ch, f);
+                if constexpr (kInt4) {
+                    if (!cache_in(p, place, h, 0, D / 2) || !step_in(p, steps, h, D - 1)) return;
+                    to_codes<TC>(p.vs, h, f);
+                    const float top = max_nan(top4(f), top4(f + 4));
+                    const Step s = make_step(max_nan(top, __shfl_xor_sync(mask, top, 1)));
+                    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.vc) + place + h * p.ch + ch / 2) = int4_codes(f, s) | int4_codes(f + 4, s) << 16;
+                    if (ch % 16 == 0) static_cast<uint8_t*>(p.vst)[steps + h * p.sth + ch / 16] = static_cast<uint8_t>(s.code);
+                } else {
+                    if (!cache_in(p, place, h, ch, 8)) return;
+                    to_codes<TC>(p.vs, h, f);
+                    store8(static_cast<TC*>(p.vc) + place + h * p.ch + ch, f);
+                }
             });
     }
 }
@@ -480,8 +607,10 @@ __global__ void __launch_bounds__(kThreads) token_read_kernel(const TokenParams 
     const int pos = p.positions[t];
     const int row = p.rows ? p.rows[t] : t;
     if (pos < 0 || row < 0) return;  // a padding token
+    constexpr bool kInt4 = std::is_same<TC, Int4>::value;
     const int ch = 8 * ((threadIdx.x & 31) % L);
-    const int64_t place = cache_place(p, t, row, pos);
+    int64_t steps = 0;
+    const int64_t place = cache_place(p, t, row, pos, kInt4 ? &steps : nullptr);
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
         const int a = max(h0 - kv * p.Hkv, 0), b = min(h1 - kv * p.Hkv, p.Hkv);
@@ -496,16 +625,33 @@ __global__ void __launch_bounds__(kThreads) token_read_kernel(const TokenParams 
                 if (vector_in(out, t, h, ch, 8, p.err)) store8(dst + h * out.sh, f);
             continue;
         }
-        walk_whole(
-            static_cast<const TC*>(kv ? p.vc : p.kc) + place + ch, p.ch, a, b, [&](int h) { return cache_in(p, place, h, ch, 8); },
-            [&](int h, float (&f)[8]) {
-                if constexpr (std::is_same<TC, __nv_fp8_e4m3>::value) {
-                    const float sc = __ldg(scale + h);
+        auto put = [&](int h, float (&f)[8]) {
+            if (std::is_same<TC, __nv_fp8_e4m3>::value || (kInt4 && scale)) {
+                const float sc = __ldg(scale + h);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] *= sc;
-                }
-                if (vector_in(out, t, h, ch, 8, p.err)) store8(dst + h * out.sh, f);
-            });
+                for (int i = 0; i < 8; ++i) f[i] *= sc;
+            }
+            if (vector_in(out, t, h, ch, 8, p.err)) store8(dst + h * out.sh, f);
+        };
+        if constexpr (kInt4) {
+            const uint8_t* codes = static_cast<const uint8_t*>(kv ? p.vc : p.kc) + place + ch / 2;
+            const uint8_t* step = static_cast<const uint8_t*>(kv ? p.vst : p.kst) + steps + ch / 16;
+            walk_heads<Eight4>(
+                a, b,
+                [&](Eight4& e, int h) {
+                    if (!cache_in(p, place, h, ch / 2, 4) || !step_in(p, steps, h, ch)) return;
+                    e.codes = *reinterpret_cast<const uint32_t*>(codes + h * p.ch);
+                    e.step = step[h * p.sth];
+                },
+                [&](const Eight4& e, int h) {
+                    float f[8];
+                    e.unpack(f);
+                    put(h, f);
+                });
+        } else {
+            walk_whole(
+                static_cast<const TC*>(kv ? p.vc : p.kc) + place + ch, p.ch, a, b, [&](int h) { return cache_in(p, place, h, ch, 8); }, put);
+        }
     }
 }
 
@@ -564,6 +710,7 @@ cudaError_t launch_write(int cache, const TokenParams& p, int64_t tile, cudaStre
         case TA_F32: return launch(token_write_kernel<D, T, float>, p, D, tile, s);
         case TA_BF16: return launch(token_write_kernel<D, T, __nv_bfloat16>, p, D, tile, s);
         case TA_E4M3: return launch(token_write_kernel<D, T, __nv_fp8_e4m3>, p, D, tile, s);
+        case TA_INT4: return launch(token_write_kernel<D, T, Int4>, p, D, tile, s);
         default: return launch(token_write_kernel<D, T, void>, p, D, tile, s);
     }
 }
@@ -573,6 +720,7 @@ cudaError_t launch_read(int cache, const TokenParams& p, cudaStream_t s) {
     switch (cache) {
         case TA_F32: return launch(token_read_kernel<D, T, float>, p, D, p.chunks, s);
         case TA_BF16: return launch(token_read_kernel<D, T, __nv_bfloat16>, p, D, p.chunks, s);
+        case TA_INT4: return launch(token_read_kernel<D, T, Int4>, p, D, p.chunks, s);
         default: return launch(token_read_kernel<D, T, __nv_fp8_e4m3>, p, D, p.chunks, s);
     }
 }
@@ -624,6 +772,50 @@ int check_scales(const ta_shape* s, const float* ks, const float* vs) {
     return aligned_to(ks, 4) && aligned_to(vs, 4) ? TA_OK : TA_ERR_ALIGN;
 }
 
+// The tokens and pages that writing and reading a cache share, once its layout is known.
+int check_places(const ta_shape* shape, const ta_paged_kv* paged, const ta_tokens* tokens, int page_shift, TokenParams* p) {
+    const int rc = check_tokens(tokens);
+    if (rc != TA_OK) return rc;
+    if (!tokens->rows && tokens->num_tokens > shape->batch) return TA_ERR_SHAPE;
+    p->positions = tokens->positions;
+    p->rows = tokens->rows;
+    p->T = tokens->num_tokens;
+    p->Hkv = shape->num_kv_heads;
+    p->B = shape->batch;
+    p->S = shape->max_seqlen;
+    if (paged) {
+        p->table_elems = static_cast<size_t>(p->B) * paged->max_pages_per_seq;
+        p->block_table = paged->block_table;
+        p->max_pages = paged->max_pages_per_seq;
+        p->page_shift = page_shift;
+        p->num_pages = paged->num_pages;
+    }
+    return TA_OK;
+}
+
+// The same for a 4-bit cache.
+int check_int4_call(const ta_shape* shape, const ta_paged_kv* paged, const ta_tokens* tokens, const ta_int4_kv* cache, TokenParams* p) {
+    Int4Layout lay;
+    int rc = int4_layout(shape, paged, cache, &lay);
+    if (rc != TA_OK) return rc;
+    if ((rc = check_places(shape, paged, tokens, lay.page_shift, p)) != TA_OK) return rc;
+    p->kc = cache->k_codes;
+    p->vc = cache->v_codes;
+    p->kst = cache->k_steps;
+    p->vst = cache->v_steps;
+    p->cb = lay.code_b;
+    p->ch = lay.code_h;
+    p->ct = lay.code_t;
+    p->stb = lay.step_b;
+    p->sth = lay.step_h;
+    p->stt = lay.step_t;
+    p->cache_elems = lay.code_bytes;
+    p->step_bytes = lay.step_bytes;
+    p->ks = cache->k_scale;
+    p->vs = cache->v_scale;
+    return TA_OK;
+}
+
 // The parts that writing and reading a cache share.
 int check_cache_call(const ta_shape* shape, const ta_paged_kv* paged, const ta_tokens* tokens, const void* kc,
                      const void* vc, const float* ks, const float* vs, TokenParams* p) {
@@ -634,29 +826,16 @@ int check_cache_call(const ta_shape* shape, const ta_paged_kv* paged, const ta_t
     if (!kc || !vc) return TA_ERR_NULL;
     if (!aligned_to(kc, 16) || !aligned_to(vc, 16)) return TA_ERR_ALIGN;
     if ((rc = check_scales(shape, ks, vs)) != TA_OK) return rc;
-    if (!tokens->rows && tokens->num_tokens > shape->batch) return TA_ERR_SHAPE;
+    if ((rc = check_places(shape, paged, tokens, lay.page_shift, p)) != TA_OK) return rc;
     p->kc = const_cast<void*>(kc);
     p->vc = const_cast<void*>(vc);
     p->cb = lay.stride_b;
     p->ch = lay.stride_h;
     p->ct = lay.stride_t;
-    p->positions = tokens->positions;
-    p->rows = tokens->rows;
     p->ks = ks;
     p->vs = vs;
-    p->T = tokens->num_tokens;
-    p->Hkv = shape->num_kv_heads;
-    p->B = shape->batch;
-    p->S = shape->max_seqlen;
     p->cache_elems = static_cast<size_t>(((paged ? paged->num_pages : p->B) - 1) * lay.stride_b + (p->Hkv - 1) * lay.stride_h +
                                          ((paged ? paged->page_size : p->S) - 1) * lay.stride_t + shape->head_dim);
-    if (paged) {
-        p->table_elems = static_cast<size_t>(p->B) * paged->max_pages_per_seq;
-        p->block_table = paged->block_table;
-        p->max_pages = paged->max_pages_per_seq;
-        p->page_shift = lay.page_shift;
-        p->num_pages = paged->num_pages;
-    }
     return TA_OK;
 }
 
@@ -724,6 +903,73 @@ extern "C" int tree_attn_norm_rope(const ta_shape* shape, const ta_tokens* token
     return enqueue(shape, &p, p.Hq + p.Hkv, -1, false, stream);
 }
 
+namespace ta {
+
+int int4_layout(const ta_shape* shape, const ta_paged_kv* paged, const ta_int4_kv* cache, Int4Layout* out) {
+    if (!shape || !cache) return TA_ERR_NULL;
+    if (shape->kv_dtype != TA_INT4) return TA_ERR_DTYPE;
+    if (shape->kv_stride_b != 0 || shape->kv_stride_h != 0 || shape->kv_stride_t != 0) return TA_ERR_SHAPE;
+    ta_shape like = *shape;  // sizes, types and pages as for a dense cache of another type
+    like.kv_dtype = TA_BF16;
+    CacheLayout lay;
+    const int rc = cache_layout(&like, paged, &lay);
+    if (rc != TA_OK) return rc;
+    if (!cache->k_codes || !cache->v_codes || !cache->k_steps || !cache->v_steps) return TA_ERR_NULL;
+    if ((cache->k_scale == nullptr) != (cache->v_scale == nullptr)) return TA_ERR_NULL;
+    const int64_t code = shape->head_dim / 2, step = shape->head_dim / 16, lim = int64_t(1) << 40;
+    if (!aligned_to(cache->k_codes, 16) || !aligned_to(cache->v_codes, 16) || !aligned_to(cache->k_steps, step) ||
+        !aligned_to(cache->v_steps, step) || !aligned_to(cache->k_scale, 4) || !aligned_to(cache->v_scale, 4))
+        return TA_ERR_ALIGN;
+    const int64_t given[6] = {cache->code_stride_b, cache->code_stride_h, cache->code_stride_t,
+                              cache->step_stride_b, cache->step_stride_h, cache->step_stride_t};
+    int64_t r[6];
+    for (int part = 0; part < 2; ++part) {
+        const int64_t *x = given + 3 * part, unit = part ? step : code;
+        int64_t* y = r + 3 * part;
+        if (x[0] == 0 && x[1] == 0 && x[2] == 0) {  // (lay: the same layout in elements)
+            y[0] = lay.stride_b / shape->head_dim * unit;
+            y[1] = lay.stride_h / shape->head_dim * unit;
+            y[2] = lay.stride_t / shape->head_dim * unit;
+        } else {
+            for (int i = 0; i < 3; ++i) {
+                if (x[i] <= 0 || x[i] >= lim) return TA_ERR_SHAPE;
+                if (x[i] % (part ? step : 16) != 0) return TA_ERR_ALIGN;
+                y[i] = x[i];
+            }
+        }
+    }
+    out->code_b = r[0], out->code_h = r[1], out->code_t = r[2];
+    out->step_b = r[3], out->step_h = r[4], out->step_t = r[5];
+    out->page_shift = lay.page_shift;
+    const int64_t nb = (paged ? paged->num_pages : shape->batch) - 1, nt = (paged ? paged->page_size : shape->max_seqlen) - 1,
+                  nh = shape->num_kv_heads - 1;
+    out->code_bytes = static_cast<size_t>(nb * r[0] + nh * r[1] + nt * r[2] + code);
+    out->step_bytes = static_cast<size_t>(nb * r[3] + nh * r[4] + nt * r[5] + step);
+    return TA_OK;
+}
+
+namespace {
+
+// Vectors and rotation of a cache write, and its launch.
+int enqueue_write(const ta_shape* shape, const ta_tokens* tokens, const ta_rope* rope, const ta_heads* q, const ta_heads* q_out,
+                  const ta_heads* k, const ta_heads* v, TokenParams* p, void* stream) {
+    int rc;
+    if ((q == nullptr) != (q_out == nullptr)) return TA_ERR_NULL;
+    if (q && !rope) return TA_ERR_SHAPE;  // without a norm or rotation there is nothing to do for queries
+    if (rope && (rc = check_rope(rope, shape->head_dim, p)) != TA_OK) return rc;
+    if ((rc = check_heads(k, shape->q_dtype, tokens, &p->k)) != TA_OK) return rc;
+    if ((rc = check_heads(v, shape->q_dtype, tokens, &p->v)) != TA_OK) return rc;
+    if (q) {
+        if ((rc = check_heads(q, shape->q_dtype, tokens, &p->q)) != TA_OK) return rc;
+        if ((rc = check_heads(q_out, shape->q_dtype, tokens, &p->qo)) != TA_OK) return rc;
+        p->Hq = shape->num_q_heads;
+    }
+    return enqueue(shape, p, p->Hq + 2 * p->Hkv, shape->kv_dtype, false, stream);
+}
+
+}  // namespace
+}  // namespace ta
+
 extern "C" int tree_attn_cache_write(const ta_shape* shape, const ta_paged_kv* paged, const ta_tokens* tokens,
                                      const ta_rope* rope, const ta_heads* q, const ta_heads* q_out,
                                      const ta_heads* k, const ta_heads* v, void* k_cache, void* v_cache,
@@ -733,17 +979,7 @@ extern "C" int tree_attn_cache_write(const ta_shape* shape, const ta_paged_kv* p
     std::memset(&p, 0, sizeof p);
     int rc = check_cache_call(shape, paged, tokens, k_cache, v_cache, k_scale, v_scale, &p);
     if (rc != TA_OK) return rc;
-    if ((q == nullptr) != (q_out == nullptr)) return TA_ERR_NULL;
-    if (q && !rope) return TA_ERR_SHAPE;  // without a norm or rotation there is nothing to do for queries
-    if (rope && (rc = check_rope(rope, shape->head_dim, &p)) != TA_OK) return rc;
-    if ((rc = check_heads(k, shape->q_dtype, tokens, &p.k)) != TA_OK) return rc;
-    if ((rc = check_heads(v, shape->q_dtype, tokens, &p.v)) != TA_OK) return rc;
-    if (q) {
-        if ((rc = check_heads(q, shape->q_dtype, tokens, &p.q)) != TA_OK) return rc;
-        if ((rc = check_heads(q_out, shape->q_dtype, tokens, &p.qo)) != TA_OK) return rc;
-        p.Hq = shape->num_q_heads;
-    }
-    return enqueue(shape, &p, p.Hq + 2 * p.Hkv, shape->kv_dtype, false, stream);
+    return enqueue_write(shape, tokens, rope, q, q_out, k, v, &p, stream);
 }
 
 extern "C" int tree_attn_cache_read(const ta_shape* shape, const ta_paged_kv* paged, const ta_tokens* tokens,
@@ -754,6 +990,29 @@ extern "C" int tree_attn_cache_read(const ta_shape* shape, const ta_paged_kv* pa
     TokenParams p;
     std::memset(&p, 0, sizeof p);
     int rc = check_cache_call(shape, paged, tokens, k_cache, v_cache, k_scale, v_scale, &p);
+    if (rc != TA_OK) return rc;
+    if ((rc = check_heads(k_out, shape->q_dtype, tokens, &p.ko)) != TA_OK) return rc;
+    if ((rc = check_heads(v_out, shape->q_dtype, tokens, &p.vo)) != TA_OK) return rc;
+    return enqueue(shape, &p, 2 * p.Hkv, shape->kv_dtype, true, stream);
+}
+
+extern "C" int tree_attn_cache_write_int4(const ta_shape* shape, const ta_paged_kv* paged, const ta_tokens* tokens,
+                                          const ta_rope* rope, const ta_heads* q, const ta_heads* q_out,
+                                          const ta_heads* k, const ta_heads* v, const ta_int4_kv* cache, void* stream) {
+    using namespace ta;
+    TokenParams p;
+    std::memset(&p, 0, sizeof p);
+    const int rc = check_int4_call(shape, paged, tokens, cache, &p);
+    if (rc != TA_OK) return rc;
+    return enqueue_write(shape, tokens, rope, q, q_out, k, v, &p, stream);
+}
+
+extern "C" int tree_attn_cache_read_int4(const ta_shape* shape, const ta_paged_kv* paged, const ta_tokens* tokens,
+                                         const ta_int4_kv* cache, const ta_heads* k_out, const ta_heads* v_out, void* stream) {
+    using namespace ta;
+    TokenParams p;
+    std::memset(&p, 0, sizeof p);
+    int rc = check_int4_call(shape, paged, tokens, cache, &p);
     if (rc != TA_OK) return rc;
     if ((rc = check_heads(k_out, shape->q_dtype, tokens, &p.ko)) != TA_OK) return rc;
     if ((rc = check_heads(v_out, shape->q_dtype, tokens, &p.vo)) != TA_OK) return rc;
