@@ -18,8 +18,9 @@
 // word of eight codes into FP16 numbers: (w & 0x000f000f) | 0x64006400 is the pair
 // 1024 + code of channels 0 and 4, and one FMA with step / 8 and -1032 step / 8 makes step / 8 *
 // (code - 8) of it, exactly: both constants have at most 11 significant bits (1032 = 8 * 129, times
-// the 4 bits of an E4M3 number), and so has the result.  The odd codes come as 1024 + 16 code
-// (mask 0x00f000f0) with step / 128 and -72 step / 8.  So the tensor cores multiply exact values.
+// the 4 bits of an E4M3 number), and so has the result.  The odd codes come as 1024 + 16 code (mask
+// 0x00f000f0) and, with -1152 step / 8, as 16 times their value, which q's odd channels and the
+// outputs' undo.  So the tensor cores multiply exact values.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -27,6 +28,7 @@
 #include <cmath>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "host.h"
@@ -77,10 +79,9 @@ struct Span {
     __device__ __forceinline__ int token(int u) const { return (u < head ? u : u - head + first) << 4; }
 };
 
-// Places of a warp's slabs, 32 at a time, one a lane: first token (-1: no slab) and byte offsets.
+// Places of a warp's slabs, 32 at a time, one a lane: byte offsets (0 for a bad page: its row is NaN in the end).
 struct Slab {
     int64_t off, steps;
-    int t0;
 };
 
 struct SpanList {
@@ -104,31 +105,39 @@ struct SpanList {
         const int i = i0 + lane;
         if (i >= n) return -1;
         if (!table) return b;
-        const int page = span.token(u + i * W) >> p.page_shift;
+        const int page = token(i) >> p.page_shift;
         return in_bounds(table - p.block_table + page, p.table_elems, p.err) ? __ldg(table + page) : -1;
     }
     // its place, once the page has arrived
     __device__ __forceinline__ Slab place(int i0, int page) {
         Slab s;
         s.off = s.steps = 0;
-        s.t0 = -1;
         const int i = i0 + lane;
         if (i >= n) return s;
         if (table && (page < 0 || page >= p.num_pages)) {
             bad = 1;
             return s;
         }
-        s.t0 = span.token(u + i * W);
-        const int64_t slot = table ? s.t0 & ((1 << p.page_shift) - 1) : s.t0;
+        const int t0 = token(i);
+        const int64_t slot = table ? t0 & ((1 << p.page_shift) - 1) : t0;
         s.off = page * p.sb + g * p.sh + slot * p.st;
         s.steps = page * p.tb + g * p.th + slot * p.tt;
         return s;
     }
+    // first token of the warp's slab i (below n)
+    __device__ __forceinline__ int token(int i) const { return span.token(u + i * W); }
     // whether some query sees token t of one of its slabs
     __device__ __forceinline__ bool seen(int t) const { return t < span.N && (t >= span.lo || t < p.sinks); }
-    // whether every query sees all tokens of the slab
+    // whether every query sees all tokens of a slab
     __device__ __forceinline__ bool whole(int t0) const {
         return t0 + 15 <= span.N - p.nq && (t0 >= span.N - p.window || t0 + 15 < p.sinks);
+    }
+    // The warp's slabs [*a, *b) that every query sees all tokens of, without those among the sinks.
+    __device__ __forceinline__ void middle(int* a, int* b) const {
+        const int ua = ((max(0, span.N - p.window) + 15) >> 4) - span.first + span.head;
+        const int ub = (max(0, span.N - p.nq + 1) >> 4) - span.first + span.head;
+        *a = min(n, ua > u ? (ua - u + W - 1) / W : 0);
+        *b = min(n, ub > u ? (ub - u + W - 1) / W : 0);
     }
 };
 
@@ -171,31 +180,82 @@ __device__ void store_partial(const SpanParams& p, size_t row0, int ncol, float 
     }
 }
 
-// The partial states of a row become its outputs; one thread a channel.
+// The partial states of a row become its outputs: weights of up to kChunk states at a time in shared memory, then
+// numerators folded by groups of threads (a float4 each, eight loads in flight) and across the groups.
 template <int D>
-__global__ void __launch_bounds__(D) span_combine_kernel(const SpanParams p) {
+__global__ void __launch_bounds__(256) span_combine_kernel(const SpanParams p) {
+    constexpr int kThreads = 256, kLanes = D / 4, kGroups = kThreads / kLanes, kChunk = 256;
+    __shared__ float w_s[kChunk], red[2][kThreads / 32];
+    __shared__ float4 acc_s[kGroups][kLanes];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     wait_primary();
+    allow_dependents();
     const size_t row = blockIdx.x;
     const float2* ml = p.part_ml + row * p.P;
-    const float* o = p.part_o + row * p.P * D + threadIdx.x;
+    const float4* o = reinterpret_cast<const float4*>(p.part_o + row * p.P * D);
     float M = -INFINITY;
-    for (int i = 0; i < p.P; ++i) M = fmaxf(M, ml[i].x);
+    for (int i = tid; i < p.P; i += kThreads) M = fmaxf(M, ml[i].x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    if (lane == 0) red[0][warp] = M;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) M = fmaxf(M, red[0][i]);
     const float Ms = (M == -INFINITY) ? 0.f : M;
-    float L = 0.f, O = 0.f;
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int c4 = tid % kLanes, grp = tid / kLanes;
+    for (int first = 0; first < p.P; first += kChunk) {
+        const int n = min(kChunk, p.P - first);
+        if (first > 0) __syncthreads();
+        if (tid < n) {
+            const float2 s = ml[first + tid];
+            const float w = (s.x == -INFINITY) ? 0.f : ex2(s.x - Ms);
+            w_s[tid] = w;
+            L = fmaf(w, s.y, L);
+        }
+        __syncthreads();
 #pragma unroll 8
-    for (int i = 0; i < p.P; ++i) {
-        const float2 s = ml[i];
-        const float w = (s.x == -INFINITY) ? 0.f : ex2(s.x - Ms);
-        L = fmaf(w, s.y, L);
-        O = fmaf(w, o[static_cast<size_t>(i) * D], O);
+        for (int i = grp; i < n; i += kGroups) {
+            const float w = w_s[i];
+            const float4 v = o[static_cast<size_t>(first + i) * kLanes + c4];
+            acc.x = fmaf(w, v.x, acc.x);
+            acc.y = fmaf(w, v.y, acc.y);
+            acc.z = fmaf(w, v.z, acc.z);
+            acc.w = fmaf(w, v.w, acc.w);
+        }
     }
-    if (in_bounds(row * D + threadIdx.x, p.out_elems, p.err)) p.out[row * D + threadIdx.x] = (L == 0.f) ? 0.f : O / L;
-    if (threadIdx.x == 0 && p.lse && in_bounds(row, p.rows, p.err)) p.lse[row] = (L == 0.f) ? -INFINITY : (M + log2f(L)) * kLn2;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+    if (lane == 0) red[1][warp] = L;
+    acc_s[grp][c4] = acc;
+    __syncthreads();
+    if (tid >= kLanes) return;
+    L = 0.f;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) L += red[1][i];
+    acc = acc_s[0][c4];
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) {
+        const float4 v = acc_s[i][c4];
+        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+    }
+    acc = L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(acc.x / L, acc.y / L, acc.z / L, acc.w / L);
+    if (in_bounds(row * D + 4 * c4 + 3, p.out_elems, p.err)) reinterpret_cast<float4*>(p.out + row * D)[c4] = acc;
+    if (tid == 0 && p.lse && in_bounds(row, p.rows, p.err)) p.lse[row] = (L == 0.f) ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 // ------------------------------------------------------------ tensor cores
-template <int D, int NT, int kCache, int W, int kStages_>
+// How the columns of a block lie in the tensor cores' tiles of 8.
+enum Columns {
+    kHalf,  // up to 4 columns in one tile: its other half multiplies the weights' low parts (FP16 operands)
+    kOne,   // up to 8
+    kTwoTiles   // up to 16
+};
+
+template <int D, int kCache, int kLayout, int W, int kStages_>
 struct SpanCfg {
+    static constexpr int NT = kLayout == kTwoTiles ? 2 : 1;
     static constexpr int kRowBytes = kCache == kInt4 ? D / 2 : (kCache == kE4m3 ? D : 2 * D);
     static constexpr int kChunks = kRowBytes / 16;                                  // 16-byte chunks of a row
     static constexpr int kVRow = kCache == kInt4 ? kRowBytes + 16 : kRowBytes;      // (4-bit values: rows apart in the banks)
@@ -207,14 +267,20 @@ struct SpanCfg {
     static constexpr int kSub = kCache == kBf16 ? 1 : 2;                            // slabs that a warp takes together
     static constexpr int kStageBytes = kSub * kPairBytes;
     static constexpr int kWarps = W, kThreads = 32 * W, kStages = kStages_;
-    static constexpr int kCols = 8 * NT;
+    static constexpr int kCols = kLayout == kHalf ? 4 : 8 * NT;
     static constexpr int kRing = kWarps * kStages * kStageBytes;
-    static constexpr int kFlagOff = kRing + kWarps * kStages * kSub * 4;
-    static constexpr int kBoxOff = (kFlagOff + 4 + 15) / 16 * 16;
+    static constexpr int kBoxOff = kRing + 16;                                      // (a flag between them)
     static constexpr int kSmem = kBoxOff + static_cast<int>(sizeof(Mailbox<D, kCols>));
     static_assert(kWarps * kCols * (D + 4 + 2) * 4 <= kRing, "merge buffers reuse the ring");
     static_assert(kStages >= 2 && kSmem <= 227 * 1024, "ring");
 };
+
+// Blocks an SM that the registers are limited for.
+template <int D, int kCache, int kLayout, bool kMulti>
+constexpr int span_blocks() {
+    if (kLayout == kTwoTiles) return 2;
+    return kMulti ? 2 : (kCache == kInt4 ? 3 : 2);
+}
 
 __device__ __forceinline__ uint32_t hfma2_bits(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t d;
@@ -226,21 +292,42 @@ __device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-// (w & mask) | magic
-__device__ __forceinline__ uint32_t pick_codes(uint32_t w, uint32_t mask) { return (w & mask) | 0x64006400u; }
+// (w & mask) | magic in one instruction (written as such, the compiler makes two of it)
+__device__ __forceinline__ uint32_t pick_codes(uint32_t w, uint32_t mask, uint32_t magic) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(w), "r"(mask), "r"(magic));
+    return d;
+}
 
-// Factors that turn pairs of codes into step / 8 * (code - 8), for a pair of steps (FP16).
+// Factors that turn pairs of codes into step / 8 * (code - 8) where they lie in the low four bits of
+// their byte, and into 16 times that where in the high ones (whose other operand, a query or the
+// finished output, takes the 1/16): 1024 + code and 1024 + 16 code, times step / 8, less 1032 and
+// 1152 (9 * 128) times it.
 struct Unpack {
-    uint32_t lo, lo_add, hi, hi_add;  // codes in the low, high four bits of their byte
+    uint32_t mul, lo_add, hi_add;
+    // for a pair of steps (FP16)
     __device__ __forceinline__ explicit Unpack(uint32_t steps) {
-        lo = hmul2_bits(steps, 0x30003000u);          // 2^-3
-        lo_add = hmul2_bits(lo, 0xe408e408u);         // -1032
-        hi = hmul2_bits(steps, 0x20002000u);          // 2^-7
-        hi_add = hmul2_bits(lo, 0xd480d480u);         // -72
+        mul = hmul2_bits(steps, 0x30003000u);          // 2^-3
+        lo_add = hmul2_bits(mul, 0xe408e408u);         // -1032
+        hi_add = hmul2_bits(mul, 0xe480e480u);         // -1152
+    }
+    // both halves those of the low or of the high one of the given pair
+    __device__ __forceinline__ Unpack(const Unpack& u, bool high) {
+        mul = both(u.mul, high);
+        lo_add = both(u.lo_add, high);
+        hi_add = both(u.hi_add, high);
+    }
+    static __device__ __forceinline__ uint32_t both(uint32_t x, bool high) {
+        uint32_t d;
+        if (high)
+            asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; mov.b32 %0, {h, h};}" : "=r"(d) : "r"(x));
+        else
+            asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; mov.b32 %0, {l, l};}" : "=r"(d) : "r"(x));
+        return d;
     }
     // channels i and i + 4 of eight (i = 0, 1) of the word's bytes; shift the word by 8 for i = 2, 3
-    __device__ __forceinline__ uint32_t even(uint32_t w) const { return hfma2_bits(pick_codes(w, 0x000f000fu), lo, lo_add); }
-    __device__ __forceinline__ uint32_t odd(uint32_t w) const { return hfma2_bits(pick_codes(w, 0x00f000f0u), hi, hi_add); }
+    __device__ __forceinline__ uint32_t even(uint32_t w) const { return hfma2_bits(pick_codes(w, 0x000f000fu, 0x64006400u), mul, lo_add); }
+    __device__ __forceinline__ uint32_t odd(uint32_t w) const { return hfma2_bits(pick_codes(w, 0x00f000f0u, 0x64006400u), mul, hi_add); }
 };
 
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
@@ -268,14 +355,23 @@ __device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, in
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes) : "memory");
 }
 
-template <int D, int NT, int kCache, int W, int kStages_>
-__global__ void __launch_bounds__(32 * W) decode_span_kernel(const SpanParams p) {
-    using Cf = SpanCfg<D, NT, kCache, W, kStages_>;
-    constexpr int J = Cf::kSub, kWarps = W, kStages = Cf::kStages;
+// A column's running maximum is raised when a logit passes it by more than this (log2 units):
+// weights stay below 2^4, and most steps need neither the maximum over the lanes nor a
+// rescaling of the state.
+constexpr float kSlack = 4.f;
+constexpr float kWeightBits = 11.f;     // FP16 weights times 2^11: below 2^15, and a low part's last bit is 2^-35
+
+// kMulti: several queries a row (masks that differ between columns).
+template <int D, int kCache, int kLayout, bool kMulti, int W, int kStages_>
+__global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti>()) decode_span_kernel(const SpanParams p) {
+    using Cf = SpanCfg<D, kCache, kLayout, W, kStages_>;
+    constexpr int J = Cf::kSub, kWarps = W, kStages = Cf::kStages, NT = Cf::NT;
     constexpr bool kTwo = kCache != kBf16;   // FP16 operands: weights in two parts
+    constexpr bool kHalves = kLayout == kHalf;
+    static_assert(!kHalves || (kTwo && !kMulti), "low parts beside the high ones");
+    const int nq = kMulti ? p.nq : 1;
     extern __shared__ __align__(128) uint8_t smem[];
-    int* t0s_all = reinterpret_cast<int*>(smem + Cf::kRing);
-    int* bad_flag = reinterpret_cast<int*>(smem + Cf::kFlagOff);
+    int* bad_flag = reinterpret_cast<int*>(smem + Cf::kRing);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gid = lane >> 2, tig = lane & 3, r8 = lane & 7;
@@ -303,7 +399,7 @@ __global__ void __launch_bounds__(32 * W) decode_span_kernel(const SpanParams p)
     uint32_t qb[NT][D / 16][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int c = nt * 8 + gid;
+        const int c = nt * 8 + (kHalves ? gid & 3 : gid);
         const bool on = c < ncol && in_bounds((row0 + c + 1) * D - 1, p.q_elems, p.err);
         const __nv_bfloat16* qh = static_cast<const __nv_bfloat16*>(p.q) + (row0 + (on ? c : 0)) * D;
         if constexpr (kCache == kInt4) {
@@ -336,7 +432,7 @@ __global__ void __launch_bounds__(32 * W) decode_span_kernel(const SpanParams p)
             m[nt][i] = -INFINITY;
             l[nt][i] = 0.f;
             sl2[nt][i] = p.scale_log2;
-            col_query[nt][i] = (c_first + nt * 8 + 2 * tig + i) % p.nq;
+            col_query[nt][i] = kMulti ? (c_first + nt * 8 + 2 * tig + i) % nq : 0;
         }
 #pragma unroll
         for (int mt = 0; mt < D / 16; ++mt)
@@ -344,55 +440,79 @@ __global__ void __launch_bounds__(32 * W) decode_span_kernel(const SpanParams p)
     }
 
     const uint32_t ring = smem_u32(smem) + warp * kStages * Cf::kStageBytes;
-    volatile int* t0s = t0s_all + warp * kStages * J;
     Slab win = list.place(0, e_next), win_next = win;
     // this lane's share of a slab's copies: chunk c_chunk of rows c_row, c_row + kRowsAtOnce, ..
     constexpr int kRowsAtOnce = 32 / Cf::kChunks;
     const int c_row = lane / Cf::kChunks, c_chunk = lane % Cf::kChunks;
+    const int64_t src_lane = c_row * p.st + c_chunk * 16, row_step = kRowsAtOnce * p.st;
+    const uint32_t slot_lane = ring + c_row * Cf::kRowBytes + (c_chunk << 4);
+    const uint32_t v_skew = Cf::kVOff + c_row * (Cf::kVRow - Cf::kRowBytes);
+    const uint8_t* step_base = lane < 16 ? p.k_steps : p.v_steps;
+    const int64_t step_lane = (lane & 15) * p.tt;
+    const uint32_t step_slot = ring + (lane < 16 ? Cf::kKStep : Cf::kVStep) + (lane & 15) * Cf::kStepRow;
 
-    // Start the copies of the warp's slabs i J .. into stage i % kStages (one group).
+    // iterations [it_a, it_b): slabs that every query sees whole, which need no masks and no checks of their rows
+    int it_a, it_b;
+    list.middle(&it_a, &it_b);
+    it_a = (it_a + J - 1) / J;
+    it_b = it_b / J;
+    const uint8_t *k_ptr = p.k + src_lane, *v_ptr = p.v + src_lane, *step_ptr = step_base + step_lane;
+
+    // Start the copies of the warp's slabs i J .. into the next stage (one group).  A slab that is not there
+    // (beside one that is) is zero-filled.
+    uint32_t stage_in = 0;  // bytes from the ring's start
     auto issue = [&](int i) {
-#pragma unroll
-        for (int sub = 0; sub < J; ++sub) {
-            const int s = i * J + sub, slot = (i % kStages) * J + sub;
-            if (s >= list.n) {
-                if (lane == 0 && in_bounds(slot, kStages * J, p.err)) t0s[slot] = -1;
-                continue;
+        if (i < n_it) {
+            const int s0 = i * J, j0 = s0 & 31;
+            if (j0 == 0) {
+                if (i > 0) win = win_next;
+                e_next = list.entry(s0 + 32);
             }
-            const int j = s & 31;
-            if (j == 0 && s > 0) win = win_next;
-            if (j == 0) e_next = list.entry(s + 32);
-            if (j == 16) win_next = list.place(s + 16, e_next);
-            const int t0 = __shfl_sync(0xffffffffu, win.t0, j);
-            const int64_t off = __shfl_sync(0xffffffffu, win.off, j);
-            if (lane == 0 && in_bounds(slot, kStages * J, p.err)) t0s[slot] = t0;
-            int64_t steps = 0;
-            if constexpr (kCache == kInt4) steps = __shfl_sync(0xffffffffu, win.steps, j);
-            if (t0 >= 0) {
-                const uint32_t base = ring + slot * Cf::kPairBytes;
+            if (j0 == 16) win_next = list.place(s0 + 16, e_next);
+            int64_t off[J], steps[J];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                off[j] = __shfl_sync(0xffffffffu, win.off, j0 + j);
+                steps[j] = 0;
+                if constexpr (kCache == kInt4) steps[j] = __shfl_sync(0xffffffffu, win.steps, j0 + j);
+            }
+            // copy(slab, row -> whether it is copied)
+            auto copy = [&](int j, auto&& row) {
+                const uint32_t base = slot_lane + stage_in + j * Cf::kPairBytes;
 #pragma unroll
                 for (int x = 0; x < kSlab / kRowsAtOnce; ++x) {
                     const int r = x * kRowsAtOnce + c_row;
-                    const int bytes = list.seen(t0 + r) ? 16 : 0;
-                    const int64_t o = off + r * p.st + c_chunk * 16;
-                    const int chunk = kCache == kInt4 ? c_chunk : c_chunk ^ (r & 7);  // (swizzled against bank conflicts)
-                    const uint32_t dk = base + r * Cf::kRowBytes + (chunk << 4), dv = base + Cf::kVOff + r * Cf::kVRow + (chunk << 4);
-                    if (!bytes_in(o, bytes, p.cache_bytes, p.err) || !in_bounds(dv + 15 - smem_u32(smem), Cf::kRing, p.err)) continue;
-                    cp_async16(dk, p.k + (bytes ? o : 0), bytes);
-                    cp_async16(dv, p.v + (bytes ? o : 0), bytes);
+                    const bool on = row(r);
+                    const int64_t o = on ? off[j] + x * row_step : -src_lane;
+                    // (BF16, E4M3: chunks swizzled by their row against bank conflicts)
+                    const uint32_t sw = kCache == kInt4 ? 0u : ((c_chunk ^ (r & 7)) << 4) - (c_chunk << 4);
+                    const uint32_t dk = base + sw + x * kRowsAtOnce * Cf::kRowBytes, dv = base + v_skew + sw + x * kRowsAtOnce * Cf::kVRow;
+                    if (!bytes_in(o + src_lane, on ? 16 : 0, p.cache_bytes, p.err) || !in_bounds(dv + 15 - smem_u32(smem), Cf::kRing, p.err)) continue;
+                    cp_async16(dk, k_ptr + o, on ? 16 : 0);
+                    cp_async16(dv, v_ptr + o, on ? 16 : 0);
                 }
                 if constexpr (kCache == kInt4) {
                     constexpr int SR = Cf::kStepRow;
-                    const int r = lane & 15;
-                    const int bytes = list.seen(t0 + r) ? SR : 0;
-                    const int64_t o = bytes ? steps + r * p.tt : 0;
-                    const uint32_t d = base + (lane < 16 ? Cf::kKStep : Cf::kVStep) + r * SR;
-                    if (bytes_in(o, bytes, p.step_bytes, p.err) && in_bounds(d + SR - 1 - smem_u32(smem), Cf::kRing, p.err))
-                        cp_async_small<SR>(d, (lane < 16 ? p.k_steps : p.v_steps) + o, bytes);
+                    const bool on = row(lane & 15);
+                    const int64_t o = on ? steps[j] : -step_lane;
+                    const uint32_t d = step_slot + stage_in + j * Cf::kPairBytes;
+                    if (bytes_in(o + step_lane, on ? SR : 0, p.step_bytes, p.err) && in_bounds(d + SR - 1 - smem_u32(smem), Cf::kRing, p.err))
+                        cp_async_small<SR>(d, step_ptr + o, on ? SR : 0);
+                }
+            };
+            if (i >= it_a && i < it_b) {
+#pragma unroll
+                for (int j = 0; j < J; ++j) copy(j, [](int) { return true; });
+            } else {
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const int t0 = list.token(s0 + j);
+                    copy(j, [&](int r) { return s0 + j < list.n && list.seen(t0 + r); });
                 }
             }
         }
         cp_async_commit();
+        stage_in = stage_in + Cf::kStageBytes == kStages * Cf::kStageBytes ? 0u : stage_in + Cf::kStageBytes;
     };
 
     // fragment addresses within a BF16 slab; chunk c of row r sits at chunk c ^ (r & 7)
@@ -412,7 +532,7 @@ __global__ void __launch_bounds__(32 * W) decode_span_kernel(const SpanParams p)
         auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
         auto hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
         const float ks = (p.k_scale ? __ldg(p.k_scale + g) : 1.f) * (kCache == kInt4 ? 8.f : 1.f);
-        vscale = (p.v_scale ? __ldg(p.v_scale + g) : 1.f) * ((kCache == kInt4 ? 8.f : 1.f) / kPScale);
+        vscale = (p.v_scale ? __ldg(p.v_scale + g) : 1.f) * (kCache == kInt4 ? 8.f : 1.f);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float amax = 0.f;
@@ -429,37 +549,44 @@ __global__ void __launch_bounds__(32 * W) decode_span_kernel(const SpanParams p)
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    qb[nt][kk][i] = half2_bits(__floats2half2_rn(lo(qb[nt][kk][i]) * qs, hi(qb[nt][kk][i]) * qs));
+                for (int i = 0; i < 2; ++i) {
+                    const float f = kCache == kInt4 && i == 1 ? qs * 0.0625f : qs;  // (the odd channels' keys come 16 times as large)
+                    qb[nt][kk][i] = half2_bits(__floats2half2_rn(lo(qb[nt][kk][i]) * f, hi(qb[nt][kk][i]) * f));
+                }
             const float back = __uint_as_float(static_cast<uint32_t>(127 - qexp) << 23);
-            sl2[nt][0] *= ks * __shfl_sync(0xffffffffu, back, 8 * tig);
+            sl2[nt][0] *= ks * __shfl_sync(0xffffffffu, back, 8 * tig);      // (column 2 tig is held by lanes 8 tig ..)
             sl2[nt][1] *= ks * __shfl_sync(0xffffffffu, back, 8 * tig + 4);
         }
     }
 
-    for (int it = 0; it < n_it; ++it) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) sl2[nt][i] = fmaxf(sl2[nt][i], 1e-37f);  // (0 times a masked logit would be NaN)
+
+    uint32_t stage_out = 0;
+    // kEdge: slabs at the window's ends, among the sinks, or not there
+    auto step = [&](int it, auto edge) {
+        constexpr bool kEdge = decltype(edge)::value;
         cp_async_wait<kStages - 2>();
         __syncwarp();  // the slab is in shared memory for every lane; every lane is done with the one before
         issue(it + kStages - 1);
         int t0[J];
         uint32_t kbase[J];
-        bool any = false, whole = true;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const int slot = (it % kStages) * J + j;
-            t0[j] = t0s[slot];
-            kbase[j] = ring + slot * Cf::kPairBytes;
-            any |= t0[j] >= 0;
-            whole = whole && t0[j] >= 0 && list.whole(t0[j]);
+            t0[j] = kEdge ? list.token(it * J + j) : 0;
+            kbase[j] = ring + stage_out + j * Cf::kPairBytes;
         }
-        if (!any) continue;  // (a missing slab beside one with tokens: masked below)
+        stage_out = stage_out + Cf::kStageBytes == kStages * Cf::kStageBytes ? 0u : stage_out + Cf::kStageBytes;
 
-        // S^T[16 tokens x columns] = K Q^T per slab, two accumulators per n-tile
-        float sacc[J][2][NT][4];
+        // S^T[16 tokens x columns] = K Q^T per slab (a slab taken alone: two accumulators per n-tile)
+        constexpr int kChains = J == 1 ? 2 : 1;
+        float sacc[J][kChains][NT][4];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < kChains; ++u)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -481,10 +608,10 @@ __global__ void __launch_bounds__(32 * W) decode_span_kernel(const SpanParams p)
                     sa = e4m3x2_to_f16x2(lds8(srow + tig));
                     sb = e4m3x2_to_f16x2(lds8(srow + tig + 8 * Cf::kStepRow));
                 }
+                const Unpack ra2(sa), rb2(sb);
 #pragma unroll
                 for (int blk = 0; blk < D / 64; ++blk) {  // 16 channels: two words
-                    const uint32_t sel = blk ? 0x3232u : 0x1010u;
-                    const Unpack ua(prmt(sa, sa, sel)), ub(prmt(sb, sb, sel));
+                    const Unpack ua(ra2, blk != 0), ub(rb2, blk != 0);
 #pragma unroll
                     for (int w = 2 * blk; w < 2 * blk + 2; ++w)
 #pragma unroll
@@ -492,7 +619,7 @@ __global__ void __launch_bounds__(32 * W) decode_span_kernel(const SpanParams p)
                             const uint32_t x = wa[w] >> (8 * h), y = wb[w] >> (8 * h);
                             const uint32_t a[4] = {ua.even(x), ub.even(y), ua.odd(x), ub.odd(y)};
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma_f16(sacc[j][h][nt], a, qb[nt][2 * w + h][0], qb[nt][2 * w + h][1]);
+                            for (int nt = 0; nt < NT; ++nt) mma_f16(sacc[j][h % kChains][nt], a, qb[nt][2 * w + h][0], qb[nt][2 * w + h][1]);
                         }
                 }
             } else if constexpr (kCache == kE4m3) {
@@ -506,7 +633,7 @@ __global__ void __launch_bounds__(32 * W) decode_span_kernel(const SpanParams p)
                     const uint32_t a[4] = {e4m3x2_to_f16x2(wa[kk] & 0xffffu), e4m3x2_to_f16x2(wb[kk] & 0xffffu),
                                            e4m3x2_to_f16x2(wa[kk] >> 16), e4m3x2_to_f16x2(wb[kk] >> 16)};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_f16(sacc[j][kk & 1][nt], a, qb[nt][kk][0], qb[nt][kk][1]);
+                    for (int nt = 0; nt < NT; ++nt) mma_f16(sacc[j][kk % kChains][nt], a, qb[nt][kk][0], qb[nt][kk][1]);
                 }
             } else {
 #pragma unroll
@@ -514,53 +641,83 @@ __global__ void __launch_bounds__(32 * W) decode_span_kernel(const SpanParams p)
                     uint32_t a[4];
                     ldsm_x4(a, kbase[j] + k_lane + (((2 * kk + k_chi) ^ r8) << 4));
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_bf16(sacc[j][kk & 1][nt], a, qb[nt][kk][0], qb[nt][kk][1]);
+                    for (int nt = 0; nt < NT; ++nt) mma_bf16(sacc[j][kk % kChains][nt], a, qb[nt][kk][0], qb[nt][kk][1]);
                 }
             }
         }
-        // Online softmax per column, P^T as B fragments: three BF16 parts (all 24 bits) or two FP16
-        // ones (22 bits), as in the decode over selected pages.
-        uint32_t bh[J][NT][2], bl[J][NT][2], bt[J][NT][2];
-        float alpha[NT][2];
+        // Online softmax per column; logits stay as they come from the tensor cores (sl2 is positive) until the exponential.
+        float sc[J][NT][4];
+        bool raise = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float sc[J][4], bm0 = -INFINITY, bm1 = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
+            for (int j = 0; j < J; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    sc[j][e] = (sacc[j][0][nt][e] + sacc[j][1][nt][e]) * sl2[nt][e & 1];
-                    if (!whole) {
+                    sc[j][nt][e] = kChains == 2 ? sacc[j][0][nt][e] + sacc[j][kChains - 1][nt][e] : sacc[j][0][nt][e];
+                    if constexpr (kEdge) {
                         const int t = t0[j] + gid + 8 * (e >> 1);
-                        if (t0[j] < 0 || !sees(p, N - p.nq + col_query[nt][e & 1], t)) sc[j][e] = -INFINITY;
+                        if (it * J + j >= list.n || !sees(p, N - nq + col_query[nt][e & 1], t)) sc[j][nt][e] = -INFINITY;
                     }
                 }
-                bm0 = fmaxf(bm0, fmaxf(sc[j][0], sc[j][2]));
-                bm1 = fmaxf(bm1, fmaxf(sc[j][1], sc[j][3]));
-            }
 #pragma unroll
-            for (int off = 4; off < 32; off <<= 1) {
-                bm0 = fmaxf(bm0, __shfl_xor_sync(0xffffffffu, bm0, off));
-                bm1 = fmaxf(bm1, __shfl_xor_sync(0xffffffffu, bm1, off));
+            for (int i = 0; i < 2; ++i) {
+                float top = fmaxf(sc[0][nt][i], sc[0][nt][2 + i]);
+#pragma unroll
+                for (int j = 1; j < J; ++j) top = fmaxf(fmaxf(top, sc[j][nt][i]), sc[j][nt][2 + i]);
+                raise = raise || top * sl2[nt][i] > m[nt][i] + kSlack;
             }
-            const float mn0 = fmaxf(m[nt][0], bm0), mn1 = fmaxf(m[nt][1], bm1);
-            const float ms0 = (mn0 == -INFINITY) ? 0.f : mn0, ms1 = (mn1 == -INFINITY) ? 0.f : mn1;
-            const float al0 = ex2(m[nt][0] - ms0), al1 = ex2(m[nt][1] - ms1);
+        }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float bm = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < J; ++j) bm = fmaxf(bm, fmaxf(sc[j][nt][i], sc[j][nt][2 + i]));
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, off));
+                    const float mn = fmaxf(m[nt][i], bm * sl2[nt][i]);
+                    const float al = ex2(m[nt][i] - ((mn == -INFINITY) ? 0.f : mn));
+                    m[nt][i] = mn;
+                    l[nt][i] *= al;
+#pragma unroll
+                    for (int mt = 0; mt < D / 16; ++mt) {
+                        oacc[nt][mt][i] *= al;
+                        oacc[nt][mt][2 + i] *= al;
+                    }
+                }
+            }
+        }
+        // P^T as B fragments: the weights as the sum of three BF16 numbers (all 24 bits) or two FP16 ones (22 bits,
+        // the low one in bl, or in the tile's other half)
+        uint32_t bh[J][NT][2], bl[J][NT][2], bt[J][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            // (FP16 weights are 2^11 times themselves, and so are their sums)
+            constexpr float kUp = kTwo ? kWeightBits : 0.f;
+            const float ms0 = kUp - ((m[nt][0] == -INFINITY) ? 0.f : m[nt][0]), ms1 = kUp - ((m[nt][1] == -INFINITY) ? 0.f : m[nt][1]);
             float ps0 = 0.f, ps1 = 0.f;
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                const float p0 = ex2(sc[j][0] - ms0), p1 = ex2(sc[j][1] - ms1);
-                const float p2 = ex2(sc[j][2] - ms0), p3 = ex2(sc[j][3] - ms1);
+                const float p0 = ex2(fmaf(sc[j][nt][0], sl2[nt][0], ms0)), p1 = ex2(fmaf(sc[j][nt][1], sl2[nt][1], ms1));
+                const float p2 = ex2(fmaf(sc[j][nt][2], sl2[nt][0], ms0)), p3 = ex2(fmaf(sc[j][nt][3], sl2[nt][1], ms1));
                 ps0 += p0 + p2;
                 ps1 += p1 + p3;
                 if constexpr (kTwo) {
-                    const float q0 = p0 * kPScale, q1 = p1 * kPScale, q2 = p2 * kPScale, q3 = p3 * kPScale;
-                    const __half2 h01 = __floats2half2_rn(q0, q1), h23 = __floats2half2_rn(q2, q3);
+                    const __half2 h01 = __floats2half2_rn(p0, p1), h23 = __floats2half2_rn(p2, p3);
                     const float2 f01 = __half22float2(h01), f23 = __half22float2(h23);
-                    bh[j][nt][0] = movtrans(half2_bits(h01));
-                    bh[j][nt][1] = movtrans(half2_bits(h23));
-                    bl[j][nt][0] = movtrans(half2_bits(__floats2half2_rn(q0 - f01.x, q1 - f01.y)));
-                    bl[j][nt][1] = movtrans(half2_bits(__floats2half2_rn(q2 - f23.x, q3 - f23.y)));
+                    const uint32_t l01 = half2_bits(__floats2half2_rn(p0 - f01.x, p1 - f01.y)), l23 = half2_bits(__floats2half2_rn(p2 - f23.x, p3 - f23.y));
+                    if constexpr (kHalves) {
+                        bh[j][nt][0] = movtrans(tig < 2 ? half2_bits(h01) : l01);
+                        bh[j][nt][1] = movtrans(tig < 2 ? half2_bits(h23) : l23);
+                    } else {
+                        bh[j][nt][0] = movtrans(half2_bits(h01));
+                        bh[j][nt][1] = movtrans(half2_bits(h23));
+                        bl[j][nt][0] = movtrans(l01);
+                        bl[j][nt][1] = movtrans(l23);
+                    }
                 } else {
                     const __nv_bfloat162 h01 = __floats2bfloat162_rn(p0, p1), h23 = __floats2bfloat162_rn(p2, p3);
                     const float2 f01 = __bfloat1622float2(h01), f23 = __bfloat1622float2(h23);
@@ -575,25 +732,21 @@ __global__ void __launch_bounds__(32 * W) decode_span_kernel(const SpanParams p)
                     bt[j][nt][1] = movtrans(bf16x2_bits(__floats2bfloat162_rn(d2 - g23.x, d3 - g23.y)));
                 }
             }
-            l[nt][0] = l[nt][0] * al0 + ps0;
-            l[nt][1] = l[nt][1] * al1 + ps1;
-            m[nt][0] = mn0;
-            m[nt][1] = mn1;
-            alpha[nt][0] = al0;
-            alpha[nt][1] = al1;
+            l[nt][0] += ps0;
+            l[nt][1] += ps1;
         }
-        // O^T = alpha O^T + V^T P^T.  The products of one step are summed on their own and added in
+        // O^T += V^T P^T.  The products of one step are summed on their own and added in
         // FP32 (the tensor cores cut off what they add to a running sum).
         // mine: which queries' columns take them (-1: all); masks: of the lane's token pairs (2 tig, 2 tig + 1) and 8 further.
         auto values = [&](int mine, auto&& keep) {
             auto add = [&](int nt, int mt, const float (&f)[4]) {
                 if (mine < 0 || col_query[nt][0] == mine) {
-                    oacc[nt][mt][0] = fmaf(oacc[nt][mt][0], alpha[nt][0], f[0]);
-                    oacc[nt][mt][2] = fmaf(oacc[nt][mt][2], alpha[nt][0], f[2]);
+                    oacc[nt][mt][0] += f[0];
+                    oacc[nt][mt][2] += f[2];
                 }
                 if (mine < 0 || col_query[nt][1] == mine) {
-                    oacc[nt][mt][1] = fmaf(oacc[nt][mt][1], alpha[nt][1], f[1]);
-                    oacc[nt][mt][3] = fmaf(oacc[nt][mt][3], alpha[nt][1], f[3]);
+                    oacc[nt][mt][1] += f[1];
+                    oacc[nt][mt][3] += f[3];
                 }
             };
             if constexpr (kCache == kInt4) {
@@ -603,21 +756,20 @@ __global__ void __launch_bounds__(32 * W) decode_span_kernel(const SpanParams p)
                 for (int j = 0; j < J; ++j) {
                     const uint32_t vrow = kbase[j] + Cf::kVOff + 2 * tig * Cf::kVRow + gid * (D / 16);
                     const uint32_t srow = kbase[j] + Cf::kVStep + 2 * tig * Cf::kStepRow + (gid * D / 8) / 16;
-                    const bool on = t0[j] >= 0;  // (else its buffer may hold anything)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int row = (r & 1) + 8 * (r >> 1);
                         if constexpr (D == 128) {
-                            const uint2 x = on ? lds64(vrow + row * Cf::kVRow) : make_uint2(0u, 0u);
+                            const uint2 x = lds64(vrow + row * Cf::kVRow);
                             w[j][r][0] = x.x, w[j][r][1] = x.y;
                         } else {
-                            w[j][r][0] = on ? lds32(vrow + row * Cf::kVRow) : 0u;
+                            w[j][r][0] = lds32(vrow + row * Cf::kVRow);
                         }
                     }
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        const uint32_t x = on ? lds8(srow + 8 * half * Cf::kStepRow) : 0u, y = on ? lds8(srow + (8 * half + 1) * Cf::kStepRow) : 0u;
-                        st[j][half] = e4m3x2_to_f16x2(x | (y << 8));
+                        const uint32_t x = lds8(srow + 8 * half * Cf::kStepRow), y = lds8(srow + (8 * half + 1) * Cf::kStepRow);
+                        st[j][half] = e4m3x2_to_f16x2(prmt(x, y, 0x0040u));
                     }
                 }
 #pragma unroll
@@ -639,7 +791,7 @@ __global__ void __launch_bounds__(32 * W) decode_span_kernel(const SpanParams p)
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) {
                                     mma_f16(f[nt], a, bh[j][nt][0], bh[j][nt][1]);
-                                    mma_f16(f[nt], a, bl[j][nt][0], bl[j][nt][1]);
+                                    if constexpr (!kHalves) mma_f16(f[nt], a, bl[j][nt][0], bl[j][nt][1]);
                                 }
                             }
 #pragma unroll
@@ -652,14 +804,8 @@ __global__ void __launch_bounds__(32 * W) decode_span_kernel(const SpanParams p)
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
                     const uint32_t vbase = kbase[j] + Cf::kVOff;
-                    uint4 va, vb, vc, vd;
-                    va = vb = vc = vd = make_uint4(0u, 0u, 0u, 0u);
-                    if (t0[j] >= 0) {  // (else its buffer may hold anything)
-                        va = lds128(vbase + r0 * 128 + c0);
-                        vb = lds128(vbase + (r0 + 1) * 128 + c1);
-                        vc = lds128(vbase + (r0 + 8) * 128 + c0);
-                        vd = lds128(vbase + (r0 + 9) * 128 + c1);
-                    }
+                    const uint4 va = lds128(vbase + r0 * 128 + c0), vb = lds128(vbase + (r0 + 1) * 128 + c1);
+                    const uint4 vc = lds128(vbase + (r0 + 8) * 128 + c0), vd = lds128(vbase + (r0 + 9) * 128 + c1);
                     xa[j][0] = va.x, xa[j][1] = va.y, xa[j][2] = va.z, xa[j][3] = va.w;
                     xb[j][0] = vb.x, xb[j][1] = vb.y, xb[j][2] = vb.z, xb[j][3] = vb.w;
                     xc[j][0] = vc.x, xc[j][1] = vc.y, xc[j][2] = vc.z, xc[j][3] = vc.w;
@@ -682,7 +828,7 @@ __global__ void __launch_bounds__(32 * W) decode_span_kernel(const SpanParams p)
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
                                 mma_f16(f[nt], a, bh[j][nt][0], bh[j][nt][1]);
-                                mma_f16(f[nt], a, bl[j][nt][0], bl[j][nt][1]);
+                                if constexpr (!kHalves) mma_f16(f[nt], a, bl[j][nt][0], bl[j][nt][1]);
                             }
                         }
 #pragma unroll
@@ -707,21 +853,21 @@ __global__ void __launch_bounds__(32 * W) decode_span_kernel(const SpanParams p)
                 }
             }
         };
-        if (whole || p.nq == 1) {
+        if constexpr (!kMulti || !kEdge) {
             values(-1, [](int, uint32_t (&)[4]) {});  // (rows that no query sees were zero-filled)
         } else {
             // A token that one query sees and another does not may be infinite or NaN, and 0 times it is
             // NaN: one query at a time, with the values that it does not see taken out.
 #pragma unroll 1
-            for (int qi = 0; qi < p.nq; ++qi) {
-                const int s = N - p.nq + qi;
+            for (int qi = 0; qi < nq; ++qi) {
+                const int s = N - nq + qi;
                 uint32_t mask[J][2];
 #pragma unroll
                 for (int j = 0; j < J; ++j)
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int t = t0[j] + 2 * tig + 8 * half;
-                        mask[j][half] = (t0[j] >= 0 && sees(p, s, t) ? 0xffffu : 0u) | (t0[j] >= 0 && sees(p, s, t + 1) ? 0xffff0000u : 0u);
+                        mask[j][half] = (sees(p, s, t) ? 0xffffu : 0u) | (sees(p, s, t + 1) ? 0xffff0000u : 0u);  // (zeros past the last slab)
                     }
                 values(qi, [&](int j, uint32_t (&a)[4]) {
                     a[0] &= mask[j][0];
@@ -731,6 +877,13 @@ __global__ void __launch_bounds__(32 * W) decode_span_kernel(const SpanParams p)
                 });
             }
         }
+    };
+    int it = 0;
+#pragma unroll 1
+    while (it < n_it) {
+#pragma unroll 1
+        for (; it >= it_a && it < it_b; ++it) step(it, std::false_type());
+        if (it < n_it) step(it++, std::true_type());
     }
     cp_async_wait<0>();
     if (list.bad) *bad_flag = 1;
@@ -739,10 +892,17 @@ __global__ void __launch_bounds__(32 * W) decode_span_kernel(const SpanParams p)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-            l[nt][0] += __shfl_xor_sync(0xffffffffu, l[nt][0], off);
-            l[nt][1] += __shfl_xor_sync(0xffffffffu, l[nt][1], off);
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], off);
+            if (kTwo) m[nt][i] -= kWeightBits;  // (numerators and denominators are 2^11 times as large)
         }
+    if constexpr (kHalves) {  // the low parts' products
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) oacc[0][mt][e] += __shfl_xor_sync(0xffffffffu, oacc[0][mt][e], 2);
+    }
     __syncthreads();  // every warp is done with its ring
     constexpr int kCols = Cf::kCols, MS = D + 4;
     float* mg_o = reinterpret_cast<float*>(smem);
@@ -752,15 +912,17 @@ __global__ void __launch_bounds__(32 * W) decode_span_kernel(const SpanParams p)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int c0 = nt * 8 + 2 * tig;
+        if (kHalves && tig >= 2) break;
 #pragma unroll
         for (int mt = 0; mt < D / 16; ++mt) {
             // channels of rows gid and gid + 8 of m-tile mt
             const int ca = kCache == kInt4 ? D / 8 * gid + 2 * mt : 16 * mt + gid, cb = kCache == kInt4 ? ca + 1 : ca + 8;
-            const float f = kCache == kInt4 ? vscale : 1.f;  // (E4M3: applied to the merged state)
-            mo[c0 * MS + ca] = oacc[nt][mt][0] * f;
-            mo[(c0 + 1) * MS + ca] = oacc[nt][mt][1] * f;
-            mo[c0 * MS + cb] = oacc[nt][mt][2] * f;
-            mo[(c0 + 1) * MS + cb] = oacc[nt][mt][3] * f;
+            // (E4M3: V's scale is applied to the merged state; 4 bits: the odd channels' values come 16 times as large)
+            const float fa = kCache == kInt4 ? vscale : 1.f, fb = kCache == kInt4 ? vscale * 0.0625f : 1.f;
+            mo[c0 * MS + ca] = oacc[nt][mt][0] * fa;
+            mo[(c0 + 1) * MS + ca] = oacc[nt][mt][1] * fa;
+            mo[c0 * MS + cb] = oacc[nt][mt][2] * fb;
+            mo[(c0 + 1) * MS + cb] = oacc[nt][mt][3] * fb;
         }
         if (gid == 0) {
             mg_m[warp * kCols + c0] = m[nt][0];
@@ -807,7 +969,6 @@ __global__ void __launch_bounds__(SpanF32Cfg<D, P, 6>::kThreads, 1) decode_span_
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) float q_all[kCols][D];
     __shared__ Mailbox<D, kCols> box;
-    __shared__ int t0s_all[Cf::kWarps * kStages];
     __shared__ int bad_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l8 = lane & 7, tok = lane >> 3;
     const int g = blockIdx.y / p.ngroups, cg = blockIdx.y - g * p.ngroups, b = blockIdx.z;
@@ -832,7 +993,6 @@ __global__ void __launch_bounds__(SpanF32Cfg<D, P, 6>::kThreads, 1) decode_span_
                                : 0.f;
     const uint32_t ring = smem_u32(smem) + r * kStages * Cf::kStageBytes;
     const uint8_t* ring_ptr = smem + r * kStages * Cf::kStageBytes;
-    volatile int* t0s = t0s_all + warp * kStages;
     const float(*qs)[D] = q_all + part * GC;
     // every lane of the ring's warps
     auto ring_sync = [&] {
@@ -852,20 +1012,17 @@ __global__ void __launch_bounds__(SpanF32Cfg<D, P, 6>::kThreads, 1) decode_span_
             if (j == 0 && i > 0) win = win_next;
             if (j == 0) e_next = list.entry(i + 32);
             if (j == 16) win_next = list.place(i + 16, e_next);
-            const int t0 = __shfl_sync(0xffffffffu, win.t0, j);
+            const int t0 = list.token(i);
             const int64_t off = __shfl_sync(0xffffffffu, win.off, j);
-            if (lane == 0) t0s[s] = t0;
-            if (t0 >= 0) {
 #pragma unroll
-                for (int x = 0; x < kSlab / (P * kRowsAtOnce); ++x) {
-                    const int row = x * P * kRowsAtOnce + c_row;
-                    const int bytes = list.seen(t0 + row) ? 16 : 0;
-                    const int64_t o = bytes ? off + row * p.st + c_chunk * 16 : 0;
-                    const uint32_t d = ring + s * Cf::kStageBytes + row * Cf::kRowBytes + c_chunk * 16;
-                    if (!bytes_in(o, bytes, p.cache_bytes, p.err) || !in_bounds(d + Cf::kSlabBytes + 15 - smem_u32(smem), Cf::kRing, p.err)) continue;
-                    cp_async16(d, p.k + o, bytes);
-                    cp_async16(d + Cf::kSlabBytes, p.v + o, bytes);
-                }
+            for (int x = 0; x < kSlab / (P * kRowsAtOnce); ++x) {
+                const int row = x * P * kRowsAtOnce + c_row;
+                const int bytes = list.seen(t0 + row) ? 16 : 0;
+                const int64_t o = bytes ? off + row * p.st + c_chunk * 16 : 0;
+                const uint32_t d = ring + s * Cf::kStageBytes + row * Cf::kRowBytes + c_chunk * 16;
+                if (!bytes_in(o, bytes, p.cache_bytes, p.err) || !in_bounds(d + Cf::kSlabBytes + 15 - smem_u32(smem), Cf::kRing, p.err)) continue;
+                cp_async16(d, p.k + o, bytes);
+                cp_async16(d + Cf::kSlabBytes, p.v + o, bytes);
             }
         }
         cp_async_commit();
@@ -891,8 +1048,7 @@ __global__ void __launch_bounds__(SpanF32Cfg<D, P, 6>::kThreads, 1) decode_span_
         cp_async_wait<kStages - 1>();
         ring_sync();  // the slab is in shared memory for every lane
         const int s = it % kStages;
-        const int t0 = t0s[s];
-        if (t0 < 0) continue;
+        const int t0 = list.token(it);
         const bool whole = list.whole(t0);
         const float* ks = reinterpret_cast<const float*>(ring_ptr + s * Cf::kStageBytes) + tok * D + 4 * l8;
         const float* vs = ks + Cf::kSlabBytes / 4;
@@ -1017,13 +1173,13 @@ struct Kernel {
     cudaError_t (*launch)(const cudaLaunchConfig_t*, const SpanParams&);
 };
 
-template <int D, int NT, int kCache, int W, int kStages>
+template <int D, int kCache, int kLayout, bool kMulti, int W, int kStages>
 const Kernel* mma_kernel() {
-    using Cf = SpanCfg<D, NT, kCache, W, kStages>;
+    using Cf = SpanCfg<D, kCache, kLayout, W, kStages>;
     static Instance inst;
-    static const Kernel k = {reinterpret_cast<const void*>(decode_span_kernel<D, NT, kCache, W, kStages>), Cf::kThreads, Cf::kSmem, W * Cf::kSub,
-                             Cf::kCols, &inst, [](const cudaLaunchConfig_t* cfg, const SpanParams& p) {
-                                 return cudaLaunchKernelEx(cfg, decode_span_kernel<D, NT, kCache, W, kStages>, p);
+    static const Kernel k = {reinterpret_cast<const void*>(decode_span_kernel<D, kCache, kLayout, kMulti, W, kStages>), Cf::kThreads, Cf::kSmem,
+                             W * Cf::kSub, Cf::kCols, &inst, [](const cudaLaunchConfig_t* cfg, const SpanParams& p) {
+                                 return cudaLaunchKernelEx(cfg, decode_span_kernel<D, kCache, kLayout, kMulti, W, kStages>, p);
                              }};
     return &k;
 }
@@ -1037,14 +1193,22 @@ const Kernel* f32_kernel() {
     return &k;
 }
 
+template <int D, int kCache, int W, int kStages>
+const Kernel* pick_mma(int cols, bool multi) {
+    if (cols > 8) return multi ? mma_kernel<D, kCache, kTwoTiles, true, W, kStages>() : mma_kernel<D, kCache, kTwoTiles, false, W, kStages>();
+    if (multi) return mma_kernel<D, kCache, kOne, true, W, kStages>();
+    if constexpr (kCache != kBf16)
+        if (cols <= 4) return mma_kernel<D, kCache, kHalf, false, W, kStages>();
+    return mma_kernel<D, kCache, kOne, false, W, kStages>();
+}
+
 template <int D>
-const Kernel* pick_kernel(int cache, int cols) {
-    const bool two = cols > 8;
+const Kernel* pick_kernel(int cache, int cols, bool multi) {
     switch (cache) {
-        case kBf16: return two ? mma_kernel<D, 2, kBf16, 4, 3>() : mma_kernel<D, 1, kBf16, 4, 3>();
-        case kInt4: return two ? mma_kernel<D, 2, kInt4, 4, 4>() : mma_kernel<D, 1, kInt4, 4, 4>();
+        case kBf16: return pick_mma<D, kBf16, 4, 3>(cols, multi);
+        case kInt4: return pick_mma<D, kInt4, 4, 2>(cols, multi);
         case kE4m3:
-            if constexpr (D == 128) return two ? mma_kernel<D, 2, kE4m3, 4, 3>() : mma_kernel<D, 1, kE4m3, 4, 3>();
+            if constexpr (D == 128) return pick_mma<D, kE4m3, 4, 3>(cols, multi);
             return nullptr;
         default:
             if (cols <= 1) return f32_kernel<D, 1, 1>();
@@ -1109,7 +1273,7 @@ int check_sizes(const ta_shape* shape, int cache, int nq, int window, int sinks,
     c->batch = shape->batch;
     Plan& plan = c->plan;
     plan.head_dim = shape->head_dim;
-    plan.kernel = shape->head_dim == 128 ? pick_kernel<128>(cache, p.cols) : pick_kernel<64>(cache, p.cols);
+    plan.kernel = shape->head_dim == 128 ? pick_kernel<128>(cache, p.cols, nq > 1) : pick_kernel<64>(cache, p.cols, nq > 1);
     p.ngroups = plan.ngroups = (p.cols + plan.kernel->cols - 1) / plan.kernel->cols;
     const int64_t lists = static_cast<int64_t>(p.Hkv) * p.ngroups;
     plan.rows = static_cast<int64_t>(shape->batch) * p.Hq * nq;
@@ -1185,7 +1349,7 @@ int enqueue(Call* c, void* workspace, size_t workspace_bytes, cudaStream_t strea
     if (!need) return TA_OK;
     cudaLaunchConfig_t end = {};
     end.gridDim = dim3(static_cast<unsigned>(plan.rows), 1, 1);
-    end.blockDim = dim3(c->head_dim, 1, 1);
+    end.blockDim = dim3(256, 1, 1);
     end.stream = stream;
     end.attrs = attr;
     end.numAttrs = 1;
