@@ -347,8 +347,7 @@ __device__ __forceinline__ void store_runs(T* dst, const Lane& c, const float (&
 
 template <typename TC>
 __device__ __forceinline__ void to_codes(const float* scale, int h, float (&f)[8]) {
-    if constexpr (std::is_same<TC, __nv_fp8_e4m3>::value || std::is_same<TC, Int4>::value) {
-        if (std::is_same<TC, Int4>::value && !scale) return;
+    if constexpr (std::is_same<TC, __nv_fp8_e4m3>::value) {
         const float sc = __ldg(scale + h);
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = f[i] / sc;
@@ -376,85 +375,84 @@ __device__ __forceinline__ int64_t cache_place(const TokenParams& p, int t, int 
 }
 
 // ------------------------------------------------------------- 4-bit caches
+// Writing one is bound by instructions (33.5 million BF16 channels: 86 MB, 12.7 us of HBM time), so quotients are
+// not divisions: with r the FP32 number next to 1 / c, q = z r and the correction q + (z - q c) r is the FP32
+// quotient itself (Markstein 1990, "Computation of elementary functions on the IBM RISC System/6000 processor";
+// for every E4M3 c and for 7 also checked over all z).  An FP32 quotient lies in the middle of two whole
+// numbers only if z / c does, so rounding it to the nearest one, ties to even, is exact.
+__device__ __forceinline__ float quotient(float z, float c, float r) {
+    const float q = z * r;
+    return fmaf(fmaf(-q, c, z), r, q);
+}
+
 // The larger one, NaN where either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
-__device__ __forceinline__ float top4(const float* f) {
-    return max_nan(max_nan(fabsf(f[0]), fabsf(f[1])), max_nan(fabsf(f[2]), fabsf(f[3])));
+__device__ __forceinline__ float top8(const float (&f)[8]) {
+    float a = max_nan(fabsf(f[0]), fabsf(f[1])), b = max_nan(fabsf(f[2]), fabsf(f[3]));
+    a = max_nan(a, max_nan(fabsf(f[4]), fabsf(f[5])));
+    b = max_nan(b, max_nan(fabsf(f[6]), fabsf(f[7])));
+    return max_nan(a, b);
 }
 
-// The step of 16 channels whose largest magnitude is `top`.
-struct Step {
-    uint32_t code;
-    float c, r;  // its value and the reciprocal
+// Codes of eight of 16 channels whose largest magnitude is `top` (each the first in the low bits), and their step.
+__device__ __forceinline__ uint32_t int4_codes(float (&z)[8], float top, uint32_t* step) {
+    // (finite values beyond 7 * 448 and infinities saturate, a NaN makes the step NaN)
+    float most;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(most) : "f"(top), "f"(3136.f));
+    *step = __nv_cvt_float_to_fp8(max_nan(quotient(most, 7.f, 1.f / 7.f), 0.001953125f), __NV_SATFINITE, __NV_E4M3);
+    const float c = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(*step), __NV_E4M3)));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(c));
+    r = fmaf(fmaf(-c, r, 1.f), r, r);
+    if (!(top <= 3136.f)) {  // (else no quotient is beyond 7.47: the step is at most 1/16 below top / 7)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = fminf(fmaxf(z[i], -7.25f * c), 7.25f * c);
+    }
+    // 1.5 * 2^23 + 8 + n has n + 8 in its last four bits
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 7; i >= 0; --i) w = (w << 4) + __float_as_uint(quotient(z[i], c, r) + 12582920.f);
+    return w - 0x3f400000u;  // (what the sum of 16^i times 0x4b400000 leaves in the word)
+}
+
+// z: FP32 quotients by a KV head's scale (infinite where they overflow).
+__device__ __forceinline__ void scale_down(float (&z)[8], const float* scale, int h) {
+    if (!scale) return;
+    const float s = __ldg(scale + h), r = 1.f / s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float q = z[i] * r;
+        z[i] = fabsf(q) < 1e37f ? quotient(z[i], s, r) : q;
+    }
+}
+
+// How a rotated vector's lanes, which hold two runs of four channels, come to hold eight neighbouring ones each: lanes
+// of a pair exchange a run (the even one takes the first runs, the odd one the second ones).
+struct Regroup {
+    bool swap, odd;
+    int ch, mate;  // first of the eight channels; the lane of the group that holds the other eight of the 16
 };
-__device__ __forceinline__ Step make_step(float top) {
-    Step s;
-    s.code = __nv_cvt_float_to_fp8(max_nan(top / 7.f, 0.001953125f), __NV_SATFINITE, __NV_E4M3);
-    s.c = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(s.code), __NV_E4M3)));
-    s.r = 1.f / s.c;
-    return s;
+__device__ __forceinline__ Regroup make_regroup(const TokenParams& p, const Lane& c, int l) {
+    const int half = p.rot >> 1;
+    Regroup g;
+    g.swap = c.on && !p.interleaved;
+    g.odd = l & 1;
+    g.ch = g.swap ? (g.odd ? half : 0) + 8 * (l >> 1) : 8 * l;
+    const int other = g.ch ^ 8;
+    g.mate = other < p.rot && !p.interleaved ? (other < half ? other >> 2 : ((other - half) >> 2) + 1) : other >> 3;
+    return g;
 }
-
-// Codes of four channels.  z r is z / step but for half a unit of FP32 twice, so the whole
-// number n next to it is the one next to z / step, except where that lies in the middle of two
-// or next to it; e = z - n step says so (it is exact: a multiple of z's last bit and no
-// longer than z, and of at most 24 bits therefore), and which of the two it should be.
-// (An FP32 number z / step that is not in the middle is at least half a unit from it.)
-// Channels that saturate take the last code whatever e is.
-__device__ __forceinline__ uint32_t int4_codes(const float* z, const Step& s) {
-    uint32_t out = 0;
+// Every lane of the group.
+__device__ __forceinline__ void regroup(const Regroup& g, float (&f)[8], unsigned mask) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float n = fminf(fmaxf(rintf(z[i] * s.r), -8.f), 8.f);
-        const float e = fmaf(-n, s.c, z[i]), e2 = 2.f * fabsf(e);
-        if (e2 > s.c || (e2 == s.c && (static_cast<int>(n) & 1))) n += copysignf(1.f, e);
-        n = fminf(fmaxf(n, -7.f), 7.f);
-        out |= static_cast<uint32_t>(static_cast<int>(n) + 8) << (4 * i);
+        const float got = __shfl_xor_sync(mask, g.odd ? f[i] : f[4 + i], 1);
+        if (g.swap) (g.odd ? f[i] : f[4 + i]) = got;
     }
-    return out;
-}
-
-// Where the other eight channels of the 16 that a lane's runs belong to are held.
-struct Partner {
-    int la, lb;   // lanes of the group
-    bool ra, rb;  // in the lane's second run
-};
-__device__ __forceinline__ Partner make_partner(const TokenParams& p, const Lane& c) {
-    const int half = p.rot >> 1;
-    auto find = [&](int ch, int* lane, bool* run) {  // holder of channel ch
-        const bool split = ch < p.rot && !p.interleaved;
-        *run = split && ch >= half;
-        *lane = split ? (ch - (*run ? half : 0)) >> 2 : ch >> 3;
-    };
-    Partner q;
-    find((c.a & ~7) ^ 8, &q.la, &q.ra);
-    find((c.b & ~7) ^ 8, &q.lb, &q.rb);
-    return q;
-}
-
-// Store a lane's two runs; `codes`, `steps`: the vector's bytes.  Every lane of the group.
-template <int L>
-__device__ __forceinline__ void store_runs_int4(const TokenParams& p, const Lane& c, const Partner& q, const float (&f)[8], uint8_t* codes,
-                                                uint8_t* steps, unsigned mask) {
-    float ma = top4(f), mb = top4(f + 4);
-    const float xa = __shfl_xor_sync(mask, ma, 1), xb = __shfl_xor_sync(mask, mb, 1);
-    if (c.on && !p.interleaved) {  // a run's neighbour holds the rest of its eight channels
-        ma = max_nan(ma, xa);
-        mb = max_nan(mb, xb);
-    } else {
-        ma = mb = max_nan(ma, mb);
-    }
-    const float aa = __shfl_sync(mask, ma, q.la, L), ab = __shfl_sync(mask, mb, q.la, L);
-    const float ba = __shfl_sync(mask, ma, q.lb, L), bb = __shfl_sync(mask, mb, q.lb, L);
-    const Step sa = make_step(max_nan(ma, q.ra ? ab : aa)), sb = make_step(max_nan(mb, q.rb ? bb : ba));
-    *reinterpret_cast<uint16_t*>(codes + (c.a >> 1)) = static_cast<uint16_t>(int4_codes(f, sa));
-    *reinterpret_cast<uint16_t*>(codes + (c.b >> 1)) = static_cast<uint16_t>(int4_codes(f + 4, sb));
-    if ((c.a & 15) == 0) steps[c.a >> 4] = static_cast<uint8_t>(sa.code);
-    if ((c.b & 15) == 0) steps[c.b >> 4] = static_cast<uint8_t>(sb.code);
 }
 
 // Eight channels of a 4-bit vector: their codes and the step.
@@ -466,6 +464,17 @@ struct Eight4 {
         for (int i = 0; i < 8; ++i) f[i] = c * static_cast<float>(static_cast<int>((codes >> (4 * i)) & 15u) - 8);
     }
 };
+
+// Store channels ch .. ch + 7 of head h; `top`: the largest magnitude of the 16 that they belong to.
+template <int D>
+__device__ __forceinline__ void store_int4(const TokenParams& p, void* codes, void* step, int64_t place, int64_t steps, int h, int ch,
+                                           float (&f)[8], float top) {
+    if (!cache_in(p, place, h, ch / 2, 4) || !step_in(p, steps, h, ch)) return;
+    uint32_t st;
+    const uint32_t w = int4_codes(f, top, &st);
+    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(codes) + place + h * p.ch + ch / 2) = w;
+    if (ch % 16 == 0) static_cast<uint8_t*>(step)[steps + h * p.sth + ch / 16] = static_cast<uint8_t>(st);
+}
 
 // Which of a token's vectors a group of the reading kernel takes.  False: nothing to
 // do.  A warp's groups take the same share of neighbouring tokens, so that they walk
@@ -494,7 +503,7 @@ __device__ __forceinline__ bool group_work(const TokenParams& p, int heads, int*
 // Each form is the faster one on its side: 700 tokens of 40 heads 4.9 against 6.8 us,
 // 32768 of 48 130.6 against 144.
 template <int D, typename T, typename TC>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 5) token_write_kernel(const TokenParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (std::is_same<TC, Int4>::value ? 6 : 7) : 5) token_write_kernel(const TokenParams p) {
     constexpr int L = D / 8, kGroups = 32 / L;
     constexpr bool kCache = !std::is_void<TC>::value, kInt4 = std::is_same<TC, Int4>::value;
     static_assert(kGroups * (D / 2) == kThreads, "one angle a thread");
@@ -555,17 +564,18 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 5) token_write_
     if (h0 < kend) {
         float w[8];
         if (p.norm) load_weight<D>(p, p.kw, c, w);
-        Partner mate;
-        if constexpr (kInt4) mate = make_partner(p, c);
+        Regroup place_of;
+        if constexpr (kInt4) place_of = make_regroup(p, c, lane % L);
         walk_runs<T>(p, p.k, t, c, max(h0 - p.Hq, 0), min(h1 - p.Hq, p.Hkv), [&](int h, float (&f)[8]) {
             norm_rotate<L>(p, c, cs, sn, w, f, mask);
             if constexpr (!kCache) {
                 if (!vector_in(p.ko, t, h, c.a, 4, p.err) || !vector_in(p.ko, t, h, c.b, 4, p.err)) return;
                 store_runs(static_cast<T*>(p.ko.data) + t * p.ko.st + h * p.ko.sh, c, f);
             } else if constexpr (kInt4) {
-                if (!cache_in(p, place, h, 0, D / 2) || !step_in(p, steps, h, D - 1)) return;
-                to_codes<TC>(p.ks, h, f);
-                store_runs_int4<L>(p, c, mate, f, static_cast<uint8_t*>(p.kc) + place + h * p.ch, static_cast<uint8_t*>(p.kst) + steps + h * p.sth, mask);
+                scale_down(f, p.ks, h);
+                regroup(place_of, f, mask);
+                const float top = top8(f);
+                store_int4<D>(p, p.kc, p.kst, place, steps, h, place_of.ch, f, max_nan(top, __shfl_sync(mask, top, place_of.mate, L)));
             } else {
                 if (!cache_in(p, place, h, c.a, 4) || !cache_in(p, place, h, c.b, 4)) return;
                 to_codes<TC>(p.ks, h, f);
@@ -581,12 +591,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 5) token_write_
             [&](int h) { return vector_in(p.v, t, h, ch, 8, p.err); },
             [&](int h, float (&f)[8]) {
                 if constexpr (kInt4) {
-                    if (!cache_in(p, place, h, 0, D / 2) || !step_in(p, steps, h, D - 1)) return;
-                    to_codes<TC>(p.vs, h, f);
-                    const float top = max_nan(top4(f), top4(f + 4));
-                    const Step s = make_step(max_nan(top, __shfl_xor_sync(mask, top, 1)));
-                    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.vc) + place + h * p.ch + ch / 2) = int4_codes(f, s) | int4_codes(f + 4, s) << 16;
-                    if (ch % 16 == 0) static_cast<uint8_t*>(p.vst)[steps + h * p.sth + ch / 16] = static_cast<uint8_t>(s.code);
+                    scale_down(f, p.vs, h);
+                    const float top = top8(f);
+                    store_int4<D>(p, p.vc, p.vst, place, steps, h, ch, f, max_nan(top, __shfl_xor_sync(mask, top, 1)));
                 } else {
                     if (!cache_in(p, place, h, ch, 8)) return;
                     to_codes<TC>(p.vs, h, f);
