@@ -53,18 +53,20 @@ struct SpanParams {
     const float* v_scale;
     float* out;
     float* lse;
-    float* part_o;             // [rows][P][d], rows = B * Hq * nq; null: the blocks of a list merge in their cluster
-    float2* part_ml;           // [rows][P]: maximum (log2 units), denominator
+    // even shares (see Shares; part_o null: the P blocks of a list are a cluster)
+    float* part_o;             // [lists of a row][P][2][columns of a list][d]
+    float2* part_ml;           // the same without d: maximum (log2 units), denominator
     int* err;
     int64_t sb, sh, st;        // bytes between rows or pages, heads, tokens
     int64_t tb, th, tt;        // the same of the steps
     int Hq, Hkv, G, nq, cols, S, ngroups;  // cols = G * nq columns of a KV head, column = head * nq + query
     int window, sinks;         // at most S
     int max_pages, page_shift, num_pages;
-    int P, C;                  // blocks of a list, of a cluster (P, or 1 with partial states)
+    int B, P, C;               // P: blocks of a list, or with even shares of all rows' lists of one head; C: of a cluster
+    int list_cols;             // columns of a list (a block serves so many)
     float scale_log2;
     // extents, for the bounds-checking build
-    size_t q_elems, cache_bytes, step_bytes, table_elems, out_elems, rows;
+    size_t q_elems, cache_bytes, step_bytes, table_elems, out_elems, rows, part_rows;
 };
 
 // The tokens of a row that some query sees, as slabs: [0, head) and [first, last).
@@ -91,12 +93,10 @@ struct SpanList {
     int b, g, u, W, n;  // the warp's first slab, its stride, its number of slabs
     int lane, bad;
 
-    __device__ __forceinline__ SpanList(const SpanParams& p_, const Span& s, int b_, int g_, int part, int warp, int W_)
+    __device__ __forceinline__ SpanList(const SpanParams& p_, const Span& s, int b_, int g_, int u0, int u1, int warp, int W_)
         : p(p_), span(s), b(b_), g(g_), W(W_), bad(0) {
         lane = threadIdx.x & 31;
         table = p.block_table ? p.block_table + static_cast<int64_t>(b) * p.max_pages : nullptr;
-        const int u0 = static_cast<int>(static_cast<int64_t>(span.count) * part / p.P);
-        const int u1 = static_cast<int>(static_cast<int64_t>(span.count) * (part + 1) / p.P);
         u = u0 + warp;
         n = u1 > u ? (u1 - u + W - 1) / W : 0;
     }
@@ -150,9 +150,122 @@ __device__ __forceinline__ bool bytes_in(int64_t o, int bytes, size_t extent, in
     return bytes == 0 || in_bounds(static_cast<size_t>(o) + bytes - 1, extent, err);
 }
 
-// The merged state of a block, written as the partial state of rows row0 .. row0 + ncol.
+// Even shares.  Rows differ in length, and the number of lists rarely fills the device evenly.  So where there is much
+// work, the slabs of all rows' lists of one KV head (and column group) are numbered through, and each of P blocks takes
+// as many: the end of a list, whole lists, the beginning of one.  Whole lists become outputs at once; the others leave
+// a partial state in slot 0 (the block's first piece) or 1, which a second kernel merges.  All heads are cut alike, so
+// that their blocks read neighbouring bytes of token-major pools at the same time (one numbering over the heads of a row
+// too, whose blocks do not: 16 rows of 18432 tokens in 4 bits 135 us, in head-major pools 87).
+constexpr int kMaxRows = 512;    // rows of a call with even shares
+constexpr int kShareSlabs = 16;  // slabs of a share, at least
+
+struct Shares {
+    int64_t total, size;
+    __device__ __forceinline__ Shares(const SpanParams& p, int64_t total_) : total(total_) {
+        size = max(static_cast<int64_t>(kShareSlabs), total < (1ll << 31) ? static_cast<int64_t>((static_cast<uint32_t>(total) + p.P - 1) / static_cast<uint32_t>(p.P))
+                                                                          : (total + p.P - 1) / p.P);
+    }
+    __device__ __forceinline__ int block_of(int64_t slab) const {
+        return static_cast<int>(slab < (1ll << 31) && size < (1ll << 31) ? static_cast<uint32_t>(slab) / static_cast<uint32_t>(size) : slab / size);
+    }
+};
+
+// Slabs of a list of row b, 0 for a length outside [0, S] (its outputs become NaN).
+__device__ __forceinline__ int row_slabs(const SpanParams& p, int N) { return N < 0 || N > p.S ? 0 : Span(p, N).count; }
+
+// pre[0 .. B]: slabs of one list of all rows before.  Every thread of the block; `sums`: [warps] in shared memory.
+template <int kThreads>
+__device__ __forceinline__ void scan_rows(const SpanParams& p, int64_t* pre, int64_t* sums, bool report) {
+    const int tid = threadIdx.x, per = (p.B + kThreads - 1) / kThreads;
+    const int first = min(p.B, tid * per), last = min(p.B, first + per);
+    int64_t mine = 0;
+    for (int i = first; i < last; ++i) {
+        const int N = p.seqlens[i], c = row_slabs(p, N);
+        if (report && (N < 0 || N > p.S)) atomicOr(p.err, kErrBadSeqlen);
+        pre[i + 1] = c;
+        mine += c;
+    }
+    int64_t upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, upto, off);
+        if ((tid & 31) >= off) upto += x;
+    }
+    if ((tid & 31) == 31) sums[tid >> 5] = upto;
+    __syncthreads();
+    int64_t base = upto - mine;
+    for (int w = 0; w < (tid >> 5); ++w) base += sums[w];
+    for (int i = first; i < last; ++i) {
+        base += pre[i + 1];
+        pre[i + 1] = base;
+    }
+    if (tid == 0) pre[0] = 0;
+    __syncthreads();
+}
+
+// The pieces of lists that a block works on, one after the other: with even shares those of its slabs (`pre` as from
+// scan_rows), else its part of the list (blockIdx.y, .z).  Kept in shared memory by one thread: two dozen registers
+// for a few uses.
+struct Piece {
+    const int64_t* pre;
+    int64_t t, t0, t1;  // the block's slabs: next, first, end
+    int b, u0, u1;      // the piece: row, slabs of its list
+    int N;              // the row's length, 0 if it is bad
+    bool bad;
+    __device__ __forceinline__ void begin(const SpanParams& p, const int64_t* pre_) {
+        pre = pre_;
+        t = t0 = 0;
+        if (!p.part_o) {
+            b = blockIdx.z;
+            t1 = 1;
+            length(p);
+            const uint32_t c = Span(p, N).count;  // (below 2^27, and P at most 16)
+            u0 = c * blockIdx.x / p.P;
+            u1 = c * (blockIdx.x + 1) / p.P;
+            return;
+        }
+        const Shares s(p, pre[p.B]);
+        t = t0 = min(s.total, s.size * blockIdx.x);
+        t1 = min(s.total, t0 + s.size);
+        if (t == t1) return;
+        int lo = 0, hi = p.B;  // the last row that begins at or before t
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (pre[mid] <= t)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        b = lo;
+        u0 = static_cast<int>(t - pre[b]);
+        cut(p);
+    }
+    __device__ __forceinline__ void length(const SpanParams& p) {
+        N = p.seqlens[b];
+        bad = N < 0 || N > p.S;
+        if (bad) N = 0;
+    }
+    __device__ __forceinline__ void cut(const SpanParams& p) {
+        u1 = static_cast<int>(min(pre[b + 1] - pre[b], u0 + (t1 - t)));
+        length(p);
+    }
+    __device__ __forceinline__ bool more() const { return t < t1; }
+    // (with even shares)
+    __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == pre[b + 1] - pre[b]; }
+    __device__ __forceinline__ int slot() const { return t == t0 ? 0 : 1; }
+    __device__ __forceinline__ void next(const SpanParams& p) {
+        t += p.part_o ? u1 - u0 : 1;
+        if (t >= t1) return;
+        u0 = 0;
+        do ++b;
+        while (pre[b + 1] == pre[b]);
+        cut(p);
+    }
+};
+
+// The merged state of a block's piece, written as the partial state `at`.
 template <int D, int kWarps, int kCols, bool kFp8, int kThreads = 32 * kWarps>
-__device__ void store_partial(const SpanParams& p, size_t row0, int ncol, float vscale, const float* mg_o, const float* mg_m,
+__device__ void store_partial(const SpanParams& p, int slot, int ncol, float vscale, const float* mg_o, const float* mg_m,
                               const float* mg_l, bool poison) {
     constexpr int MS = D + 4;
     const float nan = __int_as_float(0x7fc00000);
@@ -173,28 +286,48 @@ __device__ void store_partial(const SpanParams& p, size_t row0, int ncol, float 
         float o = sum_of<kWarps>(ow), l = sum_of<kWarps>(lw);
         if (kFp8) o *= vscale;
         if (poison) o = l = M = nan;
-        const size_t at = (row0 + h) * p.P + blockIdx.x;
-        if (!in_bounds(at, p.rows * p.P, p.err)) continue;
+        const size_t at = (2 * (static_cast<size_t>(blockIdx.y) * p.P + blockIdx.x) + slot) * kCols + h;
+        if (!in_bounds(at, p.part_rows, p.err)) continue;
         p.part_o[at * D + dd] = o;
         if (dd == 0) p.part_ml[at] = make_float2(M, l);
     }
 }
 
-// The partial states of a row become its outputs: weights of up to kChunk states at a time in shared memory, then
-// numerators folded by groups of threads (a float4 each, eight loads in flight) and across the groups.
+// The partial states of an output row become its output, if its list was cut: weights in shared memory, numerators
+// folded by groups of threads (a float4 each, eight loads in flight) and across the groups.
 template <int D>
 __global__ void __launch_bounds__(256) span_combine_kernel(const SpanParams p) {
-    constexpr int kThreads = 256, kLanes = D / 4, kGroups = kThreads / kLanes, kChunk = 256;
-    __shared__ float w_s[kChunk], red[2][kThreads / 32];
+    constexpr int kThreads = 256, kLanes = D / 4, kGroups = kThreads / kLanes;
+    __shared__ float w_s[kThreads], red[2][kThreads / 32];
     __shared__ float4 acc_s[kGroups][kLanes];
+    __shared__ int64_t pre[kMaxRows + 1], sums[kThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const size_t row = blockIdx.x;
+    const int per_row = p.Hkv * p.cols, b = static_cast<int>(row / per_row), r = static_cast<int>(row - static_cast<size_t>(b) * per_row);
+    const int g = r / p.cols, cg = (r - g * p.cols) / p.list_cols, col = r - g * p.cols - cg * p.list_cols;
+    // (the lengths are older than the first kernel, which has started: they need no wait for it)
+    scan_rows<kThreads>(p, pre, sums, false);
+    const int64_t first = pre[b], slabs = pre[b + 1] - first;
+    const Shares s(p, pre[p.B]);
+    const int k0 = slabs ? s.block_of(first) : 0, n = slabs ? s.block_of(first + slabs - 1) - k0 + 1 : 0;
+    const int N = p.seqlens[b];
     wait_primary();
     allow_dependents();
-    const size_t row = blockIdx.x;
-    const float2* ml = p.part_ml + row * p.P;
-    const float4* o = reinterpret_cast<const float4*>(p.part_o + row * p.P * D);
+    if (slabs == 0) {  // nothing to see, or a bad length
+        const float v = N < 0 || N > p.S ? __int_as_float(0x7fc00000) : 0.f;
+        for (int i = tid; i < D; i += kThreads)
+            if (in_bounds(row * D + i, p.out_elems, p.err)) p.out[row * D + i] = v;
+        if (tid == 0 && p.lse && in_bounds(row, p.rows, p.err)) p.lse[row] = v == 0.f ? -INFINITY : v;
+        return;
+    }
+    if (n == 1) return;  // the block that had the list has written the output
+    // state i is block k0 + i's: its second piece if it began before the list, else its first
+    const int first_slot = s.size * k0 < first;
+    const size_t block0 = static_cast<size_t>(g * p.ngroups + cg) * p.P + k0;
+    auto at = [&](int i) { return (2 * (block0 + i) + (i == 0 ? first_slot : 0)) * p.list_cols + col; };
     float M = -INFINITY;
-    for (int i = tid; i < p.P; i += kThreads) M = fmaxf(M, ml[i].x);
+    for (int i = tid; i < n; i += kThreads)
+        if (in_bounds(at(i), p.part_rows, p.err)) M = fmaxf(M, p.part_ml[at(i)].x);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     if (lane == 0) red[0][warp] = M;
@@ -205,20 +338,21 @@ __global__ void __launch_bounds__(256) span_combine_kernel(const SpanParams p) {
     float L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     const int c4 = tid % kLanes, grp = tid / kLanes;
-    for (int first = 0; first < p.P; first += kChunk) {
-        const int n = min(kChunk, p.P - first);
-        if (first > 0) __syncthreads();
-        if (tid < n) {
-            const float2 s = ml[first + tid];
-            const float w = (s.x == -INFINITY) ? 0.f : ex2(s.x - Ms);
+    for (int base = 0; base < n; base += kThreads) {
+        const int m = min(kThreads, n - base);
+        if (base > 0) __syncthreads();
+        if (tid < m && in_bounds(at(base + tid), p.part_rows, p.err)) {
+            const float2 x = p.part_ml[at(base + tid)];
+            const float w = (x.x == -INFINITY) ? 0.f : ex2(x.x - Ms);
             w_s[tid] = w;
-            L = fmaf(w, s.y, L);
+            L = fmaf(w, x.y, L);
         }
         __syncthreads();
 #pragma unroll 8
-        for (int i = grp; i < n; i += kGroups) {
+        for (int i = grp; i < m; i += kGroups) {
+            if (!in_bounds(at(base + i), p.part_rows, p.err)) continue;
             const float w = w_s[i];
-            const float4 v = o[static_cast<size_t>(first + i) * kLanes + c4];
+            const float4 v = reinterpret_cast<const float4*>(p.part_o + at(base + i) * D)[c4];
             acc.x = fmaf(w, v.x, acc.x);
             acc.y = fmaf(w, v.y, acc.y);
             acc.z = fmaf(w, v.z, acc.z);
@@ -269,8 +403,8 @@ struct SpanCfg {
     static constexpr int kWarps = W, kThreads = 32 * W, kStages = kStages_;
     static constexpr int kCols = kLayout == kHalf ? 4 : 8 * NT;
     static constexpr int kRing = kWarps * kStages * kStageBytes;
-    static constexpr int kBoxOff = kRing + 16;                                      // (a flag between them)
-    static constexpr int kSmem = kBoxOff + static_cast<int>(sizeof(Mailbox<D, kCols>));
+    static constexpr int kBoxOff = kRing + 16 + (sizeof(Piece) + 15) / 16 * 16;      // (a flag and the piece between them)
+    static constexpr int kSmem = kBoxOff + static_cast<int>(std::max(sizeof(Mailbox<D, kCols>), sizeof(int64_t) * (kMaxRows + 1 + kWarps)));
     static_assert(kWarps * kCols * (D + 4 + 2) * 4 <= kRing, "merge buffers reuse the ring");
     static_assert(kStages >= 2 && kSmem <= 227 * 1024, "ring");
 };
@@ -375,21 +509,24 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gid = lane >> 2, tig = lane & 3, r8 = lane & 7;
-    const int g = blockIdx.y / p.ngroups, cg = blockIdx.y - g * p.ngroups, b = blockIdx.z;
+    if (p.C > 1) cluster_arrive();  // (waited for before the states are sent)
+    wait_primary();
+    allow_dependents();
+    // the block's pieces: with even shares several, else one part of one list
+    Piece& piece = *reinterpret_cast<Piece*>(smem + Cf::kRing + 16);
+    int64_t* pre = reinterpret_cast<int64_t*>(smem + Cf::kBoxOff);  // (with even shares: no mailbox then)
+    if (p.part_o) scan_rows<Cf::kThreads>(p, pre, pre + kMaxRows + 1, blockIdx.x == 0 && blockIdx.y == 0);
+    if (threadIdx.x == 0) piece.begin(p, pre), *bad_flag = 0;
+    __syncthreads();
+    while (piece.more()) {
+    const int b = piece.b, g = blockIdx.y / p.ngroups, cg = blockIdx.y - g * p.ngroups;
     const int c_first = Cf::kCols * cg;
     const int ncol = min(Cf::kCols, p.cols - c_first);
     const size_t row0 = static_cast<size_t>(b) * p.Hq * p.nq + static_cast<size_t>(g) * p.cols + c_first;
-    if (threadIdx.x == 0) *bad_flag = 0;
-    if (p.C > 1) cluster_arrive();  // (waited for before the states are sent)
-    __syncthreads();
-    wait_primary();
-    allow_dependents();
-
-    int N = p.seqlens[b];
-    const bool bad_len = N < 0 || N > p.S;
-    if (bad_len) N = 0;
+    const int N = piece.N;
+    const bool bad_len = piece.bad;
     const Span span(p, N);
-    SpanList list(p, span, b, g, blockIdx.x, warp, kWarps);
+    SpanList list(p, span, b, g, piece.u0, piece.u1, warp, kWarps);
     const int n_it = (list.n + J - 1) / J;
     int e_next = list.entry(0);
 
@@ -933,11 +1070,15 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
     }
     __syncthreads();
     const bool poison = bad_len || *bad_flag;
-    if (p.part_o)
-        store_partial<D, kWarps, kCols, kCache == kE4m3>(p, row0, ncol, vscale, mg_o, mg_m, mg_l, poison);
+    if (p.part_o && !piece.whole())
+        store_partial<D, kWarps, kCols, kCache == kE4m3>(p, piece.slot(), ncol, vscale, mg_o, mg_m, mg_l, poison);
     else
         finish_list<D, kWarps, kCols, kCache == kE4m3>(p, row0, ncol, vscale, mg_o, mg_m, mg_l,
                                                        reinterpret_cast<Mailbox<D, kCols>*>(smem + Cf::kBoxOff), poison);
+    __syncthreads();  // (merge buffers and piece are read)
+    if (threadIdx.x == 0) piece.next(p), *bad_flag = 0;
+    __syncthreads();
+    }
 }
 
 // -------------------------------------------------------------- FP32 caches
@@ -970,21 +1111,25 @@ __global__ void __launch_bounds__(SpanF32Cfg<D, P, 6>::kThreads, 1) decode_span_
     __shared__ __align__(16) float q_all[kCols][D];
     __shared__ Mailbox<D, kCols> box;
     __shared__ int bad_flag;
+    __shared__ int64_t pre[kMaxRows + 1], sums[Cf::kWarps];
+    __shared__ Piece piece;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l8 = lane & 7, tok = lane >> 3;
-    const int g = blockIdx.y / p.ngroups, cg = blockIdx.y - g * p.ngroups, b = blockIdx.z;
+    const int r = warp / P, part = warp - r * P;  // ring, and which GC columns of it
+    if (p.C > 1) cluster_arrive();  // (waited for before the states are sent)
+    wait_primary();
+    allow_dependents();
+    if (p.part_o) scan_rows<Cf::kThreads>(p, pre, sums, blockIdx.x == 0 && blockIdx.y == 0);
+    if (threadIdx.x == 0) piece.begin(p, pre), bad_flag = 0;
+    __syncthreads();
+    while (piece.more()) {
+    const int b = piece.b, g = blockIdx.y / p.ngroups, cg = blockIdx.y - g * p.ngroups;
     const int c_first = kCols * cg;
     const int ncol = min(kCols, p.cols - c_first);
     const size_t row0 = static_cast<size_t>(b) * p.Hq * p.nq + static_cast<size_t>(g) * p.cols + c_first;
-    const int r = warp / P, part = warp - r * P;  // ring, and which GC columns of it
-    if (p.C > 1) cluster_arrive();  // (waited for before the states are sent)
-    if (threadIdx.x == 0) bad_flag = 0;
-    wait_primary();
-    allow_dependents();
-    int N = p.seqlens[b];
-    const bool bad_len = N < 0 || N > p.S;
-    if (bad_len) N = 0;
+    const int N = piece.N;
+    const bool bad_len = piece.bad;
     const Span span(p, N);
-    SpanList list(p, span, b, g, blockIdx.x, r, kRings);
+    SpanList list(p, span, b, g, piece.u0, piece.u1, r, kRings);
     const int n_it = list.n;
     int e_next = list.entry(0);
     for (int i = threadIdx.x; i < kCols * D; i += Cf::kThreads)
@@ -1157,10 +1302,14 @@ __global__ void __launch_bounds__(SpanF32Cfg<D, P, 6>::kThreads, 1) decode_span_
     }
     __syncthreads();
     const bool poison = bad_len || bad_flag;
-    if (p.part_o)
-        store_partial<D, kRings, kCols, false, Cf::kThreads>(p, row0, ncol, 1.f, mg_o, mg_m, mg_l, poison);
+    if (p.part_o && !piece.whole())
+        store_partial<D, kRings, kCols, false, Cf::kThreads>(p, piece.slot(), ncol, 1.f, mg_o, mg_m, mg_l, poison);
     else
         finish_list<D, kRings, kCols, false, Cf::kThreads>(p, row0, ncol, 1.f, mg_o, mg_m, mg_l, &box, poison);
+    __syncthreads();  // (merge buffers and piece are read)
+    if (threadIdx.x == 0) piece.next(p), bad_flag = 0;
+    __syncthreads();
+    }
 }
 
 // ---------------------------------------------------------------- host side
@@ -1218,32 +1367,45 @@ const Kernel* pick_kernel(int cache, int cols, bool multi) {
     }
 }
 
-// How a call is laid out on the device.
+// How a call is laid out on the device: clusters of P blocks for each list, or (shares) P blocks for all rows' lists of
+// one head and column group.
 struct Plan {
     const Kernel* kernel;
-    int ngroups, head_dim, P, C;
-    int64_t rows;  // of the outputs
-    // Where the partial states' maxima and denominators lie in the workspace (behind the numerators), and its bytes.
-    size_t partial_ml() const { return (static_cast<size_t>(rows) * P * head_dim * sizeof(float) + 255) / 256 * 256; }
-    size_t workspace() const { return C == P ? 0 : partial_ml() + static_cast<size_t>(rows) * P * sizeof(float2); }
+    int ngroups, head_dim, batch, P;
+    int64_t lists;  // of a row
+    bool shares;
+    int64_t rows;   // of the outputs
+    // The workspace: partial numerators, then maxima and denominators.
+    size_t states() const { return 2 * static_cast<size_t>(lists) * P * kernel->cols; }
+    size_t ml_offset() const { return states() * head_dim * sizeof(float); }
+    size_t workspace() const { return shares ? ml_offset() + states() * sizeof(float2) : 0; }
 };
 
-// Blocks of a list (P).  A call takes about (waves of blocks) x (a block's start and end + its slabs);
-// a cluster of up to 16 blocks merges without a second kernel where all fit at once.
-void pick_blocks(Plan* plan, int64_t lists, int64_t slabs, int num_sms, int blocks_per_sm, const int* fit) {
+// A call takes about (waves of blocks) x (a block's start and end + its rounds of slabs); with even shares there
+// is one wave, a second kernel, and a start and end for each piece.  A cluster of up to 16 blocks merges without a
+// second kernel where all fit at once.
+void pick_blocks(Plan* plan, int64_t slabs, int num_sms, int blocks_per_sm, const int* fit) {
     const int64_t rounds = std::max<int64_t>(1, (slabs + plan->kernel->rings - 1) / plan->kernel->rings);  // of a block that has the list to itself
-    const int64_t slots = static_cast<int64_t>(num_sms) * blocks_per_sm;
-    constexpr double kStart = 4., kMerge = 3., kSecond = 6.;   // in rounds
+    const int64_t slots = static_cast<int64_t>(num_sms) * blocks_per_sm, lists = plan->lists * plan->batch;
+    constexpr double kStart = 4., kMerge = 3., kSecond = 8.;   // in rounds
+    plan->P = 1;
+    plan->shares = false;
     double best = 0.;
-    for (int P = 1; P <= std::min<int64_t>(rounds, 512); ++P) {
-        const bool cluster = P == 1 || (P <= kMaxCluster && lists <= fit[P]);
+    for (int P = 1; P <= std::min<int64_t>(rounds, kMaxCluster); ++P) {
+        if (P > 1 && lists > fit[P]) continue;
         const double waves = static_cast<double>((lists * P + slots - 1) / slots);
-        const double cost = waves * (kStart + static_cast<double>((rounds + P - 1) / P)) + (P == 1 ? 0. : (cluster ? kMerge : kSecond));
+        const double cost = waves * (kStart + static_cast<double>((rounds + P - 1) / P)) + (P == 1 ? 0. : kMerge);
         if (P == 1 || cost < best) {
             best = cost;
             plan->P = P;
-            plan->C = cluster ? P : 1;
         }
+    }
+    if (plan->batch > kMaxRows || plan->lists > slots) return;
+    const int64_t each = slots / plan->lists;
+    const double work = static_cast<double>(plan->batch * rounds) / static_cast<double>(each), pieces = 1. + static_cast<double>(plan->batch) / static_cast<double>(each);
+    if (work + pieces * kStart + kSecond < best) {
+        plan->P = static_cast<int>(each);
+        plan->shares = true;
     }
 }
 
@@ -1273,9 +1435,11 @@ int check_sizes(const ta_shape* shape, int cache, int nq, int window, int sinks,
     c->batch = shape->batch;
     Plan& plan = c->plan;
     plan.head_dim = shape->head_dim;
+    plan.batch = p.B = shape->batch;
     plan.kernel = shape->head_dim == 128 ? pick_kernel<128>(cache, p.cols, nq > 1) : pick_kernel<64>(cache, p.cols, nq > 1);
-    p.ngroups = plan.ngroups = (p.cols + plan.kernel->cols - 1) / plan.kernel->cols;
-    const int64_t lists = static_cast<int64_t>(p.Hkv) * p.ngroups;
+    p.list_cols = plan.kernel->cols;
+    p.ngroups = plan.ngroups = (p.cols + p.list_cols - 1) / p.list_cols;
+    const int64_t lists = plan.lists = static_cast<int64_t>(p.Hkv) * p.ngroups;
     plan.rows = static_cast<int64_t>(shape->batch) * p.Hq * nq;
     if (shape->batch > 65535 || lists > 65535 || plan.rows > 0x7fffffff) return TA_ERR_SHAPE;
     const float scale = shape->scale > 0.f ? shape->scale : 1.0f / std::sqrt(static_cast<float>(shape->head_dim));
@@ -1294,9 +1458,9 @@ int make_plan(Call* c) {
     if ((rc = prepare_instance(k.fn, k.threads, k.smem, c->dev.device, k.inst)) != TA_OK) return rc;
     const int64_t seen = std::min<int64_t>(p.S, static_cast<int64_t>(p.window) + p.nq - 1 + p.sinks);
     const int* fit = k.inst->clusters[c->dev.device];
-    pick_blocks(&c->plan, static_cast<int64_t>(c->batch) * p.Hkv * p.ngroups, seen / kSlab + 2, c->dev.num_sms, std::max(1, fit[1] / c->dev.num_sms), fit);
+    pick_blocks(&c->plan, seen / kSlab + 2, c->dev.num_sms, std::max(1, fit[1] / c->dev.num_sms), fit);
     p.P = c->plan.P;
-    p.C = c->plan.C;
+    p.C = c->plan.shares ? 1 : p.P;
     p.err = c->dev.err;
     return TA_OK;
 }
@@ -1329,11 +1493,13 @@ int enqueue(Call* c, void* workspace, size_t workspace_bytes, cudaStream_t strea
     if (need) {
         if (!workspace || workspace_bytes < need) return TA_ERR_WORKSPACE;
         if (!aligned_to(workspace, 16)) return TA_ERR_ALIGN;
+        uint8_t* ws = static_cast<uint8_t*>(workspace);
         p.part_o = static_cast<float*>(workspace);
-        p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + plan.partial_ml());
+        p.part_ml = reinterpret_cast<float2*>(ws + plan.ml_offset());
+        p.part_rows = plan.states();
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(plan.P, p.Hkv * p.ngroups, c->batch);
+    cfg.gridDim = dim3(plan.P, p.Hkv * p.ngroups, plan.shares ? 1 : c->batch);
     cfg.blockDim = dim3(plan.kernel->threads, 1, 1);
     cfg.dynamicSmemBytes = plan.kernel->smem;
     cfg.stream = stream;
@@ -1341,10 +1507,10 @@ int enqueue(Call* c, void* workspace, size_t workspace_bytes, cudaStream_t strea
     attr[0] = programmatic_launch();
     attr[1] = {};
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(plan.C);
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.C);
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = plan.C > 1 ? 2 : 1;
+    cfg.numAttrs = p.C > 1 ? 2 : 1;
     if (plan.kernel->launch(&cfg, p) != cudaSuccess) return TA_ERR_CUDA;
     if (!need) return TA_OK;
     cudaLaunchConfig_t end = {};

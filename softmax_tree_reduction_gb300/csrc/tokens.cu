@@ -503,7 +503,7 @@ __device__ __forceinline__ bool group_work(const TokenParams& p, int heads, int*
 // Each form is the faster one on its side: 700 tokens of 40 heads 4.9 against 6.8 us,
 // 32768 of 48 130.6 against 144.
 template <int D, typename T, typename TC>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (std::is_same<TC, Int4>::value ? 6 : 7) : 5) token_write_kernel(const TokenParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 5) token_write_kernel(const TokenParams p) {
     constexpr int L = D / 8, kGroups = 32 / L;
     constexpr bool kCache = !std::is_void<TC>::value, kInt4 = std::is_same<TC, Int4>::value;
     static_assert(kGroups * (D / 2) == kThreads, "one angle a thread");
