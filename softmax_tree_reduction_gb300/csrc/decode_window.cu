@@ -263,34 +263,145 @@ struct Piece {
     }
 };
 
-// The merged state of a block's piece, written as the partial state `at`.
-template <int D, int kWarps, int kCols, bool kFp8, int kThreads = 32 * kWarps>
-__device__ void store_partial(const SpanParams& p, int slot, int ncol, float vscale, const float* mg_o, const float* mg_m,
-                              const float* mg_l, bool poison) {
-    constexpr int MS = D + 4;
+// What a block's warps leave in shared memory: numerators [warp][column][d + 4], maxima (log2 units) and denominators
+// [warp][column]; then, by weigh(), the weights of the warps' states and the merged maxima and denominators.
+template <int D, int kWarps, int kCols>
+struct WarpStates {
+    static constexpr int MS = D + 4;
+    float o[kWarps][kCols][MS];
+    float m[kWarps][kCols], l[kWarps][kCols], w[kWarps][kCols];
+    float2 ml[kCols];
+};
+
+// Every thread of the block, with a barrier before and after.
+template <int D, int kWarps, int kCols>
+__device__ __forceinline__ void weigh(WarpStates<D, kWarps, kCols>* s, bool poison) {
+    const int h = threadIdx.x;
+    if (h >= kCols) return;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s->m[w][h]);
+    const float Ms = (M == -INFINITY) ? 0.f : M;
+    float lw[kWarps];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const float wt = poison ? __int_as_float(0x7fc00000) : ex2(s->m[w][h] - Ms);
+        s->w[w][h] = wt;
+        lw[w] = wt * s->l[w][h];
+    }
     const float nan = __int_as_float(0x7fc00000);
-    for (int idx = threadIdx.x; idx < ncol * D; idx += kThreads) {
-        const int h = idx / D, dd = idx - h * D;
-        const int pos = kFp8 ? (dd % 16) * 8 + dd / 16 : dd;
-        float M = -INFINITY;
+    s->ml[h] = poison ? make_float2(nan, nan) : make_float2(M, sum_of<kWarps>(lw));
+}
+// Four channels from c on of column h, merged over the warps.
+template <int D, int kWarps, int kCols>
+__device__ __forceinline__ float4 merged4(const WarpStates<D, kWarps, kCols>& s, int h, int c) {
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mg_m[w * kCols + h]);
-        const float Ms = (M == -INFINITY) ? 0.f : M;
-        float ow[kWarps], lw[kWarps];
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float wt = ex2(mg_m[w * kCols + h] - Ms);
-            ow[w] = wt * mg_o[(w * kCols + h) * MS + pos];
-            lw[w] = wt * mg_l[w * kCols + h];
-        }
-        float o = sum_of<kWarps>(ow), l = sum_of<kWarps>(lw);
-        if (kFp8) o *= vscale;
-        if (poison) o = l = M = nan;
+    for (int w = 0; w < kWarps; ++w) {
+        const float wt = s.w[w][h];
+        const float4 v = *reinterpret_cast<const float4*>(&s.o[w][h][c]);
+        acc.x = fmaf(wt, v.x, acc.x);
+        acc.y = fmaf(wt, v.y, acc.y);
+        acc.z = fmaf(wt, v.z, acc.z);
+        acc.w = fmaf(wt, v.w, acc.w);
+    }
+    return acc;
+}
+__device__ __forceinline__ float4 normalised(const float4& o, float l) {
+    return l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x / l, o.y / l, o.z / l, o.w / l);
+}
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2; }
+
+// The state of a block's piece, written as a partial state.
+template <int D, int kWarps, int kCols, int kThreads>
+__device__ void store_partial(const SpanParams& p, int slot, int ncol, const WarpStates<D, kWarps, kCols>& s) {
+    for (int i = threadIdx.x; i < ncol * (D / 4); i += kThreads) {
+        const int h = i / (D / 4), c = i - h * (D / 4);
         const size_t at = (2 * (static_cast<size_t>(blockIdx.y) * p.P + blockIdx.x) + slot) * kCols + h;
         if (!in_bounds(at, p.part_rows, p.err)) continue;
-        p.part_o[at * D + dd] = o;
-        if (dd == 0) p.part_ml[at] = make_float2(M, l);
+        reinterpret_cast<float4*>(p.part_o + at * D)[c] = merged4(s, h, 4 * c);
+        if (c == 0) p.part_ml[at] = s.ml[h];
     }
+}
+
+// The same as the outputs of rows row0 .. row0 + ncol.
+template <int D, int kWarps, int kCols, int kThreads>
+__device__ void store_rows(const SpanParams& p, size_t row0, int ncol, const WarpStates<D, kWarps, kCols>& s) {
+    for (int i = threadIdx.x; i < ncol * (D / 4); i += kThreads) {
+        const int h = i / (D / 4), c = i - h * (D / 4);
+        const float2 ml = s.ml[h];
+        if (in_bounds((row0 + h) * D + 4 * c + 3, p.out_elems, p.err)) reinterpret_cast<float4*>(p.out + (row0 + h) * D)[c] = normalised(merged4(s, h, 4 * c), ml.y);
+        if (c == 0 && p.lse && in_bounds(row0 + h, p.rows, p.err)) p.lse[row0 + h] = lse_of(ml.x, ml.y);
+    }
+}
+
+// The same merged over the blocks of the cluster first.  Every block merges a share of the outputs; the others send it
+// theirs (stores into its box), so that one barrier suffices.  The caller has arrived once at the cluster's barrier
+// when it started.
+template <int D, int kCols>
+struct SpanBox {
+    float4 o[kCols * D / 4 + kMaxCluster];  // [sender][share], share = ceil(columns * D / 4 / blocks)
+    float2 ml[kMaxCluster][kCols];          // [sender]
+};
+__device__ __forceinline__ void st_dsmem4(uint32_t addr, const float4& v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+__device__ __forceinline__ void st_dsmem2(uint32_t addr, const float2& v) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.x), "f"(v.y) : "memory");
+}
+template <int D, int kWarps, int kCols, int kThreads>
+__device__ void merge_cluster(const SpanParams& p, size_t row0, int ncol, const WarpStates<D, kWarps, kCols>& s, SpanBox<D, kCols>* box) {
+    const int C = p.C, rank = static_cast<int>(cluster_rank()), items = ncol * (D / 4), share = (items + C - 1) / C;
+    cluster_wait();  // every block of the cluster has started
+    for (int i = threadIdx.x; i < items; i += kThreads) {
+        const int h = i / (D / 4), c = i - h * (D / 4), to = i / share;
+        if (!in_bounds(rank * share + i - to * share, kCols * D / 4 + kMaxCluster, p.err) || !in_bounds(to, C, p.err)) continue;
+        st_dsmem4(dsmem_addr(&box->o[rank * share + i - to * share], to), merged4(s, h, 4 * c));
+        if (c < C) st_dsmem2(dsmem_addr(&box->ml[rank][h], c), s.ml[h]);  // (to block c: there are at most D / 4)
+    }
+    cluster_arrive();
+    cluster_wait();
+    const int n = min(share, items - rank * share);
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const int idx = rank * share + i, h = idx / (D / 4), c4 = idx - h * (D / 4);
+        float2 ml[kMaxCluster];
+        float M = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+            ml[c] = c < C ? box->ml[c][h] : make_float2(-INFINITY, 0.f);
+            M = fmaxf(M, ml[c].x);
+        }
+        const float Ms = (M == -INFINITY) ? 0.f : M;
+        float L = 0.f;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+            if (c >= C) break;
+            const float w = (ml[c].x == -INFINITY) ? 0.f : ex2(ml[c].x - Ms);
+            const float4 v = box->o[c * share + i];
+            L = fmaf(w, ml[c].y, L);
+            O.x = fmaf(w, v.x, O.x);
+            O.y = fmaf(w, v.y, O.y);
+            O.z = fmaf(w, v.z, O.z);
+            O.w = fmaf(w, v.w, O.w);
+        }
+        if (in_bounds((row0 + h) * D + 4 * c4 + 3, p.out_elems, p.err)) reinterpret_cast<float4*>(p.out + (row0 + h) * D)[c4] = normalised(O, L);
+        if (c4 == 0 && p.lse && in_bounds(row0 + h, p.rows, p.err)) p.lse[row0 + h] = lse_of(M, L);
+    }
+}
+
+// What becomes of the warps' states of a piece.  Every thread of the block, after a barrier.
+template <int D, int kWarps, int kCols, int kThreads>
+__device__ __forceinline__ void finish_piece(const SpanParams& p, const Piece& piece, size_t row0, int ncol, bool poison,
+                                             WarpStates<D, kWarps, kCols>* s, SpanBox<D, kCols>* box) {
+    weigh(s, poison);
+    __syncthreads();
+    if (p.part_o && !piece.whole())
+        store_partial<D, kWarps, kCols, kThreads>(p, piece.slot(), ncol, *s);
+    else if (p.C > 1)
+        merge_cluster<D, kWarps, kCols, kThreads>(p, row0, ncol, *s, box);
+    else
+        store_rows<D, kWarps, kCols, kThreads>(p, row0, ncol, *s);
 }
 
 // The partial states of an output row become its output, if its list was cut: weights in shared memory, numerators
@@ -348,15 +459,23 @@ __global__ void __launch_bounds__(256) span_combine_kernel(const SpanParams p) {
             L = fmaf(w, x.y, L);
         }
         __syncthreads();
-#pragma unroll 8
-        for (int i = grp; i < m; i += kGroups) {
-            if (!in_bounds(at(base + i), p.part_rows, p.err)) continue;
-            const float w = w_s[i];
-            const float4 v = reinterpret_cast<const float4*>(p.part_o + at(base + i) * D)[c4];
-            acc.x = fmaf(w, v.x, acc.x);
-            acc.y = fmaf(w, v.y, acc.y);
-            acc.z = fmaf(w, v.z, acc.z);
-            acc.w = fmaf(w, v.w, acc.w);
+        constexpr int kFlight = 8;
+        for (int i0 = grp; i0 < m; i0 += kFlight * kGroups) {
+            float4 v[kFlight];
+#pragma unroll
+            for (int j = 0; j < kFlight; ++j) {
+                const int i = i0 + j * kGroups;
+                v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < m && in_bounds(at(base + i), p.part_rows, p.err)) v[j] = reinterpret_cast<const float4*>(p.part_o + at(base + i) * D)[c4];
+            }
+#pragma unroll
+            for (int j = 0; j < kFlight; ++j) {
+                const float w = i0 + j * kGroups < m ? w_s[i0 + j * kGroups] : 0.f;
+                acc.x = fmaf(w, v[j].x, acc.x);
+                acc.y = fmaf(w, v[j].y, acc.y);
+                acc.z = fmaf(w, v[j].z, acc.z);
+                acc.w = fmaf(w, v[j].w, acc.w);
+            }
         }
     }
 #pragma unroll
@@ -374,9 +493,8 @@ __global__ void __launch_bounds__(256) span_combine_kernel(const SpanParams p) {
         const float4 v = acc_s[i][c4];
         acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
     }
-    acc = L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(acc.x / L, acc.y / L, acc.z / L, acc.w / L);
-    if (in_bounds(row * D + 4 * c4 + 3, p.out_elems, p.err)) reinterpret_cast<float4*>(p.out + row * D)[c4] = acc;
-    if (tid == 0 && p.lse && in_bounds(row, p.rows, p.err)) p.lse[row] = (L == 0.f) ? -INFINITY : (M + log2f(L)) * kLn2;
+    if (in_bounds(row * D + 4 * c4 + 3, p.out_elems, p.err)) reinterpret_cast<float4*>(p.out + row * D)[c4] = normalised(acc, L);
+    if (tid == 0 && p.lse && in_bounds(row, p.rows, p.err)) p.lse[row] = lse_of(M, L);
 }
 
 // ------------------------------------------------------------ tensor cores
@@ -398,14 +516,15 @@ struct SpanCfg {
     static constexpr int kKStep = kVOff + kSlab * kVRow;
     static constexpr int kVStep = kKStep + kSlab * kStepRow;
     static constexpr int kPairBytes = kVStep + kSlab * kStepRow;                    // keys, values and steps of a slab
-    static constexpr int kSub = kCache == kBf16 ? 1 : 2;                            // slabs that a warp takes together
+    // Slabs that a warp takes together: two share a chain of products, maxima and exponentials where the registers allow
+    static constexpr int kSub = kCache == kBf16 || kLayout == kTwoTiles ? 1 : 2;
     static constexpr int kStageBytes = kSub * kPairBytes;
     static constexpr int kWarps = W, kThreads = 32 * W, kStages = kStages_;
     static constexpr int kCols = kLayout == kHalf ? 4 : 8 * NT;
     static constexpr int kRing = kWarps * kStages * kStageBytes;
     static constexpr int kBoxOff = kRing + 16 + (sizeof(Piece) + 15) / 16 * 16;      // (a flag and the piece between them)
-    static constexpr int kSmem = kBoxOff + static_cast<int>(std::max(sizeof(Mailbox<D, kCols>), sizeof(int64_t) * (kMaxRows + 1 + kWarps)));
-    static_assert(kWarps * kCols * (D + 4 + 2) * 4 <= kRing, "merge buffers reuse the ring");
+    static constexpr int kSmem = kBoxOff + static_cast<int>(std::max(sizeof(SpanBox<D, kCols>), sizeof(int64_t) * (kMaxRows + 1 + kWarps)));
+    static_assert(sizeof(WarpStates<D, kWarps, kCols>) <= kRing, "merge buffers reuse the ring");
     static_assert(kStages >= 2 && kSmem <= 227 * 1024, "ring");
 };
 
@@ -1041,40 +1160,39 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
             for (int e = 0; e < 4; ++e) oacc[0][mt][e] += __shfl_xor_sync(0xffffffffu, oacc[0][mt][e], 2);
     }
     __syncthreads();  // every warp is done with its ring
-    constexpr int kCols = Cf::kCols, MS = D + 4;
-    float* mg_o = reinterpret_cast<float*>(smem);
-    float* mg_m = mg_o + kWarps * kCols * MS;
-    float* mg_l = mg_m + kWarps * kCols;
-    float* mo = mg_o + warp * kCols * MS;
+    constexpr int kCols = Cf::kCols;
+    using States = WarpStates<D, kWarps, kCols>;
+    States* states = reinterpret_cast<States*>(smem);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int c0 = nt * 8 + 2 * tig;
         if (kHalves && tig >= 2) break;
+        float *o0 = states->o[warp][c0], *o1 = states->o[warp][c0 + 1];
 #pragma unroll
         for (int mt = 0; mt < D / 16; ++mt) {
-            // channels of rows gid and gid + 8 of m-tile mt
-            const int ca = kCache == kInt4 ? D / 8 * gid + 2 * mt : 16 * mt + gid, cb = kCache == kInt4 ? ca + 1 : ca + 8;
-            // (E4M3: V's scale is applied to the merged state; 4 bits: the odd channels' values come 16 times as large)
-            const float fa = kCache == kInt4 ? vscale : 1.f, fb = kCache == kInt4 ? vscale * 0.0625f : 1.f;
-            mo[c0 * MS + ca] = oacc[nt][mt][0] * fa;
-            mo[(c0 + 1) * MS + ca] = oacc[nt][mt][1] * fa;
-            mo[c0 * MS + cb] = oacc[nt][mt][2] * fb;
-            mo[(c0 + 1) * MS + cb] = oacc[nt][mt][3] * fb;
+            // channels of rows gid and gid + 8 of m-tile mt (4 bits: the odd channels' values come 16 times as large)
+            if constexpr (kCache == kBf16) {
+                o0[16 * mt + gid] = oacc[nt][mt][0];
+                o1[16 * mt + gid] = oacc[nt][mt][1];
+                o0[16 * mt + gid + 8] = oacc[nt][mt][2];
+                o1[16 * mt + gid + 8] = oacc[nt][mt][3];
+            } else {
+                const float vodd = kCache == kInt4 ? vscale * 0.0625f : vscale;
+                *reinterpret_cast<float2*>(o0 + D / 8 * gid + 2 * mt) = make_float2(oacc[nt][mt][0] * vscale, oacc[nt][mt][2] * vodd);
+                *reinterpret_cast<float2*>(o1 + D / 8 * gid + 2 * mt) = make_float2(oacc[nt][mt][1] * vscale, oacc[nt][mt][3] * vodd);
+            }
         }
         if (gid == 0) {
-            mg_m[warp * kCols + c0] = m[nt][0];
-            mg_m[warp * kCols + c0 + 1] = m[nt][1];
-            mg_l[warp * kCols + c0] = l[nt][0];
-            mg_l[warp * kCols + c0 + 1] = l[nt][1];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                states->m[warp][c0 + i] = m[nt][i];
+                states->l[warp][c0 + i] = l[nt][i];
+            }
         }
     }
     __syncthreads();
-    const bool poison = bad_len || *bad_flag;
-    if (p.part_o && !piece.whole())
-        store_partial<D, kWarps, kCols, kCache == kE4m3>(p, piece.slot(), ncol, vscale, mg_o, mg_m, mg_l, poison);
-    else
-        finish_list<D, kWarps, kCols, kCache == kE4m3>(p, row0, ncol, vscale, mg_o, mg_m, mg_l,
-                                                       reinterpret_cast<Mailbox<D, kCols>*>(smem + Cf::kBoxOff), poison);
+    finish_piece<D, kWarps, kCols, Cf::kThreads>(p, piece, row0, ncol, bad_len || *bad_flag, states,
+                                                 reinterpret_cast<SpanBox<D, kCols>*>(smem + Cf::kBoxOff));
     __syncthreads();  // (merge buffers and piece are read)
     if (threadIdx.x == 0) piece.next(p), *bad_flag = 0;
     __syncthreads();
@@ -1096,7 +1214,7 @@ struct SpanF32Cfg {
     static constexpr int kWarps = P * kRings;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kRing = kRings * kStages * kStageBytes;
-    static_assert(kStages >= 2 && kRings * 8 * (D + 4 + 2) * 4 <= kRing, "ring, merge buffers");
+    static_assert(kStages >= 2 && sizeof(WarpStates<D, kRings, 8>) <= kRing, "ring, merge buffers");
 };
 
 template <int D, int GC, int P>
@@ -1105,11 +1223,10 @@ __global__ void __launch_bounds__(SpanF32Cfg<D, P, 6>::kThreads, 1) decode_span_
     constexpr int kRings = Cf::kRings, kStages = Cf::kStages;
     constexpr int kCols = P * GC;
     constexpr int J = D / 32;  // float4 per lane: channels 4 (l8 + 8 j) ..
-    constexpr int MS = D + 4;
     constexpr int kSteps = kSlab / 4;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) float q_all[kCols][D];
-    __shared__ Mailbox<D, kCols> box;
+    __shared__ SpanBox<D, kCols> box;
     __shared__ int bad_flag;
     __shared__ int64_t pre[kMaxRows + 1], sums[Cf::kWarps];
     __shared__ Piece piece;
@@ -1270,9 +1387,8 @@ __global__ void __launch_bounds__(SpanF32Cfg<D, P, 6>::kThreads, 1) decode_span_
     if (list.bad) bad_flag = 1;
     if (list.bad || (bad_len && threadIdx.x == 0)) atomicOr(p.err, kErrBadSeqlen);
     __syncthreads();  // every warp is done with its ring
-    float* mg_o = reinterpret_cast<float*>(smem);
-    float* mg_m = mg_o + kRings * kCols * MS;
-    float* mg_l = mg_m + kRings * kCols;
+    using States = WarpStates<D, kRings, kCols>;
+    States* states = reinterpret_cast<States*>(smem);
     // the warp's four token groups, then its state into shared memory
 #pragma unroll
     for (int h = 0; h < GC; ++h) {
@@ -1292,20 +1408,16 @@ __global__ void __launch_bounds__(SpanF32Cfg<D, P, 6>::kThreads, 1) decode_span_
         if (tok == 0) {
 #pragma unroll
             for (int j = 0; j < J; ++j)
-                *reinterpret_cast<float4*>(&mg_o[(warp * GC + h) * MS + 4 * l8 + 32 * j]) =
+                *reinterpret_cast<float4*>(&states->o[r][part * GC + h][4 * l8 + 32 * j]) =
                     make_float4(o[h][2 * j].x, o[h][2 * j].y, o[h][2 * j + 1].x, o[h][2 * j + 1].y);
             if (l8 == 0) {
-                mg_m[warp * GC + h] = m[h];
-                mg_l[warp * GC + h] = l[h];
+                states->m[r][part * GC + h] = m[h];
+                states->l[r][part * GC + h] = l[h];
             }
         }
     }
     __syncthreads();
-    const bool poison = bad_len || bad_flag;
-    if (p.part_o && !piece.whole())
-        store_partial<D, kRings, kCols, false, Cf::kThreads>(p, piece.slot(), ncol, 1.f, mg_o, mg_m, mg_l, poison);
-    else
-        finish_list<D, kRings, kCols, false, Cf::kThreads>(p, row0, ncol, 1.f, mg_o, mg_m, mg_l, &box, poison);
+    finish_piece<D, kRings, kCols, Cf::kThreads>(p, piece, row0, ncol, bad_len || bad_flag, states, &box);
     __syncthreads();  // (merge buffers and piece are read)
     if (threadIdx.x == 0) piece.next(p), bad_flag = 0;
     __syncthreads();
@@ -1344,7 +1456,8 @@ const Kernel* f32_kernel() {
 
 template <int D, int kCache, int W, int kStages>
 const Kernel* pick_mma(int cols, bool multi) {
-    if (cols > 8) return multi ? mma_kernel<D, kCache, kTwoTiles, true, W, kStages>() : mma_kernel<D, kCache, kTwoTiles, false, W, kStages>();
+    constexpr int kDeep = kCache == kBf16 ? kStages : 2 * kStages;  // (a slab at a time)
+    if (cols > 8) return multi ? mma_kernel<D, kCache, kTwoTiles, true, W, kDeep>() : mma_kernel<D, kCache, kTwoTiles, false, W, kDeep>();
     if (multi) return mma_kernel<D, kCache, kOne, true, W, kStages>();
     if constexpr (kCache != kBf16)
         if (cols <= 4) return mma_kernel<D, kCache, kHalf, false, W, kStages>();
