@@ -14,13 +14,7 @@
 // through a cluster's shared memory, or, where a list wants more blocks than a cluster holds,
 // through partial states in the workspace and a second kernel.
 //
-// 4-bit caches.  A channel's value is step * (code - 8) * scale.  Four products of bits turn a
-// word of eight codes into FP16 numbers: (w & 0x000f000f) | 0x64006400 is the pair
-// 1024 + code of channels 0 and 4, and one FMA with step / 8 and -1032 step / 8 makes step / 8 *
-// (code - 8) of it, exactly: both constants have at most 11 significant bits (1032 = 8 * 129, times
-// the 4 bits of an E4M3 number), and so has the result.  The odd codes come as 1024 + 16 code (mask
-// 0x00f000f0) and, with -1152 step / 8, as 16 times their value, which q's odd channels and the
-// outputs' undo.  So the tensor cores multiply exact values.
+// The values of 4-bit caches are made exactly (int4.cuh), so the tensor cores multiply the values that the cache holds.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -32,6 +26,7 @@
 
 #include "common.cuh"
 #include "host.h"
+#include "int4.cuh"
 #include "kernels.h"
 #include "slabs.cuh"
 #include "warp_mma.cuh"
@@ -528,54 +523,6 @@ constexpr int span_blocks() {
     if (kLayout == kTwoTiles) return 2;
     return kMulti ? 2 : (kCache == kInt4 ? 3 : 2);
 }
-
-__device__ __forceinline__ uint32_t hfma2_bits(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t d;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-    return d;
-}
-__device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-// (w & mask) | magic in one instruction (written as such, the compiler makes two of it)
-__device__ __forceinline__ uint32_t pick_codes(uint32_t w, uint32_t mask, uint32_t magic) {
-    uint32_t d;
-    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(w), "r"(mask), "r"(magic));
-    return d;
-}
-
-// Factors that turn pairs of codes into step / 8 * (code - 8) where they lie in the low four bits of
-// their byte, and into 16 times that where in the high ones (whose other operand, a query or the
-// finished output, takes the 1/16): 1024 + code and 1024 + 16 code, times step / 8, less 1032 and
-// 1152 (9 * 128) times it.
-struct Unpack {
-    uint32_t mul, lo_add, hi_add;
-    // for a pair of steps (FP16)
-    __device__ __forceinline__ explicit Unpack(uint32_t steps) {
-        mul = hmul2_bits(steps, 0x30003000u);          // 2^-3
-        lo_add = hmul2_bits(mul, 0xe408e408u);         // -1032
-        hi_add = hmul2_bits(mul, 0xe480e480u);         // -1152
-    }
-    // both halves those of the low or of the high one of the given pair
-    __device__ __forceinline__ Unpack(const Unpack& u, bool high) {
-        mul = both(u.mul, high);
-        lo_add = both(u.lo_add, high);
-        hi_add = both(u.hi_add, high);
-    }
-    static __device__ __forceinline__ uint32_t both(uint32_t x, bool high) {
-        uint32_t d;
-        if (high)
-            asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; mov.b32 %0, {h, h};}" : "=r"(d) : "r"(x));
-        else
-            asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; mov.b32 %0, {l, l};}" : "=r"(d) : "r"(x));
-        return d;
-    }
-    // channels i and i + 4 of eight (i = 0, 1) of the word's bytes; shift the word by 8 for i = 2, 3
-    __device__ __forceinline__ uint32_t even(uint32_t w) const { return hfma2_bits(pick_codes(w, 0x000f000fu, 0x64006400u), mul, lo_add); }
-    __device__ __forceinline__ uint32_t odd(uint32_t w) const { return hfma2_bits(pick_codes(w, 0x00f000f0u, 0x64006400u), mul, hi_add); }
-};
 
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
     uint32_t v;
@@ -1506,13 +1453,15 @@ struct Plan {
 void pick_blocks(Plan* plan, int64_t slabs, int num_sms, int blocks_per_sm, const int* fit) {
     const int64_t rounds = std::max<int64_t>(1, (slabs + plan->kernel->rings - 1) / plan->kernel->rings);  // of a block that has the list to itself
     const int64_t slots = static_cast<int64_t>(num_sms) * blocks_per_sm, lists = plan->lists * plan->batch;
-    constexpr double kStart = 4., kMerge = 3., kSecond = 8.;   // in rounds
+    constexpr double kStart = 4., kMerge = 3., kSecond = 10.;  // in rounds
     plan->P = 1;
     plan->shares = false;
     double best = 0.;
     for (int P = 1; P <= std::min<int64_t>(rounds, kMaxCluster); ++P) {
         if (P > 1 && lists > fit[P]) continue;
-        const double waves = static_cast<double>((lists * P + slots - 1) / slots);
+        // (the blocks of a last wave that does not fill the device have more of its bandwidth each: half of it counts)
+        const double full = static_cast<double>(lists * P) / static_cast<double>(slots);
+        const double waves = full <= 1. ? 1. : 0.5 * (full + std::ceil(full));
         const double cost = waves * (kStart + static_cast<double>((rounds + P - 1) / P)) + (P == 1 ? 0. : kMerge);
         if (P == 1 || cost < best) {
             best = cost;
