@@ -70,9 +70,10 @@ struct Span {
     __device__ __forceinline__ Span(const SpanParams& p, int N_) : N(N_) {
         lo = max(0, N - p.nq + 1 - p.window);
         first = lo >> 4;
-        head = min((min(p.sinks, N) + 15) >> 4, first);
-        count = N > 0 ? head + ((N + 15) >> 4) - first : 0;
+        head = min(slabs(min(p.sinks, N)), first);
+        count = N > 0 ? head + slabs(N) - first : 0;
     }
+    static __device__ __forceinline__ int slabs(int tokens) { return static_cast<int>((static_cast<uint32_t>(tokens) + 15u) >> 4); }
     __device__ __forceinline__ int token(int u) const { return (u < head ? u : u - head + first) << 4; }
 };
 
@@ -129,7 +130,7 @@ struct SpanList {
     }
     // The warp's slabs [*a, *b) that every query sees all tokens of, without those among the sinks.
     __device__ __forceinline__ void middle(int* a, int* b) const {
-        const int ua = ((max(0, span.N - p.window) + 15) >> 4) - span.first + span.head;
+        const int ua = Span::slabs(max(0, span.N - p.window)) - span.first + span.head;
         const int ub = (max(0, span.N - p.nq + 1) >> 4) - span.first + span.head;
         *a = min(n, ua > u ? (ua - u + W - 1) / W : 0);
         *b = min(n, ub > u ? (ub - u + W - 1) / W : 0);
@@ -895,7 +896,8 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
         }
         // P^T as B fragments: the weights as the sum of three BF16 numbers (all 24 bits) or two FP16 ones (22 bits,
         // the low one in bl, or in the tile's other half)
-        uint32_t bh[J][NT][2], bl[J][NT][2], bt[J][NT][2];
+        uint32_t bh[J][NT][2];
+        [[maybe_unused]] uint32_t bl[J][NT][2], bt[J][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             // (FP16 weights are 2^11 times themselves, and so are their sums)
