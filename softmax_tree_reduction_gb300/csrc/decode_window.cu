@@ -550,6 +550,29 @@ __device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, in
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes) : "memory");
 }
 
+// Whether the lane's share of a slab's values (or, in 4 bits, of their steps) holds a NaN or an infinity.
+template <typename Cf, int kCache>
+__device__ __forceinline__ bool any_not_finite(uint32_t slab, int lane) {
+    if constexpr (kCache == kInt4) {
+        uint32_t found = 0;
+#pragma unroll
+        for (int i = 4 * lane; i < kSlab * Cf::kStepRow; i += 128) found |= __vcmpeq4(lds32(slab + Cf::kVStep + i) & 0x7f7f7f7fu, 0x7f7f7f7fu);
+        return found != 0;
+    } else {
+        uint32_t found = 0;
+#pragma unroll
+        for (int i = 16 * lane; i < kSlab * Cf::kRowBytes; i += 512) {
+            const uint4 x = lds128(slab + Cf::kVOff + i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t w = e == 0 ? x.x : (e == 1 ? x.y : (e == 2 ? x.z : x.w));
+                found |= kCache == kE4m3 ? __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) : __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u);
+            }
+        }
+        return found != 0;
+    }
+}
+
 // A column's running maximum is raised when a logit passes it by more than this (log2 units):
 // weights stay below 2^4, and most steps need neither the maximum over the lanes nor a
 // rescaling of the state.
@@ -1062,9 +1085,13 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
             values(-1, [](int, uint32_t (&)[4]) {});  // (rows that no query sees were zero-filled)
         } else {
             // A token that one query sees and another does not may be infinite or NaN, and 0 times it is
-            // NaN: one query at a time, with the values that it does not see taken out.
+            // NaN.  If any is: one query at a time, with the values that it does not see taken out.
+            bool odd = false;
+#pragma unroll
+            for (int j = 0; j < J; ++j) odd = odd || any_not_finite<Cf, kCache>(kbase[j], lane);
+            const bool each = __any_sync(0xffffffffu, odd);
 #pragma unroll 1
-            for (int qi = 0; qi < nq; ++qi) {
+            for (int qi = 0; qi < (each ? nq : 1); ++qi) {
                 const int s = N - nq + qi;
                 uint32_t mask[J][2];
 #pragma unroll
@@ -1072,9 +1099,9 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int t = t0[j] + 2 * tig + 8 * half;
-                        mask[j][half] = (sees(p, s, t) ? 0xffffu : 0u) | (sees(p, s, t + 1) ? 0xffff0000u : 0u);  // (zeros past the last slab)
+                        mask[j][half] = (!each || sees(p, s, t) ? 0xffffu : 0u) | (!each || sees(p, s, t + 1) ? 0xffff0000u : 0u);  // (zeros past the last slab)
                     }
-                values(qi, [&](int j, uint32_t (&a)[4]) {
+                values(each ? qi : -1, [&](int j, uint32_t (&a)[4]) {
                     a[0] &= mask[j][0];
                     a[1] &= mask[j][0];
                     a[2] &= mask[j][1];
