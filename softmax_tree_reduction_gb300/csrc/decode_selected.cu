@@ -36,6 +36,8 @@
 namespace ta {
 namespace {
 
+constexpr float kPScale = 16384.f;  // 2^14: P's FP16 hi + lo parts keep small weights (E4M3 caches)
+
 struct SelParams {
     const void* q;             // [B][Hq][d]
     const void* k;
@@ -116,6 +118,101 @@ struct SlabList {
         return w;
     }
 };
+
+// Mailbox of a block: what the cluster's blocks have sent it of their merged
+// states.  Not part of the rings: a block may still be streaming when another
+// sends.
+template <int D, int kCols>
+struct Mailbox {
+    float o[kCols * D + kMaxCluster];     // [sender][share], share = ceil(columns * D / blocks)
+    float2 ml[kMaxCluster][kCols];        // [sender]: maximum (log2 units), denominator
+};
+
+__device__ __forceinline__ void st_dsmem(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+// The warps' states, [warp][column][D + 4] numerators and [warp][column]
+// maxima (log2 units) and denominators in shared memory, become the outputs of
+// the list's columns [0, ncol): merged over the block's warps, then over the
+// cluster's blocks.  Every block merges a share of the outputs; the others
+// send it theirs (stores into its mailbox), so one barrier suffices and nobody
+// reads a peer's memory.  The caller has arrived once at the cluster's barrier
+// when it started.  kFp8: numerators of channel c sit at (c % 16) * 8 + c / 16 and
+// still lack V's scale.
+template <int D, int kWarps, int kCols, bool kFp8, int kThreads = 32 * kWarps>
+__device__ void finish_list(const SelParams& p, int b, int hq0, int ncol, float vscale, const float* mg_o,
+                            const float* mg_m, const float* mg_l, Mailbox<D, kCols>* box, bool poison) {
+    constexpr int MS = D + 4;
+    const int tid = threadIdx.x;
+    const float nan = __int_as_float(0x7fc00000);
+    const size_t row0 = static_cast<size_t>(b) * p.Hq + hq0;
+    const int C = p.C, items = ncol * D, share = (items + C - 1) / C;
+    const int rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
+    if (C > 1) cluster_wait();  // every block of the cluster has started
+#pragma unroll 1
+    for (int idx = tid; idx < items; idx += kThreads) {
+        const int h = idx / D, dd = idx - h * D;
+        const int pos = kFp8 ? (dd % 16) * 8 + dd / 16 : dd;
+        float mw[kWarps], M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            mw[w] = mg_m[w * kCols + h];
+            M = fmaxf(M, mw[w]);
+        }
+        const float Ms = (M == -INFINITY) ? 0.f : M;
+        float ow[kWarps], lw[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float wt = ex2(mw[w] - Ms);
+            ow[w] = wt * mg_o[(w * kCols + h) * MS + pos];
+            lw[w] = wt * mg_l[w * kCols + h];
+        }
+        float o = sum_of<kWarps>(ow);
+        float l = sum_of<kWarps>(lw);
+        if (kFp8) o *= vscale;
+        if (poison) o = l = M = nan;
+        if (C > 1) {
+            const int to = idx / share;
+            if (!in_bounds(rank * share + idx - to * share, kCols * D + kMaxCluster, p.err) || !in_bounds(to, C, p.err)) continue;
+            st_dsmem(dsmem_addr(&box->o[rank * share + idx - to * share], to), o);
+            if (dd < C) {  // the column's maximum and denominator, to block dd
+                const uint32_t at = dsmem_addr(&box->ml[rank][h], dd);
+                st_dsmem(at, M);
+                st_dsmem(at + 4, l);
+            }
+        } else {
+            if (in_bounds((row0 + h) * D + dd, p.out_elems, p.err)) p.out[(row0 + h) * D + dd] = l == 0.f ? 0.f : o / l;
+            if (dd == 0 && p.lse && in_bounds(row0 + h, p.rows, p.err)) p.lse[row0 + h] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+        }
+    }
+    if (C == 1) return;
+    cluster_arrive();
+    cluster_wait();
+    const int n = min(share, items - rank * share);
+    for (int i = tid; i < n; i += kThreads) {
+        const int idx = rank * share + i, h = idx / D, dd = idx - h * D;
+        float2 ml[kMaxCluster];
+        float o[kMaxCluster], M = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {  // all loads in flight at once
+            ml[c] = c < C ? box->ml[c][h] : make_float2(-INFINITY, 0.f);
+            o[c] = c < C ? box->o[c * share + i] : 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) M = fmaxf(M, ml[c].x);
+        const float Ms = (M == -INFINITY) ? 0.f : M;
+        float L = 0.f, O = 0.f;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+            const float w = (ml[c].x == -INFINITY) ? 0.f : ex2(ml[c].x - Ms);
+            L = fmaf(w, ml[c].y, L);
+            O = fmaf(w, o[c], O);
+        }
+        if (in_bounds((row0 + h) * D + dd, p.out_elems, p.err))
+            p.out[(row0 + h) * D + dd] = (L == 0.f) ? 0.f : O / L;  // NaN of a poisoned block propagates
+        if (dd == 0 && p.lse && in_bounds(row0 + h, p.rows, p.err)) p.lse[row0 + h] = (L == 0.f) ? -INFINITY : (M + log2f(L)) * kLn2;
+    }
+}
 
 // ------------------------------------------------------------ tensor cores
 template <int D, bool kFp8, int W>
@@ -502,7 +599,7 @@ __global__ void __launch_bounds__(SelCfg<D, kFp8, W>::kThreads, 1) decode_select
         }
     }
     __syncthreads();
-    finish_list<D, kWarps, kCols, kFp8>(p, static_cast<size_t>(b) * p.Hq + hq0, ncol, vscale, mg_o, mg_m, mg_l,
+    finish_list<D, kWarps, kCols, kFp8>(p, b, hq0, ncol, vscale, mg_o, mg_m, mg_l,
                                 reinterpret_cast<Mailbox<D, kCols>*>(smem + Cf::kBoxOff), bad_len || *bad_flag);
 }
 
@@ -727,7 +824,7 @@ __global__ void __launch_bounds__(F32Cfg<D, P>::kThreads, 1) decode_selected_f32
         }
     }
     __syncthreads();
-    finish_list<D, kRings, kCols, false, Cf::kThreads>(p, static_cast<size_t>(b) * p.Hq + hq0, ncol, 1.f, mg_o, mg_m, mg_l, &box, bad_len || bad_flag);
+    finish_list<D, kRings, kCols, false, Cf::kThreads>(p, b, hq0, ncol, 1.f, mg_o, mg_m, mg_l, &box, bad_len || bad_flag);
 }
 
 // ---------------------------------------------------------------- host side

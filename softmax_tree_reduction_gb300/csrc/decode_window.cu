@@ -10,9 +10,22 @@
 // Masks are applied in the slabs at the window's ends only.
 //
 // The unit of work, the rings and the products are those of the decode over selected pages:
-// every warp copies its slabs itself into a ring of its own.  The blocks of a list merge
-// through a cluster's shared memory, or, where a list wants more blocks than a cluster holds,
-// through partial states in the workspace and a second kernel.
+// every warp copies its slabs itself into a ring of its own.  Blocks of four warps, two or three an SM (as registers
+// allow): a list of a few thousand tokens has a start and an end of some 5 us, which the other blocks of its SM hide.
+// The blocks of a list merge through a cluster's shared memory; where there is much work, all rows' slabs are shared
+// evenly by the blocks that the device holds, and a second kernel merges the lists that were cut (see Shares).
+//
+// What bounds it, on a GB300 (fractions of the copy rate 6782.8 GB/s; 8 KV heads of 128 channels):
+//  BF16, E4M3, FP32   HBM: 64 rows with a window of 4096 tokens 148.9 us (1.07), 83.1 (0.96), 302.7 (1.05); 16 rows 42.4
+//                     (0.94), 25.3 (0.78), 83.5 (0.95); one row with a window of 1024 tokens 5.1 to 6.8 us: latencies.
+//  4 bits             instructions: a slab of 16 tokens takes a warp 308 of them for 4 columns (key codes 88, value codes
+//                     124, softmax and loop 63, copies 32), and the copy rate leaves an SM 392 issue slots for it; one row
+//                     of 524288 tokens 109.9 us (0.81), of 131072 34.2 (0.65: 8 us of start, merge and second kernel).
+//                     Masks and row checks in every slab: 510 instructions and 52.9 us at 131072 tokens; picks of
+//                     codes that the compiler made two instructions of each: 44.4; two products for the weights' parts where
+//                     one tile holds both, maxima over the lanes in every step: 62.8.
+//  several queries    16 columns of a KV head take all registers (two blocks an SM) and a slab at a time: 8 rows of four
+//                     queries with a window of 4096 tokens in 4 bits 22.9 us against 15.0 of one query.
 //
 // The values of 4-bit caches are made exactly (int4.cuh), so the tensor cores multiply the values that the cache holds.
 #include <cuda_bf16.h>
@@ -317,8 +330,8 @@ __device__ void store_rows(const SpanParams& p, size_t row0, int ncol, const War
 }
 
 // The same merged over the blocks of the cluster first.  Every block merges a share of the outputs; the others send it
-// theirs, and it waits for their bytes (a second barrier of the cluster in place of that: 6.0 against 5.3 us for one row
-// with a window of 128 tokens).  The caller has initialised the box's barrier and arrived once at the cluster's when it
+// theirs, and it waits for their bytes (a second barrier of the cluster in place of that, four short rows in 4 bits: 6.5
+// against 6.1 us).  The caller has initialised the box's barrier and arrived once at the cluster's when it
 // started; a block's box is written to only until its bytes are there, so that it may end then.
 template <int D, int kCols>
 struct SpanBox {
@@ -807,8 +820,8 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
         }
         stage_out = stage_out + Cf::kStageBytes == kStages * Cf::kStageBytes ? 0u : stage_out + Cf::kStageBytes;
 
-        // S^T[16 tokens x columns] = K Q^T per slab (a slab taken alone: two accumulators per n-tile)
-        constexpr int kChains = J == 1 ? 2 : 1;
+        // S^T[16 tokens x columns] = K Q^T per slab, two accumulators per n-tile
+        constexpr int kChains = 2;
         float sacc[J][kChains][NT][4];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
@@ -881,7 +894,7 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
             for (int j = 0; j < J; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    sc[j][nt][e] = kChains == 2 ? sacc[j][0][nt][e] + sacc[j][kChains - 1][nt][e] : sacc[j][0][nt][e];
+                    sc[j][nt][e] = sacc[j][0][nt][e] + sacc[j][1][nt][e];
                     if constexpr (kEdge) {
                         const int t = t0[j] + gid + 8 * (e >> 1);
                         if (it * J + j >= list.n || !sees(p, N - nq + col_query[nt][e & 1], t)) sc[j][nt][e] = -INFINITY;
