@@ -765,13 +765,14 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
     for (int i = 0; i < kStages - 1; ++i) issue(i);
 
     // E4M3 and 4-bit caches: q as FP16, each column times the power of two that brings its largest |q|
-    // into [2^14, 2^15) (exact; folded back into the column's logit scale), while
-    // the first keys are on their way.
+    // into [2^14, 2^15) (exact; folded back into the column's logit scale), with the sign of the key scale (a NaN where that is
+    // one: masked tokens stay masked), while the first keys are on their way.
     float vscale = 1.f;
     if constexpr (kTwo) {
         auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
         auto hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
         const float ks = (p.k_scale ? __ldg(p.k_scale + g) : 1.f) * (kCache == kInt4 ? 8.f : 1.f);
+        const float ks_abs = ks == ks ? fabsf(ks) : 1.f;
         vscale = (p.v_scale ? __ldg(p.v_scale + g) : 1.f) * (kCache == kInt4 ? 8.f : 1.f);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -785,7 +786,7 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
             // amax = f 2^e with f in [0.5, 1); powers of two are made from their exponent bits
             const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 126;
             const int qexp = amax > 0.f && amax < INFINITY ? max(-100, min(100, 15 - e)) : 0;
-            const float qs = __uint_as_float(static_cast<uint32_t>(127 + qexp) << 23);
+            const float q2 = __uint_as_float(static_cast<uint32_t>(127 + qexp) << 23), qs = ks == ks ? copysignf(q2, ks) : ks;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
@@ -794,15 +795,16 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
                     qb[nt][kk][i] = half2_bits(__floats2half2_rn(lo(qb[nt][kk][i]) * f, hi(qb[nt][kk][i]) * f));
                 }
             const float back = __uint_as_float(static_cast<uint32_t>(127 - qexp) << 23);
-            sl2[nt][0] *= ks * __shfl_sync(0xffffffffu, back, 8 * tig);      // (column 2 tig is held by lanes 8 tig ..)
-            sl2[nt][1] *= ks * __shfl_sync(0xffffffffu, back, 8 * tig + 4);
+            sl2[nt][0] *= ks_abs * __shfl_sync(0xffffffffu, back, 8 * tig);      // (column 2 tig is held by lanes 8 tig ..)
+            sl2[nt][1] *= ks_abs * __shfl_sync(0xffffffffu, back, 8 * tig + 4);
         }
     }
 
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) sl2[nt][i] = fmaxf(sl2[nt][i], 1e-37f);  // (0 times a masked logit would be NaN)
+        for (int i = 0; i < 2; ++i)
+            if (sl2[nt][i] == 0.f) sl2[nt][i] = 1e-37f;  // (a scale of 0, or one that underflowed: 0 times a masked logit would be NaN)
 
     uint32_t stage_out = 0;
     // kEdge: slabs at the window's ends, among the sinks, or not there

@@ -112,6 +112,33 @@ def test_ties_halves_and_neighbours(dt):
         assert torch.equal(c.cpu()[0, 0], wref.pack(n)[:, 0])
 
 
+@pytest.mark.parametrize("m", range(8))
+def test_every_number_over_a_step(m):
+    """All FP32 numbers z of 2^-2 .. 7.5 steps, for a step of each mantissa (1 + m / 8): in the middle of two codes, next to it and
+    elsewhere.  The first channel of each 16 sets the step."""
+    c = 1 + m / 8
+    first = torch.tensor(c / 4).view(torch.int32).item()
+    last = torch.tensor(7.5 * c).view(torch.int32).item()
+    at, n = first, 15 * 4 * 65536                                 # 65536 tokens of 64 channels
+    codes = torch.zeros(1, 1, 65536, 32, dtype=torch.uint8, device="cuda")
+    steps = torch.zeros(1, 1, 65536, 4, dtype=torch.uint8, device="cuda").view(FP8)
+    vc, vs = codes.clone(), steps.clone()
+    pos = torch.arange(65536, dtype=torch.int32, device="cuda")
+    rows = torch.zeros_like(pos)
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    while at <= last:
+        z = torch.arange(at, at + n, dtype=torch.int32, device="cuda").clamp(max=last).view(torch.float32).view(65536, 4, 15)
+        sign = torch.where(torch.arange(15, device="cuda") % 2 == 0, 1.0, -1.0)
+        x = torch.cat([torch.full((65536, 4, 1), 7 * c, device="cuda"), torch.where(z > 7 * c, 7 * c, z) * sign], 2)
+        ta.tree_attn_cache_write_int4(x.view(65536, 1, 64), x.view(65536, 1, 64), codes, vc, steps, vs, pos, rows=rows)
+        # (a quotient in 64 bits lies in the middle of two whole numbers only if the true one does)
+        want = (torch.round(x.double() / c).clamp(-7, 7) + 8).to(torch.uint8).view(65536, 64)
+        got = torch.stack([codes[0, 0] & 15, codes[0, 0] >> 4], -1).view(65536, 64)
+        wrong += (got != want).sum() + (steps.float() != c).sum() + (codes != vc).sum()
+        at += n
+    assert int(wrong) == 0
+
+
 @pytest.mark.parametrize("d,rot,inter", [(128, 128, 0), (128, 128, 1), (64, 64, 0), (128, 16, 0), (128, 48, 0), (64, 16, 0), (64, 48, 0), (128, 96, 1),
                                          (128, 80, 0), (64, 0, 0), (128, 112, 0), (64, 32, 1)])
 @pytest.mark.parametrize("T", [1, 33, 4100])

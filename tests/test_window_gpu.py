@@ -244,3 +244,28 @@ def test_logit_scale_and_large_queries():
         q = q.to(F32 if kind == F32 else BF16)
         lens = torch.tensor([0, 200], dtype=torch.int32)
         c.check(q, lens, 150, 2, scale=0.31)
+
+
+@pytest.mark.parametrize("kind,d,nq,G", [(FP8, 128, 1, 4), (FP8, 128, 3, 6), (INT4, 128, 1, 4), (INT4, 64, 1, 8), (INT4, 64, 4, 4)])
+def test_scales_of_either_sign_zero_and_nan(kind, d, nq, G):
+    """A cache's scales multiply whatever they are: masked tokens stay masked, a scale of 0 weighs all tokens alike, a NaN
+    reaches the outputs of its head and no other."""
+    c = Case(kind, 3, 90, 4, d, 16, "NHD", 12)
+    c.scales["k_scale"] *= torch.tensor([-1.0, 1.0, 0.0, -0.3])
+    c.scales["v_scale"] *= torch.tensor([1.0, -2.0, 1.0, 0.0])
+    c.refresh()
+    lens = torch.tensor([90, 3, 41], dtype=torch.int32)
+    q = queries(c, 3, 4 * G, nq, d)
+    for window, sinks in ((None, 0), (20, 5), (1, 0)):
+        c.check(q, lens, 90 if window is None else window, sinks)
+    good, gl = c.call(q, lens, 20, 5)
+    c.scales["k_scale"][2], c.scales["v_scale"][0] = math.nan, math.nan
+    out, lse = c.call(q, lens, 20, 5)
+    o, w = (x.view(3, 4, G, -1) for x in (out, good))
+    z, y = (x.view(3, 4, -1) for x in (lse, gl))
+    seen = torch.isfinite(y)                                       # (queries before the row's start see nothing)
+    assert torch.equal(torch.isnan(z), seen & (torch.arange(4, device="cuda") == 2).view(1, 4, 1))
+    nan = torch.isnan(out).view(3, 4, -1, d)
+    assert torch.equal(nan.all(-1), nan.any(-1))
+    assert torch.equal(nan.any(-1), seen & (torch.arange(4, device="cuda") % 2 == 0).view(1, 4, 1))
+    assert torch.equal(o[:, 1::2], w[:, 1::2]) and torch.equal(z[:, 1::2], y[:, 1::2]) and ta.tree_attn_get_device_error() == 0

@@ -365,6 +365,42 @@ def test_long_sums_keep_their_precision(kind, d):
     assert float(err) <= 1e-5 and float((lse.cpu().double() - wl[:, :, 0]).abs().max()) <= 1e-5
 
 
+@pytest.mark.parametrize("call", ["write", "read", "int4", "int4 long", "window"])
+def test_captured_before_any_other_call(call):
+    """The first call of a process is captured: what a call sets up on its device does not disturb a capture."""
+    code = """
+import torch, softmax_tree_reduction_gb300 as ta
+call = %r
+S = 50000 if "long" in call else 300
+kc = torch.randint(0, 256, (1, 2, S, 64), dtype=torch.uint8, device="cuda")
+st = torch.full((1, 2, S, 8), 0x38, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+kv = torch.randn(1, 2, S, 128, device="cuda").bfloat16()
+q, vec = torch.randn(1, 8, 128, device="cuda").bfloat16(), torch.randn(1, 2, 128, device="cuda").bfloat16()
+n, pos = torch.full((1,), S, dtype=torch.int32, device="cuda"), torch.full((1,), 7, dtype=torch.int32, device="cuda")
+out, lse = torch.zeros(1, 8, 128, device="cuda"), torch.zeros(1, 8, device="cuda")
+ko, vo = torch.zeros_like(vec), torch.zeros_like(vec)
+def run():
+    if call == "write": ta.tree_attn_cache_write_int4(vec, vec, kc, kc.clone(), st, st.clone(), pos)
+    elif call == "read": ta.tree_attn_cache_read_int4(kc, kc, st, st, pos, k_out=ko, v_out=vo)
+    elif call == "window": ta.tree_attn_decode_window(q, kv, kv, n, 100, out=out, lse=lse)
+    else: ta.tree_attn_decode_int4(q, kc, kc, st, st, n, out=out, lse=lse)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    run()
+g.replay()
+torch.cuda.synchronize()
+first = [x.clone() for x in (out, lse, ko, vo)]
+for x in (out, lse, ko, vo): x.zero_()
+run()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(first, (out, lse, ko, vo))) and ta.tree_attn_get_device_error() == 0
+print("same")
+""" % call
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, (r.stdout + r.stderr)[-2000:]
+
+
 def test_refusals_on_the_device():
     c = Case(INT4, 2, 100, 2, 128, 16, "NHD", 1)
     q = queries(c, 2, 8, 1, 128).cuda()
