@@ -81,7 +81,7 @@ struct SpanParams {
 struct Span {
     int N, lo, head, first, count;
     __device__ __forceinline__ Span(const SpanParams& p, int N_) : N(N_) {
-        lo = max(0, N - p.nq + 1 - p.window);
+        lo = max(0, max(0, N - p.nq + 1) - p.window);  // (in this order: the window may be 2^31 - 1)
         first = lo >> 4;
         head = min(slabs(min(p.sinks, N)), first);
         count = N > 0 ? head + slabs(N) - first : 0;

@@ -283,6 +283,43 @@ def test_offsets_past_32_bits(kind):
     assert ta.tree_attn_get_device_error() == 0
 
 
+@pytest.mark.parametrize("nq", [1, 16])
+@pytest.mark.parametrize("kind", [INT4, BF16, F32])
+def test_rows_of_up_to_2_31_tokens(kind, nq):
+    """The longest capacity that an int32 length can state, 2^31 - 1 tokens, in a table whose pages are all one of two: windows of
+    that many tokens with short rows, and short windows at the end of the longest row."""
+    d, page, S = 128, 1024, 2 ** 31 - 1
+    c = Case(kind, 1, 2 * page, 1, d, page, "NHD", 13)
+    value = [torch.cat(list(x[:2])) for x in c.value]                       # pages 0 and 1: token t is its slot of t % 2048
+    table = torch.arange(2, dtype=torch.int32).repeat(1 << 20)
+    for n, window, sinks in ((0, None, 0), (1, None, 0), (5, None, 3), (15, S, S), (17, None, 0), (2100, None, 2), (S, 100, 3), (S - 7, 1, 0),
+                             (S, 1500, 40), (S - 1, 17, 2050)):
+        lens = torch.tensor([n, 0], dtype=torch.int32)
+        q = queries(c, 2, 2, nq, d)
+        out, lse = c.call(q, lens, window, sinks, table.view(1, -1).expand(2, -1).contiguous(), max_seqlen=S)
+        if window is None:
+            window = S
+        first = max(0, n - nq + 1 - window)                                  # (of the tokens behind the sinks that some query sees)
+        tokens = torch.tensor(sorted(set(range(min(sinks, n))) | set(range(first, n))), dtype=torch.long)
+        k, v = (x[tokens % (2 * page)] for x in value)
+        q4 = q.view(2, 2, nq, d)
+        for i in range(nq):
+            s = n - nq + i
+            on = (tokens <= s) & ((tokens > s - window) | (tokens < sinks))
+            o, z = out.view(2, 2, nq, d)[0, :, i].cpu().double(), lse.view(2, 2, nq)[0, :, i].cpu().double()
+            if not bool(on.any()):
+                assert not bool(o.any()) and bool((z == -math.inf).all())
+                continue
+            x, kk, vv = values(q4[0, :, i]), k[on, 0], v[on, 0]
+            y = x @ kk.T / math.sqrt(d)
+            most = float((x.abs() @ kk.abs().T).max()) / math.sqrt(d)
+            to, tl = wref.tolerances(int(on.sum()), most, float(vv.abs().max()), d)
+            assert float((o - torch.softmax(y, 1) @ vv).abs().max()) <= to, (n, window, sinks, i)
+            assert float((z - torch.logsumexp(y, 1)).abs().max()) <= tl, (n, window, sinks, i)
+        assert not bool(out.view(2, 2, nq, d)[1].any()) and bool((lse.view(2, -1)[1] == -math.inf).all())
+    assert ta.tree_attn_get_device_error() == 0
+
+
 @pytest.mark.parametrize("kind,d", KINDS)
 def test_uneven_strides(kind, d):
     """Caches with room between heads, tokens and pages; codes and steps laid out differently."""
