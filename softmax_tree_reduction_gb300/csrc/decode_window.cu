@@ -25,7 +25,7 @@
 //                     codes that the compiler made two instructions of each: 44.4; two products for the weights' parts where
 //                     one tile holds both, maxima over the lanes in every step: 62.8.
 //  several queries    16 columns of a KV head take all registers (two blocks an SM) and a slab at a time: 8 rows of four
-//                     queries with a window of 4096 tokens in 4 bits 22.9 us against 15.0 of one query.
+//                     queries with a window of 4096 tokens in 4 bits 22.2 us against 15.0 of one query.
 //
 // The values of 4-bit caches are made exactly (int4.cuh), so the tensor cores multiply the values that the cache holds.
 #include <cuda_bf16.h>
@@ -633,6 +633,8 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
     const int n_it = (list.n + J - 1) / J;
     int e_next = list.entry(0);
 
+    [[maybe_unused]] const float k_scale = kTwo && p.k_scale ? __ldg(p.k_scale + g) : 1.f, v_scale = kTwo && p.v_scale ? __ldg(p.v_scale + g) : 1.f;
+
     // q fragments (B operand of S^T = K Q^T), as BF16 words: column n of n-tile t is column
     // c_first + 8 t + n, in the channel order in which a lane holds the key's bytes
     // (E4M3: k-step kk of lane tig is channels 32 tig + 4 kk ..; 4 bits: see below).
@@ -771,9 +773,8 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
     if constexpr (kTwo) {
         auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
         auto hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
-        const float ks = (p.k_scale ? __ldg(p.k_scale + g) : 1.f) * (kCache == kInt4 ? 8.f : 1.f);
-        const float ks_abs = ks == ks ? fabsf(ks) : 1.f;
-        vscale = (p.v_scale ? __ldg(p.v_scale + g) : 1.f) * (kCache == kInt4 ? 8.f : 1.f);
+        const float ks = k_scale * (kCache == kInt4 ? 8.f : 1.f), ks_abs = ks == ks ? fabsf(ks) : 1.f;
+        vscale = v_scale * (kCache == kInt4 ? 8.f : 1.f);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float amax = 0.f;

@@ -5,6 +5,7 @@ import math
 import os
 import subprocess
 import sys
+import threading
 
 import pytest
 import torch
@@ -388,6 +389,46 @@ def test_two_streams_and_two_graphs_at_once():
     for (run, o, z), w in zip(runs, want):
         assert torch.equal(o, w[0]) and torch.equal(z, w[1])
     assert ta.tree_attn_get_device_error() == 0
+
+
+def test_four_host_threads():
+    """Calls of all kinds from four host threads, each on a stream of its own."""
+    cases = [Case(INT4, 2, 40000, 2, 128, 16, "NHD", 21), Case(BF16, 3, 700, 2, 128, 0, "HND", 22), Case(FP8, 3, 700, 2, 128, 16, "NHD", 23),
+             Case(F32, 2, 300, 2, 64, 16, "HND", 24)]
+    work = []
+    for c in cases:
+        B = 3 if c.S == 700 else 2
+        q = queries(c, B, 8, 2, c.d).cuda()
+        lens = torch.randint(c.S // 2, c.S + 1, (B,), generator=c.g, dtype=torch.int32).cuda()
+        kw = {k: v.cuda() for k, v in c.scales.items()}
+        h = c.device()
+        if c.page:
+            kw.update(block_table=c.table.cuda(), max_seqlen=c.S)
+        if c.kind == INT4:
+            work.append(lambda h=h, q=q, lens=lens, kw=kw: ta.tree_attn_decode_int4(q, h[0], h[2], h[1], h[3], lens, **kw))
+        else:
+            work.append(lambda h=h, q=q, lens=lens, kw=kw: ta.tree_attn_decode_window(q, *h, lens, 400, 7, **kw))
+    want = [f() for f in work]
+    torch.cuda.synchronize()
+    wrong, start = [], threading.Barrier(4)
+
+    def run(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                start.wait()
+                for n in range(40):
+                    j = (i + n) % 4
+                    out, lse = work[j]()
+                    if not (torch.equal(out, want[j][0]) and torch.equal(lse, want[j][1])):
+                        wrong.append((i, n))
+        except Exception as e:                                               # noqa: BLE001
+            wrong.append(e)
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == [] and ta.tree_attn_get_device_error() == 0
 
 
 @pytest.mark.parametrize("kind,d", KINDS)
