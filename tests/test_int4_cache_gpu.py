@@ -183,6 +183,37 @@ def test_write_with_norm_and_rotation(T, d, rot, inter, dt):
     assert ta.tree_attn_get_device_error() == 0
 
 
+@pytest.mark.parametrize("dt,d,hkv", [(BF16, 128, 2), (F32, 64, 3), (BF16, 64, 1)])
+def test_views_of_one_tensor_and_repeated_reads(dt, d, hkv):
+    """Queries, keys and values as views of one product, queries turned in place; outputs as views of one tensor; places read twice."""
+    g = torch.Generator().manual_seed(3)
+    T, hq = 75, 2 * hkv
+    x = heads(g, T, hq + 2 * hkv, d, dt, 1.5).cuda()
+    q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+    f = (10000.0 ** (-torch.arange(d // 2) / (d // 2))).float().cuda()
+    rows, pos = torch.randint(0, 4, (T,), generator=g, dtype=torch.int32).cuda(), torch.arange(T, dtype=torch.int32).cuda()
+    caches = []
+    for dense in (True, False):
+        y = x.clone()
+        a, b, c = (y[:, :hq], y[:, hq:hq + hkv], y[:, hq + hkv:]) if not dense else (q.contiguous(), k.contiguous(), v.contiguous())
+        kc, vc = (torch.zeros(4, hkv, 80, d // 2, dtype=torch.uint8, device="cuda") for _ in range(2))
+        ks, vs = (torch.zeros(4, hkv, 80, d // 16, dtype=torch.uint8, device="cuda").view(FP8) for _ in range(2))
+        qo = ta.tree_attn_cache_write_int4(b, c, kc, vc, ks, vs, pos, rows=rows, q=a, q_out=a, inv_freq=f)
+        assert qo is a
+        caches.append([a.clone(), kc, vc, ks.view(torch.uint8), vs.view(torch.uint8)])
+        if not dense:
+            assert torch.equal(y[:, hq:], x[:, hq:])
+    assert all(torch.equal(m, n) for m, n in zip(*caches))
+    _, kc, vc, ks, vs = caches[0]
+    ks, vs = ks.view(FP8), vs.view(FP8)
+    k1, v1 = ta.tree_attn_cache_read_int4(kc, vc, ks, vs, pos, rows=rows, dtype=dt)
+    twice = torch.arange(T).repeat_interleave(2).flip(0).cuda()
+    both = torch.full((2 * T, 2 * hkv + 1, d), 5.0, dtype=dt, device="cuda")
+    ta.tree_attn_cache_read_int4(kc, vc, ks, vs, pos[twice].contiguous(), rows=rows[twice].contiguous(), k_out=both[:, :hkv], v_out=both[:, hkv + 1:])
+    assert torch.equal(both[:, :hkv], k1[twice]) and torch.equal(both[:, hkv + 1:], v1[twice]) and bool((both[:, hkv] == 5).all())
+    assert ta.tree_attn_get_device_error() == 0
+
+
 def test_values_not_finite():
     d, hkv = 128, 2
     k = torch.ones(4, hkv, d)
