@@ -784,9 +784,9 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
                 for (int i = 0; i < 2; ++i) amax = fmaxf(amax, fmaxf(fabsf(lo(qb[nt][kk][i])), fabsf(hi(qb[nt][kk][i]))));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            // amax = f 2^e with f in [0.5, 1); powers of two are made from their exponent bits
+            // amax = f 2^e with f in [0.5, 1); powers of two are made from their exponent bits (15 - e is -113 or more)
             const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 126;
-            const int qexp = amax > 0.f && amax < INFINITY ? max(-100, min(100, 15 - e)) : 0;
+            const int qexp = amax > 0.f && amax < INFINITY ? min(126, 15 - e) : 0;
             const float q2 = __uint_as_float(static_cast<uint32_t>(127 + qexp) << 23), qs = ks == ks ? copysignf(q2, ks) : ks;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
@@ -796,8 +796,9 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
                     qb[nt][kk][i] = half2_bits(__floats2half2_rn(lo(qb[nt][kk][i]) * f, hi(qb[nt][kk][i]) * f));
                 }
             const float back = __uint_as_float(static_cast<uint32_t>(127 - qexp) << 23);
-            sl2[nt][0] *= ks_abs * __shfl_sync(0xffffffffu, back, 8 * tig);      // (column 2 tig is held by lanes 8 tig ..)
-            sl2[nt][1] *= ks_abs * __shfl_sync(0xffffffffu, back, 8 * tig + 4);
+            // (column 2 tig is held by lanes 8 tig ..; the power of two first: a small logit scale goes with large queries)
+            sl2[nt][0] = sl2[nt][0] * __shfl_sync(0xffffffffu, back, 8 * tig) * ks_abs;
+            sl2[nt][1] = sl2[nt][1] * __shfl_sync(0xffffffffu, back, 8 * tig + 4) * ks_abs;
         }
     }
 
