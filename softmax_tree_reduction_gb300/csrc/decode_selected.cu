@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(SelCfg<D, kFp8, W>::kThreads, 1) decode_select
         for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
         // amax = f 2^e with f in [0.5, 1); powers of two are made from their exponent bits
         const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 126;
-        const int qexp = amax > 0.f && amax < INFINITY ? max(-100, min(100, 15 - e)) : 0;
+        const int qexp = amax > 0.f && amax < INFINITY ? min(126, 15 - e) : 0;  // (15 - e is -113 or more)
         const float qs = __uint_as_float(static_cast<uint32_t>(127 + qexp) << 23);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -377,7 +377,8 @@ __global__ void __launch_bounds__(SelCfg<D, kFp8, W>::kThreads, 1) decode_select
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     qb[nt][kk][i] = half2_bits(__floats2half2_rn(lo(qb[nt][kk][i]) * qs, hi(qb[nt][kk][i]) * qs));
-        sl2 *= __ldg(p.k_scale + g) * __uint_as_float(static_cast<uint32_t>(127 - qexp) << 23);
+        // (the power of two first: a small logit scale goes with large queries)
+        sl2 = sl2 * __uint_as_float(static_cast<uint32_t>(127 - qexp) << 23) * __ldg(p.k_scale + g);
         vscale = __ldg(p.v_scale + g) * (1.f / kPScale);
     }
 

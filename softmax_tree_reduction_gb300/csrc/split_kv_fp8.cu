@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(Fp8Cfg<HB>::kThreads, 1)
     if (amax > 0.f) {
         int e;
         frexpf(amax, &e);  // amax = f * 2^e, f in [0.5, 1)
-        qexp = max(-100, min(100, 15 - e));
+        qexp = max(-113, min(126, 15 - e));  // (-113: the largest BF16 numbers)
     }
     const float qs = ldexpf(1.f, qexp);
     uint32_t qb[NT][D / 16][2];
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(Fp8Cfg<HB>::kThreads, 1)
             qb[nt][kk][1] =
                 half2_bits(__floats2half2_rn(lo(qw[nt][2 * kk + 1]) * qs, hi(qw[nt][2 * kk + 1]) * qs));
         }
-    const float sl2 = p.scale_log2 * ks / qs;
+    const float sl2 = p.scale_log2 / qs * ks;  // (in this order: a small logit scale goes with large queries)
 
     // causal limits of this thread's columns (2 tig, 2 tig + 1 of each n-tile)
     const int causal_from = p.causal ? N - p.nq + 1 : 0x7fffffff;

@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(Tc05F8Cfg<NCP, CPT>::kThreads, 1)
     if (amax > 0.f) {
         int e;
         frexpf(amax, &e);  // amax = f 2^e, f in [0.5, 1)
-        qexp = max(-100, min(100, 8 - e));
+        qexp = max(-120, min(126, 8 - e));  // (-120: the largest BF16 numbers)
     }
     const float qsc = ldexpf(1.f, qexp);
     for (int idx = ct; idx < NCP * 16; idx += NT) {
@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(Tc05F8Cfg<NCP, CPT>::kThreads, 1)
         N = 0;
     }
     const int causal_from = p.causal ? N - p.nq + 1 : 0x7fffffff;
-    const float sl2 = p.scale_log2 * ks / qsc;
+    const float sl2 = p.scale_log2 / qsc * ks;  // (in this order: a small logit scale goes with large queries)
     float lp[CPT];  // this thread's partial denominators of its columns, relative to m_ref
 #pragma unroll
     for (int i = 0; i < CPT; ++i) lp[i] = 0.f;
