@@ -526,7 +526,7 @@ typedef struct {
     int64_t step_stride_b;   /* bytes; multiples of head_dim / 16; all three 0: the layout above */
     int64_t step_stride_h;
     int64_t step_stride_t;
-    const float *k_scale;    /* device float [num_kv_heads], within 2^-100 .. 2^100; both or neither */
+    const float *k_scale;    /* device float [num_kv_heads], within 2^-60 .. 2^60; both or neither */
     const float *v_scale;
 } ta_int4_kv;
 

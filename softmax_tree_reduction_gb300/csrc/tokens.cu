@@ -430,7 +430,8 @@ __device__ __forceinline__ uint32_t int4_codes(float (&z)[8], float top, uint32_
     return w - 0x3f400000u;  // (what the sum of 16^i times 0x4b400000 leaves in the word)
 }
 
-// z: FP32 quotients by a KV head's scale (infinite where they overflow).
+// z: FP32 quotients by a KV head's scale (infinite where they overflow).  From scales of 2^-93 on the correction of every
+// quotient that has a code other than 0 (2^-10 or more) is a multiple of 2^-149 before its rounding, so exact.
 __device__ __forceinline__ void scale_down(float (&z)[8], const float* scale, int h) {
     if (!scale) return;
     const float s = __ldg(scale + h), r = 1.f / s;

@@ -115,3 +115,42 @@ def test_small_keys_turned(size, d, rot, inter, norm, dt):
     assert bool(((n * ss - want).abs() <= ss / 2 + off)[near].all())
     between = ~far & ~near                                            # 7 .. 7.5 steps: rounded or clamped to the outermost code
     assert torch.equal(n[between], 7 * torch.sign(want[between])) and ta.tree_attn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("power", [-90, -60, 0, 60, 100])
+def test_scales_at_and_beyond_the_ends_of_their_range(power):
+    """Quotients by a scale next to the middle of two codes of the smallest step, where a correction that lost its last bits
+    would round to the other side (as it would at scales of 2^-100); and random vectors."""
+    near = [(0xC00001, 31457284), (0xC00009, 31457304), (0x800002, 20971524), (0x800006, 20971534), (0x80000A, 20971544), (0x80000E, 20971554),
+            (0xC00003, 31457286), (0xC00007, 31457296), (0xC0000F, 31457316)]
+    sc = torch.tensor([m * 2.0 ** (power - 23) for m, _ in near], dtype=torch.float64).float()
+    z = torch.tensor([n * 2.0 ** (power - 32) for _, n in near], dtype=torch.float64).float()
+    g = torch.Generator().manual_seed(power + 100)
+    k = torch.randn(300, len(near), 64, generator=g) * sc[:, None] * 0.05
+    k[0] = 0
+    k[0, :, 0] = sc * 7 * 2.0 ** -9                                      # a step of 2^-9
+    k[0, :, 1], k[0, :, 6], k[0, :, 15] = z, -z, z
+    k[0, :, 16:32] = -k[0, :, :16]
+    _, got = write_rows(k, k.flip(0), k_scale=sc.cuda(), v_scale=sc.cuda())
+    for i, x in enumerate((k, k.flip(0))):
+        n, st = wref.quantize(x, sc)
+        assert torch.equal(got[2 + i], st.view(torch.uint8)) and torch.equal(got[i], wref.pack(n))
+
+
+@pytest.mark.parametrize("d,G,nq", [(128, 4, 1), (64, 8, 1), (128, 8, 2)])
+@pytest.mark.parametrize("power", [-60, 60])
+def test_attention_at_the_ends_of_the_scales_range(power, d, G, nq):
+    """Scales times a power of two: the same bits of the outputs times it, or with the inverse in the logit scale.  Steps up to 448 and
+    thousands of tokens of like weight, so that sums come as large as they can."""
+    g = torch.Generator().manual_seed(d + G)
+    T, hkv = 3000, 2
+    codes = [torch.randint(0, 256, (1, hkv, T, d // 2), generator=g, dtype=torch.uint8).cuda() for _ in range(2)]
+    codes[1][:, :, :, 0] = 0xFF
+    steps = [torch.randint(lo, 0x7F, (1, hkv, T, d // 16), generator=g, dtype=torch.uint8).cuda().view(FP8) for lo in (1, 0x7C)]
+    q = (torch.randn(1, hkv * G, nq, d, generator=g) * 2.0 ** -12).to(BF16).cuda()
+    lens = torch.tensor([T], dtype=torch.int32).cuda()
+    ks, vs = ((torch.rand(hkv, generator=g) * 0.5 + 0.5).cuda() for _ in range(2))
+    out, lse = ta.tree_attn_decode_int4(q, *codes, *steps, lens, scale=0.125, k_scale=ks, v_scale=vs)
+    o, z = ta.tree_attn_decode_int4(q, *codes, *steps, lens, scale=0.125 * 2.0 ** -power, k_scale=ks * 2.0 ** power, v_scale=vs * 2.0 ** power)
+    assert torch.equal(o, out * 2.0 ** power) and torch.equal(z, lse)
+    assert bool(torch.isfinite(o).all()) and bool(torch.isfinite(lse).all()) and ta.tree_attn_get_device_error() == 0
