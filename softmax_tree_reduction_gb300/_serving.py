@@ -239,8 +239,9 @@ def tree_attn_cache_write_int4(k: torch.Tensor, v: torch.Tensor, k_codes: torch.
     ``block_table`` (two channels a byte, the even one in the low half), and steps, float8_e4m3fn
     [.., d / 16]; a channel's value is scale * step * (code - 8) with the FP32 scale of its KV head
     (``k_scale``/``v_scale``, both or neither).  Each 16 channels get the step next to a seventh of
-    their largest magnitude and the codes next to their quotients by it.  The other arguments are
-    tree_attn_cache_write's.  Returns q_out (None without q).
+    their largest magnitude and the codes next to their quotients by it.  Steps lie between 2^-9 and 448 and
+    are coarse below 2^-6: heads whose vectors are small (below about 0.05) want a scale, for instance their
+    largest magnitude / 448.  The other arguments are tree_attn_cache_write's.  Returns q_out (None without q).
     """
     if stream is not None or (q is not None and q_out is None):
         stream, ctx = _on(stream, k)

@@ -18,14 +18,18 @@
 // What bounds it, on a GB300 (fractions of the copy rate 6782.8 GB/s; 8 KV heads of 128 channels):
 //  BF16, E4M3, FP32   HBM: 64 rows with a window of 4096 tokens 148.9 us (1.07), 83.1 (0.96), 302.7 (1.05); 16 rows 42.4
 //                     (0.94), 25.3 (0.78), 83.5 (0.95); one row with a window of 1024 tokens 5.1 to 6.8 us: latencies.
-//  4 bits             instructions: a slab of 16 tokens takes a warp 308 of them for 4 columns (key codes 88, value codes
-//                     124, softmax and loop 63, copies 32), and the copy rate leaves an SM 392 issue slots for it; one row
-//                     of 524288 tokens 109.9 us (0.81), of 131072 34.2 (0.65: 8 us of start, merge and second kernel).
+//  4 bits             issue: a slab of 16 tokens takes a warp 308 instructions for 4 columns (key codes 88, value codes
+//                     124, softmax and loop 63, copies 32), and the copy rate leaves an SM 392 issue slots for it; the
+//                     three warps a scheduler that the registers allow fill 65 % of them (a warp waits 0.15 of the time for
+//                     a pipe, 0.12 for its dispatch, 0.16 for the instruction before, 0.22 for other warps' turns, 0.05
+//                     for loads).  One row of 524288 tokens 109.5 us (0.81), of 131072 34.1 (0.65: 8 us of start, merge and second kernel).
 //                     Masks and row checks in every slab: 510 instructions and 52.9 us at 131072 tokens; picks of
 //                     codes that the compiler made two instructions of each: 44.4; two products for the weights' parts where
 //                     one tile holds both, maxima over the lanes in every step: 62.8.
-//  several queries    16 columns of a KV head take all registers (two blocks an SM) and a slab at a time: 8 rows of four
-//                     queries with a window of 4096 tokens in 4 bits 22.2 us against 15.0 of one query.
+//  several queries    16 columns of a KV head take all registers (two blocks an SM, two warps a scheduler) and a slab at a
+//                     time, one chain of dependent steps: issue is 37 to 39 % busy, a warp waits 0.3 of the time for the
+//                     instruction before.  8 rows of four queries with a window of 4096 tokens in 4 bits 22.2 us
+//                     against 15.0 of one query; 16 rows, E4M3 37.3 (25.6), BF16 47.1 (42.8).  FP32, 244 (84.5): see below.
 //
 // The values of 4-bit caches are made exactly (int4.cuh), so the tensor cores multiply the values that the cache holds.
 #include <cuda_bf16.h>
@@ -824,7 +828,8 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
         }
         stage_out = stage_out + Cf::kStageBytes == kStages * Cf::kStageBytes ? 0u : stage_out + Cf::kStageBytes;
 
-        // S^T[16 tokens x columns] = K Q^T per slab, two accumulators per n-tile
+        // S^T[16 tokens x columns] = K Q^T per slab, two accumulators per n-tile (one where two slabs are two chains
+        // already: 16 ragged rows in 4 bits 82.3 us against 81.8, the others alike)
         constexpr int kChains = 2;
         float sacc[J][kChains][NT][4];
 #pragma unroll
@@ -1195,7 +1200,10 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
 // -------------------------------------------------------------- FP32 caches
 // CUDA cores, as in the decode over selected pages: eight lanes hold a token's channels and a
 // warp's four groups take every fourth token of a slab; from 3 columns of a KV head on two warps
-// share a ring and take half of the columns each.
+// share a ring and take half of the columns each.  More than 8 columns take several blocks, which read the cache again (from
+// L2).  16 columns (four queries of 16 rows with a window of 4096 tokens) 244 us against 84.5 for 4: three times the
+// instructions (124 M; issue 48 % busy, a third of the time of the three warps a scheduler waiting for shared memory and
+// shuffles), and 256 blocks, one an SM, are two waves of 152.
 template <int D, int P, int kRings_>
 struct SpanF32Cfg {
     static constexpr int kRowBytes = 4 * D;

@@ -1,5 +1,7 @@
 // Reading the codes of 4-bit caches.
 //
+// Small whole numbers become FP16 ones by putting their bits under the exponent of 1024, a widely published
+// method; the constants for E4M3 steps are derived here.
 // A channel's value is step * (code - 8) * scale.  (w & 0x000f000f) | 0x64006400 is a word of eight codes as
 // the FP16 pair 1024 + code of channels 0 and 4, and one FMA with step / 8 and -1032 step / 8 makes step / 8 * (code -
 // 8) of it, exactly: both constants have at most 11 significant bits (1032 = 8 * 129, times the 4 bits of an

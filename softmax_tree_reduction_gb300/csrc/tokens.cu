@@ -376,13 +376,14 @@ __device__ __forceinline__ int64_t cache_place(const TokenParams& p, int t, int 
 }
 
 // ------------------------------------------------------------- 4-bit caches
-// Writing one is bound by instructions (16384 tokens of 8 + 8 BF16 heads, 86 MB: 26.8 us against 12.7 at the copy rate, 137
-// instructions for 512 channels; with divisions and a step for each run of four channels 54.2), so quotients are
-// not divisions: with r the FP32 number next to 1 / c, q = z r and the correction q + (z - q c) r is the FP32
-// quotient itself (Markstein 1990, "Computation of elementary functions on the IBM RISC System/6000 processor";
-// for every E4M3 c and for 7 also checked over all z).  An FP32 quotient lies in the middle of two whole
-// numbers only if z / c does, so rounding it to the nearest one, ties to even, is exact.  Reading 65536 tokens
-// back as BF16: 57 us (0.89 of the copy rate).
+// Writing one (16384 tokens of 8 + 8 BF16 heads, 86 MB: 26.8 us against 12.7 at the copy rate) takes 137 instructions for 512
+// channels, which keep issue 59 % busy: six warps a scheduler wait 0.28 of the time for the loads of the next four
+// vectors, which start when the codes of the last four are done, and 0.2 for results of the instruction before.
+// With divisions and a step for each run of four channels it took 54.2, so quotients are not divisions: with r the
+// FP32 number next to 1 / c, q = z r and the correction q + (z - q c) r is the FP32 quotient itself (Markstein 1990,
+// "Computation of elementary functions on the IBM RISC System/6000 processor"; for every E4M3 c and for 7 also
+// checked over all z).  An FP32 quotient lies in the middle of two whole numbers only if z / c does, so rounding it to
+// the nearest one, ties to even, is exact.  Reading 65536 tokens back as BF16: 57 us (0.89 of the copy rate).
 __device__ __forceinline__ float quotient(float z, float c, float r) {
     const float q = z * r;
     return fmaf(fmaf(-q, c, z), r, q);
