@@ -596,9 +596,102 @@ __device__ __forceinline__ bool any_not_finite(uint32_t slab, int lane) {
 constexpr float kSlack = 4.f;
 constexpr float kWeightBits = 11.f;     // FP16 weights times 2^11: below 2^15, and a low part's last bit is 2^-35
 
+// Logits of millions (log2 units).  A maximum is a rounded product, and what an FMA leaves of a logit less its maximum holds what
+// was rounded off: up to 2^-2 at 2^22, but as much as FP16 weights have room for at 2^24, and BF16 ones at 2^30.  A block that met
+// a maximum beyond these bounds makes its states once more (plain_state).  That costs other calls in 4 bits 1 to 2 % (registers
+// for the call: 131072 tokens 34.1 -> 34.5 us, 16 ragged rows 81.8 -> 83.0); rounded logits in the steps themselves 2 to 5 %, the
+// function inlined 5 %.
+template <int kCache>
+constexpr float kFar = kCache == kBf16 ? 67108864.f : 4194304.f;  // 2^26, 2^22
+
+// A warp's state of its slabs without tensor cores, logits rounded before the maximum is taken from them: token by token for
+// each column, a lane holding D / 32 channels.
+template <int D, int kCache, int kWarps, int kCols>
+__device__ __noinline__ void plain_state(const SpanParams& p, const Piece& piece, WarpStates<D, kWarps, kCols>* states) {
+    constexpr int E = D / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ch = E * lane;
+    const int g = blockIdx.y / p.ngroups, c_first = kCols * (blockIdx.y - g * p.ngroups), ncol = min(kCols, p.cols - c_first);
+    const size_t row0 = static_cast<size_t>(piece.b) * p.Hq * p.nq + static_cast<size_t>(g) * p.cols + c_first;
+    const float k_scale = kCache != kBf16 && p.k_scale ? __ldg(p.k_scale + g) : 1.f, v_scale = kCache != kBf16 && p.v_scale ? __ldg(p.v_scale + g) : 1.f;
+    const Span span(p, piece.N);
+    const int32_t* table = p.block_table ? p.block_table + static_cast<int64_t>(piece.b) * p.max_pages : nullptr;
+    // channels ch .. of a vector whose bytes (and steps) lie at these offsets
+    auto vec = [&](const uint8_t* x, const uint8_t* steps, int64_t off, int64_t step_off, float (&f)[E]) {
+        if constexpr (kCache == kInt4) {
+            if (!bytes_in(off + ch / 2, E / 2, p.cache_bytes, p.err) || !bytes_in(step_off + ch / 16, 1, p.step_bytes, p.err)) return;
+            const float step = __half2float(__ushort_as_half(static_cast<unsigned short>(e4m3x2_to_f16x2(__ldg(steps + step_off + ch / 16)) & 0xffffu)));
+#pragma unroll
+            for (int e = 0; e < E; ++e) f[e] = step * static_cast<float>(((__ldg(x + off + (ch + e) / 2) >> (4 * (e & 1))) & 15) - 8);
+        } else if constexpr (kCache == kE4m3) {
+            if (!bytes_in(off + ch, E, p.cache_bytes, p.err)) return;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                f[e] = __half2float(__ushort_as_half(static_cast<unsigned short>(e4m3x2_to_f16x2(__ldg(x + off + ch + e)) & 0xffffu)));
+        } else {
+            if (!bytes_in(off + 2 * ch, 2 * E, p.cache_bytes, p.err)) return;
+#pragma unroll
+            for (int e = 0; e < E; ++e) f[e] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(x + off)[ch + e]);
+        }
+    };
+#pragma unroll 1
+    for (int c = 0; c < kCols; ++c) {
+        float m = -INFINITY, l = 0.f, o[E], q[E], amax = 0.f;
+        const bool on = c < ncol && in_bounds((row0 + c + 1) * D - 1, p.q_elems, p.err);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            o[e] = 0.f;
+            q[e] = on ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[(row0 + c) * D + ch + e]) : 0.f;
+            amax = fmaxf(amax, fabsf(q[e]));
+        }
+        // (E4M3 and 4 bits: products as large as those of the tensor cores' operands)
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+        const int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 126;
+        const int qexp = kCache != kBf16 && amax > 0.f && amax < INFINITY ? min(126, 15 - ex) : 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) q[e] *= __uint_as_float(static_cast<uint32_t>(127 + qexp) << 23);
+        const float scale = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - qexp) << 23) * k_scale;
+        const int s = piece.N - p.nq + (c_first + c) % p.nq;
+#pragma unroll 1
+        for (int u = piece.u0 + warp; on && u < piece.u1; u += kWarps) {
+            const int t0 = span.token(u);
+            int page = piece.b;
+            if (table) {
+                const int at = t0 >> p.page_shift;
+                page = in_bounds(table - p.block_table + at, p.table_elems, p.err) ? __ldg(table + at) : -1;
+                if (page < 0 || page >= p.num_pages) continue;  // (reported already; the row is NaN)
+            }
+            const int64_t slot = table ? t0 & ((1 << p.page_shift) - 1) : t0;
+            const int64_t off = page * p.sb + g * p.sh + slot * p.st, steps = page * p.tb + g * p.th + slot * p.tt;
+#pragma unroll 1
+            for (int i = 0; i < kSlab; ++i) {
+                if (t0 + i >= piece.N || !sees(p, s, t0 + i)) continue;
+                float k[E] = {}, v[E] = {};
+                vec(p.k, p.k_steps, off + i * p.st, steps + i * p.tt, k);
+                vec(p.v, p.v_steps, off + i * p.st, steps + i * p.tt, v);
+                float y = 0.f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) y = fmaf(q[e], k[e], y);
+#pragma unroll
+                for (int x = 16; x > 0; x >>= 1) y += __shfl_xor_sync(0xffffffffu, y, x);
+                y = __fmul_rn(y, scale);
+                const float mn = fmaxf(m, y), ms = (mn == -INFINITY) ? 0.f : mn;
+                const float al = ex2(m - ms), w = ex2(__fsub_rn(y, ms));
+                m = mn;
+                l = fmaf(l, al, w);
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = fmaf(w, v[e], o[e] * al);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) states->o[warp][c][ch + e] = o[e] * v_scale;
+        if (lane == 0) states->m[warp][c] = m, states->l[warp][c] = l;
+    }
+}
+
 // kMulti: several queries a row (masks that differ between columns).
 template <int D, int kCache, int kLayout, bool kMulti, int W, int kStages_>
-__global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti>()) decode_span_kernel(const SpanParams p) {
+__global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti>()) decode_span_kernel(const __grid_constant__ SpanParams p) {
     using Cf = SpanCfg<D, kCache, kLayout, W, kStages_>;
     constexpr int J = Cf::kSub, kWarps = W, kStages = Cf::kStages, NT = Cf::NT;
     constexpr bool kTwo = kCache != kBf16;   // FP16 operands: weights in two parts
@@ -606,7 +699,7 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
     static_assert(!kHalves || (kTwo && !kMulti), "low parts beside the high ones");
     const int nq = kMulti ? p.nq : 1;
     extern __shared__ __align__(128) uint8_t smem[];
-    int* bad_flag = reinterpret_cast<int*>(smem + Cf::kRing);
+    int* bad_flag = reinterpret_cast<int*>(smem + Cf::kRing);  // [0] a bad page, [1] a maximum beyond kFar
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gid = lane >> 2, tig = lane & 3, r8 = lane & 7;
@@ -623,7 +716,7 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
     Piece& piece = *reinterpret_cast<Piece*>(smem + Cf::kRing + 16);
     int* pre = reinterpret_cast<int*>(smem + Cf::kBoxOff);  // (with even shares: no box then)
     if (p.part_o && warp == 0) scan_rows(p, pre, blockIdx.x == 0 && blockIdx.y == 0);
-    if (threadIdx.x == 0) piece.begin(p, pre), *bad_flag = 0;
+    if (threadIdx.x == 0) piece.begin(p, pre), bad_flag[0] = bad_flag[1] = 0;
     __syncthreads();
     while (piece.more()) {
     const int b = piece.b, g = blockIdx.y / p.ngroups, cg = blockIdx.y - g * p.ngroups;
@@ -918,6 +1011,7 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
             }
         }
         if (__any_sync(0xffffffffu, raise)) {
+            bool beyond = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -930,6 +1024,7 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
                     const float mn = fmaxf(m[nt][i], bm * sl2[nt][i]);
                     const float al = ex2(m[nt][i] - ((mn == -INFINITY) ? 0.f : mn));
                     m[nt][i] = mn;
+                    beyond = beyond || (fabsf(mn) > kFar<kCache> && mn > -INFINITY);
                     l[nt][i] *= al;
 #pragma unroll
                     for (int mt = 0; mt < D / 16; ++mt) {
@@ -938,6 +1033,7 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
                     }
                 }
             }
+            if (beyond) bad_flag[1] = 1;
         }
         // P^T as B fragments: the weights as the sum of three BF16 numbers (all 24 bits) or two FP16 ones (22 bits,
         // the low one in bl, or in the tile's other half)
@@ -1189,10 +1285,14 @@ __global__ void __launch_bounds__(32 * W, span_blocks<D, kCache, kLayout, kMulti
         }
     }
     __syncthreads();
+    if (bad_flag[1]) {
+        plain_state<D, kCache, kWarps, kCols>(p, piece, states);
+        __syncthreads();
+    }
     finish_piece<D, kWarps, kCols, Cf::kThreads>(p, piece, row0, ncol, bad_len || *bad_flag, states,
                                                  reinterpret_cast<SpanBox<D, kCols>*>(smem + Cf::kBoxOff));
     __syncthreads();  // (merge buffers and piece are read)
-    if (threadIdx.x == 0) piece.next(p), *bad_flag = 0;
+    if (threadIdx.x == 0) piece.next(p), bad_flag[0] = bad_flag[1] = 0;
     __syncthreads();
     }
 }
