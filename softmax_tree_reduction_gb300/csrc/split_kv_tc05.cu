@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(Tc05Cfg<NCP, CPT>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < CPT; ++i) {
                 lp[i] *= alpha_s[c_base + i];
-                xs[i] += shift_s[c_base + i];
+                xs[i] = on_grid(xs[i] + shift_s[c_base + i], m_ref[c_base + i]);
                 mneg |= static_cast<uint32_t>(m_ref[c_base + i] == -INFINITY) << i;
             }
             mneg &= gmask;

@@ -340,6 +340,15 @@ __device__ __forceinline__ bool softmax_any(bool pred) {
     return out != 0;
 }
 
+// The offset x of a logit from its reference m, where m is 2^26 or more: rounded to whole units of m's last place, as the logit
+// itself would be.  (An FMA leaves what is beyond them, up to half a unit: 2^8 and more at 2^32, where the weight of the
+// very maximum would overflow or vanish.)
+__device__ __forceinline__ float on_grid(float x, float m) {
+    const uint32_t e = __float_as_uint(m) & 0x7f800000u;
+    const float g = e >= 0x4c800000u && e < 0x7f800000u ? __uint_as_float(e | 0x400000u) : 0.f;  // 1.5 * 2^e
+    return __fsub_rn(__fadd_rn(x, g), g);
+}
+
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
