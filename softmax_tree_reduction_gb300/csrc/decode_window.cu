@@ -22,13 +22,13 @@
 //                     124, softmax and loop 63, copies 32), and the copy rate leaves an SM 392 issue slots for it; the
 //                     three warps a scheduler that the registers allow fill 65 % of them (a warp waits 0.15 of the time for
 //                     a pipe, 0.12 for its dispatch, 0.16 for the instruction before, 0.22 for other warps' turns, 0.05
-//                     for loads).  One row of 524288 tokens 109.5 us (0.81), of 131072 34.1 (0.65: 8 us of start, merge and second kernel).
+//                     for loads).  One row of 524288 tokens 110.7 us (0.80), of 131072 34.5 (0.65: 8 us of start, merge and second kernel).
 //                     Masks and row checks in every slab: 510 instructions and 52.9 us at 131072 tokens; picks of
 //                     codes that the compiler made two instructions of each: 44.4; two products for the weights' parts where
 //                     one tile holds both, maxima over the lanes in every step: 62.8.
 //  several queries    16 columns of a KV head take all registers (two blocks an SM, two warps a scheduler) and a slab at a
 //                     time, one chain of dependent steps: issue is 37 to 39 % busy, a warp waits 0.3 of the time for the
-//                     instruction before.  8 rows of four queries with a window of 4096 tokens in 4 bits 22.2 us
+//                     instruction before.  8 rows of four queries with a window of 4096 tokens in 4 bits 22.1 us
 //                     against 15.0 of one query; 16 rows, E4M3 37.3 (25.6), BF16 47.1 (42.8).  FP32, 244 (84.5): see below.
 //
 // The values of 4-bit caches are made exactly (int4.cuh), so the tensor cores multiply the values that the cache holds.
