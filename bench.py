@@ -48,15 +48,15 @@ NCU_TRAFFIC = {
         "src_sha256": "fabe09c7fc7fd0f9f4420c4d3e546adec36ce0456347c5c323a30b74167dd509"},
     # tcgen05 kernel, the same layer with 8 and 16 queries per row (32 and 64 columns per KV head)
     ("tc05", "llama3.1-8b-decode-layer", 8): {
-        "bytes_per_launch": 537041152 + 2807296, "num_splits": 19,
-        "src_sha256": "4b30520dfbe8833e98e24e31fd99df4d8cd64c5336da4dbcb3f8cb0042c944e3"},
+        "bytes_per_launch": 537043456 + 3120896, "num_splits": 19,
+        "src_sha256": "c66fa06b2e862760b4c698566f21c7835b2b9ced61dd2d1b3faf3dcbbcca0b01"},
     ("tc05", "llama3.1-8b-decode-layer", 16): {
-        "bytes_per_launch": 537189632 + 3212032, "num_splits": 19,
-        "src_sha256": "4b30520dfbe8833e98e24e31fd99df4d8cd64c5336da4dbcb3f8cb0042c944e3"},
+        "bytes_per_launch": 537191424 + 2684160, "num_splits": 19,
+        "src_sha256": "c66fa06b2e862760b4c698566f21c7835b2b9ced61dd2d1b3faf3dcbbcca0b01"},
     # tcgen05 FP8 kernel, the same layer's E4M3 cache with 8 queries per row (32 columns per KV head)
     ("fp8tc05", "llama3.1-8b-decode-layer", 8): {
-        "bytes_per_launch": 268612096 + 2792192, "num_splits": 19,
-        "src_sha256": "dfe2297c48880c3d45ba1cfd07fbf263ee900528c572e6cd5c9fed58e6f65f62"},
+        "bytes_per_launch": 268614400 + 2772224, "num_splits": 19,
+        "src_sha256": "390284d42f5619962a2885eda7966e0665abc1a62844445e0e2ab83377f7e812"},
 }
 
 
